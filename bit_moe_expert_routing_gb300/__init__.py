@@ -58,9 +58,29 @@ class moe_route_view(ctypes.Structure):
                 ("h", ctypes.c_void_p), ("y_acc", ctypes.c_void_p)]
 
 
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("k_biases", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("v_biases", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class moe_kv_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("max_kv", ctypes.c_int), ("q_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int)]
+
+
+class moe_attention(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 # name -> (restype, argtypes), mirroring include/moe.h
 _VP, _CI, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _W = ctypes.POINTER(moe_weights)
+_KC, _KB, _AT = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch), ctypes.POINTER(moe_attention)
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "moe_workspace_size": (_SZ, [_W, _CI]),
     "moe_layer_forward": (_CI, [_W, _VP, _CI, _VP, _VP, _SZ, _VP]),
@@ -78,6 +98,10 @@ SIGNATURES = {
     "moe_debug_dequant": (_CI, [ctypes.POINTER(moe_qmatrix), _CI, _CI, _CI, _VP, _VP]),
     "moe_expanded_weights_bytes": (_SZ, [_W]),
     "moe_layer_forward_expanded": (_CI, [_W, _VP, _CI, _VP, _VP, _SZ, _VP, _SZ, _VP]),
+    "moe_kv_append": (_CI, [_KC, _KB, _VP, _LL, _VP, _LL, _VP]),
+    "moe_kv_read": (_CI, [_KC, _KB, _VP, _VP, _VP]),
+    "moe_attention_workspace_size": (_SZ, [_KC, _KB, _AT]),
+    "moe_attention_forward": (_CI, [_KC, _KB, _AT, _VP, _LL, _VP, _VP, _VP, _SZ, _VP]),
     "moe_last_launch_count": (_CI, []),
     "moe_status_string": (ctypes.c_char_p, [_CI]),
 }
@@ -185,6 +209,23 @@ def moe_debug_dequant(m: moe_qmatrix, expert, rows, K, out_ptr, stream) -> int:
     return lib().moe_debug_dequant(ctypes.byref(m), expert, rows, K, out_ptr, stream)
 
 
+def moe_kv_append(cache, batch, k_ptr, k_stride, v_ptr, v_stride, stream) -> int:
+    return lib().moe_kv_append(ctypes.byref(cache), ctypes.byref(batch), k_ptr, k_stride, v_ptr, v_stride, stream)
+
+
+def moe_kv_read(cache, batch, k_ptr, v_ptr, stream) -> int:
+    return lib().moe_kv_read(ctypes.byref(cache), ctypes.byref(batch), k_ptr, v_ptr, stream)
+
+
+def moe_attention_workspace_size(cache, batch, attn: moe_attention) -> int:
+    return lib().moe_attention_workspace_size(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(attn))
+
+
+def moe_attention_forward(cache, batch, attn, q_ptr, q_stride, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return lib().moe_attention_forward(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(attn), q_ptr, q_stride,
+                                       out_ptr, lse_ptr, ws_ptr, ws_bytes, stream)
+
+
 def moe_last_launch_count() -> int:
     return lib().moe_last_launch_count()
 
@@ -276,3 +317,127 @@ def ws_tensor(workspace, ptr: int, shape, dtype):
     off = int(ptr) - workspace.data_ptr()
     assert 0 <= off and off + n * itemsize <= workspace.numel() and off % itemsize == 0
     return workspace[off:off + n * itemsize].view(dtype).reshape(shape)
+
+
+class KVBatch:
+    """The sequences of one step (moe_kv_batch): int32 device tensors `q_off`
+    [n_seqs + 1], `kv_len` [n_seqs] and `block_table` [n_seqs, pages], and the
+    host's bounds on them. The tensors are kept, not copied: a serving loop
+    may update them in place between steps."""
+
+    def __init__(self, q_off, kv_len, block_table, n_tokens: int, max_new: int, max_kv: int):
+        import torch
+        for name, t, nd in (("q_off", q_off, 1), ("kv_len", kv_len, 1), ("block_table", block_table, 2)):
+            if t.dtype != torch.int32 or t.dim() != nd or t.device.type != "cuda" or (t.numel() and t.stride(-1) != 1):
+                raise ValueError(f"{name}: a CUDA int32 tensor with {nd} dimension(s), last one contiguous")
+        n = kv_len.shape[0]
+        if q_off.shape[0] != n + 1 or block_table.shape[0] != n:
+            raise ValueError("q_off has n_seqs + 1 entries, kv_len and block_table n_seqs")
+        # a row may be read up to its stride: take the width where rows are the tensor's own
+        stride = block_table.stride(0) if n > 1 else block_table.shape[1]
+        if stride != block_table.shape[1]:
+            raise ValueError("block_table: contiguous")
+        self._t = (q_off, kv_len, block_table)
+        self.n_tokens = n_tokens
+        self.c = moe_kv_batch(n, n_tokens, max_new, max_kv, q_off.data_ptr(), kv_len.data_ptr(),
+                              block_table.data_ptr(), stride)
+
+
+class KVCache:
+    """A 4-bit key/value cache: the arrays of moe_kv_cache as torch tensors
+    (codes int32 [pages, kv heads, page size, head dim / 8]; scales and biases
+    bf16 [pages, kv heads, page size, head dim / 64]) and the operations on
+    it. Calls are enqueued on `stream` (the current one by default); tensors
+    they make are made there, and tensors they are given must be ready there."""
+
+    def __init__(self, k_codes, k_scales, k_biases, v_codes, v_scales, v_biases):
+        import torch
+        pages, heads, size, words = k_codes.shape
+        for codes, scales, biases in ((k_codes, k_scales, k_biases), (v_codes, v_scales, v_biases)):
+            for t, dt, n in ((codes, torch.int32, words), (scales, torch.bfloat16, words // 8),
+                             (biases, torch.bfloat16, words // 8)):
+                if t.shape != (pages, heads, size, n) or t.dtype != dt or not t.is_contiguous() or \
+                        t.device != k_codes.device or t.device.type != "cuda":
+                    raise ValueError("a cache has contiguous CUDA codes int32 [pages, kv heads, page size, head dim / 8] "
+                                     "and scales, biases bf16 [pages, kv heads, page size, head dim / 64]")
+        self.k_codes, self.k_scales, self.k_biases = k_codes, k_scales, k_biases
+        self.v_codes, self.v_scales, self.v_biases = v_codes, v_scales, v_biases
+        self.kv_heads, self.head_dim = heads, words * 8
+        self.status = torch.zeros(256, dtype=torch.uint8, device=k_codes.device)
+        self.c = moe_kv_cache(pages, size, heads, words * 8, k_codes.data_ptr(), k_scales.data_ptr(),
+                              k_biases.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), v_biases.data_ptr(),
+                              self.status.data_ptr())
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        a = []
+        for _ in range(2):
+            a.append(torch.zeros(n_pages, kv_heads, page_size, head_dim // 8, dtype=torch.int32, device=device))
+            for _ in range(2):
+                a.append(torch.zeros(n_pages, kv_heads, page_size, head_dim // 64, dtype=torch.bfloat16, device=device))
+        return cls(*a)
+
+    def _rows(self, name, t, n_tokens, heads):
+        import torch
+        if t.dtype != torch.bfloat16 or t.shape != (n_tokens, heads, self.head_dim) or t.device != self.k_codes.device:
+            raise ValueError(f"{name}: bf16 [{n_tokens}, {heads}, {self.head_dim}] on the cache's device")
+        if n_tokens == 0:
+            return heads * self.head_dim
+        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
+            raise ValueError(f"{name}: the heads of a token are contiguous")
+        return t.stride(0) if n_tokens > 1 else heads * self.head_dim
+
+    def append(self, k, v, batch: KVBatch, stream=None):
+        """Quantises k, v (bf16 [n_tokens, kv heads, head dim]) into the cache."""
+        ks = self._rows("k", k, batch.n_tokens, self.kv_heads)
+        vs = self._rows("v", v, batch.n_tokens, self.kv_heads)
+        _check(moe_kv_append(self.c, batch.c, k.data_ptr(), ks, v.data_ptr(), vs, _stream_ptr(stream)), "moe_kv_append")
+
+    def read(self, batch: KVBatch, stream=None):
+        """The step's tokens as the cache holds them: (k, v) bf16 [n_tokens, kv heads, head dim]."""
+        import contextlib
+        import torch
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            kv = torch.empty(2, batch.n_tokens, self.kv_heads, self.head_dim, dtype=torch.bfloat16,
+                             device=self.k_codes.device)
+        k, v = kv[0], kv[1]
+        _check(moe_kv_read(self.c, batch.c, k.data_ptr(), v.data_ptr(), _stream_ptr(stream)), "moe_kv_read")
+        return k, v
+
+    def attention_workspace(self, heads: int, batch: KVBatch, window: int = 0, sinks: int = 0):
+        """A workspace for attention() with these arguments (a larger batch's serves a smaller one)."""
+        import torch
+        n = moe_attention_workspace_size(self.c, batch.c, moe_attention(heads, window, sinks, 1.0))
+        if n == 0:
+            raise MoEError(MOE_ERR_ARG, "moe_attention_workspace_size")
+        return torch.empty(n, dtype=torch.uint8, device=self.k_codes.device)
+
+    def attention(self, q, batch: KVBatch, scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
+                  lse: bool = False, workspace=None, stream=None):
+        """Causal attention of the step's tokens over the cache: q bf16
+        [n_tokens, heads, head dim] -> out (the same shape), or (out, lse) with
+        lse fp32 [n_tokens, heads]. scale: 1 / sqrt(head dim) by default."""
+        import contextlib
+        import torch
+        if q.dim() != 3:
+            raise ValueError("q: bf16 [n_tokens, heads, head dim]")
+        n, heads = batch.n_tokens, q.shape[1]
+        qs = self._rows("q", q, n, heads)
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            if out is None:
+                out = torch.empty(n, heads, self.head_dim, dtype=torch.bfloat16, device=q.device)
+            elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
+                raise ValueError("out: contiguous, of q's shape, type and device")
+            l = torch.empty(n, heads, dtype=torch.float32, device=q.device) if lse else None
+            if workspace is None:
+                workspace = self.attention_workspace(heads, batch, window, sinks)
+        at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
+        _check(moe_attention_forward(self.c, batch.c, at, q.data_ptr(), qs, out.data_ptr(),
+                                     l.data_ptr() if lse else None, workspace.data_ptr(), workspace.numel(),
+                                     _stream_ptr(stream)), "moe_attention_forward")
+        return (out, l) if lse else out
+
+    def check(self, stream=None):
+        """Synchronises the stream and raises if a call since the last check met a device-side error."""
+        _check(moe_get_device_status(ctypes.c_void_p(self.status.data_ptr()), _stream_ptr(stream)), "kv cache")

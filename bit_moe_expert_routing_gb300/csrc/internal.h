@@ -123,6 +123,9 @@ cudaError_t launch_pdl(const Ctx& c, void (*kernel)(KArgs...), dim3 grid, dim3 b
 // timing is on, records an event after each one.
 void launch_done(const Ctx& c, const char* name);
 void timing_begin(const Ctx& c);
+// The same for calls that have no Ctx: with the options a call took at its start.
+void launch_done(const Options& opt, cudaStream_t s, const char* name);
+void timing_begin(const Options& opt, cudaStream_t s);
 
 // Routing: logits, top-k + weights + per-chunk histogram, scan + block map,
 // scatter. Returns the first CUDA error. With yacc_zeroed given, the router

@@ -1,0 +1,114 @@
+// C entry points of the 4-bit key/value cache and its attention: argument
+// checks on the host and the choice of kernels.
+#include <cmath>
+
+#include "kv.cuh"
+
+namespace moe {
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+moe_status make_args(const moe_kv_cache* c, const moe_kv_batch* b, KvArgs* a) {
+  if (!c || !b) return MOE_ERR_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return MOE_ERR_SHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 256 || c->n_pages < 1) return MOE_ERR_SHAPE;
+  if (b->n_seqs < 0 || b->n_tokens < 0 || b->n_tokens > kMaxTokens || b->n_seqs > 65535) return MOE_ERR_ARG;
+  if (b->max_new < 0 || b->max_kv < 0 || b->max_kv > (1 << 24) || b->table_stride < 0) return MOE_ERR_ARG;
+  const void* arrays[] = {c->k_codes, c->k_scales, c->k_biases, c->v_codes, c->v_scales, c->v_biases};
+  for (const void* p : arrays)
+    if (!p || !aligned(p, 16)) return MOE_ERR_ARG;
+  if (!c->status || !aligned(c->status, 256)) return MOE_ERR_ARG;
+  if (b->n_tokens > 0) {
+    if (b->n_seqs < 1 || b->max_new < 1 || !b->q_off || !b->kv_len || !b->block_table) return MOE_ERR_ARG;
+    if (!aligned(b->q_off, 4) || !aligned(b->kv_len, 4) || !aligned(b->block_table, 4)) return MOE_ERR_ARG;
+  }
+  *a = KvArgs{{c->k_codes, c->v_codes},
+              {c->k_scales, c->v_scales},
+              {c->k_biases, c->v_biases},
+              static_cast<WsHeader*>(c->status),
+              b->q_off,
+              b->kv_len,
+              b->block_table,
+              b->table_stride,
+              b->n_seqs,
+              b->n_tokens,
+              b->max_new < b->n_tokens ? b->max_new : b->n_tokens,
+              b->max_kv,
+              c->n_pages,
+              __builtin_ctz(c->page_size),
+              c->kv_heads,
+              c->head_dim};
+  return MOE_OK;
+}
+
+// A strided [n_tokens, heads, head_dim] operand.
+bool operand_ok(const void* p, long long stride, int heads, int dim) {
+  return p && aligned(p, 16) && stride % 8 == 0 && stride >= (long long)heads * dim;
+}
+
+moe_status check_attention(const KvArgs& kv, const moe_attention* a) {
+  if (!a) return MOE_ERR_ARG;
+  if (a->heads < kv.kv_heads || a->heads % kv.kv_heads || a->heads / kv.kv_heads > 64) return MOE_ERR_SHAPE;
+  if (a->window < 0 || a->sinks < 0 || !std::isfinite(a->scale)) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+KvCall begin_call(void* stream) {
+  const KvCall c{options_snapshot(), static_cast<cudaStream_t>(stream)};
+  timing_begin(c.opt, c.stream);
+  return c;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const uint16_t* k, long long k_stride,
+                         const uint16_t* v, long long v_stride, void* stream) {
+  KvArgs a;
+  reset_launch_count();
+  if (moe_status s = make_args(cache, batch, &a)) return s;
+  if (a.n_tokens == 0) return MOE_OK;
+  if (!operand_ok(k, k_stride, a.kv_heads, a.dim) || !operand_ok(v, v_stride, a.kv_heads, a.dim)) return MOE_ERR_ARG;
+  return status_of(kv_append(a, k, k_stride, v, v_stride, begin_call(stream)));
+}
+
+moe_status moe_kv_read(const moe_kv_cache* cache, const moe_kv_batch* batch, uint16_t* k, uint16_t* v, void* stream) {
+  KvArgs a;
+  reset_launch_count();
+  if (moe_status s = make_args(cache, batch, &a)) return s;
+  if (!aligned(k, 16) || !aligned(v, 16)) return MOE_ERR_ARG;
+  if (a.n_tokens == 0 || (!k && !v)) return MOE_OK;
+  return status_of(kv_read(a, k, v, begin_call(stream)));
+}
+
+size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at) {
+  KvArgs a;
+  if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
+  return 256;
+}
+
+moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
+                                 const uint16_t* q, long long q_stride, uint16_t* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  KvArgs a;
+  reset_launch_count();
+  if (moe_status s = make_args(cache, batch, &a)) return s;
+  if (moe_status s = check_attention(a, at)) return s;
+  if (a.n_tokens == 0) return MOE_OK;
+  if (!operand_ok(q, q_stride, at->heads, a.dim) || !out || !aligned(out, 16) || out == q) return MOE_ERR_ARG;
+  if (lse && !aligned(lse, 4)) return MOE_ERR_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_attention_workspace_size(cache, batch, at))
+    return MOE_ERR_WORKSPACE;
+  const AttnArgs g{a, q, q_stride, out, lse, at->heads, at->heads / a.kv_heads, at->window, at->sinks, at->scale};
+  return status_of(attention_simple(g, begin_call(stream)));
+}
+
+}  // extern "C"

@@ -229,14 +229,18 @@ bool ensure_smem_limit(const void* func, int bytes) {
   return true;
 }
 
-void launch_done(const Ctx& c, const char* name) {
+void launch_done(const Options& opt, cudaStream_t s, const char* name) {
   ++t_launches;
-  if (c.opt.kernel_timing) mark(name, c.stream);
+  if (opt.kernel_timing) mark(name, s);
 }
 
-void timing_begin(const Ctx& c) {
-  if (c.opt.kernel_timing) mark(nullptr, c.stream);
+void timing_begin(const Options& opt, cudaStream_t s) {
+  if (opt.kernel_timing) mark(nullptr, s);
 }
+
+void launch_done(const Ctx& c, const char* name) { launch_done(c.opt, c.stream, name); }
+
+void timing_begin(const Ctx& c) { timing_begin(c.opt, c.stream); }
 
 Options options_snapshot() {
   std::lock_guard<std::mutex> lk(g_opt_mu);

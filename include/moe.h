@@ -313,6 +313,105 @@ moe_status moe_layer_forward_static(const moe_weights* w, const uint16_t* x, int
  * first device-side error any pass of the last static call recorded. */
 moe_status moe_get_device_status_static(void* stream);
 
+/* ---- 4-bit key/value cache and the attention that reads it ----
+ *
+ * The grouped-query attention layers beside the expert layer ("Optimizing
+ * on-device inference for Apple Silicon", section "Attention cache") keep
+ * keys and values per token; here in the number format of the weights: 4-bit
+ * codes, groups of 64 along the head, one bf16 scale and one bf16 bias per
+ * group. A cached value is bf16(scale * code + bias), rounded once to nearest
+ * even, the operand value that moe_debug_dequant() shows. Every entry point
+ * below sees exactly these values.
+ *
+ * The cache is n_pages pages of page_size token slots that the caller hands
+ * out to sequences in any order. All arrays are device memory owned by the
+ * caller, 16-byte aligned:
+ *   codes  [n_pages, kv_heads, page_size, head_dim / 8] uint32 (as moe_qmatrix)
+ *   scales [n_pages, kv_heads, page_size, head_dim / 64] bf16, biases the same
+ *   status 256 bytes, 256-byte aligned, zeroed by the caller once: the first
+ *          device-side error since moe_get_device_status(status, stream) last
+ *          read it. A position whose page index is missing or out of range
+ *          records MOE_ERR_DEVICE_CHECK and is left out (not written, read as
+ *          zero, not attended to); so does a number that the cache cannot
+ *          hold (moe_kv_append).
+ * Requirements: head_dim 64, 128 or 256; page_size a power of two from 16 to
+ * 256; 1 <= kv_heads <= 256; n_pages >= 1. */
+typedef struct {
+  int n_pages, page_size, kv_heads, head_dim;
+  uint32_t* k_codes;
+  uint16_t* k_scales;
+  uint16_t* k_biases;
+  uint32_t* v_codes;
+  uint16_t* v_scales;
+  uint16_t* v_biases;
+  void* status;
+} moe_kv_cache;
+
+/* The sequences of one step (int32 device arrays, owned by the caller). The
+ * step's tokens are numbered 0 .. n_tokens - 1, sequence after sequence.
+ *   q_off       [n_seqs + 1] first token of each sequence, ascending, q_off[0]
+ *               = 0 and q_off[n_seqs] = n_tokens; a sequence may have none
+ *   kv_len      [n_seqs] positions of each sequence, the step's tokens
+ *               included: token i of the step, in sequence b, is at position
+ *               kv_len[b] - (q_off[b + 1] - i). Tokens at negative positions
+ *               are padding: not written, read as zero, attending to nothing.
+ *   block_table [n_seqs, table_stride]: page of positions page_size * j ..
+ *               page_size * (j + 1) - 1; entries past kv_len are not read
+ *   max_new     upper bound of every sequence's step tokens
+ *   max_kv      upper bound of every kv_len, at most 2^24 (bounds chosen by
+ *               the caller on the host: no call copies device data back); a
+ *               sequence past a bound records MOE_ERR_DEVICE_CHECK and what
+ *               lies past it is left out */
+typedef struct {
+  int n_seqs, n_tokens, max_new, max_kv;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  int table_stride;
+} moe_kv_batch;
+
+/* Quantises the step's keys and values into the cache. k, v: device bf16
+ * [n_tokens, kv_heads, head_dim], 16-byte aligned, k_stride / v_stride
+ * elements between tokens (a multiple of 8, at least kv_heads * head_dim; the
+ * heads of a token are contiguous), so slices of a fused projection work.
+ * Per group of 64: bias = min, scale = bf16((max - min) / 15), code =
+ * clamp(round((x - bias) / scale), 0, 15), ties to even; scale 0 gives code 0.
+ * The cache holds magnitudes up to 2^16: larger ones and infinities are
+ * stored as +-2^16 and NaN as 0, each recording MOE_ERR_DEVICE_CHECK.
+ * Two tokens of a step must not share a slot. n_tokens = 0 is a no-op. */
+moe_status moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const uint16_t* k, long long k_stride,
+                         const uint16_t* v, long long v_stride, void* stream);
+
+/* Reads the values of the step's tokens back: k, v device bf16 [n_tokens,
+ * kv_heads, head_dim], 16-byte aligned, contiguous; either may be NULL. With
+ * q_off = 0, kv_len[0], kv_len[0] + kv_len[1], ... it reads every sequence
+ * whole. */
+moe_status moe_kv_read(const moe_kv_cache* cache, const moe_kv_batch* batch, uint16_t* k, uint16_t* v, void* stream);
+
+/* What a token attends to and how: `heads` query heads (a multiple of
+ * kv_heads, at most 64 times it; head h reads kv head h / (heads / kv_heads)).
+ * A token at position p sees position j <= p if window is 0, or j > p -
+ * window, or j < sinks. scale multiplies the scores (finite). */
+typedef struct {
+  int heads, window, sinks;
+  float scale;
+} moe_attention;
+
+/* out[i, h] = sum_j softmax_j(scale * q[i, h] . k[j]) v[j] over the positions
+ * that token i sees, in the cache (append the step's tokens first). A token
+ * that sees nothing gets 0. q: device bf16 [n_tokens, heads, head_dim],
+ * 16-byte aligned, q_stride elements between tokens as k_stride above; out:
+ * device bf16, contiguous, 16-byte aligned, not overlapping q. lse: NULL, or
+ * device fp32 [n_tokens, heads], the natural logarithm of the row's sum of
+ * exp(score), -inf for a row that sees nothing (what merging with attention
+ * over other keys needs). workspace: device, 256-byte aligned, at least
+ * moe_attention_workspace_size() bytes; no contents kept. Enqueued on
+ * `stream`, no host synchronisation. n_tokens = 0 is a no-op. */
+size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* a);
+moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* a,
+                                 const uint16_t* q, long long q_stride, uint16_t* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Number of this library's kernels the last forward call on this thread
  * launched (all of its passes). */
 int moe_last_launch_count(void);
