@@ -12,13 +12,14 @@ namespace {
 constexpr int kKeys = 32, kHeads = 8;
 
 template <int DIM>
-__global__ void __launch_bounds__(kHeads * 32) attention_simple_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kHeads * 32) attention_simple_kernel(const AttnArgs a, int max_rows) {
   __shared__ float q[kHeads][DIM];
   __shared__ float t[kKeys][DIM + 1];
   const int i = blockIdx.x, kvh = blockIdx.y, hs = blockIdx.z * kHeads;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int b = kv_seq_of(a.kv, i);
   const SeqInfo si = kv_seq(a.kv, b);
+  if (si.n_new * a.group <= max_rows) return;
   const int pos = si.kv - (si.first + si.n_new - i);
   const bool mine = hs + warp < a.group;
   const int head = kvh * a.group + hs + warp;
@@ -97,14 +98,14 @@ __global__ void __launch_bounds__(kHeads * 32) attention_simple_kernel(const Att
 
 }  // namespace
 
-cudaError_t attention_simple(const AttnArgs& a, const KvCall& c) {
+cudaError_t attention_simple(const AttnArgs& a, int max_rows, const KvCall& c) {
   const dim3 grid(a.kv.n_tokens, a.kv.kv_heads, (a.group + kHeads - 1) / kHeads);
   if (a.kv.dim == 64)
-    attention_simple_kernel<64><<<grid, kHeads * 32, 0, c.stream>>>(a);
+    attention_simple_kernel<64><<<grid, kHeads * 32, 0, c.stream>>>(a, max_rows);
   else if (a.kv.dim == 128)
-    attention_simple_kernel<128><<<grid, kHeads * 32, 0, c.stream>>>(a);
+    attention_simple_kernel<128><<<grid, kHeads * 32, 0, c.stream>>>(a, max_rows);
   else
-    attention_simple_kernel<256><<<grid, kHeads * 32, 0, c.stream>>>(a);
+    attention_simple_kernel<256><<<grid, kHeads * 32, 0, c.stream>>>(a, max_rows);
   return c.launched("attention_simple");
 }
 

@@ -95,6 +95,10 @@ struct AttnArgs {
 cudaError_t kv_append(const KvArgs& a, const uint16_t* k, long long ks, const uint16_t* v, long long vs,
                       const KvCall& c);
 cudaError_t kv_read(const KvArgs& a, uint16_t* k, uint16_t* v, const KvCall& c);
-cudaError_t attention_simple(const AttnArgs& a, const KvCall& c);
+// Sequences with at most max_rows rows (step tokens x query heads per kv head).
+size_t attention_few_workspace(const AttnArgs& a, int max_rows);
+cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, const KvCall& c);
+// Sequences with more rows than that.
+cudaError_t attention_simple(const AttnArgs& a, int max_rows, const KvCall& c);
 
 }  // namespace moe

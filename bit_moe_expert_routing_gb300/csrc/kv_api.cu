@@ -55,6 +55,23 @@ moe_status check_attention(const KvArgs& kv, const moe_attention* a) {
   return MOE_OK;
 }
 
+// Sequences with at most this many rows (step tokens x query heads per kv
+// head) take the few-row kernel.
+constexpr int kFewRows = 64;
+
+bool any_many(const AttnArgs& a) { return (long long)a.kv.max_new * a.group > kFewRows; }
+
+AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
+  AttnArgs g{};
+  g.kv = kv;
+  g.heads = at->heads;
+  g.group = at->heads / kv.kv_heads;
+  g.window = at->window;
+  g.sinks = at->sinks;
+  g.scale = at->scale;
+  return g;
+}
+
 moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 KvCall begin_call(void* stream) {
@@ -92,7 +109,7 @@ moe_status moe_kv_read(const moe_kv_cache* cache, const moe_kv_batch* batch, uin
 size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at) {
   KvArgs a;
   if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
-  return 256;
+  return (attention_few_workspace(attn_args(a, at), kFewRows) + 511) & ~size_t(255);
 }
 
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
@@ -107,8 +124,14 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   if (lse && !aligned(lse, 4)) return MOE_ERR_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_attention_workspace_size(cache, batch, at))
     return MOE_ERR_WORKSPACE;
-  const AttnArgs g{a, q, q_stride, out, lse, at->heads, at->heads / a.kv_heads, at->window, at->sinks, at->scale};
-  return status_of(attention_simple(g, begin_call(stream)));
+  AttnArgs g = attn_args(a, at);
+  g.q = q;
+  g.q_stride = q_stride;
+  g.out = out;
+  g.lse = lse;
+  const KvCall c = begin_call(stream);
+  if (cudaError_t e = attention_few(g, kFewRows, workspace, c)) return status_of(e);
+  return any_many(g) ? status_of(attention_simple(g, kFewRows, c)) : MOE_OK;
 }
 
 }  // extern "C"
