@@ -1,0 +1,924 @@
+// Attention of many rows (prompts and chunks) over the 4-bit cache, on the
+// tcgen05 tensor cores.
+//
+// Two matrix products per (row, key): 4 DIM operations, and a cached element
+// is used by every row of its kv head, so the products bound the work. The
+// codes are therefore expanded once per call, not once per row tile:
+//
+//   expand   writes the visible keys and values as bf16 tiles of 128 keys into
+//            the workspace, laid out exactly as the MMA reads shared memory
+//            (128-byte-swizzled, keys K-major; values transposed, so K-major
+//            in the second product too), in units of 16 KB. It stays in L2.
+//            One extra CTA cuts the work (below).
+//   many     S = Q K^T per 128-row tile and 128 keys into tensor memory, the
+//            softmax warps turn it into P (bf16, in S's place), O += P V with
+//            P read from tensor memory.
+//   combine  joins row tiles that the cut divided between CTAs.
+//
+// The cut: a unit is one row tile times one key tile. All units of all
+// sequences and kv heads are numbered row tile by row tile, and one CTA per SM
+// takes an equal, contiguous range, so that neither causal masks, ragged
+// lengths nor few row tiles leave SMs idle. A row tile that falls into several
+// ranges leaves fp32 partial outputs.
+//
+// A CTA holds QT row tiles of 128 (two for DIM <= 128; one for 256, whose
+// output fills tensor memory): S tiles alternate between two slots, ordered
+// S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ..., so that the softmax of one
+// tile runs under the products of the other. All eight softmax warps work on
+// each S tile, two threads per row, 64 keys each.
+#include <algorithm>
+
+#include "kv.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 128;                  // keys per tile
+constexpr uint32_t kUnit = 16384;         // bytes of a ring unit: 128 rows of 128 bytes
+constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kThreads = 320;
+constexpr int kRing = 9;
+
+template <int DIM>
+struct ManyCfg {
+  static constexpr int QT = DIM == 256 ? 1 : 2;
+  static constexpr int kRows = 128 * QT;
+  static constexpr int UN = DIM / 64;     // units of a key or value tile
+  static constexpr uint32_t kTileBytes = uint32_t(UN) * kUnit;
+  static constexpr uint32_t kQTile = 128 * DIM * 2;
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffRing = QT * kQTile;
+  static constexpr uint32_t kOffEx = kOffRing + kRing * kUnit;  // [2][2][128] floats: row maxima of the halves
+  static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
+  static constexpr int kBars = 2 * kRing + 1 + 2 + 2 + QT + 1;  // full, empty, qfull, sfull, pready, pvdone, drain
+  static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+  static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct RowTile {
+  int seq, row0;  // sequence, first row within it
+};
+
+struct PlanHdr {
+  long long units;  // of one kv head
+  int row_tiles, pad;
+};
+
+struct ManyArgs {
+  AttnArgs a;
+  int max_few;             // sequences with at most this many rows are not taken
+  int b0, nb, h0, nh;      // sequences and kv heads of this pass
+  int tiles_max;           // key tiles per (sequence, kv head) in the expanded arrays
+  uint8_t* kx;             // expanded keys, values: [nb][nh][tiles_max] tiles
+  uint8_t* vx;
+  uint8_t* bad;            // [nb][tiles_max]: bit i set if the page of keys 16 i .. 16 i + 15 is missing
+  PlanHdr* plan;
+  long long* unit_off;     // [row tiles + 1] first unit of each row tile
+  RowTile* row_tile;
+  int max_row_tiles;
+  int ctas;                // of the many kernel
+  float* part_o;           // [2 ctas][rows][DIM]
+  float* part_lse;         // [2 ctas][rows], base 2
+};
+
+// Key tiles that rows at positions minpos .. maxpos read: sink tiles [0,
+// n_sink), then [first, first + n - n_sink); at least one, so that rows that
+// see nothing are written too.
+struct Range {
+  int n_sink, first, n;
+  __device__ __forceinline__ int tile(int t) const { return t < n_sink ? t : first + t - n_sink; }
+  __device__ __forceinline__ int index(int tile) const { return tile < first ? tile : n_sink + tile - first; }
+};
+__device__ __forceinline__ Range range_of(int minpos, int maxpos, int window, int sinks) {
+  Range r{0, 0, 1};
+  if (maxpos < 0) return r;
+  if (window > 0) {
+    r.first = max(0, minpos - window + 1) / kBK;
+    r.n_sink = min((min(sinks, maxpos + 1) + kBK - 1) / kBK, r.first);
+  }
+  r.n = r.n_sink + maxpos / kBK - r.first + 1;
+  return r;
+}
+
+__device__ __forceinline__ bool taken(const ManyArgs& m, const SeqInfo& s) { return s.n_new * m.a.group > m.max_few; }
+
+__device__ __forceinline__ Range seq_range(const ManyArgs& m, const SeqInfo& s) {
+  return range_of(s.kv - s.n_new, s.kv - 1, m.a.window, m.a.sinks);
+}
+__device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s, int row0, int rows) {
+  const int base = s.kv - s.n_new, last = min(row0 + rows, s.n_new * m.a.group) - 1;
+  return range_of(base + row0 / m.a.group, base + last / m.a.group, m.a.window, m.a.sinks);
+}
+
+// Byte offset of 16-byte chunk c of row r in a 1024-aligned 128-byte-swizzled K-major block.
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return uint32_t((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// ---- the cut ------------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 256;
+
+// Inclusive scan over the CTA of one value per thread; *total gets the sum.
+__device__ long long block_scan(long long v, long long* total, long long* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long u = __shfl_up_sync(~0u, v, off);
+    if (lane >= off) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) buf[warp] = v;
+  __syncthreads();
+  long long before = 0, sum = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += buf[w];
+    sum += buf[w];
+  }
+  *total = sum;
+  return v + before;
+}
+
+__device__ void make_plan(const ManyArgs& m, int rows) {
+  __shared__ long long buf[kPlanThreads / 32];
+  // row tiles of the sequences, in order
+  long long n_rt = 0;
+  for (int base = 0; base < m.nb; base += kPlanThreads) {
+    const int b = base + threadIdx.x;
+    int mine = 0;
+    SeqInfo s{0, 0, 0};
+    if (b < m.nb) {
+      s = kv_seq(m.a.kv, m.b0 + b);
+      if (taken(m, s)) mine = (s.n_new * m.a.group + rows - 1) / rows;
+    }
+    long long total;
+    const long long end = block_scan(mine, &total, buf);
+    const long long first = n_rt + end - mine;
+    for (int i = 0; i < mine && first + i < m.max_row_tiles; ++i) m.row_tile[first + i] = RowTile{m.b0 + b, i * rows};
+    n_rt += total;
+  }
+  if (n_rt > m.max_row_tiles) n_rt = m.max_row_tiles;  // (the host's bound; reached only by inconsistent offsets)
+  __syncthreads();
+  long long units = 0;
+  for (long long base = 0; base < n_rt; base += kPlanThreads) {
+    const long long i = base + threadIdx.x;
+    long long mine = 0;
+    if (i < n_rt) {
+      const RowTile rt = m.row_tile[i];
+      mine = rows_range(m, kv_seq(m.a.kv, rt.seq), rt.row0, rows).n;
+    }
+    long long total;
+    const long long end = block_scan(mine, &total, buf);
+    if (i < n_rt) m.unit_off[i] = units + end - mine;
+    units += total;
+  }
+  if (threadIdx.x == 0) {
+    m.unit_off[n_rt] = units;
+    m.plan->units = units;
+    m.plan->row_tiles = int(n_rt);
+  }
+}
+
+// ---- expand -------------------------------------------------------------------------------
+
+// Pairs (codes in bits 0..3 of both halves of p) -> bf16 scale * code + bias, rounded once.
+__device__ __forceinline__ uint32_t dq_pair(uint32_t p, __nv_bfloat162 s2, __nv_bfloat162 b2) {
+  const __nv_bfloat162 k128 = __halves2bfloat162(__ushort_as_bfloat16(0x4300), __ushort_as_bfloat16(0x4300));
+  const uint32_t x = (p & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 r = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), k128), s2, b2);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// CTA 0 makes the plan; the others expand one key tile of one (sequence, kv
+// head): the keys row by row, the values eight keys of eight dims at a time,
+// which leaves the transposed 16-byte chunks in registers.
+template <int DIM>
+__global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs m) {
+  griddep_launch();
+  if (blockIdx.x == 0) {
+    make_plan(m, ManyCfg<DIM>::kRows);
+    return;
+  }
+  __shared__ long long rows16[kBK / 16];  // first cache row of each 16 keys, -1: zeros
+  int x = blockIdx.x - 1;
+  const int t = x % m.tiles_max;
+  x /= m.tiles_max;
+  const int h = x % m.nh, bi = x / m.nh, b = m.b0 + bi;
+  const KvArgs& kv = m.a.kv;
+  const SeqInfo s = kv_seq(kv, b);
+  if (!taken(m, s)) return;
+  const Range r = seq_range(m, s);
+  if (t >= r.n) return;
+  const int k0 = r.tile(t) * kBK, minpos = s.kv - s.n_new, maxpos = s.kv - 1;
+  const int lo = m.a.window > 0 ? max(0, minpos - m.a.window + 1) : 0;
+  if (threadIdx.x < 32) {
+    bool missing = false;
+    if (threadIdx.x < kBK / 16) {
+      const int k = k0 + 16 * threadIdx.x;
+      long long row = -1;
+      if (k <= maxpos && (k + 16 > lo || k < m.a.sinks)) {
+        row = kv_page_row(kv, b, k >> kv.page_bits, m.h0 + h);
+        missing = row < 0;
+        if (row >= 0) row += k & ((1 << kv.page_bits) - 1);
+      }
+      rows16[threadIdx.x] = row;
+    }
+    const unsigned bits = __ballot_sync(~0u, missing);
+    if (threadIdx.x == 0 && h == 0) m.bad[(long long)bi * m.tiles_max + t] = uint8_t(bits);
+  }
+  __syncthreads();
+  const long long tile = ((long long)bi * m.nh + h) * m.tiles_max + t;
+  constexpr int W = DIM / 8, G = DIM / 64;
+  uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
+  for (int e = threadIdx.x; e < kBK * W; e += kPlanThreads) {
+    const int key = e / W, w = e % W;
+    uint32_t o[4] = {0, 0, 0, 0};
+    const long long r16 = rows16[key >> 4];
+    if (r16 >= 0 && k0 + key <= maxpos) {
+      const long long row = r16 + (key & 15);
+      const __nv_bfloat16 sc = __ushort_as_bfloat16(kv.scales[0][row * G + w / 8]);
+      const __nv_bfloat16 bi16 = __ushort_as_bfloat16(kv.biases[0][row * G + w / 8]);
+      dq8_bf16(kv.codes[0][row * W + w], __halves2bfloat162(sc, sc), __halves2bfloat162(bi16, bi16), o);
+    }
+    *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  uint8_t* vd = m.vx + tile * ManyCfg<DIM>::kTileBytes;
+  // lanes: eight 8-key chunks (one 128-byte row of 64 keys) by four words
+  for (int e = threadIdx.x; e < (kBK / 8) * W; e += kPlanThreads) {
+    const int ko = e & 7, w = (e >> 3) % W, kb = (e >> 3) / W;  // 8-key chunk in its block, word, block of 64 keys
+    const int key0 = kb * 64 + ko * 8;
+    uint32_t c[8];
+    uint32_t sc[8], bs[8];
+    const long long r16 = rows16[key0 >> 4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = sc[i] = bs[i] = 0;
+      if (r16 >= 0 && k0 + key0 + i <= maxpos) {
+        const long long row = r16 + (key0 & 15) + i;
+        c[i] = kv.codes[1][row * W + w];
+        sc[i] = kv.scales[1][row * G + w / 8];
+        bs[i] = kv.biases[1][row * G + w / 8];
+      }
+    }
+    uint32_t o[8][4];  // [dim][pair of keys]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t s2 = sc[2 * i] | sc[2 * i + 1] << 16, b2 = bs[2 * i] | bs[2 * i + 1] << 16;
+      const __nv_bfloat162 sp = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+      const __nv_bfloat162 bp = *reinterpret_cast<const __nv_bfloat162*>(&b2);
+      const uint32_t lo2 = __byte_perm(c[2 * i], c[2 * i + 1], 0x5410), hi2 = __byte_perm(c[2 * i], c[2 * i + 1], 0x7632);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        o[n][i] = dq_pair(lo2 >> (4 * n), sp, bp);
+        o[n + 4][i] = dq_pair(hi2 >> (4 * n), sp, bp);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int d = 8 * w + n;
+      const uint32_t at = DIM == 64    ? kb * 8192 + sw128(d, ko)
+                          : DIM == 128 ? kb * kUnit + sw128(d, ko)
+                                       : (kb * 2 + d / 128) * kUnit + sw128(d & 127, ko);
+      *reinterpret_cast<uint4*>(vd + at) = make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
+    }
+  }
+}
+
+// ---- tcgen05 ------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart, version 1.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// kind::f16: bf16 A and B, fp32 D, both K-major, M = 128, N = n.
+constexpr uint32_t idesc_n(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// The wait, with a load's registers as operands: no use of them may be scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---- the range of a CTA -------------------------------------------------------------------
+
+// One CTA's part of a row tile: its key tiles [j0, j1) of n.
+struct Segment {
+  int h, rt, j0, j1, n;
+  RowTile tile;
+  bool first;  // the CTA's first segment
+};
+
+// Steps through the segments of the units [u, end).
+struct Cursor {
+  const ManyArgs& m;
+  long long u, begin, end, units;
+  int rt;
+  __device__ Cursor(const ManyArgs& args) : m(args), rt(-1) {
+    units = m.plan->units;
+    const long long all = units * m.nh;
+    begin = u = all * blockIdx.x / m.ctas;
+    end = all * (blockIdx.x + 1) / m.ctas;
+  }
+  __device__ bool next(Segment* s) {
+    if (u >= end) return false;
+    const int h = int(u / units);
+    const long long at = u % units;
+    if (rt < 0) {  // the last row tile that starts at or before `at`
+      int lo = 0, hi = m.plan->row_tiles - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (m.unit_off[mid] <= at)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      rt = lo;
+    }
+    const long long o0 = m.unit_off[rt], o1 = m.unit_off[rt + 1];
+    s->h = h;
+    s->rt = rt;
+    s->n = int(o1 - o0);
+    s->j0 = int(at - o0);
+    s->j1 = int(min(o1 - o0, at - o0 + (end - u)));
+    s->tile = m.row_tile[rt];
+    s->first = u == begin;
+    u += s->j1 - s->j0;
+    if (s->j1 == s->n) rt = rt + 1 == m.plan->row_tiles ? 0 : rt + 1;
+    return true;
+  }
+};
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
+  using C = ManyCfg<DIM>;
+  constexpr int QT = C::QT, UN = C::UN;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + C::kOffBar;
+  auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty = [&](uint32_t s) { return bar0 + 8u * (kRing + s); };
+  const uint32_t qfull = bar0 + 8u * (2 * kRing);
+  auto sfull = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + 1 + s); };
+  auto pready = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + 3 + s); };
+  auto pvdone = [&](uint32_t q) { return bar0 + 8u * (2 * kRing + 5 + q); };
+  const uint32_t drain = bar0 + 8u * (2 * kRing + 5 + QT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
+  const AttnArgs& a = m.a;
+  WsHeader* hdr = a.kv.hdr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    mbar_init(qfull, kSoftWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), kSoftWarps);
+    for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S slots at columns 0 and 128, O at 256
+  griddep_wait();
+  griddep_launch();
+
+  // Ring position of key tile i and value tile i of a segment of n tiles, in
+  // the order of their first use: K0 V0 K1 V1 ... with two row tiles, K0 K1
+  // V0 K2 V1 ... with one (its S tiles run two ahead).
+  auto k_at = [](int i) { return QT == 2 ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
+  auto v_at = [](int i, int n) { return QT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+
+  if (warp == kWarpTma) {
+    if (lane == 0) {
+      Cursor cur(m);
+      Segment s;
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && cur.next(&s)) {
+        const SeqInfo si = kv_seq(a.kv, s.tile.seq);
+        const Range all = seq_range(m, si), mine = rows_range(m, si, s.tile.row0, C::kRows);
+        const long long tile0 = ((long long)(s.tile.seq - m.b0) * m.nh + s.h) * m.tiles_max;
+        const int n = s.j1 - s.j0;
+        for (int p = 0; p < 2 * n && ok; ++p) {
+          // which tile has ring position p
+          const bool is_v = QT == 2 ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
+          const int i = QT == 2 ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
+          const int t = all.index(mine.tile(s.j0 + i));
+          const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + t) * C::kTileBytes;
+          for (int u = 0; u < UN; ++u, ++it) {
+            const uint32_t slot = it % kRing;
+            if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
+            mbar_arrive_tx(full(slot), kUnit);
+            bulk_g2s(base + C::kOffRing + slot * kUnit, src + u * kUnit, kUnit, full(slot));
+          }
+        }
+      }
+      if (!ok) {  // copies in flight land before the CTA leaves (bounded)
+        const uint32_t from = it > kRing ? it - kRing : 0;
+        for (uint32_t i = from; i < it; ++i) mbar_wait(full(i % kRing), (i / kRing) & 1u, abort_flag, hdr, kWaitLimit, true, 221);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0) {
+      Cursor cur(m);
+      Segment s;
+      uint32_t ring = 0, nq = 0, g0 = 0;  // before this segment: ring units, segments, S tiles
+      bool ok = true;
+      constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM < 128 ? DIM : 128);
+      while (ok && cur.next(&s)) {
+        const int n = s.j1 - s.j0, total = n * QT;
+        if (!(ok = mbar_wait(qfull, nq & 1u, abort_flag, hdr, kWaitLimit, false, 222))) break;
+        ++nq;
+        tc_fence_after();
+        auto wait_unit = [&](uint32_t seq) {
+          return mbar_wait(full(seq % kRing), (seq / kRing) & 1u, abort_flag, hdr, kWaitLimit, false, 223);
+        };
+        auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
+          const int q = x % QT, i = x / QT;
+          const uint32_t sl = (g0 + x) & 1u, d = tmem + sl * 128;
+          for (int u = 0; u < UN; ++u) {
+            const uint32_t seq = ring + k_at(i) * UN + u, slot = seq % kRing;
+            if (q == 0) {
+              if (!(ok = wait_unit(seq))) return;
+              tc_fence_after();
+            }
+            const uint32_t qa = base + C::kOffQ + q * C::kQTile + u * kUnit, kb = base + C::kOffRing + slot * kUnit;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_ss(d, smem_desc(qa + kk * 32), smem_desc(kb + kk * 32), kIdS, (u | kk) != 0);
+            if (q == QT - 1) umma_commit(empty(slot));
+          }
+          umma_commit(sfull(sl));
+        };
+        auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
+          const int q = x % QT, i = x / QT;
+          const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
+          for (int u = 0; u < UN; ++u) {
+            const uint32_t seq = ring + v_at(i, n) * UN + u, slot = seq % kRing;
+            if (q == 0) {
+              if (!(ok = wait_unit(seq))) return;
+              tc_fence_after();
+            }
+            const uint32_t vb = base + C::kOffRing + slot * kUnit;
+            // a unit holds both blocks of 64 keys (DIM 64), one block (128), or one block of half the dims (256)
+            const int kb0 = DIM == 64 ? 0 : DIM == 128 ? u : u / 2;
+            const uint32_t od = o + (DIM == 256 ? (u & 1) * 128 : 0);
+#pragma unroll
+            for (int kb = 0; kb < (DIM == 64 ? 2 : 1); ++kb)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts(od, p + (kb0 + kb) * 32 + kk * 8, smem_desc(vb + kb * 8192 + kk * 32), kIdO,
+                        i > 0 || kb0 + kb > 0 || kk > 0);
+            if (q == QT - 1) umma_commit(empty(slot));
+          }
+          umma_commit(pvdone(q));
+        };
+        qk(0);
+        if (ok && total > 1) qk(1);
+        for (int x = 0; x < total && ok; ++x) {
+          const uint32_t g = g0 + x;
+          if (!(ok = mbar_wait(pready(g & 1u), (g >> 1) & 1u, abort_flag, hdr, kWaitLimit, false, 224))) break;
+          tc_fence_after();
+          pv(x);
+          if (ok && x + 2 < total) qk(x + 2);
+        }
+        g0 += total;
+        ring += 2 * n * UN;
+      }
+      // every MMA has completed before the CTA leaves (bounded)
+      umma_commit(drain);
+      mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
+    }
+  } else {
+    // ---------------- softmax: eight warps, thread (row, half of the keys) ----------------
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;  // the tensor-memory lanes this warp may access
+    float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
+    // |scale| in base 2; a negative scale flips the sign of q, scale 0 clears q
+    const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
+    Cursor cur(m);
+    Segment s;
+    uint32_t g = 0, pv0 = 0, exn = 0;  // S tiles so far, products O += P V per row tile so far, exchanges so far
+    // After a failed wait a warp keeps going without waiting, so that the
+    // others never hang in a barrier; the status says that the output is void.
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+      if (ok) ok = mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site);
+    };
+    // the larger / the sum of the two halves' values of a row
+    auto exchange = [&](float v) {
+      float* e = ex + (exn & 1u) * 256;
+      ++exn;
+      e[half * 128 + row] = v;
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
+      return e[(half ^ 1) * 128 + row];
+    };
+    while (cur.next(&s)) {
+      const SeqInfo si = kv_seq(a.kv, s.tile.seq);
+      const Range all = seq_range(m, si), mine = rows_range(m, si, s.tile.row0, C::kRows);
+      const int n_rows = min(C::kRows, si.n_new * a.group - s.tile.row0);
+      const int kvh = m.h0 + s.h, base_pos = si.kv - si.n_new;
+      // query rows into shared memory, rows past the end as zeros
+      for (int e = threadIdx.x; e < C::kRows * (DIM / 8); e += kSoftWarps * 32) {
+        const int r = e / (DIM / 8), c = e % (DIM / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < n_rows) {
+          const int rr = s.tile.row0 + r;
+          v = *reinterpret_cast<const uint4*>(a.q + (si.first + rr / a.group) * a.q_stride +
+                                              (kvh * a.group + rr % a.group) * DIM + c * 8);
+          if (a.scale < 0.f) {
+            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+          } else if (a.scale == 0.f) {  // (NaN and infinities stay NaN)
+            v.x = pack2(bf16lo(v.x) * 0.f, bf16hi(v.x) * 0.f), v.y = pack2(bf16lo(v.y) * 0.f, bf16hi(v.y) * 0.f);
+            v.z = pack2(bf16lo(v.z) * 0.f, bf16hi(v.z) * 0.f), v.w = pack2(bf16lo(v.w) * 0.f, bf16hi(v.w) * 0.f);
+          }
+        }
+        *reinterpret_cast<uint4*>(gbase + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kUnit + sw128(r & 127, c & 7)) = v;
+      }
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull);
+
+      float ref[QT], sum[QT];
+      int pos[QT], minpos[QT], maxpos[QT];
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        ref[q] = -INFINITY, sum[q] = 0.f;
+        const int last = si.n_new * a.group - 1, r0 = s.tile.row0 + q * 128;
+        pos[q] = base_pos + min(r0 + row, last) / a.group;
+        minpos[q] = base_pos + min(r0, last) / a.group;
+        maxpos[q] = base_pos + min(r0 + 127, last) / a.group;
+      }
+      const int n = s.j1 - s.j0;
+      const uint8_t* bad = m.bad + (long long)(s.tile.seq - m.b0) * m.tiles_max;
+      unsigned bad_next = bad[all.index(mine.tile(s.j0))];
+      for (int i = 0; i < n; ++i) {
+        const int k0 = mine.tile(s.j0 + i) * kBK;
+        const unsigned missing = bad_next;
+        if (i + 1 < n) bad_next = bad[all.index(mine.tile(s.j0 + i + 1))];
+#pragma unroll
+        for (int q = 0; q < QT; ++q, ++g) {
+          const uint32_t sl = tmem + lanes + (g & 1u) * 128;
+          wait(sfull(g & 1u), (g >> 1) & 1u, 226);
+          tc_fence_after();
+          uint32_t v[64];
+          tmem_ld32(sl + half * 64, v);
+          tmem_ld32(sl + half * 64 + 32, v + 32);
+          tmem_wait_ld32(v);
+          tmem_wait_ld32(v + 32);
+          const bool whole = missing == 0 && k0 + kBK - 1 <= minpos[q] &&
+                             (a.window == 0 || k0 > maxpos[q] - a.window || k0 + kBK <= a.sinks);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              const int key = k0 + half * 64 + e;
+              const bool sees = key <= pos[q] && (a.window == 0 || key > pos[q] - a.window || key < a.sinks) &&
+                                !((missing >> (half * 4 + e / 16)) & 1u);
+              if (!sees) v[e] = 0xff800000u;  // -inf
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          top = fmaxf(top, exchange(top)) * c2;
+          // the reference maximum moves only when a score passes it by 2^8: probabilities are floating point, so
+          // nothing is lost, and the output is hardly ever rescaled
+          const bool grew = top > ref[q] + 8.f;
+          if (__any_sync(~0u, grew)) {
+            const float to = fmaxf(ref[q], top);
+            const float al = to == -INFINITY ? 1.f : ex2(ref[q] - to);
+            ref[q] = to;
+            sum[q] *= al;
+            if (i > 0) {
+              wait(pvdone(q), (pv0 + i - 1) & 1u, 227);
+              tc_fence_after();
+              const uint32_t oc = tmem + lanes + 256 + q * DIM + half * (DIM / 2);
+#pragma unroll 1
+              for (int cc = 0; cc < DIM / 2; cc += 32) {
+                uint32_t o[32];
+                tmem_ld32(oc + cc, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st32(oc + cc, o);
+                tmem_wait_st();
+              }
+            }
+          }
+          const float r = ref[q] == -INFINITY ? 0.f : ref[q];
+          const float2 c22 = make_float2(c2, c2), r22 = make_float2(-r, -r);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c22, r22);
+            x.x = ex2(x.x), x.y = ex2(x.y);
+            acc[e & 1] = __fadd2_rn(acc[e & 1], x);
+            p[e] = pack2(x.x, x.y);
+          }
+          acc[0] = __fadd2_rn(acc[0], acc[1]);
+          sum[q] += acc[0].x + acc[0].y;
+          tmem_st32(sl + half * 32, p);
+          tmem_wait_st();
+          // A parity wait tells only consecutive phases apart, so the output's wait for the segment's last product has
+          // to know that the one before is done, and learns it here: the last one cannot be until this P is there.
+          if (i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pready(g & 1u));
+        }
+      }
+      pv0 += n;
+      // output: each thread half of its rows' dims
+#pragma unroll
+      for (int q = 0; q < QT; ++q) {
+        const float tot = sum[q] + exchange(sum[q]);
+        const float inv = tot != 0.f ? 1.f / tot : 0.f;
+        const float lse = tot != 0.f ? ref[q] + log2f(tot) : -INFINITY;
+        wait(pvdone(q), (pv0 - 1) & 1u, 228);
+        tc_fence_after();
+        const int r = q * 128 + row;
+        const bool valid = r < n_rows;
+        const int rr = s.tile.row0 + (valid ? r : 0);
+        const long long at = (long long)(si.first + rr / a.group) * a.heads + kvh * a.group + rr % a.group;
+        const bool part = s.j0 > 0 || s.j1 < s.n;
+        const long long prow = (long long)(2 * blockIdx.x + (s.j0 > 0 && s.first ? 1 : 0)) * C::kRows + r;
+        const uint32_t oc = tmem + lanes + 256 + q * DIM + half * (DIM / 2);
+#pragma unroll 1
+        for (int cc = 0; cc < DIM / 2; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32(oc + cc, o);
+          tmem_wait_ld32(o);
+          const int d = half * (DIM / 2) + cc;
+          if (part) {
+            float* dst = m.part_o + prow * DIM + d;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + e) =
+                  make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                              __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+          } else if (valid) {
+            uint16_t* dst = a.out + at * DIM + d;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (half == 0) {
+          if (part)
+            m.part_lse[prow] = lse;
+          else if (valid && a.lse)
+            a.lse[at] = lse * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Joins the row tiles that are divided between CTAs. CTA (c, slice): the row
+// tile that the end of CTA c's range divides, if c holds its first unit.
+template <int DIM>
+__global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
+  griddep_wait();
+  constexpr int kRows = ManyCfg<DIM>::kRows;
+  const long long units = m.plan->units, all = units * m.nh;
+  const long long end = all * (blockIdx.x + 1) / m.ctas;
+  if (end >= all || end == all * blockIdx.x / m.ctas) return;
+  const int h = int(end / units);
+  int lo = 0, hi = m.plan->row_tiles - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (m.unit_off[mid] <= end % units)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const long long u0 = h * units + m.unit_off[lo], u1 = h * units + m.unit_off[lo + 1];
+  if (u0 == end) return;  // the cut is between two row tiles
+  auto cta_of = [&](long long u) { return int(((u + 1) * m.ctas - 1) / all); };
+  const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
+  if (c0 != int(blockIdx.x)) return;
+  const RowTile rt = m.row_tile[lo];
+  const SeqInfo si = kv_seq(m.a.kv, rt.seq);
+  const int n_rows = min(kRows, si.n_new * m.a.group - rt.row0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // A CTA whose range starts inside the row tile holds its part as its first
+  // segment (slot 1 of its two), else as its last or only one (slot 0); with
+  // fewer units than CTAs some hold none.
+  auto slot = [&](int c) { return 2 * c + (c > c0 ? 1 : 0); };
+  auto holds = [&](int c) { return all * c / m.ctas < all * (c + 1) / m.ctas; };
+  for (int r = blockIdx.y * 8 + warp; r < n_rows; r += gridDim.y * 8) {
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+      if (holds(c)) top = fmaxf(top, m.part_lse[(long long)slot(c) * kRows + r]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float o[DIM / 32], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      if (!holds(c)) continue;
+      const long long pr = (long long)slot(c) * kRows + r;
+      const float w = ex2(m.part_lse[pr] - ref);
+      sum += w;
+#pragma unroll
+      for (int j = 0; j < DIM / 32; ++j) o[j] += w * m.part_o[pr * DIM + lane + 32 * j];
+    }
+    const int rr = rt.row0 + r;
+    const long long at = (long long)(si.first + rr / m.a.group) * m.a.heads + (m.h0 + h) * m.a.group + rr % m.a.group;
+#pragma unroll
+    for (int j = 0; j < DIM / 32; ++j) m.a.out[at * DIM + lane + 32 * j] = f32_to_bf16(sum != 0.f ? o[j] / sum : 0.f);
+    if (m.a.lse && lane == 0) m.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+// Expanded tiles of one pass take at most this, if one sequence's kv head
+// fits: the step runs as passes over kv heads, then over sequences.
+constexpr size_t kPassBytes = size_t(2) << 30;
+
+size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct ManyPlan {
+  int rows, tiles_max, nb, nh, ctas, max_row_tiles;
+  size_t kx, vx, bad, plan, unit_off, row_tile, part_o, part_lse, total;
+};
+
+ManyPlan plan(const AttnArgs& a) {
+  ManyPlan p{};
+  const int dim = a.kv.dim;
+  p.rows = dim == 256 ? 128 : 256;
+  long long keys = a.kv.max_kv;
+  if (a.window > 0)
+    keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kBK);
+  p.tiles_max = std::max(1, int((keys + kBK - 1) / kBK));
+  const size_t head_bytes = size_t(p.tiles_max) * kBK * dim * 2 * 2;  // keys and values of a (sequence, kv head)
+  const size_t fit = std::max<size_t>(1, kPassBytes / head_bytes);
+  p.nh = int(std::min<size_t>(a.kv.kv_heads, fit));
+  p.nb = int(std::min<size_t>(a.kv.n_seqs, std::max<size_t>(1, fit / p.nh)));
+  p.ctas = num_sms();
+  p.max_row_tiles = int(((long long)a.kv.n_tokens * a.group + p.rows - 1) / p.rows + p.nb);
+  size_t o = 0;
+  auto put = [&](size_t bytes) {
+    const size_t at = o;
+    o = al256(o + bytes);
+    return at;
+  };
+  p.kx = put(size_t(p.nb) * p.nh * head_bytes / 2);
+  p.vx = put(size_t(p.nb) * p.nh * head_bytes / 2);
+  p.bad = put(size_t(p.nb) * p.tiles_max);
+  p.plan = put(sizeof(PlanHdr));
+  p.unit_off = put((size_t(p.max_row_tiles) + 1) * 8);
+  p.row_tile = put(size_t(p.max_row_tiles) * sizeof(RowTile));
+  p.part_o = put(size_t(2) * p.ctas * p.rows * dim * 4);
+  p.part_lse = put(size_t(2) * p.ctas * p.rows * 4);
+  p.total = o;
+  return p;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(const KvCall& c, const char* name, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
+                             Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) return e;
+  return c.launched(name);
+}
+
+template <int DIM>
+cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
+  using C = ManyCfg<DIM>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(&attention_many_kernel<DIM>), C::kSmem)) return cudaErrorInvalidValue;
+  for (m.b0 = 0; m.b0 < m.a.kv.n_seqs; m.b0 += p.nb)
+    for (m.h0 = 0; m.h0 < m.a.kv.kv_heads; m.h0 += p.nh) {
+      m.nb = std::min(p.nb, m.a.kv.n_seqs - m.b0);
+      m.nh = std::min(p.nh, m.a.kv.kv_heads - m.h0);
+      const long long grid = 1 + 1ll * m.nb * m.nh * p.tiles_max;
+      if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+      attention_expand_kernel<DIM><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
+      if (cudaError_t e = c.launched("attention_expand")) return e;
+      if (cudaError_t e = launch_dependent(c, "attention_many", attention_many_kernel<DIM>, dim3(p.ctas), kThreads, C::kSmem, m))
+        return e;
+      if (cudaError_t e = launch_dependent(c, "attention_many_combine", attention_many_combine_kernel<DIM>,
+                                           dim3(p.ctas, 8), 256, 0, m))
+        return e;
+    }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t attention_many_workspace(const AttnArgs& a) { return a.kv.n_seqs > 0 ? plan(a).total : 0; }
+
+cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCall& c) {
+  const ManyPlan p = plan(a);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  ManyArgs m{};
+  m.a = a;
+  m.max_few = max_few;
+  m.tiles_max = p.tiles_max;
+  m.kx = w + p.kx;
+  m.vx = w + p.vx;
+  m.bad = w + p.bad;
+  m.plan = reinterpret_cast<PlanHdr*>(w + p.plan);
+  m.unit_off = reinterpret_cast<long long*>(w + p.unit_off);
+  m.row_tile = reinterpret_cast<RowTile*>(w + p.row_tile);
+  m.max_row_tiles = p.max_row_tiles;
+  m.ctas = p.ctas;
+  m.part_o = reinterpret_cast<float*>(w + p.part_o);
+  m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
+  return a.kv.dim == 64 ? launch<64>(m, p, c) : a.kv.dim == 128 ? launch<128>(m, p, c) : launch<256>(m, p, c);
+}
+
+}  // namespace moe

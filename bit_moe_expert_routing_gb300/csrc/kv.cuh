@@ -99,6 +99,7 @@ cudaError_t kv_read(const KvArgs& a, uint16_t* k, uint16_t* v, const KvCall& c);
 size_t attention_few_workspace(const AttnArgs& a, int max_rows);
 cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, const KvCall& c);
 // Sequences with more rows than that.
-cudaError_t attention_simple(const AttnArgs& a, int max_rows, const KvCall& c);
+size_t attention_many_workspace(const AttnArgs& a);
+cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCall& c);
 
 }  // namespace moe

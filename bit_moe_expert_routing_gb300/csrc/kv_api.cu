@@ -109,7 +109,10 @@ moe_status moe_kv_read(const moe_kv_cache* cache, const moe_kv_batch* batch, uin
 size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at) {
   KvArgs a;
   if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
-  return (attention_few_workspace(attn_args(a, at), kFewRows) + 511) & ~size_t(255);
+  const AttnArgs g = attn_args(a, at);
+  // the two parts run one after the other on the stream and share the space
+  const size_t few = attention_few_workspace(g, kFewRows), many = any_many(g) ? attention_many_workspace(g) : 0;
+  return ((few > many ? few : many) + 511) & ~size_t(255);
 }
 
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
@@ -131,7 +134,7 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   g.lse = lse;
   const KvCall c = begin_call(stream);
   if (cudaError_t e = attention_few(g, kFewRows, workspace, c)) return status_of(e);
-  return any_many(g) ? status_of(attention_simple(g, kFewRows, c)) : MOE_OK;
+  return any_many(g) ? status_of(attention_many(g, kFewRows, workspace, c)) : MOE_OK;
 }
 
 }  // extern "C"
