@@ -595,24 +595,23 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 }
 
 // Joins the splits of a row: out = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s
-// - max). One CTA of eight warps per row; a warp takes every eighth split.
+// - max). One CTA of eight warps per (sequence, kv head, row that the kernel
+// above may take); a warp takes every eighth split.
 template <int DIM>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group) {
+__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group, int rows_max) {
   __shared__ float acc[8][DIM];
   __shared__ float2 ms[8];
-  griddep_wait();
   const AttnArgs& a = f.a;
-  const int i = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+  const int r = blockIdx.x % rows_max, kvh = blockIdx.x / rows_max % a.kv.kv_heads, b = blockIdx.x / rows_max / a.kv.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = kv_seq_of(a.kv, i);
   const SeqInfo si = kv_seq(a.kv, b);
-  const int r = (i - si.first) * a.group + h % a.group;
-  if (si.n_new <= 0) return;
   const Group gr = group_of(f, si, rows_per_group, r / rows_per_group);
-  if (gr.splits <= 1) return;
+  if (gr.splits <= 1 || r % rows_per_group >= gr.n_rows) return;
+  griddep_wait();
+  const long long at = (long long)(si.first + r / a.group) * a.heads + kvh * a.group + r % a.group;
   const long long all_rows = (long long)a.kv.n_tokens * a.heads;
   float top = -INFINITY;
-  for (int s = lane; s < gr.splits; s += 32) top = fmaxf(top, f.part_lse[s * all_rows + blockIdx.x]);
+  for (int s = lane; s < gr.splits; s += 32) top = fmaxf(top, f.part_lse[s * all_rows + at]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
   const float ref = top == -INFINITY ? 0.f : top;
@@ -620,9 +619,9 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
 #pragma unroll
   for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
   for (int s = warp; s < gr.splits; s += 8) {
-    const float w = ex2(f.part_lse[s * all_rows + blockIdx.x] - ref);
+    const float w = ex2(f.part_lse[s * all_rows + at] - ref);
     sum += w;
-    const float* p = f.part_o + (s * all_rows + blockIdx.x) * DIM;
+    const float* p = f.part_o + (s * all_rows + at) * DIM;
 #pragma unroll
     for (int j = 0; j < DIM / 32; ++j) o[j] += w * p[lane + 32 * j];
   }
@@ -638,9 +637,9 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += acc[w][d];
-    a.out[(long long)blockIdx.x * DIM + d] = f32_to_bf16(tot != 0.f ? v / tot : 0.f);
+    a.out[at * DIM + d] = f32_to_bf16(tot != 0.f ? v / tot : 0.f);
   }
-  if (d == 0 && a.lse) a.lse[blockIdx.x] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+  if (d == 0 && a.lse) a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Host plan: rows per group (from the most rows a sequence can have), tiles
@@ -684,7 +683,10 @@ cudaError_t launch(const FewArgs& f, const KvCall& c) {
   if (cudaError_t e = c.launched("attention_few")) return e;
   if (f.n_split == 1) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(f.a.kv.n_tokens) * f.a.heads);
+  const int rows_max = int(std::min<long long>((long long)f.a.kv.max_new * f.a.group, f.max_rows));
+  const long long rows = 1ll * rows_max * f.a.kv.kv_heads * f.a.kv.n_seqs;
+  if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(unsigned(rows));
   cfg.blockDim = dim3(256);
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[1];
@@ -692,7 +694,7 @@ cudaError_t launch(const FewArgs& f, const KvCall& c) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM>, f, C::kRows)) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM>, f, C::kRows, rows_max)) return e;
   return c.launched("attention_combine");
 }
 

@@ -36,8 +36,10 @@ namespace {
 
 constexpr int kBK = 128;                  // keys per tile
 constexpr uint32_t kUnit = 16384;         // bytes of a ring unit: 128 rows of 128 bytes
-constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kThreads = 320;
+constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
 constexpr int kRing = 9;
+constexpr int kDescs = 4;                 // segment descriptors in flight
+constexpr int kTileCost = 1;              // units added to every row tile: its set-up and output
 
 template <int DIM>
 struct ManyCfg {
@@ -50,8 +52,10 @@ struct ManyCfg {
   static constexpr uint32_t kOffRing = QT * kQTile;
   static constexpr uint32_t kOffEx = kOffRing + kRing * kUnit;  // [2][2][128] floats: row maxima of the halves
   static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
-  static constexpr int kBars = 2 * kRing + 1 + 2 + 2 + QT + 1;  // full, empty, qfull, sfull, pready, pvdone, drain
-  static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+  // full, empty [kRing]; qfull, qempty, ofree, drain; sfull, pready [2]; pvdone [QT]; dfull, dempty [kDescs]
+  static constexpr int kBars = 2 * kRing + 4 + 4 + QT + 2 * kDescs;
+  static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
+  static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 64;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -74,12 +78,14 @@ struct ManyArgs {
   uint8_t* vx;
   uint8_t* bad;            // [nb][tiles_max]: bit i set if the page of keys 16 i .. 16 i + 15 is missing
   PlanHdr* plan;
-  long long* unit_off;     // [row tiles + 1] first unit of each row tile
+  long long* unit_off;     // [row tiles + 1] first unit of each row tile (kTileCost + its key tiles each)
   RowTile* row_tile;
   int max_row_tiles;
   int ctas;                // of the many kernel
   float* part_o;           // [2 ctas][rows][DIM]
   float* part_lse;         // [2 ctas][rows], base 2
+  unsigned long long inv_group;  // ceil(2^32 / group): row / group for rows below 2^26
+  __device__ __forceinline__ int token(int row) const { return int((unsigned(row) * inv_group) >> 32); }
 };
 
 // Key tiles that rows at positions minpos .. maxpos read: sink tiles [0,
@@ -108,7 +114,7 @@ __device__ __forceinline__ Range seq_range(const ManyArgs& m, const SeqInfo& s) 
 }
 __device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s, int row0, int rows) {
   const int base = s.kv - s.n_new, last = min(row0 + rows, s.n_new * m.a.group) - 1;
-  return range_of(base + row0 / m.a.group, base + last / m.a.group, m.a.window, m.a.sinks);
+  return range_of(base + m.token(row0), base + m.token(last), m.a.window, m.a.sinks);
 }
 
 // Byte offset of 16-byte chunk c of row r in a 1024-aligned 128-byte-swizzled K-major block.
@@ -166,7 +172,7 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
     long long mine = 0;
     if (i < n_rt) {
       const RowTile rt = m.row_tile[i];
-      mine = rows_range(m, kv_seq(m.a.kv, rt.seq), rt.row0, rows).n;
+      mine = kTileCost + rows_range(m, kv_seq(m.a.kv, rt.seq), rt.row0, rows).n;
     }
     long long total;
     const long long end = block_scan(mine, &total, buf);
@@ -231,6 +237,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   const long long tile = ((long long)bi * m.nh + h) * m.tiles_max + t;
   constexpr int W = DIM / 8, G = DIM / 64;
   uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
+  // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
+  const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
   for (int e = threadIdx.x; e < kBK * W; e += kPlanThreads) {
     const int key = e / W, w = e % W;
     uint32_t o[4] = {0, 0, 0, 0};
@@ -241,7 +249,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
       const __nv_bfloat16 bi16 = __ushort_as_bfloat16(kv.biases[0][row * G + w / 8]);
       dq8_bf16(kv.codes[0][row * W + w], __halves2bfloat162(sc, sc), __halves2bfloat162(bi16, bi16), o);
     }
-    *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) =
+        make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
   }
   uint8_t* vd = m.vx + tile * ManyCfg<DIM>::kTileBytes;
   // lanes: eight 8-key chunks (one 128-byte row of 64 keys) by four words
@@ -359,32 +368,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// ---- the range of a CTA -------------------------------------------------------------------
+// ---- the segments of a CTA ------------------------------------------------------------------
 
-// One CTA's part of a row tile: its key tiles [j0, j1) of n.
-struct Segment {
-  int h, rt, j0, j1, n;
-  RowTile tile;
-  bool first;  // the CTA's first segment
+// One CTA's part of a row tile: its key tiles [j0, j1) of n. j1 = 0: no more.
+struct __align__(16) Segment {
+  int seq, head, row0, n_rows;   // sequence and kv head (within the pass), first row, rows
+  int j0, j1, n, part;           // part: slot of the partial output, -1 if the row tile is whole
+  int first, base_pos, last;     // sequence's first step token, position of its token 0, its last row
+  int all_sink, all_first;       // Range of the sequence's expanded tiles
+  int my_sink, my_first;         // Range of the row tile
+  int pad;
+  __device__ __forceinline__ int tile(int j) const { return j < my_sink ? j : my_first + j - my_sink; }
+  __device__ __forceinline__ int index(int j) const {
+    const int t = tile(j);
+    return t < all_first ? t : all_sink + t - all_first;
+  }
 };
+static_assert(sizeof(Segment) == 64, "descriptor size");
 
-// Steps through the segments of the units [u, end).
+// Steps through the units [u, end) of a CTA. Every row tile has kTileCost
+// units more than key tiles; a part that holds none of the latter is skipped.
 struct Cursor {
   const ManyArgs& m;
-  long long u, begin, end, units;
-  int rt;
-  __device__ Cursor(const ManyArgs& args) : m(args), rt(-1) {
+  long long u, end, units;
+  int rt, head;
+  __device__ Cursor(const ManyArgs& args) : m(args), rt(-1), head(0) {
     units = m.plan->units;
     const long long all = units * m.nh;
-    begin = u = all * blockIdx.x / m.ctas;
+    u = all * blockIdx.x / m.ctas;
     end = all * (blockIdx.x + 1) / m.ctas;
-  }
-  __device__ bool next(Segment* s) {
-    if (u >= end) return false;
-    const int h = int(u / units);
-    const long long at = u % units;
-    if (rt < 0) {  // the last row tile that starts at or before `at`
-      int lo = 0, hi = m.plan->row_tiles - 1;
+    if (u < end) {
+      head = int(u / units);
+      const long long at = u - head * units;
+      int lo = 0, hi = m.plan->row_tiles - 1;  // the last row tile that starts at or before `at`
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (m.unit_off[mid] <= at)
@@ -394,19 +410,45 @@ struct Cursor {
       }
       rt = lo;
     }
-    const long long o0 = m.unit_off[rt], o1 = m.unit_off[rt + 1];
-    s->h = h;
-    s->rt = rt;
-    s->n = int(o1 - o0);
-    s->j0 = int(at - o0);
-    s->j1 = int(min(o1 - o0, at - o0 + (end - u)));
-    s->tile = m.row_tile[rt];
-    s->first = u == begin;
-    u += s->j1 - s->j0;
-    if (s->j1 == s->n) rt = rt + 1 == m.plan->row_tiles ? 0 : rt + 1;
-    return true;
+  }
+  __device__ void next(Segment* s, int rows) {
+    s->j1 = 0;
+    while (u < end && s->j1 == 0) {
+      const long long base = head * units, o0 = base + m.unit_off[rt], o1 = base + m.unit_off[rt + 1];
+      const long long stop = end < o1 ? end : o1;
+      const int n = int(o1 - o0) - kTileCost;
+      const int j0 = max(0, int(u - o0) - kTileCost), j1 = max(0, int(stop - o0) - kTileCost);
+      if (j1 > j0) {
+        const RowTile t = m.row_tile[rt];
+        const SeqInfo si = kv_seq(m.a.kv, t.seq);
+        const Range all = seq_range(m, si), mine = rows_range(m, si, t.row0, rows);
+        s->seq = t.seq - m.b0;
+        s->head = head;
+        s->row0 = t.row0;
+        s->last = si.n_new * m.a.group - 1;
+        s->n_rows = min(rows, s->last + 1 - t.row0);
+        s->j0 = j0;
+        s->j1 = j1;
+        s->n = n;
+        s->part = j0 == 0 && j1 == n ? -1 : 2 * int(blockIdx.x) + (j0 > 0 ? 1 : 0);
+        s->first = si.first;
+        s->base_pos = si.kv - si.n_new;
+        s->all_sink = all.n_sink, s->all_first = all.first;
+        s->my_sink = mine.n_sink, s->my_first = mine.first;
+      }
+      u = stop;
+      if (stop == o1 && ++rt == m.plan->row_tiles) rt = 0, ++head;
+    }
   }
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// Arrives on `bar` once every cp.async of this thread has landed (counted in the barrier's arrivals).
+__device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
@@ -419,11 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const uint32_t bar0 = base + C::kOffBar;
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kRing + s); };
-  const uint32_t qfull = bar0 + 8u * (2 * kRing);
-  auto sfull = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + 1 + s); };
-  auto pready = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + 3 + s); };
-  auto pvdone = [&](uint32_t q) { return bar0 + 8u * (2 * kRing + 5 + q); };
-  const uint32_t drain = bar0 + 8u * (2 * kRing + 5 + QT);
+  const uint32_t qfull = bar0 + 8u * (2 * kRing), qempty = qfull + 8, ofree = qfull + 16, drain = qfull + 24;
+  auto sfull = [&](uint32_t s) { return qfull + 32 + 8u * s; };
+  auto pready = [&](uint32_t s) { return qfull + 48 + 8u * s; };
+  auto pvdone = [&](uint32_t q) { return qfull + 64 + 8u * q; };
+  auto dfull = [&](uint32_t i) { return qfull + 64 + 8u * (QT + i % kDescs); };
+  auto dempty = [&](uint32_t i) { return qfull + 64 + 8u * (QT + kDescs + i % kDescs); };
+  Segment* descs = reinterpret_cast<Segment*>(gbase + C::kOffDesc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
   const AttnArgs& a = m.a;
@@ -432,7 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    mbar_init(qfull, kSoftWarps);
+    mbar_init(qfull, kLoadWarps * 32);
+    mbar_init(qempty, 1);
+    mbar_init(ofree, kSoftWarps);
+    for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps);
     for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), kSoftWarps);
     for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
     mbar_init(drain, 1);
@@ -457,23 +504,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   auto k_at = [](int i) { return QT == 2 ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
   auto v_at = [](int i, int n) { return QT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
+  // Segment i, once its descriptor is there; every reader arrives on dempty(i) when it needs it no more.
+  auto descriptor = [&](uint32_t i, Segment* s, bool& ok) {
+    if (ok) ok = mbar_wait(dfull(i), (i / kDescs) & 1u, abort_flag, hdr, kWaitLimit, false, 219);
+    s->j1 = 0;
+    if (ok) *s = descs[i % kDescs];
+    return ok && s->j1 > 0;
+  };
+
   if (warp == kWarpTma) {
     if (lane == 0) {
-      Cursor cur(m);
       Segment s;
       uint32_t it = 0;
       bool ok = true;
-      while (ok && cur.next(&s)) {
-        const SeqInfo si = kv_seq(a.kv, s.tile.seq);
-        const Range all = seq_range(m, si), mine = rows_range(m, si, s.tile.row0, C::kRows);
-        const long long tile0 = ((long long)(s.tile.seq - m.b0) * m.nh + s.h) * m.tiles_max;
+      for (uint32_t sg = 0; descriptor(sg, &s, ok); ++sg) {
+        mbar_arrive(dempty(sg));
+        const long long tile0 = ((long long)s.seq * m.nh + s.head) * m.tiles_max;
         const int n = s.j1 - s.j0;
         for (int p = 0; p < 2 * n && ok; ++p) {
           // which tile has ring position p
           const bool is_v = QT == 2 ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
           const int i = QT == 2 ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
-          const int t = all.index(mine.tile(s.j0 + i));
-          const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + t) * C::kTileBytes;
+          const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + s.index(s.j0 + i)) * C::kTileBytes;
           for (int u = 0; u < UN; ++u, ++it) {
             const uint32_t slot = it % kRing;
             if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
@@ -489,15 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     }
   } else if (warp == kWarpMma) {
     if (lane == 0) {
-      Cursor cur(m);
       Segment s;
-      uint32_t ring = 0, nq = 0, g0 = 0;  // before this segment: ring units, segments, S tiles
+      uint32_t ring = 0, g0 = 0;  // before this segment: ring units, S tiles
       bool ok = true;
       constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM < 128 ? DIM : 128);
-      while (ok && cur.next(&s)) {
+      for (uint32_t sg = 0; descriptor(sg, &s, ok); ++sg) {
+        mbar_arrive(dempty(sg));
         const int n = s.j1 - s.j0, total = n * QT;
-        if (!(ok = mbar_wait(qfull, nq & 1u, abort_flag, hdr, kWaitLimit, false, 222))) break;
-        ++nq;
+        if (!(ok = mbar_wait(qfull, sg & 1u, abort_flag, hdr, kWaitLimit, false, 222))) break;
+        fence_proxy_async();  // the loader warps' copies, for the tensor core
         tc_fence_after();
         auto wait_unit = [&](uint32_t seq) {
           return mbar_wait(full(seq % kRing), (seq / kRing) & 1u, abort_flag, hdr, kWaitLimit, false, 223);
@@ -517,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             if (q == QT - 1) umma_commit(empty(slot));
           }
           umma_commit(sfull(sl));
+          if (x == total - 1) umma_commit(qempty);
         };
         auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
           const int q = x % QT, i = x / QT;
@@ -546,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         for (int x = 0; x < total && ok; ++x) {
           const uint32_t g = g0 + x;
           if (!(ok = mbar_wait(pready(g & 1u), (g >> 1) & 1u, abort_flag, hdr, kWaitLimit, false, 224))) break;
+          if (x == 0 && sg > 0 && !(ok = mbar_wait(ofree, (sg - 1) & 1u, abort_flag, hdr, kWaitLimit, false, 230))) break;
           tc_fence_after();
           pv(x);
           if (ok && x + 2 < total) qk(x + 2);
@@ -557,14 +611,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       umma_commit(drain);
       mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
     }
+  } else if (warp >= kWarpLoad) {
+    // ---------------- segments and query rows: two warps; lane 0 of the first steps through the units ----------
+    Cursor cur(m);
+    Segment s;
+    bool ok = true;
+    auto produce = [&](uint32_t i) {
+      if (warp != kWarpLoad || lane != 0 || !ok) return;
+      if (i >= kDescs && !(ok = mbar_wait(dempty(i), ((i / kDescs) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 231))) return;
+      cur.next(&s, C::kRows);
+      descs[i % kDescs] = s;
+      mbar_arrive(dfull(i));
+    };
+    produce(0);
+    __syncwarp();
+    for (uint32_t sg = 0;; ++sg) {
+      if (!__all_sync(~0u, descriptor(sg, &s, ok))) break;
+      const Segment mine = s;
+      produce(sg + 1);  // one ahead, before this segment's rows
+      __syncwarp();
+      if (sg > 0 && ok) ok = mbar_wait(qempty, (sg - 1) & 1u, abort_flag, hdr, kWaitLimit, false, 232);
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+      constexpr int CH = DIM / 8;  // 16-byte chunks of a row
+      const int tid = threadIdx.x - kWarpLoad * 32, c = tid % CH;
+      const uint16_t* qh = a.q + (m.h0 + mine.head) * a.group * DIM + c * 8;
+      for (int r = tid / CH; r < C::kRows; r += kLoadWarps * 32 / CH) {
+        const int rr = min(mine.row0 + r, mine.last), t = m.token(rr);
+        const uint16_t* src = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
+        cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kUnit + sw128(r & 127, c & 7), src,
+                   r < mine.n_rows ? 16u : 0u);
+      }
+      cp_async_arrive_noinc(qfull);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dempty(sg));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---------------- softmax: eight warps, thread (row, half of the keys) ----------------
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;  // the tensor-memory lanes this warp may access
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
-    // |scale| in base 2; a negative scale flips the sign of q, scale 0 clears q
+    // |scale| in base 2 (the keys carry the sign; for scale 0 they are zeros)
     const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
-    Cursor cur(m);
     Segment s;
     uint32_t g = 0, pv0 = 0, exn = 0;  // S tiles so far, products O += P V per row tile so far, exchanges so far
     // After a failed wait a warp keeps going without waiting, so that the
@@ -581,50 +670,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
       return e[(half ^ 1) * 128 + row];
     };
-    while (cur.next(&s)) {
-      const SeqInfo si = kv_seq(a.kv, s.tile.seq);
-      const Range all = seq_range(m, si), mine = rows_range(m, si, s.tile.row0, C::kRows);
-      const int n_rows = min(C::kRows, si.n_new * a.group - s.tile.row0);
-      const int kvh = m.h0 + s.h, base_pos = si.kv - si.n_new;
-      // query rows into shared memory, rows past the end as zeros
-      for (int e = threadIdx.x; e < C::kRows * (DIM / 8); e += kSoftWarps * 32) {
-        const int r = e / (DIM / 8), c = e % (DIM / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < n_rows) {
-          const int rr = s.tile.row0 + r;
-          v = *reinterpret_cast<const uint4*>(a.q + (si.first + rr / a.group) * a.q_stride +
-                                              (kvh * a.group + rr % a.group) * DIM + c * 8);
-          if (a.scale < 0.f) {
-            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-          } else if (a.scale == 0.f) {  // (NaN and infinities stay NaN)
-            v.x = pack2(bf16lo(v.x) * 0.f, bf16hi(v.x) * 0.f), v.y = pack2(bf16lo(v.y) * 0.f, bf16hi(v.y) * 0.f);
-            v.z = pack2(bf16lo(v.z) * 0.f, bf16hi(v.z) * 0.f), v.w = pack2(bf16lo(v.w) * 0.f, bf16hi(v.w) * 0.f);
-          }
-        }
-        *reinterpret_cast<uint4*>(gbase + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kUnit + sw128(r & 127, c & 7)) = v;
-      }
-      fence_proxy_async();
-      tc_fence_before();
+    for (uint32_t sg = 0;; ++sg) {
+      // The eight warps agree on whether there is a segment: after a failed wait the flag has them all leave here.
+      int more = descriptor(sg, &s, ok);
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
-
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.b32 p, %0, 0;\n bar.red.and.pred p, 1, %1, p;\n selp.s32 %0, 1, 0, p;\n}"
+          : "+r"(more)
+          : "n"(kSoftWarps * 32)
+          : "memory");
+      if (!more) break;
+      if (lane == 0) mbar_arrive(dempty(sg));
       float ref[QT], sum[QT];
       int pos[QT], minpos[QT], maxpos[QT];
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
         ref[q] = -INFINITY, sum[q] = 0.f;
-        const int last = si.n_new * a.group - 1, r0 = s.tile.row0 + q * 128;
-        pos[q] = base_pos + min(r0 + row, last) / a.group;
-        minpos[q] = base_pos + min(r0, last) / a.group;
-        maxpos[q] = base_pos + min(r0 + 127, last) / a.group;
+        const int r0 = s.row0 + q * 128;
+        pos[q] = s.base_pos + m.token(min(r0 + row, s.last));
+        minpos[q] = s.base_pos + m.token(min(r0, s.last));
+        maxpos[q] = s.base_pos + m.token(min(r0 + 127, s.last));
       }
       const int n = s.j1 - s.j0;
-      const uint8_t* bad = m.bad + (long long)(s.tile.seq - m.b0) * m.tiles_max;
-      unsigned bad_next = bad[all.index(mine.tile(s.j0))];
+      const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
+      unsigned bad_next = bad[s.index(s.j0)];
       for (int i = 0; i < n; ++i) {
-        const int k0 = mine.tile(s.j0 + i) * kBK;
+        const int k0 = s.tile(s.j0 + i) * kBK;
         const unsigned missing = bad_next;
-        if (i + 1 < n) bad_next = bad[all.index(mine.tile(s.j0 + i + 1))];
+        if (i + 1 < n) bad_next = bad[s.index(s.j0 + i + 1)];
 #pragma unroll
         for (int q = 0; q < QT; ++q, ++g) {
           const uint32_t sl = tmem + lanes + (g & 1u) * 128;
@@ -708,11 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         wait(pvdone(q), (pv0 - 1) & 1u, 228);
         tc_fence_after();
         const int r = q * 128 + row;
-        const bool valid = r < n_rows;
-        const int rr = s.tile.row0 + (valid ? r : 0);
-        const long long at = (long long)(si.first + rr / a.group) * a.heads + kvh * a.group + rr % a.group;
-        const bool part = s.j0 > 0 || s.j1 < s.n;
-        const long long prow = (long long)(2 * blockIdx.x + (s.j0 > 0 && s.first ? 1 : 0)) * C::kRows + r;
+        const bool valid = r < s.n_rows, part = s.part >= 0;
+        const int rr = min(s.row0 + r, s.last), t = m.token(rr);
+        const long long at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
+        const long long prow = (long long)s.part * C::kRows + r;
         const uint32_t oc = tmem + lanes + 256 + q * DIM + half * (DIM / 2);
 #pragma unroll 1
         for (int cc = 0; cc < DIM / 2; cc += 32) {
@@ -747,6 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);
     }
   }
 
@@ -771,7 +845,7 @@ __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyA
   int lo = 0, hi = m.plan->row_tiles - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (m.unit_off[mid] <= end % units)
+    if (m.unit_off[mid] <= end - h * units)
       lo = mid;
     else
       hi = mid - 1;
@@ -783,13 +857,16 @@ __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyA
   if (c0 != int(blockIdx.x)) return;
   const RowTile rt = m.row_tile[lo];
   const SeqInfo si = kv_seq(m.a.kv, rt.seq);
-  const int n_rows = min(kRows, si.n_new * m.a.group - rt.row0);
+  const int n_rows = min(kRows, si.n_new * m.a.group - rt.row0), n_tiles = int(u1 - u0) - kTileCost;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // A CTA whose range starts inside the row tile holds its part as its first
-  // segment (slot 1 of its two), else as its last or only one (slot 0); with
-  // fewer units than CTAs some hold none.
-  auto slot = [&](int c) { return 2 * c + (c > c0 ? 1 : 0); };
-  auto holds = [&](int c) { return all * c / m.ctas < all * (c + 1) / m.ctas; };
+  // key tiles [from(c), to(c)) of the row tile are CTA c's; its part is in slot
+  // 1 of its two if it begins inside the row tile
+  auto tile_at = [&](long long u) { return min(n_tiles, max(0, int(max(0ll, min(u, u1) - u0)) - kTileCost)); };
+  auto from = [&](int c) { return tile_at(all * c / m.ctas); };
+  auto holds = [&](int c) { return from(c + 1) > from(c); };
+  auto slot = [&](int c) { return 2 * c + (from(c) > 0 ? 1 : 0); };
+  for (int c = c0; c <= c1; ++c)
+    if (from(c + 1) - from(c) == n_tiles) return;  // one CTA has them all, and wrote the output
   for (int r = blockIdx.y * 8 + warp; r < n_rows; r += gridDim.y * 8) {
     float top = -INFINITY;
     for (int c = c0; c <= c1; ++c)
@@ -918,6 +995,7 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.ctas = p.ctas;
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
+  m.inv_group = ((1ull << 32) + a.group - 1) / a.group;
   return a.kv.dim == 64 ? launch<64>(m, p, c) : a.kv.dim == 128 ? launch<128>(m, p, c) : launch<256>(m, p, c);
 }
 

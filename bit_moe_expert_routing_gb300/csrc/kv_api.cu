@@ -61,6 +61,12 @@ constexpr int kFewRows = 64;
 
 bool any_many(const AttnArgs& a) { return (long long)a.kv.max_new * a.group > kFewRows; }
 
+// Whether a sequence may have so few; when the step's tokens are max_new for
+// every sequence, all are alike.
+bool any_few(const AttnArgs& a) {
+  return !any_many(a) || (long long)a.kv.n_seqs * a.kv.max_new != a.kv.n_tokens;
+}
+
 AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
   AttnArgs g{};
   g.kv = kv;
@@ -133,7 +139,8 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   g.out = out;
   g.lse = lse;
   const KvCall c = begin_call(stream);
-  if (cudaError_t e = attention_few(g, kFewRows, workspace, c)) return status_of(e);
+  if (any_few(g))
+    if (cudaError_t e = attention_few(g, kFewRows, workspace, c)) return status_of(e);
   return any_many(g) ? status_of(attention_many(g, kFewRows, workspace, c)) : MOE_OK;
 }
 
