@@ -60,13 +60,21 @@ struct ManyCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
-struct RowTile {
-  int seq, row0;  // sequence, first row within it
+struct __align__(16) RowTile {
+  int seq, row0;        // sequence, first row within it
+  int first, n_new, kv;  // of the sequence
+  int pad[3];
+  __device__ __forceinline__ SeqInfo info() const { return SeqInfo{first, n_new, kv}; }
 };
 
 struct PlanHdr {
   long long units;  // of one kv head
   int row_tiles, pad;
+};
+
+struct __align__(16) CtaRange {
+  long long begin;  // first unit of all kv heads' units
+  int head, rt;     // its kv head and row tile
 };
 
 struct ManyArgs {
@@ -80,6 +88,7 @@ struct ManyArgs {
   PlanHdr* plan;
   long long* unit_off;     // [row tiles + 1] first unit of each row tile (kTileCost + its key tiles each)
   RowTile* row_tile;
+  CtaRange* range;         // [ctas + 1] where each CTA's units begin; the last entry ends them
   int max_row_tiles;
   int ctas;                // of the many kernel
   float* part_o;           // [2 ctas][rows][DIM]
@@ -94,7 +103,6 @@ struct ManyArgs {
 struct Range {
   int n_sink, first, n;
   __device__ __forceinline__ int tile(int t) const { return t < n_sink ? t : first + t - n_sink; }
-  __device__ __forceinline__ int index(int tile) const { return tile < first ? tile : n_sink + tile - first; }
 };
 __device__ __forceinline__ Range range_of(int minpos, int maxpos, int window, int sinks) {
   Range r{0, 0, 1};
@@ -148,8 +156,9 @@ __device__ long long block_scan(long long v, long long* total, long long* buf) {
 
 __device__ void make_plan(const ManyArgs& m, int rows) {
   __shared__ long long buf[kPlanThreads / 32];
-  // row tiles of the sequences, in order
-  long long n_rt = 0;
+  __shared__ SeqInfo info[kPlanThreads];
+  __shared__ int ends[kPlanThreads];  // row tiles up to and with each sequence of the chunk
+  long long n_rt = 0, units = 0;
   for (int base = 0; base < m.nb; base += kPlanThreads) {
     const int b = base + threadIdx.x;
     int mine = 0;
@@ -159,30 +168,58 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
       if (taken(m, s)) mine = (s.n_new * m.a.group + rows - 1) / rows;
     }
     long long total;
-    const long long end = block_scan(mine, &total, buf);
-    const long long first = n_rt + end - mine;
-    for (int i = 0; i < mine && first + i < m.max_row_tiles; ++i) m.row_tile[first + i] = RowTile{m.b0 + b, i * rows};
-    n_rt += total;
-  }
-  if (n_rt > m.max_row_tiles) n_rt = m.max_row_tiles;  // (the host's bound; reached only by inconsistent offsets)
-  __syncthreads();
-  long long units = 0;
-  for (long long base = 0; base < n_rt; base += kPlanThreads) {
-    const long long i = base + threadIdx.x;
-    long long mine = 0;
-    if (i < n_rt) {
-      const RowTile rt = m.row_tile[i];
-      mine = kTileCost + rows_range(m, kv_seq(m.a.kv, rt.seq), rt.row0, rows).n;
+    ends[threadIdx.x] = int(block_scan(mine, &total, buf));
+    info[threadIdx.x] = s;
+    __syncthreads();
+    for (int c0 = 0; c0 < total; c0 += kPlanThreads) {
+      const int i = c0 + threadIdx.x;
+      int n = 0;
+      if (i < total && n_rt + i < m.max_row_tiles) {  // (the host's bound; passed only by inconsistent offsets)
+        int lo = 0, hi = kPlanThreads - 1;  // the first sequence with ends > i
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (ends[mid] > i)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        const SeqInfo q = info[lo];
+        const int row0 = (i - (lo ? ends[lo - 1] : 0)) * rows;
+        m.row_tile[n_rt + i] = RowTile{m.b0 + base + lo, row0, q.first, q.n_new, q.kv, {}};
+        n = kTileCost + rows_range(m, q, row0, rows).n;
+      }
+      long long sum;
+      const long long end = block_scan(n, &sum, buf);
+      if (n) m.unit_off[n_rt + i] = units + end - n;
+      units += sum;
     }
-    long long total;
-    const long long end = block_scan(mine, &total, buf);
-    if (i < n_rt) m.unit_off[i] = units + end - mine;
-    units += total;
+    n_rt += total;
+    __syncthreads();
   }
+  if (n_rt > m.max_row_tiles) n_rt = m.max_row_tiles;
   if (threadIdx.x == 0) {
     m.unit_off[n_rt] = units;
     m.plan->units = units;
     m.plan->row_tiles = int(n_rt);
+  }
+  __syncthreads();
+  const long long all = units * m.nh;
+  for (int c = threadIdx.x; c <= m.ctas; c += kPlanThreads) {
+    const long long begin = all * c / m.ctas;
+    CtaRange r{begin, 0, 0};
+    if (begin < all) {
+      r.head = int(begin / units);
+      const long long at = begin - r.head * units;
+      int hi = int(n_rt) - 1;  // the last row tile that starts at or before `at`
+      while (r.rt < hi) {
+        const int mid = (r.rt + hi + 1) >> 1;
+        if (m.unit_off[mid] <= at)
+          r.rt = mid;
+        else
+          hi = mid - 1;
+      }
+    }
+    m.range[c] = r;
   }
 }
 
@@ -299,29 +336,57 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart, version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
-         (uint64_t(2) << 61);
-}
+// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
+// 1024 bytes apart, version 1. Low half: the start address in 16-byte units
+// and the leading offset; the high half is the same for all.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
 // kind::f16: bf16 A and B, fp32 D, both K-major, M = 128, N = n.
 constexpr uint32_t idesc_n(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Four K = 16 steps of a 64-wide K block, by one elected lane of the converged
+// warp: D += A B^T with A in shared memory, or in tensor memory. The first
+// step overwrites D when acc is 0. (One asm statement with warp-uniform
+// operands: issued by a single lane of a divergent warp, with its operands in
+// per-thread registers, an MMA took ~130 cycles to issue, twice its run time.)
+__device__ __forceinline__ void umma4_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred e, p, t;\n .reg .b32 x1, x2, x3, y1, y2, y3;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " add.u32 x1, %1, 2;\n add.u32 x2, %1, 4;\n add.u32 x3, %1, 6;\n"
+      " add.u32 y1, %2, 2;\n add.u32 y2, %2, 4;\n add.u32 y3, %2, 6;\n"
+      " mov.b64 a0, {%1, %3};\n mov.b64 a1, {x1, %3};\n mov.b64 a2, {x2, %3};\n mov.b64 a3, {x3, %3};\n"
+      " mov.b64 b0, {%2, %3};\n mov.b64 b1, {y1, %3};\n mov.b64 b2, {y2, %3};\n mov.b64 b3, {y3, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, %5, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %4, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %4, t;\n}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred e, p, t;\n .reg .b32 x1, x2, x3, y1, y2, y3;\n .reg .b64 b0, b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " add.u32 x1, %1, 8;\n add.u32 x2, %1, 16;\n add.u32 x3, %1, 24;\n"
+      " add.u32 y1, %2, 2;\n add.u32 y2, %2, 4;\n add.u32 y3, %2, 6;\n"
+      " mov.b64 b0, {%2, %3};\n mov.b64 b1, {y1, %3};\n mov.b64 b2, {y2, %3};\n mov.b64 b3, {y3, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, %5, %5;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x3], b3, %4, t;\n}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
+// `bar` receives one arrival when every MMA that the elected lane issued before has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -354,6 +419,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 32 bytes, a whole sector, in one store (32-byte aligned).
+__device__ __forceinline__ void st_v8(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -392,24 +463,13 @@ struct Cursor {
   const ManyArgs& m;
   long long u, end, units;
   int rt, head;
-  __device__ Cursor(const ManyArgs& args) : m(args), rt(-1), head(0) {
+  __device__ Cursor(const ManyArgs& args) : m(args) {
+    const CtaRange r = m.range[blockIdx.x];
     units = m.plan->units;
-    const long long all = units * m.nh;
-    u = all * blockIdx.x / m.ctas;
-    end = all * (blockIdx.x + 1) / m.ctas;
-    if (u < end) {
-      head = int(u / units);
-      const long long at = u - head * units;
-      int lo = 0, hi = m.plan->row_tiles - 1;  // the last row tile that starts at or before `at`
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (m.unit_off[mid] <= at)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      rt = lo;
-    }
+    u = r.begin;
+    end = m.range[blockIdx.x + 1].begin;
+    head = r.head;
+    rt = r.rt;
   }
   __device__ void next(Segment* s, int rows) {
     s->j1 = 0;
@@ -420,7 +480,7 @@ struct Cursor {
       const int j0 = max(0, int(u - o0) - kTileCost), j1 = max(0, int(stop - o0) - kTileCost);
       if (j1 > j0) {
         const RowTile t = m.row_tile[rt];
-        const SeqInfo si = kv_seq(m.a.kv, t.seq);
+        const SeqInfo si = t.info();
         const Range all = seq_range(m, si), mine = rows_range(m, si, t.row0, rows);
         s->seq = t.seq - m.b0;
         s->head = head;
@@ -472,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
   const AttnArgs& a = m.a;
   WsHeader* hdr = a.kv.hdr;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (known to be warp-uniform)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
@@ -540,77 +600,70 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       }
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0) {
-      Segment s;
-      uint32_t ring = 0, g0 = 0;  // before this segment: ring units, S tiles
-      bool ok = true;
-      constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM < 128 ? DIM : 128);
-      for (uint32_t sg = 0; descriptor(sg, &s, ok); ++sg) {
-        mbar_arrive(dempty(sg));
-        const int n = s.j1 - s.j0, total = n * QT;
-        if (!(ok = mbar_wait(qfull, sg & 1u, abort_flag, hdr, kWaitLimit, false, 222))) break;
-        fence_proxy_async();  // the loader warps' copies, for the tensor core
-        tc_fence_after();
-        auto wait_unit = [&](uint32_t seq) {
-          return mbar_wait(full(seq % kRing), (seq / kRing) & 1u, abort_flag, hdr, kWaitLimit, false, 223);
-        };
-        auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
-          const int q = x % QT, i = x / QT;
-          const uint32_t sl = (g0 + x) & 1u, d = tmem + sl * 128;
-          for (int u = 0; u < UN; ++u) {
-            const uint32_t seq = ring + k_at(i) * UN + u, slot = seq % kRing;
-            if (q == 0) {
-              if (!(ok = wait_unit(seq))) return;
-              tc_fence_after();
-            }
-            const uint32_t qa = base + C::kOffQ + q * C::kQTile + u * kUnit, kb = base + C::kOffRing + slot * kUnit;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_ss(d, smem_desc(qa + kk * 32), smem_desc(kb + kk * 32), kIdS, (u | kk) != 0);
-            if (q == QT - 1) umma_commit(empty(slot));
-          }
-          umma_commit(sfull(sl));
-          if (x == total - 1) umma_commit(qempty);
-        };
-        auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
-          const int q = x % QT, i = x / QT;
-          const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
-          for (int u = 0; u < UN; ++u) {
-            const uint32_t seq = ring + v_at(i, n) * UN + u, slot = seq % kRing;
-            if (q == 0) {
-              if (!(ok = wait_unit(seq))) return;
-              tc_fence_after();
-            }
-            const uint32_t vb = base + C::kOffRing + slot * kUnit;
-            // a unit holds both blocks of 64 keys (DIM 64), one block (128), or one block of half the dims (256)
-            const int kb0 = DIM == 64 ? 0 : DIM == 128 ? u : u / 2;
-            const uint32_t od = o + (DIM == 256 ? (u & 1) * 128 : 0);
-#pragma unroll
-            for (int kb = 0; kb < (DIM == 64 ? 2 : 1); ++kb)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_ts(od, p + (kb0 + kb) * 32 + kk * 8, smem_desc(vb + kb * 8192 + kk * 32), kIdO,
-                        i > 0 || kb0 + kb > 0 || kk > 0);
-            if (q == QT - 1) umma_commit(empty(slot));
-          }
-          umma_commit(pvdone(q));
-        };
-        qk(0);
-        if (ok && total > 1) qk(1);
-        for (int x = 0; x < total && ok; ++x) {
-          const uint32_t g = g0 + x;
-          if (!(ok = mbar_wait(pready(g & 1u), (g >> 1) & 1u, abort_flag, hdr, kWaitLimit, false, 224))) break;
-          if (x == 0 && sg > 0 && !(ok = mbar_wait(ofree, (sg - 1) & 1u, abort_flag, hdr, kWaitLimit, false, 230))) break;
-          tc_fence_after();
-          pv(x);
-          if (ok && x + 2 < total) qk(x + 2);
+    // the whole warp, converged; every wait's outcome is made warp-uniform
+    Segment s;
+    uint32_t ring = 0, g0 = 0;  // before this segment: ring units, S tiles
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+      ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site));
+      tc_fence_after();
+      return ok;
+    };
+    constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM < 128 ? DIM : 128);
+    for (uint32_t sg = 0;; ++sg) {
+      if (!__all_sync(~0u, descriptor(sg, &s, ok))) break;
+      if (lane == 0) mbar_arrive(dempty(sg));
+      __syncwarp();
+      const int n = s.j1 - s.j0, total = n * QT;
+      if (!wait(qfull, sg & 1u, 222)) break;
+      fence_proxy_async();  // the loader warps' copies, for the tensor core
+      auto wait_unit = [&](uint32_t seq) { return wait(full(seq % kRing), (seq / kRing) & 1u, 223); };
+      auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
+        const int q = x % QT, i = x / QT;
+        const uint32_t sl = (g0 + x) & 1u, d = tmem + sl * 128;
+        for (int u = 0; u < UN; ++u) {
+          const uint32_t seq = ring + k_at(i) * UN + u, slot = seq % kRing;
+          if (q == 0 && !wait_unit(seq)) return;
+          umma4_ss(d, desc_lo(base + C::kOffQ + q * C::kQTile + u * kUnit), desc_lo(base + C::kOffRing + slot * kUnit),
+                   kIdS, u != 0);
+          if (q == QT - 1) umma_commit(empty(slot));
         }
-        g0 += total;
-        ring += 2 * n * UN;
+        umma_commit(sfull(sl));
+        if (x == total - 1) umma_commit(qempty);
+      };
+      auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
+        const int q = x % QT, i = x / QT;
+        const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
+        for (int u = 0; u < UN; ++u) {
+          const uint32_t seq = ring + v_at(i, n) * UN + u, slot = seq % kRing;
+          if (q == 0 && !wait_unit(seq)) return;
+          const uint32_t vb = base + C::kOffRing + slot * kUnit;
+          // a unit holds both blocks of 64 keys (DIM 64), one block (128), or one block of half the dims (256)
+          const int kb0 = DIM == 64 ? 0 : DIM == 128 ? u : u / 2;
+          const uint32_t od = o + (DIM == 256 ? (u & 1) * 128 : 0);
+#pragma unroll
+          for (int kb = 0; kb < (DIM == 64 ? 2 : 1); ++kb)
+            umma4_ts(od, p + (kb0 + kb) * 32, desc_lo(vb + kb * 8192), kIdO, i > 0 || kb0 + kb > 0);
+          if (q == QT - 1) umma_commit(empty(slot));
+        }
+        umma_commit(pvdone(q));
+      };
+      qk(0);
+      if (ok && total > 1) qk(1);
+      for (int x = 0; x < total && ok; ++x) {
+        const uint32_t g = g0 + x;
+        if (!wait(pready(g & 1u), (g >> 1) & 1u, 224)) break;
+        if (x == 0 && sg > 0 && !wait(ofree, (sg - 1) & 1u, 230)) break;
+        pv(x);
+        if (ok && x + 2 < total) qk(x + 2);
       }
-      // every MMA has completed before the CTA leaves (bounded)
-      umma_commit(drain);
-      mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
+      g0 += total;
+      ring += 2 * n * UN;
     }
+    // every MMA has completed before the CTA leaves (bounded)
+    __syncwarp();
+    umma_commit(drain);
+    mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
   } else if (warp >= kWarpLoad) {
     // ---------------- segments and query rows: two warps; lane 0 of the first steps through the units ----------
     Cursor cur(m);
@@ -636,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       constexpr int CH = DIM / 8;  // 16-byte chunks of a row
       const int tid = threadIdx.x - kWarpLoad * 32, c = tid % CH;
       const uint16_t* qh = a.q + (m.h0 + mine.head) * a.group * DIM + c * 8;
+#pragma unroll 8
       for (int r = tid / CH; r < C::kRows; r += kLoadWarps * 32 / CH) {
         const int rr = min(mine.row0 + r, mine.last), t = m.token(rr);
         const uint16_t* src = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
@@ -654,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
     // |scale| in base 2 (the keys carry the sign; for scale 0 they are zeros)
     const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;  // rows are multiples of 128 bytes
     Segment s;
     uint32_t g = 0, pv0 = 0, exn = 0;  // S tiles so far, products O += P V per row tile so far, exchanges so far
     // After a failed wait a warp keeps going without waiting, so that the
@@ -711,12 +766,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           const bool whole = missing == 0 && k0 + kBK - 1 <= minpos[q] &&
                              (a.window == 0 || k0 > maxpos[q] - a.window || k0 + kBK <= a.sinks);
           if (!whole) {
+            // bit e: this row sees key k0 + 64 half + e, from the interval (or the sinks) that it sees
+            const int kb = k0 + half * 64;
+            auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };  // bits under x
+            uint64_t sees = below(pos[q] + 1 - kb);
+            if (a.window > 0) sees &= ~below(pos[q] - a.window + 1 - kb) | below(a.sinks - kb);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              const int key = k0 + half * 64 + e;
-              const bool sees = key <= pos[q] && (a.window == 0 || key > pos[q] - a.window || key < a.sinks) &&
-                                !((missing >> (half * 4 + e / 16)) & 1u);
-              if (!sees) v[e] = 0xff800000u;  // -inf
+            for (int i16 = 0; i16 < 4; ++i16)
+              if ((missing >> (half * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
+            const uint32_t s0 = uint32_t(sees), s1 = uint32_t(sees >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(s0 & (1u << e))) v[e] = 0xff800000u;  // -inf
+              if (!(s1 & (1u << e))) v[32 + e] = 0xff800000u;
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -795,19 +857,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           if (part) {
             float* dst = m.part_o + prow * DIM + d;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + e) =
-                  make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                              __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_v8(dst + e, o + e);
           } else if (valid) {
             uint16_t* dst = a.out + at * DIM + d;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
+            for (int e = 0; e < 32; e += 2)
+              o[e / 2] = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+            if (wide) {
+              st_v8(dst, o), st_v8(dst + 16, o + 8);
+            } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
@@ -832,59 +895,54 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   }
 }
 
-// Joins the row tiles that are divided between CTAs. CTA (c, slice): the row
-// tile that the end of CTA c's range divides, if c holds its first unit.
+// Joins the row tiles that are divided between CTAs. CTA (c, slice): eight
+// rows of the row tile that the end of CTA c's range divides, if c holds its
+// first unit.
 template <int DIM>
 __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
   griddep_wait();
   constexpr int kRows = ManyCfg<DIM>::kRows;
-  const long long units = m.plan->units, all = units * m.nh;
-  const long long end = all * (blockIdx.x + 1) / m.ctas;
-  if (end >= all || end == all * blockIdx.x / m.ctas) return;
-  const int h = int(end / units);
-  int lo = 0, hi = m.plan->row_tiles - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (m.unit_off[mid] <= end - h * units)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const long long u0 = h * units + m.unit_off[lo], u1 = h * units + m.unit_off[lo + 1];
-  if (u0 == end) return;  // the cut is between two row tiles
-  auto cta_of = [&](long long u) { return int(((u + 1) * m.ctas - 1) / all); };
-  const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
-  if (c0 != int(blockIdx.x)) return;
-  const RowTile rt = m.row_tile[lo];
-  const SeqInfo si = kv_seq(m.a.kv, rt.seq);
-  const int n_rows = min(kRows, si.n_new * m.a.group - rt.row0), n_tiles = int(u1 - u0) - kTileCost;
+  const int c0 = blockIdx.x;
+  const CtaRange cut = m.range[c0 + 1];
+  const long long units = m.plan->units, begin = m.range[c0].begin;
+  if (cut.begin >= units * m.nh || cut.begin == begin) return;
+  const long long u0 = cut.head * units + m.unit_off[cut.rt], u1 = cut.head * units + m.unit_off[cut.rt + 1];
+  if (u0 == cut.begin || u0 < begin) return;  // the cut is between two row tiles, or an earlier CTA has the first unit
+  const RowTile rt = m.row_tile[cut.rt];
+  const int n_rows = min(kRows, rt.n_new * m.a.group - rt.row0), n_tiles = int(u1 - u0) - kTileCost;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // key tiles [from(c), to(c)) of the row tile are CTA c's; its part is in slot
-  // 1 of its two if it begins inside the row tile
+  // key tiles [from, to) of the row tile are CTA c's; its part is in slot 1 of
+  // its two if it begins inside the row tile
   auto tile_at = [&](long long u) { return min(n_tiles, max(0, int(max(0ll, min(u, u1) - u0)) - kTileCost)); };
-  auto from = [&](int c) { return tile_at(all * c / m.ctas); };
-  auto holds = [&](int c) { return from(c + 1) > from(c); };
-  auto slot = [&](int c) { return 2 * c + (from(c) > 0 ? 1 : 0); };
-  for (int c = c0; c <= c1; ++c)
-    if (from(c + 1) - from(c) == n_tiles) return;  // one CTA has them all, and wrote the output
-  for (int r = blockIdx.y * 8 + warp; r < n_rows; r += gridDim.y * 8) {
+  // the last CTA that holds a part
+  int c1 = c0;
+  while (m.range[c1 + 1].begin < u1) ++c1;
+  const int r = blockIdx.y * 8 + warp;
+  if (r < n_rows) {
     float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-      if (holds(c)) top = fmaxf(top, m.part_lse[(long long)slot(c) * kRows + r]);
+    for (int c = c0, from = 0; c <= c1; ++c) {
+      const int to = tile_at(m.range[c + 1].begin);
+      if (to - from == n_tiles) return;  // one CTA has them all, and wrote the output
+      if (to > from) top = fmaxf(top, m.part_lse[(2ll * c + (from > 0)) * kRows + r]);
+      from = to;
+    }
     const float ref = top == -INFINITY ? 0.f : top;
     float o[DIM / 32], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      if (!holds(c)) continue;
-      const long long pr = (long long)slot(c) * kRows + r;
-      const float w = ex2(m.part_lse[pr] - ref);
-      sum += w;
+    for (int c = c0, from = 0; c <= c1; ++c) {
+      const int to = tile_at(m.range[c + 1].begin);
+      if (to > from) {
+        const long long pr = (2ll * c + (from > 0)) * kRows + r;
+        const float w = ex2(m.part_lse[pr] - ref);
+        sum += w;
 #pragma unroll
-      for (int j = 0; j < DIM / 32; ++j) o[j] += w * m.part_o[pr * DIM + lane + 32 * j];
+        for (int j = 0; j < DIM / 32; ++j) o[j] += w * m.part_o[pr * DIM + lane + 32 * j];
+      }
+      from = to;
     }
     const int rr = rt.row0 + r;
-    const long long at = (long long)(si.first + rr / m.a.group) * m.a.heads + (m.h0 + h) * m.a.group + rr % m.a.group;
+    const long long at = (long long)(rt.first + m.token(rr)) * m.a.heads + (m.h0 + cut.head) * m.a.group + rr - m.token(rr) * m.a.group;
 #pragma unroll
     for (int j = 0; j < DIM / 32; ++j) m.a.out[at * DIM + lane + 32 * j] = f32_to_bf16(sum != 0.f ? o[j] / sum : 0.f);
     if (m.a.lse && lane == 0) m.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -901,7 +959,7 @@ size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ManyPlan {
   int rows, tiles_max, nb, nh, ctas, max_row_tiles;
-  size_t kx, vx, bad, plan, unit_off, row_tile, part_o, part_lse, total;
+  size_t kx, vx, bad, plan, unit_off, row_tile, range, part_o, part_lse, total;
 };
 
 ManyPlan plan(const AttnArgs& a) {
@@ -930,6 +988,7 @@ ManyPlan plan(const AttnArgs& a) {
   p.plan = put(sizeof(PlanHdr));
   p.unit_off = put((size_t(p.max_row_tiles) + 1) * 8);
   p.row_tile = put(size_t(p.max_row_tiles) * sizeof(RowTile));
+  p.range = put((size_t(p.ctas) + 1) * sizeof(CtaRange));
   p.part_o = put(size_t(2) * p.ctas * p.rows * dim * 4);
   p.part_lse = put(size_t(2) * p.ctas * p.rows * 4);
   p.total = o;
@@ -968,7 +1027,7 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
       if (cudaError_t e = launch_dependent(c, "attention_many", attention_many_kernel<DIM>, dim3(p.ctas), kThreads, C::kSmem, m))
         return e;
       if (cudaError_t e = launch_dependent(c, "attention_many_combine", attention_many_combine_kernel<DIM>,
-                                           dim3(p.ctas, 8), 256, 0, m))
+                                           dim3(p.ctas, C::kRows / 8), 256, 0, m))
         return e;
     }
   return cudaSuccess;
@@ -991,6 +1050,7 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.plan = reinterpret_cast<PlanHdr*>(w + p.plan);
   m.unit_off = reinterpret_cast<long long*>(w + p.unit_off);
   m.row_tile = reinterpret_cast<RowTile*>(w + p.row_tile);
+  m.range = reinterpret_cast<CtaRange*>(w + p.range);
   m.max_row_tiles = p.max_row_tiles;
   m.ctas = p.ctas;
   m.part_o = reinterpret_cast<float*>(w + p.part_o);

@@ -261,7 +261,7 @@ def test_attention_is_repeatable_and_takes_strided_queries(new, kv):
     wide[:, 2:10] = q
     assert torch.equal(cache.attention(wide[:, 2:10], dev), out)
     # without lse, into a given output, with a workspace full of junk
-    o = torch.full_like(q, math.nan)
+    o = torch.full((q.numel() + 8,), math.nan, dtype=torch.bfloat16, device="cuda")[8:].view_as(q)  # 16-byte aligned, no more
     ws = cache.attention_workspace(8, dev)
     ws.fill_(0xFF)
     assert cache.attention(q, dev, out=o, workspace=ws) is o and torch.equal(o, out)
