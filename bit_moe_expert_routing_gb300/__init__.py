@@ -341,6 +341,7 @@ class KVBatch:
         self.n_tokens = n_tokens
         self.c = moe_kv_batch(n, n_tokens, max_new, max_kv, q_off.data_ptr(), kv_len.data_ptr(),
                               block_table.data_ptr(), stride)
+        self._ref = ctypes.byref(self.c)
 
 
 class KVCache:
@@ -362,11 +363,13 @@ class KVCache:
                                      "and scales, biases bf16 [pages, kv heads, page size, head dim / 64]")
         self.k_codes, self.k_scales, self.k_biases = k_codes, k_scales, k_biases
         self.v_codes, self.v_scales, self.v_biases = v_codes, v_scales, v_biases
-        self.kv_heads, self.head_dim = heads, words * 8
+        self.kv_heads, self.head_dim, self.device = heads, words * 8, k_codes.device
         self.status = torch.zeros(256, dtype=torch.uint8, device=k_codes.device)
         self.c = moe_kv_cache(pages, size, heads, words * 8, k_codes.data_ptr(), k_scales.data_ptr(),
                               k_biases.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), v_biases.data_ptr(),
                               self.status.data_ptr())
+        self._ref = ctypes.byref(self.c)
+        self._torch, self._bf16 = torch, torch.bfloat16  # (an import statement costs as much as a check)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -378,31 +381,42 @@ class KVCache:
                 a.append(torch.zeros(n_pages, kv_heads, page_size, head_dim // 64, dtype=torch.bfloat16, device=device))
         return cls(*a)
 
+    def _stream(self, stream):
+        if stream is not None:
+            return stream.cuda_stream
+        return self._torch._C._cuda_getCurrentRawStream(self.device.index)  # without the stream object's 2 us
+
     def _rows(self, name, t, n_tokens, heads):
-        import torch
-        if t.dtype != torch.bfloat16 or t.shape != (n_tokens, heads, self.head_dim) or t.device != self.k_codes.device:
-            raise ValueError(f"{name}: bf16 [{n_tokens}, {heads}, {self.head_dim}] on the cache's device")
+        """Checks a [n_tokens, heads, head dim] operand; its elements between tokens."""
+        d = self.head_dim
+        if t.shape != (n_tokens, heads, d) or t.dtype != self._bf16 or t.device != self.device:
+            raise ValueError(f"{name}: bf16 [{n_tokens}, {heads}, {d}] on the cache's device")
+        s = t.stride()
         if n_tokens == 0:
-            return heads * self.head_dim
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != self.head_dim):
+            return heads * d
+        if s[2] != 1 or (heads > 1 and s[1] != d):
             raise ValueError(f"{name}: the heads of a token are contiguous")
-        return t.stride(0) if n_tokens > 1 else heads * self.head_dim
+        return s[0] if n_tokens > 1 else heads * d
 
     def append(self, k, v, batch: KVBatch, stream=None):
         """Quantises k, v (bf16 [n_tokens, kv heads, head dim]) into the cache."""
         ks = self._rows("k", k, batch.n_tokens, self.kv_heads)
         vs = self._rows("v", v, batch.n_tokens, self.kv_heads)
-        _check(moe_kv_append(self.c, batch.c, k.data_ptr(), ks, v.data_ptr(), vs, _stream_ptr(stream)), "moe_kv_append")
+        st = lib().moe_kv_append(self._ref, batch._ref, k.data_ptr(), ks, v.data_ptr(), vs, self._stream(stream))
+        if st:
+            _check(st, "moe_kv_append")
 
     def read(self, batch: KVBatch, stream=None):
         """The step's tokens as the cache holds them: (k, v) bf16 [n_tokens, kv heads, head dim]."""
-        import contextlib
-        import torch
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            kv = torch.empty(2, batch.n_tokens, self.kv_heads, self.head_dim, dtype=torch.bfloat16,
-                             device=self.k_codes.device)
-        k, v = kv[0], kv[1]
-        _check(moe_kv_read(self.c, batch.c, k.data_ptr(), v.data_ptr(), _stream_ptr(stream)), "moe_kv_read")
+        if stream is not None:
+            with self._torch.cuda.stream(stream):
+                return self.read(batch)
+        shape = (batch.n_tokens, self.kv_heads, self.head_dim)
+        k = self._torch.empty(shape, dtype=self._bf16, device=self.device)
+        v = self._torch.empty(shape, dtype=self._bf16, device=self.device)
+        st = lib().moe_kv_read(self._ref, batch._ref, k.data_ptr(), v.data_ptr(), self._stream(None))
+        if st:
+            _check(st, "moe_kv_read")
         return k, v
 
     def attention_workspace(self, heads: int, batch: KVBatch, window: int = 0, sinks: int = 0):
@@ -411,31 +425,36 @@ class KVCache:
         n = moe_attention_workspace_size(self.c, batch.c, moe_attention(heads, window, sinks, 1.0))
         if n == 0:
             raise MoEError(MOE_ERR_ARG, "moe_attention_workspace_size")
-        return torch.empty(n, dtype=torch.uint8, device=self.k_codes.device)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def attention(self, q, batch: KVBatch, scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
                   lse: bool = False, workspace=None, stream=None):
         """Causal attention of the step's tokens over the cache: q bf16
         [n_tokens, heads, head dim] -> out (the same shape), or (out, lse) with
         lse fp32 [n_tokens, heads]. scale: 1 / sqrt(head dim) by default."""
-        import contextlib
-        import torch
+        torch = self._torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.attention(q, batch, scale, window, sinks, out, lse, workspace)
         if q.dim() != 3:
             raise ValueError("q: bf16 [n_tokens, heads, head dim]")
-        n, heads = batch.n_tokens, q.shape[1]
-        qs = self._rows("q", q, n, heads)
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            if out is None:
-                out = torch.empty(n, heads, self.head_dim, dtype=torch.bfloat16, device=q.device)
-            elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != q.device:
-                raise ValueError("out: contiguous, of q's shape, type and device")
-            l = torch.empty(n, heads, dtype=torch.float32, device=q.device) if lse else None
-            if workspace is None:
-                workspace = self.attention_workspace(heads, batch, window, sinks)
+        n, heads, _ = shape = q.shape
+        qs = self._rows("q", q, batch.n_tokens, heads)
+        if out is None:
+            out = torch.empty(shape, dtype=self._bf16, device=self.device)
+        elif out.shape != shape or out.dtype != self._bf16 or not out.is_contiguous() or out.device != self.device:
+            raise ValueError("out: contiguous, of q's shape, type and device")
+        l = lp = None
+        if lse:
+            l = torch.empty((n, heads), dtype=torch.float32, device=self.device)
+            lp = l.data_ptr()
+        if workspace is None:
+            workspace = self.attention_workspace(heads, batch, window, sinks)
         at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
-        _check(moe_attention_forward(self.c, batch.c, at, q.data_ptr(), qs, out.data_ptr(),
-                                     l.data_ptr() if lse else None, workspace.data_ptr(), workspace.numel(),
-                                     _stream_ptr(stream)), "moe_attention_forward")
+        st = lib().moe_attention_forward(self._ref, batch._ref, ctypes.byref(at), q.data_ptr(), qs, out.data_ptr(), lp,
+                                         workspace.data_ptr(), workspace.numel(), self._stream(None))
+        if st:
+            _check(st, "moe_attention_forward")
         return (out, l) if lse else out
 
     def check(self, stream=None):
