@@ -26,11 +26,17 @@
 // the keys and into the output for the values. (The cache holds magnitudes
 // up to 2^16, so scale * 2^113 is finite.)
 //
-// Work split: a CTA takes (sequence, kv head, group of 8 NT rows, range of
-// 32-key tiles), its four warps alternate tiles, each with its own ring of
-// bulk copies, so that nothing but the final merge joins the warps. Ranges
-// are cut so that the GPU is full; a sequence cut into several leaves fp32
-// partial outputs, which attention_combine_kernel joins.
+// Work split: an item is (sequence, kv head, group of 8 NT rows), and its
+// units are its 32-key tiles. One wave of CTAs takes equal, contiguous ranges
+// of all items' units, whatever the sequences' lengths; an item that is cut
+// leaves fp32 partial outputs, which attention_combine_kernel joins. (A grid of
+// fixed-length splits took 107 us for 64 ragged sequences of up to 8191
+// positions, 60 of them in prologues and merges.) When no item has more than
+// kWholeTiles, an item is a CTA's whole work and nothing is cut. The four warps
+// of a CTA alternate tiles, each with its own ring of asynchronous copies, so
+// that nothing but the merge of an item's end joins them. (cp.async rather than
+// bulk copies: a tile is six runs of one or two pages, and six bulk copies by
+// six lanes take the warp 1200 cycles to issue.)
 #include <algorithm>
 
 #include "kv.cuh"
@@ -58,14 +64,12 @@ struct FewCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kSteps = DIM / 16;
   static constexpr bool kQReg = NT * DIM <= 256;  // query fragments in registers; else read from shared memory
-  static constexpr int kQBytes = NT * kSteps * 32 * 8;
+  static constexpr int kQBytes = kQReg ? 0 : NT * kSteps * 32 * 8;
   static constexpr int kOffRing = kQBytes;
-  static constexpr int kOffBar = kOffRing + kWarps * kStages * Stage<DIM>::kBytes;
-  static constexpr int kOffMl = kOffBar + kWarps * kStages * 8;       // [warp][row] (max, sum)
-  static constexpr int kOffAbort = kOffMl + kWarps * kRows * 8;
-  static constexpr int kSmem = kOffAbort + 16;
-  // the merge puts two warps' outputs into the ring's place
-  static_assert(2 * kRows * DIM * 4 <= kWarps * kStages * Stage<DIM>::kBytes, "merge buffer");
+  static constexpr int kOffMl = kOffRing + kWarps * kStages * Stage<DIM>::kBytes;  // [warp][row] (max, sum)
+  static constexpr int kSmem = kOffMl + kWarps * kRows * 8;
+  // the merge puts three warps' outputs into the ring's place
+  static_assert(3 * kRows * DIM * 4 <= kWarps * kStages * Stage<DIM>::kBytes, "merge buffer");
   static constexpr int kMinCtas = NT * DIM <= 128 ? 4 : 2;
 };
 
@@ -106,6 +110,10 @@ __device__ __forceinline__ Sb make_sb(uint32_t s2, uint32_t b2) {
   return Sb{mul2(s2, kMulLo), mul2(s2, kMulHi), mul2(b2, kMulBias)};
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds_u16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
 // The tiles that a group of rows at positions minpos .. maxpos reads: the
@@ -126,38 +134,99 @@ __device__ __forceinline__ Tiles tiles_of(int minpos, int maxpos, int window, in
   return t;
 }
 
+constexpr int kWholeTiles = 16;
+constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
+
 struct FewArgs {
   AttnArgs a;
   int max_rows;      // sequences with more rows than this are left to the other kernels
-  int row_groups;    // groups of 8 NT rows per (sequence, kv head)
-  int chunk;         // tiles per split
-  int n_split;       // splits per group, at most
-  float* part_o;     // [split][token * heads + head][DIM], normalised
-  float* part_lse;   // [split][token * heads + head], base 2
+  int row_groups;    // groups of 8 NT rows per (sequence, kv head), at most
+  int whole;         // every CTA takes one item, whole
+  int max_ctas;      // else: CTAs of the grid
+  float* part_o;     // [2 max_ctas][8 NT][DIM], normalised
+  float* part_lse;   // [2 max_ctas][8 NT], base 2
+  unsigned long long inv_group;  // ceil(2^32 / group): row / group for the rows of a sequence
+  __device__ __forceinline__ int token(int row) const { return int((unsigned(row) * inv_group) >> 32); }
 };
 
-// Sizes shared with the combine kernel.
-struct Group {
-  int n_rows, minpos, maxpos;
+// A sequence as its items: `groups` per kv head, each with `tiles.n` units
+// (the sequence's tiles; a row group that sees fewer masks the rest).
+struct SeqItems {
+  SeqInfo s;
+  int groups, rows;  // row groups of a kv head, rows of all of them
   Tiles tiles;
-  int splits;
+  __device__ __forceinline__ long long units(int kv_heads) const { return (long long)groups * kv_heads * tiles.n; }
 };
-__device__ __forceinline__ Group group_of(const FewArgs& f, const SeqInfo& s, int rows_per_group, int rg) {
-  Group g;
-  const int G = f.a.group, r0 = rg * rows_per_group;
-  g.n_rows = min(s.n_new * G - r0, rows_per_group);
-  if (s.n_new * G > f.max_rows) g.n_rows = 0;
-  if (g.n_rows <= 0) {
-    g.n_rows = g.splits = 0;
-    return g;
-  }
-  const int base = s.kv - s.n_new;
-  g.minpos = base + r0 / G;
-  g.maxpos = base + (r0 + g.n_rows - 1) / G;
-  g.tiles = tiles_of(g.minpos, g.maxpos, f.a.window, f.a.sinks);
-  g.splits = max(1, (g.tiles.n + f.chunk - 1) / f.chunk);
-  return g;
+__device__ __forceinline__ SeqItems items_of(const FewArgs& f, int b, int rows_per_group) {
+  SeqItems q;
+  q.s = kv_seq(f.a.kv, b);
+  q.rows = q.s.n_new * f.a.group;
+  if (q.rows > f.max_rows) q.rows = 0;
+  q.groups = (q.rows + rows_per_group - 1) / rows_per_group;
+  q.tiles = tiles_of(q.s.kv - q.s.n_new, q.s.kv - 1, f.a.window, f.a.sinks);
+  if (q.tiles.n == 0) q.tiles.n = 1;  // rows that see nothing are written too
+  return q;
 }
+
+// The units of all sequences, and where unit ranges begin. One CTA computes
+// it, kScanThreads sequences at a time.
+template <int THREADS>
+struct Cut {
+  const FewArgs& f;
+  const int rows;
+  long long* sums;  // [THREADS] shared memory
+  long long total;
+  int ctas;
+
+  // prefix sums of the units of sequences c0 .. c0 + THREADS - 1 in `sums`; their total
+  __device__ long long chunk(int c0) {
+    const int b = c0 + threadIdx.x;
+    long long v = b < f.a.kv.n_seqs ? items_of(f, b, rows).units(f.a.kv.kv_heads) : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(~0u, v, off);
+      if (lane >= off) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    __syncthreads();
+    sums[threadIdx.x] = v + before;
+    __syncthreads();
+    return sums[THREADS - 1];
+  }
+  __device__ Cut(const FewArgs& args, int rows_per_group, long long* shared) : f(args), rows(rows_per_group), sums(shared) {
+    total = 0;
+    for (int c0 = 0; c0 < f.a.kv.n_seqs; c0 += THREADS) total += chunk(c0);
+    const long long want = (total + kMinTiles - 1) / kMinTiles;
+    ctas = int(want < f.max_ctas ? (want > 1 ? want : 1) : f.max_ctas);
+  }
+  __device__ long long begin(int c) const { return total * c / ctas; }
+  __device__ int cta_of(long long u) const { return int(((u + 1) * ctas - 1) / total); }
+  // sequence that holds unit u < total, and u's place within it
+  __device__ int find(long long u, long long* at) {
+    long long base = 0;
+    for (int c0 = 0;; c0 += THREADS) {
+      const long long n = f.a.kv.n_seqs <= THREADS ? total : chunk(c0);
+      if (u - base < n) {
+        int lo = 0, hi = THREADS - 1;  // the first with sums > u - base
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (sums[mid] > u - base)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        *at = u - base - (lo ? sums[lo - 1] : 0);
+        return c0 + lo;
+      }
+      base += n;
+    }
+  }
+};
 
 template <int DIM, int NT>
 __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attention_few_kernel(const FewArgs f) {
@@ -170,113 +239,190 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   const AttnArgs& a = f.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   griddep_launch();
-
-  int x = blockIdx.x;
-  const int split = x % f.n_split;
-  x /= f.n_split;
-  const int rg = x % f.row_groups;
-  x /= f.row_groups;
-  const int kvh = x % a.kv.kv_heads, b = x / a.kv.kv_heads;
-  const SeqInfo si = kv_seq(a.kv, b);
-  const Group gr = group_of(f, si, C::kRows, rg);
-  if (split >= gr.splits) return;
-  const int t_begin = split * f.chunk, t_end = min(gr.tiles.n, t_begin + f.chunk);
-  const int lo_all = a.window > 0 ? max(0, gr.minpos - a.window + 1) : 0;  // first windowed key any row sees
-
   uint8_t* ring = smem + C::kOffRing + warp * kStages * St::kBytes;
   const uint32_t ring_s = smem_u32(ring);
-  const uint32_t bar_s = smem_u32(smem + C::kOffBar) + warp * kStages * 8;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
-  if (lane == 0)
-    for (int s = 0; s < kStages; ++s) mbar_init(bar_s + 8 * s, 1);
-  if (threadIdx.x == 0) *abort_flag = 0;
-  mbar_init_fence();
-  __syncwarp();
 
-  // Copies of a tile: one lane per (page piece, array). A piece is the part
-  // of the tile in one page: 16 or 32 keys.
-  const int piece = a.kv.page_bits < 5 ? 16 : 32;
-  const int n_pieces = kTile / piece;
-  const int my_piece = lane / 6, my_array = lane % 6;  // array: keys' codes, scales, biases, values' the same
-  const bool copier = my_piece < n_pieces;
-  // page of this lane's piece of a tile: the table's entry if some row sees a key of the piece, else -1
-  auto entry_of = [&](int t) -> int {
-    if (!copier || t >= t_end) return -1;
-    const int k0 = gr.tiles.key0(t) + my_piece * piece;
-    if (k0 > gr.maxpos || (a.window > 0 && k0 + piece <= lo_all && k0 >= a.sinks)) return -1;
-    const int j = k0 >> a.kv.page_bits;
-    int e = -1;
-    if (j < a.kv.table_stride) e = a.kv.table[(long long)b * a.kv.table_stride + j];
-    if (e < 0 || e >= a.kv.n_pages) {
-      e = -1;
-      report(a.kv.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
-    }
+  // this CTA's units: `left` of them from tile t_begin of item `item` of sequence b on
+  int b, item, t_begin;
+  long long left;
+  SeqItems sq;
+  if (f.whole) {
+    const int per_seq = a.kv.kv_heads * f.row_groups;
+    b = blockIdx.x / per_seq;
+    const int x = blockIdx.x - b * per_seq, h = x / f.row_groups, r = x - h * f.row_groups;
+    sq = items_of(f, b, C::kRows);
+    if (r >= sq.groups) return;
+    item = h * sq.groups + r;
+    t_begin = 0;
+    left = sq.tiles.n;
+  } else {
+    Cut<kWarps * 32> cut(f, C::kRows, reinterpret_cast<long long*>(smem + C::kOffRing));
+    if (int(blockIdx.x) >= cut.ctas) return;
+    const long long begin = cut.begin(blockIdx.x);
+    left = cut.begin(blockIdx.x + 1) - begin;
+    if (left <= 0) return;
+    long long at;
+    b = cut.find(begin, &at);
+    sq = items_of(f, b, C::kRows);
+    item = int(at / sq.tiles.n);
+    t_begin = int(at - (long long)item * sq.tiles.n);
+    __syncthreads();  // the prefix sums' place becomes the ring's
+  }
+  while (left > 0) {
+  if (item >= sq.groups * a.kv.kv_heads) {  // the next sequence that has items (there is one: units are left)
+    item = t_begin = 0;
+    do sq = items_of(f, ++b, C::kRows);
+    while (sq.groups == 0);
+  }
+  const SeqInfo si = sq.s;
+  const int kvh = item / sq.groups, rg = item - kvh * sq.groups;
+  const int t_end = int(min((long long)sq.tiles.n, t_begin + left));
+  struct {
+    int n_rows, minpos, maxpos;
+    Tiles tiles;
+  } gr;
+  gr.n_rows = min(sq.rows - rg * C::kRows, C::kRows);
+  gr.minpos = si.kv - si.n_new + f.token(rg * C::kRows);
+  gr.maxpos = si.kv - si.n_new + f.token(rg * C::kRows + gr.n_rows - 1);
+  gr.tiles = sq.tiles;
+  const int lo_all = a.window > 0 ? max(0, gr.minpos - a.window + 1) : 0;  // first windowed key any row sees
+
+  // Copies of a tile, 16 bytes per lane and instruction, each array's rows in
+  // Copies of a tile, 16 bytes per lane and instruction, each array's rows in
+  // order. Its two halves of 16 keys may lie in different pages. The table's
+  // entries are loaded a tile ahead of use: always from some valid address,
+  // with what the entry means kept apart, so that nothing waits for the load
+  // before the entry is used.
+  struct Entry {
+    int page, state;  // state: 0 an entry, 1 the table has none, 2 no row sees a key of that half
+  };
+  const bool has_table = a.kv.table_stride > 0;
+  const int* table = has_table ? a.kv.table + (long long)b * a.kv.table_stride : a.kv.kv_len;
+  const int last_entry = has_table ? a.kv.table_stride - 1 : 0;
+  auto entry_of = [&](int t, int half) -> Entry {
+    const int k0 = gr.tiles.key0(t) + 16 * half, j = k0 >> a.kv.page_bits;
+    Entry e;
+    // (volatile: as an ordinary load the compiler moves it to its use, one iteration on)
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e.page) : "l"(table + min(j, last_entry)));
+    const bool unseen = t >= t_end || k0 > gr.maxpos || (a.window > 0 && k0 + 16 <= lo_all && k0 >= a.sinks);
+    e.state = unseen ? 2 : j >= a.kv.table_stride ? 1 : 0;
     return e;
   };
-  // array pointers by index arithmetic would index the parameter space: pick once
-  const uint8_t* src_base;
-  int row_bytes, dst_off;
-  {
-    const int which = my_array / 3, kind = my_array % 3;
-    src_base = kind == 0   ? reinterpret_cast<const uint8_t*>(which ? a.kv.codes[1] : a.kv.codes[0])
-               : kind == 1 ? reinterpret_cast<const uint8_t*>(which ? a.kv.scales[1] : a.kv.scales[0])
-                           : reinterpret_cast<const uint8_t*>(which ? a.kv.biases[1] : a.kv.biases[0]);
-    row_bytes = kind == 0 ? DIM / 2 : DIM / 32;
-    dst_off = which * St::kHalf + (kind == 0 ? 0 : St::kCodes + (kind - 1) * St::kSb);
-  }
-  // Issues tile t into stage s with page entry e (of this lane's piece);
-  // returns which pieces are there.
-  auto issue = [&](int t, int s, int e) -> unsigned {
-    const unsigned have = __ballot_sync(~0u, e >= 0);
-    const uint32_t bar = bar_s + 8 * s;
-    const int n = __popc(have) / 6;
-    if (lane == 0) mbar_arrive_tx(bar, uint32_t(n) * piece * (2 * (DIM / 2) + 4 * (DIM / 32)));
-    __syncwarp();
-    if (e >= 0) {
-      const int k0 = gr.tiles.key0(t) + my_piece * piece;
-      const long long row = ((long long)e * a.kv.kv_heads + kvh << a.kv.page_bits) + (k0 & ((1 << a.kv.page_bits) - 1));
-      bulk_g2s(ring_s + s * St::kBytes + dst_off + my_piece * piece * row_bytes, src_base + row * row_bytes,
-               piece * row_bytes, bar);
-    }
-    return (have & 1u) | (n_pieces == 2 ? (have >> 5) & 2u : (have & 1u) << 1);  // bit i: keys 16 i .. 16 i + 15
+  // The lane's sources: 16 bytes of a code row block, and its place among the
+  // scales and biases (keys' scales, biases, values' scales, biases).
+  constexpr int kSbChunks = St::kSb / 16;  // 16-byte chunks of one array's tile
+  constexpr int kSbIters = (4 * kSbChunks + 31) / 32;
+  auto sb_of = [&](int x) -> const uint8_t* {
+    const int arr = x / kSbChunks;
+    const uint16_t* p = arr == 0 ? a.kv.scales[0] : arr == 1 ? a.kv.biases[0] : arr == 2 ? a.kv.scales[1] : a.kv.biases[1];
+    return reinterpret_cast<const uint8_t*>(p) + x % kSbChunks * 16;
   };
-  unsigned there[kStages];
-  int nxt = entry_of(t_begin + warp);
+  const uint8_t* kc0 = reinterpret_cast<const uint8_t*>(a.kv.codes[0]) + lane * 16;
+  const uint8_t* vc0 = reinterpret_cast<const uint8_t*>(a.kv.codes[1]) + lane * 16;
+  const uint8_t* sb0 = sb_of(lane % (4 * kSbChunks));
+  const uint32_t sb_dst = (lane / kSbChunks >> 1) * St::kHalf + St::kCodes + (lane / kSbChunks & 1) * St::kSb + lane % kSbChunks * 16;
+  const int page_mask = (1 << a.kv.page_bits) - 1;
+  // Copies keys [16 h0, 16 h1) of a tile whose first key is cache row `row`.
+  auto copy = [&](uint32_t dst, long long row, int h0, int h1) {
+    constexpr int kHalfCodes = St::kCodes / 2;
+    const uint8_t* kc = kc0 + row * (DIM / 2);
+    const uint8_t* vc = vc0 + row * (DIM / 2);
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    const int t = t_begin + warp + s * kWarps;
-    there[s] = 0;
-    if (t < t_end) {
-      const int e = nxt;
-      nxt = entry_of(t + kWarps);
-      there[s] = issue(t, s, e);
+    for (int i = 0; i < 2 * kHalfCodes; i += 512)
+      if (i >= h0 * kHalfCodes && i < h1 * kHalfCodes) {
+        cp_async16(dst + lane * 16 + i, kc + i);
+        cp_async16(dst + lane * 16 + St::kHalf + i, vc + i);
+      }
+#pragma unroll
+    for (int i = 0; i < kSbIters; ++i) {
+      const int x = lane + 32 * i, h = x % kSbChunks >= kSbChunks / 2;  // the half of the tile that the chunk is of
+      if (x < 4 * kSbChunks && h >= h0 && h < h1) {
+        if (kSbIters == 1)
+          cp_async16(dst + sb_dst, sb0 + row * (DIM / 32));
+        else
+          cp_async16(dst + (x / kSbChunks >> 1) * St::kHalf + St::kCodes + (x / kSbChunks & 1) * St::kSb + x % kSbChunks * 16,
+                     sb_of(x) + row * (DIM / 32));
+      }
     }
+  };
+  // Issues tile t into stage s with the entries of its halves; returns which
+  // halves are there. One commit group per call, empty or not.
+  auto issue = [&](int t, int s, Entry e0, Entry e1) -> unsigned {
+    unsigned have = 0;
+    if (t < t_end) {
+      const uint32_t dst = ring_s + s * St::kBytes;
+      const int in_page = gr.tiles.key0(t) & page_mask;
+      auto row_of = [&](Entry e) { return (((long long)e.page * a.kv.kv_heads + kvh) << a.kv.page_bits) + in_page; };
+      auto valid = [&](Entry e) {
+        const bool ok = e.state == 0 && unsigned(e.page) < unsigned(a.kv.n_pages);
+        if (!ok && e.state != 2) report(a.kv.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
+        return ok;
+      };
+      const bool v0 = valid(e0), v1 = valid(e1);
+      have = unsigned(v0) | unsigned(v1) << 1;
+      if (v0 && v1 && page_mask >= kTile - 1) {
+        copy(dst, row_of(e0), 0, 2);
+      } else {  // (pages of 16: the second half's page begins where the tile's row 16 is)
+        if (v0) copy(dst, row_of(e0), 0, 1);
+        if (v1) copy(dst, row_of(e1) - (page_mask == 15 ? 16 : 0), 1, 2);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return have;
+  };
+  unsigned there = 0;  // two bits per stage
+  Entry nxt0, nxt1;
+  {
+    Entry e0[kStages], e1[kStages];
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      e0[s] = entry_of(t_begin + warp + s * kWarps, 0);
+      e1[s] = entry_of(t_begin + warp + s * kWarps, 1);
+    }
+    nxt0 = entry_of(t_begin + warp + kStages * kWarps, 0);
+    nxt1 = entry_of(t_begin + warp + kStages * kWarps, 1);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) there |= issue(t_begin + warp + s * kWarps, s, e0[s], e1[s]) << (2 * s);
   }
 
-  // Query fragments, while the first tiles are on their way: B fragment of
-  // step 2 m + h for row n = lane / 4 holds, for word W = KW c + m, dims 8 W +
-  // 2 h + {0, 4} and 8 W + 2 h + {1, 5}.
-  uint2* qs = reinterpret_cast<uint2*>(smem);
-  for (int e = threadIdx.x; e < NT * kSteps * 32; e += kWarps * 32) {
-    const int l = e & 31, step = (e >> 5) % kSteps, nt = (e >> 5) / kSteps;
-    const int row = 8 * nt + (l >> 2);
-    uint2 v = make_uint2(0, 0);
+  // Query fragments, while the first tiles are on their way. The B fragments
+  // of steps 2 m and 2 m + 1 for row n = lane / 4 hold the eight dims of word
+  // W = KW c + m: pairs (0, 4), (1, 5) and (2, 6), (3, 7). The scores are
+  // multiplied by |scale|; a negative scale flips the queries, 0 clears them.
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+  auto q_words = [&](int n, int m, int ln) -> uint4 {
+    const int row = 8 * n + (ln >> 2);
+    uint4 v = make_uint4(0, 0, 0, 0);
     if (row < gr.n_rows) {
-      const int r = rg * C::kRows + row;
-      const uint16_t* q = a.q + (si.first + r / a.group) * a.q_stride + (kvh * a.group + r % a.group) * DIM +
-                          8 * (KW * (l & 3) + step / 2) + 2 * (step & 1);
-      v = make_uint2(q[0] | uint32_t(q[4]) << 16, q[1] | uint32_t(q[5]) << 16);
+      const int r = rg * C::kRows + row, t = f.token(r);
+      v = *reinterpret_cast<const uint4*>(a.q + (si.first + t) * a.q_stride + (kvh * a.group + r - t * a.group) * DIM +
+                                          8 * (KW * (ln & 3) + m));
+      if (a.scale == 0.f) v = make_uint4(mul2(v.x, 0), mul2(v.y, 0), mul2(v.z, 0), mul2(v.w, 0));
     }
-    qs[e] = v;
-  }
-  __syncthreads();
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
+                      __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
+  };
+  uint2* qs = reinterpret_cast<uint2*>(smem);
   uint2 qr[C::kQReg ? NT : 1][C::kQReg ? kSteps : 1];
   if (C::kQReg) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) qr[n][s] = qs[(n * kSteps + s) * 32 + lane];
+      for (int m = 0; m < KW; ++m) {
+        const uint4 v = q_words(n, m, lane);
+        qr[C::kQReg ? n : 0][C::kQReg ? 2 * m : 0] = make_uint2(v.x, v.y);
+        qr[C::kQReg ? n : 0][C::kQReg ? 2 * m + 1 : 0] = make_uint2(v.z, v.w);
+      }
+  } else {
+#pragma unroll
+    for (int e = warp; e < NT * KW; e += kWarps) {
+      const int n = e / KW, m = e % KW;
+      const uint4 v = q_words(n, m, lane);
+      qs[(n * kSteps + 2 * m) * 32 + lane] = make_uint2(v.x, v.y);
+      qs[(n * kSteps + 2 * m + 1) * 32 + lane] = make_uint2(v.z, v.w);
+    }
   }
+  __syncthreads();
 
   float o[NT][kSteps][4];  // O^T: [rows' tile][value tile][fragment]
   float m[NT][2], l[NT][2];  // per row 2 c + i of a tile: reference maximum (base 2), this lane's part of the sum
@@ -289,27 +435,41 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
   }
-  const float to_log2 = a.scale * (1.4426950408889634f * kUnscale);
+  const float to_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * (1.4426950408889634f * kUnscale);
   // Key of fragment index i (0..15) in a 16-key half of a tile: the two rows
   // of each pair swap for every other pair, which spreads both the key and
   // the value reads over the shared-memory banks.
   const int krow = 2 * (g >> 1) + ((g & 1) ^ ((g >> 1) & 1));
   const int vrow0 = 2 * c + (c & 1), vrow1 = 2 * c + ((c & 1) ^ 1);
+  // byte selector: this lane's group of rows 2 c and 2 c + 1, from the words of the two rows, in the rows' fragment order
+  uint32_t vsel;
+  {
+    const uint32_t odd = DIM == 64 ? 0 : DIM == 128 ? g >> 2 : (g >> 1) & 1;  // second group of its word
+    const uint32_t r0 = DIM == 64 ? 0x10 : 0x10 + 0x22 * odd, r1 = DIM == 64 ? 0x32 : 0x54 + 0x22 * odd;
+    vsel = c & 1 ? r0 << 8 | r1 : r1 << 8 | r0;
+  }
 
   int stage = 0;
-  uint32_t phase = 0;
-  bool ok = true;
   for (int t = t_begin + warp; t < t_end; t += kWarps) {
-    if (!(ok = mbar_wait(bar_s + 8 * stage, phase, abort_flag, a.kv.hdr, kWaitLimit, false, 210))) break;
-    unsigned have = 0;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s)
-      if (s == stage) have = there[s];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");  // this lane's copies of the tile
+    __syncwarp();                                                          // and the other lanes'
+    const unsigned have = (there >> (2 * stage)) & 3u;
     const uint8_t* kc = ring + stage * St::kBytes;
     const uint8_t* vc = kc + St::kHalf;
     const int k0 = gr.tiles.key0(t);
     const bool whole = have == 3 && k0 + kTile - 1 <= gr.minpos &&
                        (a.window == 0 || k0 > gr.maxpos - a.window || k0 + kTile <= a.sinks);
+
+    if (!whole) {  // a slot that no row sees may hold anything: its zero probability needs a finite value
+      const int key = k0 + lane;
+      const bool used = ((have >> (lane >> 4)) & 1u) && key <= gr.maxpos && (a.window == 0 || key >= lo_all || key < a.sinks);
+      if (!used) {
+        uint16_t* z = reinterpret_cast<uint16_t*>(ring + stage * St::kBytes + St::kHalf + St::kCodes) + lane * (DIM / 64);
+#pragma unroll
+        for (int i = 0; i < DIM / 64; ++i) z[i] = z[i + St::kSb / 2] = 0;
+      }
+      __syncwarp();
+    }
 
     // scores
     float sc[NT][2][4];
@@ -357,19 +517,13 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
                 C::kQReg ? qr[C::kQReg ? n : 0][C::kQReg ? 2 * j + h : 0] : qs[(n * kSteps + 2 * j + h) * 32 + lane]);
       }
     }
-    // base-2 scores; what a row does not see is -inf
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][u][i] *= to_log2;
+    // what a row does not see is -inf
     if (!whole) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int pos = si.kv - si.n_new + (rg * C::kRows + 8 * n + 2 * c + i) / a.group;
+          const int pos = si.kv - si.n_new + f.token(rg * C::kRows + 8 * n + 2 * c + i);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -383,17 +537,14 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     }
     // running maximum: the reference moves only when a score passes it by 2^8, which costs no precision (the
     // probabilities are floating point) and leaves most tiles without a rescaling
-    float mx[NT][2];
+    float mx[NT][2];  // of this lane's keys
     bool grew = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float v = fmaxf(fmaxf(sc[n][0][i], sc[n][0][2 + i]), fmaxf(sc[n][1][i], sc[n][1][2 + i]));
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, off));
-        mx[n][i] = v;
-        grew |= v > m[n][i] + 8.f;
+        mx[n][i] = fmaxf(fmaxf(sc[n][0][i], sc[n][0][2 + i]), fmaxf(sc[n][1][i], sc[n][1][2 + i])) * to_log2;
+        grew |= mx[n][i] > m[n][i] + 8.f;
       }
     if (__any_sync(~0u, grew)) {
 #pragma unroll
@@ -401,7 +552,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         float al[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float v = fmaxf(m[n][i], mx[n][i]);
+          float v = fmaxf(m[n][i], mx[n][i]);
+#pragma unroll
+          for (int off = 4; off <= 16; off <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, off));
           al[i] = v == -INFINITY ? 1.f : ex2(m[n][i] - v);
           m[n][i] = v;
           l[n][i] *= al[i];
@@ -421,7 +574,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float* s = sc[n][u];
-        s[0] = ex2(s[0] - r0), s[1] = ex2(s[1] - r1), s[2] = ex2(s[2] - r0), s[3] = ex2(s[3] - r1);
+        s[0] = ex2(fmaf(s[0], to_log2, -r0)), s[1] = ex2(fmaf(s[1], to_log2, -r1));
+        s[2] = ex2(fmaf(s[2], to_log2, -r0)), s[3] = ex2(fmaf(s[3], to_log2, -r1));
         l[n][0] += s[0] + s[2], l[n][1] += s[1] + s[3];
         uint32_t h0, h1;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h0) : "f"(s[1]), "f"(s[0]));
@@ -434,7 +588,6 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t w[4][VW];
-      uint32_t ss[4], bb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // keys of fragment indexes 2 c, 2 c + 1, 2 c + 8, 2 c + 9
         const int row = 16 * u + 8 * (i >> 1) + ((i & 1) ? vrow1 : vrow0);
@@ -448,18 +601,26 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
           const uint4 v = *reinterpret_cast<const uint4*>(p);
           w[i][0] = v.x, w[i][1 % VW] = v.y, w[i][2 % VW] = v.z, w[i][3 % VW] = v.w;
         }
-        const uint8_t* ps = vc + St::kCodes + (row * (DIM / 64) + (g * VW) / 8) * 2;
-        ss[i] = lds_u16(ps), bb[i] = lds_u16(ps + St::kSb);
-        if (!whole) {  // a slot that no row sees may hold anything: its zero probability needs a finite value
-          const int key = k0 + row;
-          const bool used = ((have >> u) & 1u) && key <= gr.maxpos &&
-                            (a.window == 0 || key >= lo_all || key < a.sinks);
-          if (!used) ss[i] = bb[i] = 0;
-        }
       }
+      // scales and biases of the key pairs, from neighbouring rows
       Sb sb[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) sb[h] = make_sb(ss[2 * h] | ss[2 * h + 1] << 16, bb[2 * h] | bb[2 * h + 1] << 16);
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* ps = vc + St::kCodes + (16 * u + 8 * h + 2 * c) * (DIM / 32);
+        uint32_t s2, b2;
+        if (DIM == 64) {  // one group: two rows are one word
+          s2 = __byte_perm(*reinterpret_cast<const uint32_t*>(ps), 0, vsel);
+          b2 = __byte_perm(*reinterpret_cast<const uint32_t*>(ps + St::kSb), 0, vsel);
+        } else if (DIM == 128) {  // two groups: a word per row
+          const uint2 sw = *reinterpret_cast<const uint2*>(ps), bw = *reinterpret_cast<const uint2*>(ps + St::kSb);
+          s2 = __byte_perm(sw.x, sw.y, vsel), b2 = __byte_perm(bw.x, bw.y, vsel);
+        } else {  // four groups: this lane's is in word g / 4 of the two of a row
+          const uint8_t* pg = ps + (g >> 2) * 4;
+          s2 = __byte_perm(*reinterpret_cast<const uint32_t*>(pg), *reinterpret_cast<const uint32_t*>(pg + 8), vsel);
+          b2 = __byte_perm(*reinterpret_cast<const uint32_t*>(pg + St::kSb), *reinterpret_cast<const uint32_t*>(pg + St::kSb + 8), vsel);
+        }
+        sb[h] = make_sb(s2, b2);
+      }
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         uint32_t v[2][4];  // byte k of the pair's two words, in bits 0..7 and 16..23
@@ -483,26 +644,18 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
       }
     }
     __syncwarp();  // every lane has read the stage
-    {
-      const int tn = t + kStages * kWarps;
-      unsigned h = 0;
-      if (tn < t_end) {
-        const int e = nxt;
-        nxt = entry_of(tn + kWarps);
-        h = issue(tn, stage, e);
-      }
-#pragma unroll
-      for (int s = 0; s < kStages; ++s)
-        if (s == stage) there[s] = h;
-    }
-    if (++stage == kStages) stage = 0, phase ^= 1;
-  }
-  if (!ok) {  // a wait gave up: the copies in flight may still land, wait for each again (bounded) before leaving
-    for (int s = 0; s < kStages; ++s) mbar_wait(bar_s + 8 * s, s < stage ? phase ^ 1 : phase, abort_flag, a.kv.hdr, kWaitLimit, true, 211);
+    const int tn = t + kStages * kWarps;
+    const unsigned h = issue(tn, stage, nxt0, nxt1);
+    nxt0 = entry_of(tn + kWarps, 0);
+    nxt1 = entry_of(tn + kWarps, 1);
+    there = (there & ~(3u << (2 * stage))) | h << (2 * stage);
+    if (++stage == kStages) stage = 0;
   }
 
-  // Merge of the four warps: sums over the lanes that share a row, then the
-  // outputs of warps 2, 3 into 0, 1 and of 1 into 0 (two buffers in the ring).
+  // Merge of the four warps. Sums over the lanes that share a row first; then
+  // every (row tile, value word) of the output has an owner warp, which adds
+  // the others' fragments from the ring's place and writes it: a lane holds
+  // eight neighbouring dims of two rows.
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -516,14 +669,17 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 #pragma unroll
       for (int i = 0; i < 2; ++i) ml[warp * C::kRows + 8 * n + 2 * c + i] = make_float2(m[n][i], l[n][i]);
   __syncthreads();
+  float4* buf = reinterpret_cast<float4*>(smem + C::kOffRing);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float fac[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float top = -INFINITY, sum = 0.f;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + 8 * n + 2 * c + i].x);
       const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = ml[w * C::kRows + 8 * n + 2 * c + i];
         sum += ex2(v.x - ref) * v.y;
@@ -533,119 +689,189 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
       l[n][i] = sum != 0.f ? top + log2f(sum) : -INFINITY;
     }
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      o[n][j][0] *= fac[0], o[n][j][1] *= fac[1];
-      o[n][j][2] *= fac[0], o[n][j][3] *= fac[1];
-    }
-  }
-  float* buf = reinterpret_cast<float*>(smem + C::kOffRing);
-  // fragment (j = 4 word + k) of lane (g, c): dims 8 (VW g + word) + 2 k + {0, 1} of rows 2 c, 2 c + 1
-  auto each = [&](auto&& fn) {
+    for (int w = 0; w < VW; ++w) {
+      const int owner = (n * VW + w) % kWarps;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const int d = 8 * (VW * g + j / 4) + 2 * (j % 4);
-        fn(8 * n + 2 * c, d, o[n][j][0], o[n][j][2]);
-        fn(8 * n + 2 * c + 1, d, o[n][j][1], o[n][j][3]);
+      for (int k = 0; k < 4; ++k) {
+        float(&x)[4] = o[n][4 * w + k];
+        x[0] *= fac[0], x[1] *= fac[1], x[2] *= fac[0], x[3] *= fac[1];
+        if (warp != owner)
+          buf[(((n * VW + w) * 3 + warp - (warp > owner)) * 4 + k) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
       }
-  };
-#pragma unroll
-  for (int from = 2; from >= 1; from >>= 1) {
-    if (warp >= from && warp < 2 * from)
-      each([&](int r, int d, float& x0, float& x1) {
-        *reinterpret_cast<float2*>(buf + ((warp - from) * C::kRows + r) * DIM + d) = make_float2(x0, x1);
-      });
-    __syncthreads();
-    if (warp < from)
-      each([&](int r, int d, float& x0, float& x1) {
-        const float2 v = *reinterpret_cast<const float2*>(buf + (warp * C::kRows + r) * DIM + d);
-        x0 += v.x, x1 += v.y;
-      });
-    __syncthreads();
-  }
-  if (warp == 0)
-    each([&](int r, int d, float& x0, float& x1) {
-      *reinterpret_cast<float2*>(buf + r * DIM + d) = make_float2(x0, x1);
-    });
-  if (warp == 0 && g == 0)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) ml[8 * n + 2 * c + i].x = l[n][i];
-  __syncthreads();
-  const long long all_rows = (long long)a.kv.n_tokens * a.heads;
-  for (int e = threadIdx.x; e < gr.n_rows * (DIM / 4); e += kWarps * 32) {
-    const int row = e / (DIM / 4), d = e % (DIM / 4) * 4;
-    const int r = rg * C::kRows + row;
-    const long long at = (long long)(si.first + r / a.group) * a.heads + kvh * a.group + r % a.group;
-    const float4 v = *reinterpret_cast<const float4*>(buf + row * DIM + d);
-    const float lse = ml[row].x;
-    if (gr.splits == 1) {
-      uint2 w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v.y), "f"(v.x));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v.w), "f"(v.z));
-      *reinterpret_cast<uint2*>(a.out + at * DIM + d) = w;
-      if (d == 0 && a.lse) a.lse[at] = lse * 0.6931471805599453f;
-    } else {
-      *reinterpret_cast<float4*>(f.part_o + (split * all_rows + at) * DIM + d) = v;
-      if (d == 0) f.part_lse[split * all_rows + at] = lse;
     }
+  }
+  __syncthreads();
+  const bool cut_item = t_begin > 0 || t_end < sq.tiles.n;
+  const int slot = 2 * blockIdx.x + (t_begin > 0);  // a CTA's parts: one that begins in an item, one that ends in one
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      if (warp != (n * VW + w) % kWarps) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int from = 0; from < 3; ++from) {
+          const float4 v = buf[(((n * VW + w) * 3 + from) * 4 + k) * 32 + lane];
+          float(&x)[4] = o[n][4 * w + k];
+          x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * n + 2 * c + i;
+        if (row >= gr.n_rows) continue;
+        const int r = rg * C::kRows + row, t = f.token(r), d = 8 * (VW * g + w);
+        const long long at = (long long)(si.first + t) * a.heads + kvh * a.group + r - t * a.group;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[2 * k] = o[n][4 * w + k][i], v[2 * k + 1] = o[n][4 * w + k][2 + i];
+        if (!cut_item) {
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(v[2 * k + 1]), "f"(v[2 * k]));
+          *reinterpret_cast<uint4*>(a.out + at * DIM + d) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (g == 0 && w == 0 && a.lse) a.lse[at] = l[n][i] * 0.6931471805599453f;
+        } else {
+          float4* dst = reinterpret_cast<float4*>(f.part_o + (size_t(slot) * C::kRows + row) * DIM + d);
+          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (g == 0 && w == 0) f.part_lse[slot * C::kRows + row] = l[n][i];
+        }
+      }
+    }
+  left -= t_end - t_begin;
+  t_begin = 0;
+  ++item;
+  __syncthreads();  // the merge's place becomes the ring's again
   }
 }
 
-// Joins the splits of a row: out = sum_s 2^(lse_s - max) o_s / sum_s 2^(lse_s
-// - max). One CTA of eight warps per (sequence, kv head, row that the kernel
-// above may take); a warp takes every eighth split.
-template <int DIM>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group, int rows_max) {
-  __shared__ float acc[8][DIM];
-  __shared__ float2 ms[8];
+// Joins the parts of the items that are cut: out = sum_p 2^(lse_p - max) o_p /
+// sum_p 2^(lse_p - max). One CTA per (place for an item, row, SLICE dims): few
+// items with many parts want all of the GPU on them, SLICE / 4 threads on the
+// dims and the CTA's groups of those threads on the parts, eight loads in
+// flight each. With rows_cta = 0 (many items, then of few parts) one CTA per
+// item, a warp per row.
+template <int DIM, int SLICE>
+__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group, int rows_cta) {
+  constexpr int kLanes = SLICE / 4, kGroups = 256 / kLanes;
+  constexpr int kMaxParts = 1024;  // (no item has more parts than there are CTAs)
+  __shared__ float weight[kMaxParts];
+  __shared__ float4 acc[kGroups][kLanes];
+  __shared__ float red[16];
+  __shared__ long long sums[256];
   const AttnArgs& a = f.a;
-  const int r = blockIdx.x % rows_max, kvh = blockIdx.x / rows_max % a.kv.kv_heads, b = blockIdx.x / rows_max / a.kv.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const SeqInfo si = kv_seq(a.kv, b);
-  const Group gr = group_of(f, si, rows_per_group, r / rows_per_group);
-  if (gr.splits <= 1 || r % rows_per_group >= gr.n_rows) return;
+  int x = blockIdx.x, row0 = 0, rows_n = 1;
+  if (rows_cta > 0) {
+    row0 = x % rows_cta;
+    x /= rows_cta;
+  }
+  const int per_seq = a.kv.kv_heads * f.row_groups;
+  const int b = x / per_seq, y = x - b * per_seq, kvh = y / f.row_groups, rg = y - kvh * f.row_groups;
+  const SeqItems sq = items_of(f, b, rows_per_group);
+  if (rg >= sq.groups) return;
+  const int n_rows = min(sq.rows - rg * rows_per_group, rows_per_group);
+  if (row0 >= n_rows) return;
+  if (rows_cta == 0) rows_n = n_rows;
+  // the item's first unit: those of the sequences before, then of the items before
+  Cut<256> cut(f, rows_per_group, sums);
+  long long u0 = 0;
+  for (int c0 = 0; c0 <= b; c0 += 256) {
+    const long long n = a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
+    u0 += b < c0 + 256 ? (b > c0 ? sums[b - c0 - 1] : 0) : n;
+  }
+  u0 += (long long)(kvh * sq.groups + rg) * sq.tiles.n;
+  const int p0 = cut.cta_of(u0), n = cut.cta_of(u0 + sq.tiles.n - 1) - p0 + 1;
+  if (n <= 1) return;
+  // part 0 ends its CTA's range, in slot 0; the others begin theirs inside the item, in slot 1
+  auto slot = [&](int p) { return 2 * (p0 + p) + (p > 0); };
+  const int tok0 = rg * rows_per_group;
   griddep_wait();
-  const long long at = (long long)(si.first + r / a.group) * a.heads + kvh * a.group + r % a.group;
-  const long long all_rows = (long long)a.kv.n_tokens * a.heads;
+  if (rows_cta == 0) {
+    for (int row = warp; row < rows_n; row += 8) {
+      float top = -INFINITY;
+      for (int p = 0; p < n; ++p) top = fmaxf(top, f.part_lse[slot(p) * rows_per_group + row]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float o[DIM / 32], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
+      for (int p = 0; p < n; ++p) {
+        const size_t at = size_t(slot(p)) * rows_per_group + row;
+        const float w = ex2(f.part_lse[at] - ref);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < DIM / 32; ++j) o[j] += w * f.part_o[at * DIM + lane + 32 * j];
+      }
+      const int r = tok0 + row, t = f.token(r);
+      const long long at = (long long)(sq.s.first + t) * a.heads + kvh * a.group + r - t * a.group;
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int j = 0; j < DIM / 32; ++j) a.out[at * DIM + lane + 32 * j] = f32_to_bf16(o[j] * inv);
+      if (lane == 0 && a.lse) a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+    return;
+  }
+  const int grp = threadIdx.x / kLanes, d = blockIdx.y * SLICE + 4 * (threadIdx.x % kLanes);
   float top = -INFINITY;
-  for (int s = lane; s < gr.splits; s += 32) top = fmaxf(top, f.part_lse[s * all_rows + at]);
+  for (int p = threadIdx.x; p < n; p += 256) {
+    const float v = f.part_lse[slot(p) * rows_per_group + row0];
+    weight[p] = v;
+    top = fmaxf(top, v);
+  }
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float o[DIM / 32], sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
-  for (int s = warp; s < gr.splits; s += 8) {
-    const float w = ex2(f.part_lse[s * all_rows + at] - ref);
-    sum += w;
-    const float* p = f.part_o + (s * all_rows + at) * DIM;
-#pragma unroll
-    for (int j = 0; j < DIM / 32; ++j) o[j] += w * p[lane + 32 * j];
-  }
-#pragma unroll
-  for (int j = 0; j < DIM / 32; ++j) acc[warp][lane + 32 * j] = o[j];
-  if (lane == 0) ms[warp].x = sum;
+  if (lane == 0) red[warp] = top;
   __syncthreads();
-  float tot = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) tot += ms[w].x;
-  const int d = threadIdx.x;
-  if (d < DIM) {
-    float v = 0.f;
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int p1 = grp; p1 < n; p1 += 8 * kGroups) {
+    float4 v[8];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += acc[w][d];
-    a.out[at * DIM + d] = f32_to_bf16(tot != 0.f ? v / tot : 0.f);
+    for (int k = 0; k < 8; ++k) {
+      const int p = p1 + k * kGroups;
+      v[k] = p < n ? *reinterpret_cast<const float4*>(f.part_o + (size_t(slot(p)) * rows_per_group + row0) * DIM + d)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int p = p1 + k * kGroups;
+      const float w = p < n ? ex2(weight[p] - ref) : 0.f;
+      sum += w;
+      o.x += w * v[k].x, o.y += w * v[k].y, o.z += w * v[k].z, o.w += w * v[k].w;
+    }
   }
-  if (d == 0 && a.lse) a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+  acc[grp][threadIdx.x % kLanes] = o;
+  __syncthreads();  // (and everyone has read the maxima)
+  if (threadIdx.x % kLanes == 0) red[grp] = sum;
+  __syncthreads();
+  if (grp == 0) {
+    float tot = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const float4 q = acc[k][threadIdx.x];
+      tot += red[k];
+      v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+    }
+    const float inv = tot != 0.f ? 1.f / tot : 0.f;
+    const int r = tok0 + row0, t = f.token(r);
+    const long long at = (long long)(sq.s.first + t) * a.heads + kvh * a.group + r - t * a.group;
+    uint2 h;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y * inv), "f"(v.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(v.w * inv), "f"(v.z * inv));
+    *reinterpret_cast<uint2*>(a.out + at * DIM + d) = h;
+    if (d == 0 && a.lse) a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
-// Host plan: rows per group (from the most rows a sequence can have), tiles
-// per split and their number.
+// Host plan: row tiles per group (from the most rows a sequence can have),
+// and whether items are cut.
 struct FewPlan {
-  int nt, row_groups, chunk, n_split;
+  int nt, row_groups, whole, ctas;
   size_t part_rows;
 };
 
@@ -653,22 +879,14 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   FewPlan p;
   const long long rows = std::min<long long>((long long)a.kv.max_new * a.group, max_rows);
   p.nt = rows <= 8 ? 1 : rows <= 16 || a.kv.dim == 256 ? 2 : 4;
-  p.row_groups = int((rows + 8 * p.nt - 1) / (8 * p.nt));
+  p.row_groups = std::max(1, int((rows + 8 * p.nt - 1) / (8 * p.nt)));
   long long keys = a.kv.max_kv;
-  if (a.window > 0) keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kTile);
-  const int tiles = std::max(1, int((keys + kTile - 1) / kTile));
-  // enough splits to give every SM a few CTAs, none shorter than two tiles
-  // per warp
-  const long long items = std::max(1ll, (long long)a.kv.n_seqs * a.kv.kv_heads * p.row_groups);
-  const int per_sm = a.kv.dim == 256 || p.nt > 1 ? 2 : 4;
-  const long long want = std::max(1ll, (long long)num_sms() * per_sm / items);
-  int chunk = int((tiles + want - 1) / want);
-  chunk = std::max(chunk, 2 * kWarps);
-  chunk = std::min(chunk, 32);
-  chunk = (chunk + kWarps - 1) / kWarps * kWarps;
-  p.chunk = chunk;
-  p.n_split = (tiles + chunk - 1) / chunk;
-  p.part_rows = p.n_split > 1 ? size_t(p.n_split) * a.kv.n_tokens * a.heads : 0;
+  if (a.window > 0)
+    keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kTile);
+  p.whole = (keys + kTile - 1) / kTile <= kWholeTiles;
+  const int per_sm = a.kv.dim * p.nt <= 128 ? 4 : 2;  // CTAs that fit (registers and the rings)
+  p.ctas = num_sms() * per_sm;
+  p.part_rows = p.whole ? 0 : size_t(2) * p.ctas * 8 * p.nt;
   return p;
 }
 
@@ -677,16 +895,15 @@ cudaError_t launch(const FewArgs& f, const KvCall& c) {
   using C = FewCfg<DIM, NT>;
   const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT>);
   if (!ensure_smem_limit(fn, C::kSmem)) return cudaErrorInvalidValue;
-  const long long grid = 1ll * f.n_split * f.row_groups * f.a.kv.kv_heads * f.a.kv.n_seqs;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  attention_few_kernel<DIM, NT><<<unsigned(grid), kWarps * 32, C::kSmem, c.stream>>>(f);
+  const long long items = 1ll * f.row_groups * f.a.kv.kv_heads * f.a.kv.n_seqs;
+  if (items * C::kRows > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  attention_few_kernel<DIM, NT><<<unsigned(f.whole ? items : f.max_ctas), kWarps * 32, C::kSmem, c.stream>>>(f);
   if (cudaError_t e = c.launched("attention_few")) return e;
-  if (f.n_split == 1) return cudaSuccess;
+  if (f.whole) return cudaSuccess;
+  const int rows = int(std::min<long long>({(long long)f.a.kv.max_new * f.a.group, f.max_rows, C::kRows}));
+  const bool spread = items * 4 <= f.max_ctas, narrow = spread && items * 64 <= f.max_ctas;  // by the parts of an item
   cudaLaunchConfig_t cfg = {};
-  const int rows_max = int(std::min<long long>((long long)f.a.kv.max_new * f.a.group, f.max_rows));
-  const long long rows = 1ll * rows_max * f.a.kv.kv_heads * f.a.kv.n_seqs;
-  if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(unsigned(rows));
+  cfg.gridDim = spread ? dim3(unsigned(items * rows), narrow ? DIM / 64 : 1) : dim3(unsigned(items));
   cfg.blockDim = dim3(256);
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[1];
@@ -694,7 +911,8 @@ cudaError_t launch(const FewArgs& f, const KvCall& c) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM>, f, C::kRows, rows_max)) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, narrow ? attention_combine_kernel<DIM, 64> : attention_combine_kernel<DIM, DIM>, f, C::kRows,
+                                         spread ? rows : 0)) return e;
   return c.launched("attention_combine");
 }
 
@@ -708,7 +926,8 @@ size_t attention_few_workspace(const AttnArgs& a, int max_rows) {
 cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, const KvCall& c) {
   const FewPlan p = plan(a, max_rows);
   float* part = static_cast<float*>(ws);
-  const FewArgs f{a, max_rows, p.row_groups, p.chunk, p.n_split, part, part + p.part_rows * a.kv.dim};
+  const FewArgs f{a,    max_rows, p.row_groups, p.whole, p.ctas, part, part + p.part_rows * a.kv.dim,
+                  ((1ull << 32) + a.group - 1) / a.group};
   switch (a.kv.dim * 8 + p.nt) {
     case 64 * 8 + 1: return launch<64, 1>(f, c);
     case 64 * 8 + 2: return launch<64, 2>(f, c);
