@@ -175,8 +175,8 @@ struct Cut {
   const FewArgs& f;
   const int rows;
   long long* sums;  // [THREADS] shared memory
-  long long total;
-  int ctas;
+  long long total, each;
+  int ctas, more;
 
   // prefix sums of the units of sequences c0 .. c0 + THREADS - 1 in `sums`; their total
   __device__ long long chunk(int c0) {
@@ -200,14 +200,29 @@ struct Cut {
   }
   __device__ Cut(const FewArgs& args, int rows_per_group, long long* shared) : f(args), rows(rows_per_group), sums(shared) {
     total = 0;
-    for (int c0 = 0; c0 < f.a.kv.n_seqs; c0 += THREADS) total += chunk(c0);
+    if (f.a.kv.n_seqs == 1) {  // one request: no sums to make
+      total = items_of(f, 0, rows).units(f.a.kv.kv_heads);
+    } else {
+      for (int c0 = 0; c0 < f.a.kv.n_seqs; c0 += THREADS) total += chunk(c0);
+    }
     const long long want = (total + kMinTiles - 1) / kMinTiles;
     ctas = int(want < f.max_ctas ? (want > 1 ? want : 1) : f.max_ctas);
+    each = total < 0x7fffffff ? unsigned(total) / unsigned(ctas) : total / ctas;
+    more = int(total - each * ctas);
   }
-  __device__ long long begin(int c) const { return total * c / ctas; }
-  __device__ int cta_of(long long u) const { return int(((u + 1) * ctas - 1) / total); }
+  // the first `more` CTAs take each + 1 units, the others `each`
+  __device__ long long begin(int c) const { return each * c + min(c, more); }
+  __device__ int cta_of(long long u) const {
+    const long long split = (each + 1) * more;
+    if (total < 0x7fffffff) return u < split ? unsigned(u) / unsigned(each + 1) : more + unsigned(u - split) / unsigned(each);
+    return int(u < split ? u / (each + 1) : more + (u - split) / each);
+  }
   // sequence that holds unit u < total, and u's place within it
-  __device__ int find(long long u, long long* at) {
+  __device__ int find(long long u, int* at) {
+    if (f.a.kv.n_seqs == 1) {
+      *at = int(u);
+      return 0;
+    }
     long long base = 0;
     for (int c0 = 0;; c0 += THREADS) {
       const long long n = f.a.kv.n_seqs <= THREADS ? total : chunk(c0);
@@ -220,7 +235,7 @@ struct Cut {
           else
             lo = mid + 1;
         }
-        *at = u - base - (lo ? sums[lo - 1] : 0);
+        *at = int(u - base - (lo ? sums[lo - 1] : 0));
         return c0 + lo;
       }
       base += n;
@@ -261,11 +276,11 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     const long long begin = cut.begin(blockIdx.x);
     left = cut.begin(blockIdx.x + 1) - begin;
     if (left <= 0) return;
-    long long at;
+    int at;  // (a sequence has at most 8 * 256 * 2^19 units)
     b = cut.find(begin, &at);
     sq = items_of(f, b, C::kRows);
-    item = int(at / sq.tiles.n);
-    t_begin = int(at - (long long)item * sq.tiles.n);
+    item = at / sq.tiles.n;
+    t_begin = at - item * sq.tiles.n;
     __syncthreads();  // the prefix sums' place becomes the ring's
   }
   while (left > 0) {
@@ -286,6 +301,22 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   gr.maxpos = si.kv - si.n_new + f.token(rg * C::kRows + gr.n_rows - 1);
   gr.tiles = sq.tiles;
   const int lo_all = a.window > 0 ? max(0, gr.minpos - a.window + 1) : 0;  // first windowed key any row sees
+
+  // The queries' words for the fragments below, asked for before anything
+  // waits: word W = KW c + m of row n = lane / 4 (this warp's share of the
+  // words, where the fragments go through shared memory).
+  constexpr int kQWords = C::kQReg ? NT * KW : NT * KW / kWarps;
+  uint4 qw[kQWords];
+#pragma unroll
+  for (int e = 0; e < kQWords; ++e) {
+    const int x = C::kQReg ? e : e * kWarps + warp, n = x / KW, m = x % KW, row = 8 * n + g;
+    qw[e] = make_uint4(0, 0, 0, 0);
+    if (row < gr.n_rows) {
+      const int r = rg * C::kRows + row, t = f.token(r);
+      qw[e] = *reinterpret_cast<const uint4*>(a.q + (si.first + t) * a.q_stride + (kvh * a.group + r - t * a.group) * DIM +
+                                              8 * (KW * c + m));
+    }
+  }
 
   // Copies of a tile, 16 bytes per lane and instruction, each array's rows in
   // Copies of a tile, 16 bytes per lane and instruction, each array's rows in
@@ -385,41 +416,25 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     for (int s = 0; s < kStages; ++s) there |= issue(t_begin + warp + s * kWarps, s, e0[s], e1[s]) << (2 * s);
   }
 
-  // Query fragments, while the first tiles are on their way. The B fragments
-  // of steps 2 m and 2 m + 1 for row n = lane / 4 hold the eight dims of word
-  // W = KW c + m: pairs (0, 4), (1, 5) and (2, 6), (3, 7). The scores are
+  // Query fragments: the B fragments of steps 2 m and 2 m + 1 hold the eight
+  // dims of a word as pairs (0, 4), (1, 5) and (2, 6), (3, 7). The scores are
   // multiplied by |scale|; a negative scale flips the queries, 0 clears them.
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-  auto q_words = [&](int n, int m, int ln) -> uint4 {
-    const int row = 8 * n + (ln >> 2);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < gr.n_rows) {
-      const int r = rg * C::kRows + row, t = f.token(r);
-      v = *reinterpret_cast<const uint4*>(a.q + (si.first + t) * a.q_stride + (kvh * a.group + r - t * a.group) * DIM +
-                                          8 * (KW * (ln & 3) + m));
-      if (a.scale == 0.f) v = make_uint4(mul2(v.x, 0), mul2(v.y, 0), mul2(v.z, 0), mul2(v.w, 0));
-    }
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
-                      __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
-  };
   uint2* qs = reinterpret_cast<uint2*>(smem);
   uint2 qr[C::kQReg ? NT : 1][C::kQReg ? kSteps : 1];
-  if (C::kQReg) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < KW; ++m) {
-        const uint4 v = q_words(n, m, lane);
-        qr[C::kQReg ? n : 0][C::kQReg ? 2 * m : 0] = make_uint2(v.x, v.y);
-        qr[C::kQReg ? n : 0][C::kQReg ? 2 * m + 1 : 0] = make_uint2(v.z, v.w);
-      }
-  } else {
-#pragma unroll
-    for (int e = warp; e < NT * KW; e += kWarps) {
-      const int n = e / KW, m = e % KW;
-      const uint4 v = q_words(n, m, lane);
-      qs[(n * kSteps + 2 * m) * 32 + lane] = make_uint2(v.x, v.y);
-      qs[(n * kSteps + 2 * m + 1) * 32 + lane] = make_uint2(v.z, v.w);
+  for (int e = 0; e < kQWords; ++e) {
+    uint4 v = qw[e];
+    if (a.scale == 0.f) v = make_uint4(mul2(v.x, 0), mul2(v.y, 0), mul2(v.z, 0), mul2(v.w, 0));
+    const uint2 lo = make_uint2(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip);
+    const uint2 hi = make_uint2(__byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
+    if (C::kQReg) {
+      qr[C::kQReg ? e / KW : 0][C::kQReg ? 2 * (e % KW) : 0] = lo;
+      qr[C::kQReg ? e / KW : 0][C::kQReg ? 2 * (e % KW) + 1 : 0] = hi;
+    } else {
+      const int x = e * kWarps + warp, n = x / KW, m = x % KW;
+      qs[(n * kSteps + 2 * m) * 32 + lane] = lo;
+      qs[(n * kSteps + 2 * m + 1) * 32 + lane] = hi;
     }
   }
   __syncthreads();
@@ -471,14 +486,15 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
       __syncwarp();
     }
 
-    // scores
-    float sc[NT][2][4];
+    // scores; with one row tile two sums, which halves the chain of dependent products
+    constexpr int kTwo = NT == 1 ? 1 : 0;
+    float sc[NT][2][4], sc2[1][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][u][i] = 0.f;
+        for (int i = 0; i < 4; ++i) sc[n][u][i] = sc2[n < kTwo ? n : 0][i] = 0.f;
       uint32_t w[2][KW];
       Sb sb[2];
 #pragma unroll
@@ -513,9 +529,12 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma(sc[n][u], p[0][2 * h], p[1][2 * h], p[0][2 * h + 1], p[1][2 * h + 1],
+            mma(h && n < kTwo ? sc2[n < kTwo ? n : 0] : sc[n][u], p[0][2 * h], p[1][2 * h], p[0][2 * h + 1], p[1][2 * h + 1],
                 C::kQReg ? qr[C::kQReg ? n : 0][C::kQReg ? 2 * j + h : 0] : qs[(n * kSteps + 2 * j + h) * 32 + lane]);
       }
+      if (kTwo)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[0][u][i] += sc2[0][i];
     }
     // what a row does not see is -inf
     if (!whole) {
@@ -777,7 +796,7 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
   // the item's first unit: those of the sequences before, then of the items before
   Cut<256> cut(f, rows_per_group, sums);
   long long u0 = 0;
-  for (int c0 = 0; c0 <= b; c0 += 256) {
+  for (int c0 = 0; c0 <= b && a.kv.n_seqs > 1; c0 += 256) {
     const long long n = a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
     u0 += b < c0 + 256 ? (b > c0 ? sums[b - c0 - 1] : 0) : n;
   }
