@@ -266,16 +266,16 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     b = blockIdx.x / per_seq;
     const int x = blockIdx.x - b * per_seq, h = x / f.row_groups, r = x - h * f.row_groups;
     sq = items_of(f, b, C::kRows);
-    if (r >= sq.groups) return;
+    if (r >= sq.groups) return griddep_wait();
     item = h * sq.groups + r;
     t_begin = 0;
     left = sq.tiles.n;
   } else {
     Cut<kWarps * 32> cut(f, C::kRows, reinterpret_cast<long long*>(smem + C::kOffRing));
-    if (int(blockIdx.x) >= cut.ctas) return;
+    if (int(blockIdx.x) >= cut.ctas) return griddep_wait();
     const long long begin = cut.begin(blockIdx.x);
     left = cut.begin(blockIdx.x + 1) - begin;
-    if (left <= 0) return;
+    if (left <= 0) return griddep_wait();
     int at;  // (a sequence has at most 8 * 256 * 2^19 units)
     b = cut.find(begin, &at);
     sq = items_of(f, b, C::kRows);
@@ -763,6 +763,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   ++item;
   __syncthreads();  // the merge's place becomes the ring's again
   }
+  // Launched beside the many-row kernels it has not waited for them: it does not end before them, so that what
+  // follows on the stream may rely on both.
+  griddep_wait();
 }
 
 // Joins the parts of the items that are cut: out = sum_p 2^(lse_p - max) o_p /
@@ -910,24 +913,31 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
 }
 
 template <int DIM, int NT>
-cudaError_t launch(const FewArgs& f, const KvCall& c) {
+cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   using C = FewCfg<DIM, NT>;
   const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT>);
   if (!ensure_smem_limit(fn, C::kSmem)) return cudaErrorInvalidValue;
   const long long items = 1ll * f.row_groups * f.a.kv.kv_heads * f.a.kv.n_seqs;
   if (items * C::kRows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  attention_few_kernel<DIM, NT><<<unsigned(f.whole ? items : f.max_ctas), kWarps * 32, C::kSmem, c.stream>>>(f);
-  if (cudaError_t e = c.launched("attention_few")) return e;
-  if (f.whole) return cudaSuccess;
-  const int rows = int(std::min<long long>({(long long)f.a.kv.max_new * f.a.group, f.max_rows, C::kRows}));
-  const bool spread = items * 4 <= f.max_ctas, narrow = spread && items * 64 <= f.max_ctas;  // by the parts of an item
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = spread ? dim3(unsigned(items * rows), narrow ? DIM / 64 : 1) : dim3(unsigned(items));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(unsigned(f.whole ? items : f.max_ctas));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_few_kernel<DIM, NT>, f)) return e;
+  if (cudaError_t e = c.launched("attention_few")) return e;
+  if (f.whole) return cudaSuccess;
+  const int rows = int(std::min<long long>({(long long)f.a.kv.max_new * f.a.group, f.max_rows, C::kRows}));
+  const bool spread = items * 4 <= f.max_ctas, narrow = spread && items * 64 <= f.max_ctas;  // by the parts of an item
+  cfg = {};
+  cfg.gridDim = spread ? dim3(unsigned(items * rows), narrow ? DIM / 64 : 1) : dim3(unsigned(items));
+  cfg.blockDim = dim3(256);
+  cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, narrow ? attention_combine_kernel<DIM, 64> : attention_combine_kernel<DIM, DIM>, f, C::kRows,
@@ -942,20 +952,20 @@ size_t attention_few_workspace(const AttnArgs& a, int max_rows) {
   return p.part_rows * (size_t(a.kv.dim) + 1) * 4;
 }
 
-cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, const KvCall& c) {
+cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside, const KvCall& c) {
   const FewPlan p = plan(a, max_rows);
   float* part = static_cast<float*>(ws);
   const FewArgs f{a,    max_rows, p.row_groups, p.whole, p.ctas, part, part + p.part_rows * a.kv.dim,
                   ((1ull << 32) + a.group - 1) / a.group};
   switch (a.kv.dim * 8 + p.nt) {
-    case 64 * 8 + 1: return launch<64, 1>(f, c);
-    case 64 * 8 + 2: return launch<64, 2>(f, c);
-    case 64 * 8 + 4: return launch<64, 4>(f, c);
-    case 128 * 8 + 1: return launch<128, 1>(f, c);
-    case 128 * 8 + 2: return launch<128, 2>(f, c);
-    case 128 * 8 + 4: return launch<128, 4>(f, c);
-    case 256 * 8 + 1: return launch<256, 1>(f, c);
-    default: return launch<256, 2>(f, c);
+    case 64 * 8 + 1: return launch<64, 1>(f, beside, c);
+    case 64 * 8 + 2: return launch<64, 2>(f, beside, c);
+    case 64 * 8 + 4: return launch<64, 4>(f, beside, c);
+    case 128 * 8 + 1: return launch<128, 1>(f, beside, c);
+    case 128 * 8 + 2: return launch<128, 2>(f, beside, c);
+    case 128 * 8 + 4: return launch<128, 4>(f, beside, c);
+    case 256 * 8 + 1: return launch<256, 1>(f, beside, c);
+    default: return launch<256, 2>(f, beside, c);
   }
 }
 

@@ -13,7 +13,7 @@
 //   many     S = Q K^T per 128-row tile and 128 keys into tensor memory, the
 //            softmax warps turn it into P (bf16, in S's place), O += P V with
 //            P read from tensor memory.
-//   combine  joins row tiles that the cut divided between CTAs.
+//            The CTA that finishes a row tile's last part joins the parts.
 //
 // The cut: a unit is one row tile times one key tile. All units of all
 // sequences and kv heads are numbered row tile by row tile, and one CTA per SM
@@ -55,7 +55,7 @@ struct ManyCfg {
   // full, empty [kRing]; qfull, qempty, ofree, drain; sfull, pready [2]; pvdone [QT]; dfull, dempty [kDescs]
   static constexpr int kBars = 2 * kRing + 4 + 4 + QT + 2 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
-  static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 64;
+  static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 80;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -91,6 +91,7 @@ struct ManyArgs {
   CtaRange* range;         // [ctas + 1] where each CTA's units begin; the last entry ends them
   int max_row_tiles;
   int ctas;                // of the many kernel
+  int* arrived;            // [ctas] parts written of the row tile whose first part is the CTA's
   float* part_o;           // [2 ctas][rows][DIM]
   float* part_lse;         // [2 ctas][rows], base 2
   unsigned long long inv_group;  // ceil(2^32 / group): row / group for rows below 2^26
@@ -220,6 +221,7 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
       }
     }
     m.range[c] = r;
+    if (c < m.ctas) m.arrived[c] = 0;
   }
 }
 
@@ -233,8 +235,8 @@ __device__ __forceinline__ uint32_t dq_pair(uint32_t p, __nv_bfloat162 s2, __nv_
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// CTA 0 makes the plan; the others expand one key tile of one (sequence, kv
-// head): the keys row by row, the values eight keys of eight dims at a time,
+// CTA 0 makes the plan; the others expand the keys or the values of one key
+// tile of one (sequence, kv head): the keys row by row, the values eight keys of eight dims at a time,
 // which leaves the transposed 16-byte chunks in registers.
 template <int DIM>
 __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs m) {
@@ -244,7 +246,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
     return;
   }
   __shared__ long long rows16[kBK / 16];  // first cache row of each 16 keys, -1: zeros
-  int x = blockIdx.x - 1;
+  int x = (blockIdx.x - 1) >> 1;
+  const bool values = (blockIdx.x - 1) & 1;
   const int t = x % m.tiles_max;
   x /= m.tiles_max;
   const int h = x % m.nh, bi = x / m.nh, b = m.b0 + bi;
@@ -268,26 +271,43 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
       rows16[threadIdx.x] = row;
     }
     const unsigned bits = __ballot_sync(~0u, missing);
-    if (threadIdx.x == 0 && h == 0) m.bad[(long long)bi * m.tiles_max + t] = uint8_t(bits);
+    if (threadIdx.x == 0 && h == 0 && !values) m.bad[(long long)bi * m.tiles_max + t] = uint8_t(bits);
   }
   __syncthreads();
   const long long tile = ((long long)bi * m.nh + h) * m.tiles_max + t;
   constexpr int W = DIM / 8, G = DIM / 64;
-  uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
-  // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
-  const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
-  for (int e = threadIdx.x; e < kBK * W; e += kPlanThreads) {
-    const int key = e / W, w = e % W;
-    uint32_t o[4] = {0, 0, 0, 0};
-    const long long r16 = rows16[key >> 4];
-    if (r16 >= 0 && k0 + key <= maxpos) {
-      const long long row = r16 + (key & 15);
-      const __nv_bfloat16 sc = __ushort_as_bfloat16(kv.scales[0][row * G + w / 8]);
-      const __nv_bfloat16 bi16 = __ushort_as_bfloat16(kv.biases[0][row * G + w / 8]);
-      dq8_bf16(kv.codes[0][row * W + w], __halves2bfloat162(sc, sc), __halves2bfloat162(bi16, bi16), o);
+  if (!values) {
+    uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
+    // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
+    const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    constexpr int kBatch = 4;  // loads in flight before the first is used
+    const int w = threadIdx.x % W;
+    for (int p = 0; p < kBK * W / kPlanThreads; p += kBatch) {
+      uint32_t c[kBatch];
+      uint16_t sc[kBatch], bs[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int key = (p + i) * (kPlanThreads / W) + threadIdx.x / W;
+        const long long r16 = rows16[key >> 4];
+        c[i] = sc[i] = bs[i] = 0;
+        if (r16 >= 0 && k0 + key <= maxpos) {
+          const long long row = r16 + (key & 15);
+          c[i] = kv.codes[0][row * W + w];
+          sc[i] = kv.scales[0][row * G + w / 8];
+          bs[i] = kv.biases[0][row * G + w / 8];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int key = (p + i) * (kPlanThreads / W) + threadIdx.x / W;
+        const __nv_bfloat16 s16 = __ushort_as_bfloat16(sc[i]), b16 = __ushort_as_bfloat16(bs[i]);
+        uint32_t o[4];
+        dq8_bf16(c[i], __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
+        *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) =
+            make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
+      }
     }
-    *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) =
-        make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
+    return;
   }
   uint8_t* vd = m.vx + tile * ManyCfg<DIM>::kTileBytes;
   // lanes: eight 8-key chunks (one 128-byte row of 64 keys) by four words
@@ -448,14 +468,21 @@ struct __align__(16) Segment {
   int first, base_pos, last;     // sequence's first step token, position of its token 0, its last row
   int all_sink, all_first;       // Range of the sequence's expanded tiles
   int my_sink, my_first;         // Range of the row tile
-  int pad;
+  int parts, c0, c1;             // of a divided row tile: its parts, the first and last CTA with units of it
+  long long u0;                  // its first unit
   __device__ __forceinline__ int tile(int j) const { return j < my_sink ? j : my_first + j - my_sink; }
   __device__ __forceinline__ int index(int j) const {
     const int t = tile(j);
     return t < all_first ? t : all_sink + t - all_first;
   }
 };
-static_assert(sizeof(Segment) == 64, "descriptor size");
+static_assert(sizeof(Segment) == 80, "descriptor size");
+
+// Key tiles before unit `u` of a row tile of n key tiles that begins at unit u0.
+__device__ __forceinline__ int tiles_before(long long u, long long u0, int n) {
+  const long long t = u - u0 - kTileCost;
+  return t <= 0 ? 0 : t < n ? int(t) : n;
+}
 
 // Steps through the units [u, end) of a CTA. Every row tile has kTileCost
 // units more than key tiles; a part that holds none of the latter is skipped.
@@ -495,6 +522,18 @@ struct Cursor {
         s->base_pos = si.kv - si.n_new;
         s->all_sink = all.n_sink, s->all_first = all.first;
         s->my_sink = mine.n_sink, s->my_first = mine.first;
+        if (s->part >= 0) {
+          s->u0 = o0;
+          s->c0 = s->c1 = blockIdx.x;
+          while (m.range[s->c0].begin > o0) --s->c0;
+          while (m.range[s->c1 + 1].begin < o1) ++s->c1;
+          s->parts = 0;
+          for (int c = s->c0, from = 0; c <= s->c1; ++c) {
+            const int to = tiles_before(m.range[c + 1].begin, o0, n);
+            s->parts += to > from;
+            from = to;
+          }
+        }
       }
       u = stop;
       if (stop == o1 && ++rt == m.plan->row_tiles) rt = 0, ++head;
@@ -884,6 +923,74 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree);
+      if (s.part >= 0) {
+        // the part is written; whoever completes the count joins all parts, in the order of their CTAs
+        __threadfence();
+        int* last = reinterpret_cast<int*>(gbase + C::kOffMisc + 8);
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
+        if (threadIdx.x == 0) *last = atomicAdd(m.arrived + s.c0, 1) == s.parts - 1;
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
+        if (*last) {
+          __threadfence();
+          // A warp joins rows warp, warp + 8, ..., lane l holding the maximum and sum of row warp + 8 l, and takes the
+          // rows' values in batches with all of a part's loads in flight.
+          constexpr int kV = DIM / 128 + (DIM < 128), kBatch = DIM == 256 ? 4 : 8;
+          const bool mine = DIM >= 128 || lane < DIM / 4;  // DIM 64: half of the lanes hold a row
+          const int my_row = warp + kSoftWarps * lane;
+          const bool has_row = my_row < s.n_rows;
+          // parts in order: fn(row of the part buffers at which the part begins)
+          auto each_part = [&](auto&& fn) {
+            for (int c = s.c0, from = 0; c <= s.c1; ++c) {
+              const int to = tiles_before(m.range[c + 1].begin, s.u0, s.n);
+              if (to > from) fn((2ll * c + (from > 0)) * C::kRows);
+              from = to;
+            }
+          };
+          float top = -INFINITY, tot = 0.f;
+          each_part([&](long long at) { top = has_row ? fmaxf(top, __ldcg(m.part_lse + at + my_row)) : top; });
+          const float r0 = top == -INFINITY ? 0.f : top;
+          each_part([&](long long at) { tot += has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) : 0.f; });
+          const float inv = tot != 0.f ? 1.f / tot : 0.f;
+          const int rr = min(s.row0 + my_row, s.last), t = m.token(rr);
+          const long long my_at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
+          if (has_row && a.lse) a.lse[my_at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+          for (int b0 = 0; warp + kSoftWarps * b0 < s.n_rows; b0 += kBatch) {
+            float4 o[kBatch][kV];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+              for (int k = 0; k < kV; ++k) o[b][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            each_part([&](long long at) {
+              const float w = has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) * inv : 0.f;
+              float4 v[kBatch][kV];
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b) {
+                const int r = warp + kSoftWarps * (b0 + b);
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                  v[b][k] = mine && r < s.n_rows ? __ldcg(reinterpret_cast<const float4*>(m.part_o + (at + r) * DIM) + lane + 32 * k)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b) {
+                const float wb = __shfl_sync(~0u, w, (b0 + b) & 31);
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                  o[b][k].x += wb * v[b][k].x, o[b][k].y += wb * v[b][k].y, o[b][k].z += wb * v[b][k].z, o[b][k].w += wb * v[b][k].w;
+              }
+            });
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              const long long at = __shfl_sync(~0u, my_at, (b0 + b) & 31);
+              if (mine && warp + kSoftWarps * (b0 + b) < s.n_rows)
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                  *reinterpret_cast<uint2*>(a.out + at * DIM + 4 * (lane + 32 * k)) =
+                      make_uint2(pack2(o[b][k].x, o[b][k].y), pack2(o[b][k].z, o[b][k].w));
+            }
+          }
+        }
+      }
     }
   }
 
@@ -892,60 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   if (warp == kWarpMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-  }
-}
-
-// Joins the row tiles that are divided between CTAs. CTA (c, slice): eight
-// rows of the row tile that the end of CTA c's range divides, if c holds its
-// first unit.
-template <int DIM>
-__global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
-  griddep_wait();
-  constexpr int kRows = ManyCfg<DIM>::kRows;
-  const int c0 = blockIdx.x;
-  const CtaRange cut = m.range[c0 + 1];
-  const long long units = m.plan->units, begin = m.range[c0].begin;
-  if (cut.begin >= units * m.nh || cut.begin == begin) return;
-  const long long u0 = cut.head * units + m.unit_off[cut.rt], u1 = cut.head * units + m.unit_off[cut.rt + 1];
-  if (u0 == cut.begin || u0 < begin) return;  // the cut is between two row tiles, or an earlier CTA has the first unit
-  const RowTile rt = m.row_tile[cut.rt];
-  const int n_rows = min(kRows, rt.n_new * m.a.group - rt.row0), n_tiles = int(u1 - u0) - kTileCost;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // key tiles [from, to) of the row tile are CTA c's; its part is in slot 1 of
-  // its two if it begins inside the row tile
-  auto tile_at = [&](long long u) { return min(n_tiles, max(0, int(max(0ll, min(u, u1) - u0)) - kTileCost)); };
-  // the last CTA that holds a part
-  int c1 = c0;
-  while (m.range[c1 + 1].begin < u1) ++c1;
-  const int r = blockIdx.y * 8 + warp;
-  if (r < n_rows) {
-    float top = -INFINITY;
-    for (int c = c0, from = 0; c <= c1; ++c) {
-      const int to = tile_at(m.range[c + 1].begin);
-      if (to - from == n_tiles) return;  // one CTA has them all, and wrote the output
-      if (to > from) top = fmaxf(top, m.part_lse[(2ll * c + (from > 0)) * kRows + r]);
-      from = to;
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float o[DIM / 32], sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
-    for (int c = c0, from = 0; c <= c1; ++c) {
-      const int to = tile_at(m.range[c + 1].begin);
-      if (to > from) {
-        const long long pr = (2ll * c + (from > 0)) * kRows + r;
-        const float w = ex2(m.part_lse[pr] - ref);
-        sum += w;
-#pragma unroll
-        for (int j = 0; j < DIM / 32; ++j) o[j] += w * m.part_o[pr * DIM + lane + 32 * j];
-      }
-      from = to;
-    }
-    const int rr = rt.row0 + r;
-    const long long at = (long long)(rt.first + m.token(rr)) * m.a.heads + (m.h0 + cut.head) * m.a.group + rr - m.token(rr) * m.a.group;
-#pragma unroll
-    for (int j = 0; j < DIM / 32; ++j) m.a.out[at * DIM + lane + 32 * j] = f32_to_bf16(sum != 0.f ? o[j] / sum : 0.f);
-    if (m.a.lse && lane == 0) m.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -959,7 +1012,7 @@ size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ManyPlan {
   int rows, tiles_max, nb, nh, ctas, max_row_tiles;
-  size_t kx, vx, bad, plan, unit_off, row_tile, range, part_o, part_lse, total;
+  size_t kx, vx, bad, plan, unit_off, row_tile, range, arrived, part_o, part_lse, total;
 };
 
 ManyPlan plan(const AttnArgs& a) {
@@ -989,6 +1042,7 @@ ManyPlan plan(const AttnArgs& a) {
   p.unit_off = put((size_t(p.max_row_tiles) + 1) * 8);
   p.row_tile = put(size_t(p.max_row_tiles) * sizeof(RowTile));
   p.range = put((size_t(p.ctas) + 1) * sizeof(CtaRange));
+  p.arrived = put(size_t(p.ctas) * 4);
   p.part_o = put(size_t(2) * p.ctas * p.rows * dim * 4);
   p.part_lse = put(size_t(2) * p.ctas * p.rows * 4);
   p.total = o;
@@ -1020,14 +1074,11 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
     for (m.h0 = 0; m.h0 < m.a.kv.kv_heads; m.h0 += p.nh) {
       m.nb = std::min(p.nb, m.a.kv.n_seqs - m.b0);
       m.nh = std::min(p.nh, m.a.kv.kv_heads - m.h0);
-      const long long grid = 1 + 1ll * m.nb * m.nh * p.tiles_max;
+      const long long grid = 1 + 2ll * m.nb * m.nh * p.tiles_max;
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
       attention_expand_kernel<DIM><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
       if (cudaError_t e = c.launched("attention_expand")) return e;
       if (cudaError_t e = launch_dependent(c, "attention_many", attention_many_kernel<DIM>, dim3(p.ctas), kThreads, C::kSmem, m))
-        return e;
-      if (cudaError_t e = launch_dependent(c, "attention_many_combine", attention_many_combine_kernel<DIM>,
-                                           dim3(p.ctas, C::kRows / 8), 256, 0, m))
         return e;
     }
   return cudaSuccess;
@@ -1053,6 +1104,7 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.range = reinterpret_cast<CtaRange*>(w + p.range);
   m.max_row_tiles = p.max_row_tiles;
   m.ctas = p.ctas;
+  m.arrived = reinterpret_cast<int*>(w + p.arrived);
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
   m.inv_group = ((1ull << 32) + a.group - 1) / a.group;

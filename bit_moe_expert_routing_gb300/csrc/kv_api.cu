@@ -67,6 +67,12 @@ bool any_few(const AttnArgs& a) {
   return !any_many(a) || (long long)a.kv.n_seqs * a.kv.max_new != a.kv.n_tokens;
 }
 
+// The few-row kernels' part of the workspace, before the many-row kernels'
+// (both are used when a step has sequences of both kinds).
+size_t few_bytes(const AttnArgs& a) {
+  return any_few(a) ? (attention_few_workspace(a, kFewRows) + 255) & ~size_t(255) : 0;
+}
+
 AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
   AttnArgs g{};
   g.kv = kv;
@@ -116,9 +122,7 @@ size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batc
   KvArgs a;
   if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
   const AttnArgs g = attn_args(a, at);
-  // the two parts run one after the other on the stream and share the space
-  const size_t few = attention_few_workspace(g, kFewRows), many = any_many(g) ? attention_many_workspace(g) : 0;
-  return ((few > many ? few : many) + 511) & ~size_t(255);
+  return ((few_bytes(g) + (any_many(g) ? attention_many_workspace(g) : 0)) + 511) & ~size_t(255);
 }
 
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
@@ -139,9 +143,10 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   g.out = out;
   g.lse = lse;
   const KvCall c = begin_call(stream);
-  if (any_few(g))
-    if (cudaError_t e = attention_few(g, kFewRows, workspace, c)) return status_of(e);
-  return any_many(g) ? status_of(attention_many(g, kFewRows, workspace, c)) : MOE_OK;
+  const bool many = any_many(g);
+  if (many)
+    if (cudaError_t e = attention_many(g, kFewRows, static_cast<char*>(workspace) + few_bytes(g), c)) return status_of(e);
+  return any_few(g) ? status_of(attention_few(g, kFewRows, workspace, many, c)) : MOE_OK;
 }
 
 }  // extern "C"
