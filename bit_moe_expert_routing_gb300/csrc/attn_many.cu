@@ -24,8 +24,7 @@
 // A CTA holds QT row tiles of 128 (two for DIM <= 128; one for 256, whose
 // output fills tensor memory): S tiles alternate between two slots, ordered
 // S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ..., so that the softmax of one
-// tile runs under the products of the other. All eight softmax warps work on
-// each S tile, two threads per row, 64 keys each.
+// tile runs under the products of the other.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -430,6 +429,27 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     mbar_init(qempty, 1);
     mbar_init(ofree, kSoftWarps);
     for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps);
-    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), kSoftWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), kSoftWarps / QT);  // (row tile q has slot q)
     for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -611,6 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     return ok && s->j1 > 0;
   };
 
+  // Registers: launched with 168 per thread; the softmax warps hold a row of S
+  // (208), the other four warps need few (88): 2 * 208 + 88 = 3 * 168.
+  if (warp >= kSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == kWarpTma) {
     if (lane == 0) {
       Segment s;
@@ -703,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     __syncwarp();
     umma_commit(drain);
     mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
-  } else if (warp >= kWarpLoad) {
+  } else {
     // ---------------- segments and query rows: two warps; lane 0 of the first steps through the units ----------
     Cursor cur(m);
     Segment s;
@@ -740,23 +764,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       if (lane == 0) mbar_arrive(dempty(sg));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  }
   } else {
-    // ---------------- softmax: eight warps, thread (row, half of the keys) ----------------
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------- softmax: eight warps ----------------
+    // Two row tiles: four warps each, a thread per row with all 128 keys, so that one tile's loads and maxima run
+    // beside the other's exponentials. One row tile: two threads per row with 64 keys each (its products take twice
+    // as long as a tile's softmax, and this halves the softmax's latency); they exchange maxima.
+    constexpr int kCols = 128 / (3 - QT), kOCols = DIM / (3 - QT);  // of a thread: keys of an S tile, dims of O
+    const int wg = warp >> 2, q = QT == 2 ? wg : 0, half = QT == 2 ? 0 : wg, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;  // the tensor-memory lanes this warp may access
+    const uint32_t ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
     // |scale| in base 2 (the keys carry the sign; for scale 0 they are zeros)
     const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;  // rows are multiples of 128 bytes
     Segment s;
-    uint32_t g = 0, pv0 = 0, exn = 0;  // S tiles so far, products O += P V per row tile so far, exchanges so far
+    uint32_t g0 = 0, pv0 = 0, exn = 0;  // before this segment: S tiles, products O += P V per row tile, exchanges
     // After a failed wait a warp keeps going without waiting, so that the
     // others never hang in a barrier; the status says that the output is void.
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, int site) {
       if (ok) ok = mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site);
     };
-    // the larger / the sum of the two halves' values of a row
+    // the other half's value of this row
     auto exchange = [&](float v) {
       float* e = ex + (exn & 1u) * 256;
       ++exn;
@@ -775,16 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           : "memory");
       if (!more) break;
       if (lane == 0) mbar_arrive(dempty(sg));
-      float ref[QT], sum[QT];
-      int pos[QT], minpos[QT], maxpos[QT];
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        ref[q] = -INFINITY, sum[q] = 0.f;
-        const int r0 = s.row0 + q * 128;
-        pos[q] = s.base_pos + m.token(min(r0 + row, s.last));
-        minpos[q] = s.base_pos + m.token(min(r0, s.last));
-        maxpos[q] = s.base_pos + m.token(min(r0 + 127, s.last));
-      }
+      float ref = -INFINITY, sum = 0.f;
+      const int r0 = s.row0 + q * 128;
+      const int pos = s.base_pos + m.token(min(r0 + row, s.last));
+      const int minpos = s.base_pos + m.token(min(r0, s.last)), maxpos = s.base_pos + m.token(min(r0 + 127, s.last));
       const int n = s.j1 - s.j0;
       const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
       unsigned bad_next = bad[s.index(s.j0)];
@@ -792,93 +817,96 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const int k0 = s.tile(s.j0 + i) * kBK;
         const unsigned missing = bad_next;
         if (i + 1 < n) bad_next = bad[s.index(s.j0 + i + 1)];
+        const uint32_t g = g0 + i * QT + q;
+        const uint32_t sl = tmem + lanes + (g & 1u) * 128;
+        wait(sfull(g & 1u), (g >> 1) & 1u, 226);
+        tc_fence_after();
+        uint32_t v[kCols];
 #pragma unroll
-        for (int q = 0; q < QT; ++q, ++g) {
-          const uint32_t sl = tmem + lanes + (g & 1u) * 128;
-          wait(sfull(g & 1u), (g >> 1) & 1u, 226);
-          tc_fence_after();
-          uint32_t v[64];
-          tmem_ld32(sl + half * 64, v);
-          tmem_ld32(sl + half * 64 + 32, v + 32);
-          tmem_wait_ld32(v);
-          tmem_wait_ld32(v + 32);
-          const bool whole = missing == 0 && k0 + kBK - 1 <= minpos[q] &&
-                             (a.window == 0 || k0 > maxpos[q] - a.window || k0 + kBK <= a.sinks);
-          if (!whole) {
-            // bit e: this row sees key k0 + 64 half + e, from the interval (or the sinks) that it sees
-            const int kb = k0 + half * 64;
+        for (int c = 0; c < kCols; c += 32) tmem_ld32(sl + half * 64 + c, v + c);
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) tmem_wait_ld32(v + c);
+        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos &&
+                           (a.window == 0 || k0 > maxpos - a.window || k0 + kBK <= a.sinks);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 64) {
+            // bit e: this row sees key kb + e, from the interval (or the sinks) that it sees
+            const int h = QT == 2 ? c / 64 : half, kb = k0 + h * 64;
             auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };  // bits under x
-            uint64_t sees = below(pos[q] + 1 - kb);
-            if (a.window > 0) sees &= ~below(pos[q] - a.window + 1 - kb) | below(a.sinks - kb);
+            uint64_t sees = below(pos + 1 - kb);
+            if (a.window > 0) sees &= ~below(pos - a.window + 1 - kb) | below(a.sinks - kb);
 #pragma unroll
             for (int i16 = 0; i16 < 4; ++i16)
-              if ((missing >> (half * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
+              if ((missing >> (h * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
             const uint32_t s0 = uint32_t(sees), s1 = uint32_t(sees >> 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              if (!(s0 & (1u << e))) v[e] = 0xff800000u;  // -inf
-              if (!(s1 & (1u << e))) v[32 + e] = 0xff800000u;
+              if (!(s0 & (1u << e))) v[c + e] = 0xff800000u;  // -inf
+              if (!(s1 & (1u << e))) v[c + 32 + e] = 0xff800000u;
             }
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          top = fmaxf(top, exchange(top)) * c2;
-          // the reference maximum moves only when a score passes it by 2^8: probabilities are floating point, so
-          // nothing is lost, and the output is hardly ever rescaled
-          const bool grew = top > ref[q] + 8.f;
-          if (__any_sync(~0u, grew)) {
-            const float to = fmaxf(ref[q], top);
-            const float al = to == -INFINITY ? 1.f : ex2(ref[q] - to);
-            ref[q] = to;
-            sum[q] *= al;
-            if (i > 0) {
-              wait(pvdone(q), (pv0 + i - 1) & 1u, 227);
-              tc_fence_after();
-              const uint32_t oc = tmem + lanes + 256 + q * DIM + half * (DIM / 2);
+        for (int e = 0; e < kCols; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (QT == 1) top = fmaxf(top, exchange(top));
+        top *= c2;
+        // the reference maximum moves only when a score passes it by 2^8: probabilities are floating point, so
+        // nothing is lost, and the output is hardly ever rescaled
+        if (__any_sync(~0u, top > ref + 8.f)) {
+          const float to = fmaxf(ref, top);
+          const float al = to == -INFINITY ? 1.f : ex2(ref - to);
+          ref = to;
+          sum *= al;
+          if (i > 0) {
+            wait(pvdone(q), (pv0 + i - 1) & 1u, 227);
+            tc_fence_after();
 #pragma unroll 1
-              for (int cc = 0; cc < DIM / 2; cc += 32) {
-                uint32_t o[32];
-                tmem_ld32(oc + cc, o);
-                tmem_wait_ld32(o);
+            for (int cc = 0; cc < kOCols; cc += 16) {
+              uint32_t o[16];
+              tmem_ld16(ocol + cc, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                tmem_st32(oc + cc, o);
-                tmem_wait_st();
-              }
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tmem_st16(ocol + cc, o);
+              tmem_wait_st();
             }
           }
-          const float r = ref[q] == -INFINITY ? 0.f : ref[q];
-          const float2 c22 = make_float2(c2, c2), r22 = make_float2(-r, -r);
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        }
+        const float r = ref == -INFINITY ? 0.f : ref;
+        const float2 c22 = make_float2(c2, c2), r22 = make_float2(-r, -r);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kCols; c += 64) {
           uint32_t p[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c22, r22);
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1])), c22, r22);
             x.x = ex2(x.x), x.y = ex2(x.y);
             acc[e & 1] = __fadd2_rn(acc[e & 1], x);
             p[e] = pack2(x.x, x.y);
           }
-          acc[0] = __fadd2_rn(acc[0], acc[1]);
-          sum[q] += acc[0].x + acc[0].y;
-          tmem_st32(sl + half * 32, p);
-          tmem_wait_st();
-          // A parity wait tells only consecutive phases apart, so the output's wait for the segment's last product has
-          // to know that the one before is done, and learns it here: the last one cannot be until this P is there.
-          if (i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pready(g & 1u));
+          tmem_st32(sl + half * 32 + c / 2, p);
+          tmem_wait_st();  // (the store reads its registers as it goes)
         }
+        acc[0] = __fadd2_rn(acc[0], acc[1]);
+        sum += acc[0].x + acc[0].y;
+        // A parity wait tells only consecutive phases apart, so the output's wait for the segment's last product has
+        // to know that the one before is done, and learns it here: the last one cannot be until this P is there.
+        if (i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready(g & 1u));
       }
+      g0 += n * QT;
       pv0 += n;
-      // output: each thread half of its rows' dims
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        const float tot = sum[q] + exchange(sum[q]);
+      // output: a row's dims, or half of them
+      {
+        const float tot = QT == 1 ? sum + exchange(sum) : sum;
         const float inv = tot != 0.f ? 1.f / tot : 0.f;
-        const float lse = tot != 0.f ? ref[q] + log2f(tot) : -INFINITY;
+        const float lse = tot != 0.f ? ref + log2f(tot) : -INFINITY;
         wait(pvdone(q), (pv0 - 1) & 1u, 228);
         tc_fence_after();
         const int r = q * 128 + row;
@@ -886,13 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const int rr = min(s.row0 + r, s.last), t = m.token(rr);
         const long long at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
         const long long prow = (long long)s.part * C::kRows + r;
-        const uint32_t oc = tmem + lanes + 256 + q * DIM + half * (DIM / 2);
 #pragma unroll 1
-        for (int cc = 0; cc < DIM / 2; cc += 32) {
+        for (int cc = 0; cc < kOCols; cc += 32) {
           uint32_t o[32];
-          tmem_ld32(oc + cc, o);
+          tmem_ld32(ocol + cc, o);
           tmem_wait_ld32(o);
-          const int d = half * (DIM / 2) + cc;
+          const int d = half * kOCols + cc;
           if (part) {
             float* dst = m.part_o + prow * DIM + d;
 #pragma unroll
