@@ -369,6 +369,7 @@ class KVCache:
                               k_biases.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), v_biases.data_ptr(),
                               self.status.data_ptr())
         self._ref = ctypes.byref(self.c)
+        self._settings = {}  # moe_attention structs by their values
         self._torch, self._bf16 = torch, torch.bfloat16  # (an import statement costs as much as a check)
 
     @classmethod
@@ -441,7 +442,7 @@ class KVCache:
         n, heads, _ = shape = q.shape
         qs = self._rows("q", q, batch.n_tokens, heads)
         if out is None:
-            out = torch.empty(shape, dtype=self._bf16, device=self.device)
+            out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=self._bf16, device=self.device)
         elif out.shape != shape or out.dtype != self._bf16 or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out: contiguous, of q's shape, type and device")
         l = lp = None
@@ -450,8 +451,13 @@ class KVCache:
             lp = l.data_ptr()
         if workspace is None:
             workspace = self.attention_workspace(heads, batch, window, sinks)
-        at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
-        st = lib().moe_attention_forward(self._ref, batch._ref, ctypes.byref(at), q.data_ptr(), qs, out.data_ptr(), lp,
+        at = self._settings.get((heads, window, sinks, scale))
+        if at is None:
+            if len(self._settings) > 64:
+                self._settings.clear()
+            at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
+            self._settings[heads, window, sinks, scale] = at = ctypes.byref(at)
+        st = lib().moe_attention_forward(self._ref, batch._ref, at, q.data_ptr(), qs, out.data_ptr(), lp,
                                          workspace.data_ptr(), workspace.numel(), self._stream(None))
         if st:
             _check(st, "moe_attention_forward")

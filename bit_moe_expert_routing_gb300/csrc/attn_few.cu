@@ -29,10 +29,10 @@
 // Work split: an item is (sequence, kv head, group of 8 NT rows), and its
 // units are its 32-key tiles. One wave of CTAs takes equal, contiguous ranges
 // of all items' units, whatever the sequences' lengths; an item that is cut
-// leaves fp32 partial outputs, which attention_combine_kernel joins. (A grid of
+// leaves fp32 partial outputs, which a combine kernel joins. (A grid of
 // fixed-length splits took 107 us for 64 ragged sequences of up to 8191
 // positions, 60 of them in prologues and merges.) When no item has more than
-// kWholeTiles, an item is a CTA's whole work and nothing is cut. The four warps
+// kWholeElements, an item is a CTA's whole work and nothing is cut. The four warps
 // of a CTA alternate tiles, each with its own ring of asynchronous copies, so
 // that nothing but the merge of an item's end joins them. (cp.async rather than
 // bulk copies: a tile is six runs of one or two pages, and six bulk copies by
@@ -134,7 +134,11 @@ __device__ __forceinline__ Tiles tiles_of(int minpos, int maxpos, int window, in
   return t;
 }
 
-constexpr int kWholeTiles = 16;
+// An item of at most so many cached elements (keys x dims) is not worth
+// cutting: the combine kernel costs what three of its four warps' share does.
+// (Heads of 64 with a window of 1024 + 4 keys, 256 items: whole 12.9 us, cut
+// 18.4; heads of 256 with 600 keys, 64 items: whole 16.8 us, cut 15.9.)
+constexpr long long kWholeElements = 72 * 1024;
 constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
 
 struct FewArgs {
@@ -768,76 +772,121 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   griddep_wait();
 }
 
+// Where an item's parts are: parts p = 0 .. n - 1 of CTAs p0 + p. Part 0 ends
+// its CTA's range and is in slot 0; the others begin theirs inside the item,
+// in slot 1.
+struct Parts {
+  SeqItems sq;
+  int kvh, rg, n_rows, p0, n;
+  __device__ __forceinline__ int slot(int p) const { return 2 * (p0 + p) + (p > 0); }
+  // place of row `row` of the group in the outputs
+  __device__ __forceinline__ long long place(const FewArgs& f, int rows_per_group, int row) const {
+    const int r = rg * rows_per_group + row, t = f.token(r);
+    return (long long)(sq.s.first + t) * f.a.heads + kvh * f.a.group + r - t * f.a.group;
+  }
+};
+// The parts of item x of the grid's items (by one CTA of 256 threads; what
+// they are counted from is input, so this runs beside the kernel before).
+__device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_group) {
+  __shared__ long long sums[256];
+  Parts q;
+  q.n = 0;
+  const int per_seq = f.a.kv.kv_heads * f.row_groups;
+  const int b = x / per_seq, y = x - b * per_seq;
+  q.kvh = y / f.row_groups;
+  q.rg = y - q.kvh * f.row_groups;
+  q.sq = items_of(f, b, rows_per_group);
+  q.n_rows = min(q.sq.rows - q.rg * rows_per_group, rows_per_group);
+  if (q.n_rows <= 0) return q;
+  // the item's first unit: those of the sequences before, then of the items before
+  Cut<256> cut(f, rows_per_group, sums);
+  long long u0 = 0;
+  for (int c0 = 0; c0 <= b && f.a.kv.n_seqs > 1; c0 += 256) {
+    const long long n = f.a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
+    u0 += b < c0 + 256 ? (b > c0 ? sums[b - c0 - 1] : 0) : n;
+  }
+  u0 += (long long)(q.kvh * q.sq.groups + q.rg) * q.sq.tiles.n;
+  q.p0 = cut.cta_of(u0);
+  q.n = cut.cta_of(u0 + q.sq.tiles.n - 1) - q.p0 + 1;
+  return q;
+}
+
 // Joins the parts of the items that are cut: out = sum_p 2^(lse_p - max) o_p /
-// sum_p 2^(lse_p - max). One CTA per (place for an item, row, SLICE dims): few
-// items with many parts want all of the GPU on them, SLICE / 4 threads on the
-// dims and the CTA's groups of those threads on the parts, eight loads in
-// flight each. With rows_cta = 0 (many items, then of few parts) one CTA per
-// item, a warp per row.
-template <int DIM, int SLICE>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group, int rows_cta) {
-  constexpr int kLanes = SLICE / 4, kGroups = 256 / kLanes;
+// sum_p 2^(lse_p - max). A warp per row, a CTA per eight rows of an item; the
+// lanes first hold the parts' weights, then the dims, with eight parts' loads
+// in flight.
+template <int DIM>
+__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group) {
+  constexpr int kV = DIM / 128 + (DIM < 128);  // float4 of a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
+  const Parts q = parts_of(f, blockIdx.x, rows_per_group);
+  if (q.n <= 1 || row >= q.n_rows) return;
+  const long long at = q.place(f, rows_per_group, row);
+  griddep_wait();
+  float top = -INFINITY;
+  for (int p = lane; p < q.n; p += 32) top = fmaxf(top, f.part_lse[q.slot(p) * rows_per_group + row]);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float4 o[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = DIM >= 128 || lane < DIM / 4;
+  for (int c0 = 0; c0 < q.n; c0 += 32) {
+    const int n = min(32, q.n - c0);
+    const float w = lane < n ? ex2(f.part_lse[q.slot(c0 + lane) * rows_per_group + row] - ref) : 0.f;
+    for (int p = 0; p < n; p += 8) {
+      float4 v[8][kV];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+          v[i][k] = mine && p + i < n ? reinterpret_cast<const float4*>(
+                                            f.part_o + (size_t(q.slot(c0 + p + i)) * rows_per_group + row) * DIM)[lane + 32 * k]
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl_sync(~0u, w, p + i);
+        sum += wi;
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+          o[k].x += wi * v[i][k].x, o[k].y += wi * v[i][k].y, o[k].z += wi * v[i][k].z, o[k].w += wi * v[i][k].w;
+      }
+    }
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  if (mine)
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      uint2 h;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(o[k].y * inv), "f"(o[k].x * inv));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(o[k].w * inv), "f"(o[k].z * inv));
+      *reinterpret_cast<uint2*>(f.a.out + at * DIM + 4 * (lane + 32 * k)) = h;
+    }
+  if (lane == 0 && f.a.lse) f.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The same for few items with many parts each, which want all of the GPU: a
+// CTA per (item, row, 64 dims), sixteen threads on the dims and sixteen such
+// groups on the parts, eight loads in flight each.
+template <int DIM>
+__global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewArgs f, int rows_per_group, int rows) {
+  constexpr int kLanes = 16, kGroups = 16;
   constexpr int kMaxParts = 1024;  // (no item has more parts than there are CTAs)
   __shared__ float weight[kMaxParts];
   __shared__ float4 acc[kGroups][kLanes];
   __shared__ float red[16];
-  __shared__ long long sums[256];
-  const AttnArgs& a = f.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int x = blockIdx.x, row0 = 0, rows_n = 1;
-  if (rows_cta > 0) {
-    row0 = x % rows_cta;
-    x /= rows_cta;
-  }
-  const int per_seq = a.kv.kv_heads * f.row_groups;
-  const int b = x / per_seq, y = x - b * per_seq, kvh = y / f.row_groups, rg = y - kvh * f.row_groups;
-  const SeqItems sq = items_of(f, b, rows_per_group);
-  if (rg >= sq.groups) return;
-  const int n_rows = min(sq.rows - rg * rows_per_group, rows_per_group);
-  if (row0 >= n_rows) return;
-  if (rows_cta == 0) rows_n = n_rows;
-  // the item's first unit: those of the sequences before, then of the items before
-  Cut<256> cut(f, rows_per_group, sums);
-  long long u0 = 0;
-  for (int c0 = 0; c0 <= b && a.kv.n_seqs > 1; c0 += 256) {
-    const long long n = a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
-    u0 += b < c0 + 256 ? (b > c0 ? sums[b - c0 - 1] : 0) : n;
-  }
-  u0 += (long long)(kvh * sq.groups + rg) * sq.tiles.n;
-  const int p0 = cut.cta_of(u0), n = cut.cta_of(u0 + sq.tiles.n - 1) - p0 + 1;
-  if (n <= 1) return;
-  // part 0 ends its CTA's range, in slot 0; the others begin theirs inside the item, in slot 1
-  auto slot = [&](int p) { return 2 * (p0 + p) + (p > 0); };
-  const int tok0 = rg * rows_per_group;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x % rows;
+  const Parts q = parts_of(f, blockIdx.x / rows, rows_per_group);
+  const int n = q.n;
+  if (n <= 1 || row >= q.n_rows) return;
+  const long long at = q.place(f, rows_per_group, row);
+  const int grp = threadIdx.x / kLanes, d = blockIdx.y * 64 + 4 * (threadIdx.x % kLanes);
   griddep_wait();
-  if (rows_cta == 0) {
-    for (int row = warp; row < rows_n; row += 8) {
-      float top = -INFINITY;
-      for (int p = 0; p < n; ++p) top = fmaxf(top, f.part_lse[slot(p) * rows_per_group + row]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float o[DIM / 32], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < DIM / 32; ++j) o[j] = 0.f;
-      for (int p = 0; p < n; ++p) {
-        const size_t at = size_t(slot(p)) * rows_per_group + row;
-        const float w = ex2(f.part_lse[at] - ref);
-        sum += w;
-#pragma unroll
-        for (int j = 0; j < DIM / 32; ++j) o[j] += w * f.part_o[at * DIM + lane + 32 * j];
-      }
-      const int r = tok0 + row, t = f.token(r);
-      const long long at = (long long)(sq.s.first + t) * a.heads + kvh * a.group + r - t * a.group;
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-      for (int j = 0; j < DIM / 32; ++j) a.out[at * DIM + lane + 32 * j] = f32_to_bf16(o[j] * inv);
-      if (lane == 0 && a.lse) a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    }
-    return;
-  }
-  const int grp = threadIdx.x / kLanes, d = blockIdx.y * SLICE + 4 * (threadIdx.x % kLanes);
   float top = -INFINITY;
   for (int p = threadIdx.x; p < n; p += 256) {
-    const float v = f.part_lse[slot(p) * rows_per_group + row0];
+    const float v = f.part_lse[q.slot(p) * rows_per_group + row];
     weight[p] = v;
     top = fmaxf(top, v);
   }
@@ -855,7 +904,7 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int p = p1 + k * kGroups;
-      v[k] = p < n ? *reinterpret_cast<const float4*>(f.part_o + (size_t(slot(p)) * rows_per_group + row0) * DIM + d)
+      v[k] = p < n ? *reinterpret_cast<const float4*>(f.part_o + (size_t(q.slot(p)) * rows_per_group + row) * DIM + d)
                    : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
@@ -875,18 +924,16 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-      const float4 q = acc[k][threadIdx.x];
+      const float4 w = acc[k][threadIdx.x];
       tot += red[k];
-      v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
     const float inv = tot != 0.f ? 1.f / tot : 0.f;
-    const int r = tok0 + row0, t = f.token(r);
-    const long long at = (long long)(sq.s.first + t) * a.heads + kvh * a.group + r - t * a.group;
     uint2 h;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y * inv), "f"(v.x * inv));
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(v.w * inv), "f"(v.z * inv));
-    *reinterpret_cast<uint2*>(a.out + at * DIM + d) = h;
-    if (d == 0 && a.lse) a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+    *reinterpret_cast<uint2*>(f.a.out + at * DIM + d) = h;
+    if (d == 0 && f.a.lse) f.a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -905,7 +952,7 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   long long keys = a.kv.max_kv;
   if (a.window > 0)
     keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kTile);
-  p.whole = (keys + kTile - 1) / kTile <= kWholeTiles;
+  p.whole = keys * a.kv.dim <= kWholeElements;
   const int per_sm = a.kv.dim * p.nt <= 128 ? 4 : 2;  // CTAs that fit (registers and the rings)
   p.ctas = num_sms() * per_sm;
   p.part_rows = p.whole ? 0 : size_t(2) * p.ctas * 8 * p.nt;
@@ -933,15 +980,16 @@ cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   if (cudaError_t e = c.launched("attention_few")) return e;
   if (f.whole) return cudaSuccess;
   const int rows = int(std::min<long long>({(long long)f.a.kv.max_new * f.a.group, f.max_rows, C::kRows}));
-  const bool spread = items * 4 <= f.max_ctas, narrow = spread && items * 64 <= f.max_ctas;  // by the parts of an item
+  const bool wide = items * 32 <= f.max_ctas;  // more than 32 parts each
   cfg = {};
-  cfg.gridDim = spread ? dim3(unsigned(items * rows), narrow ? DIM / 64 : 1) : dim3(unsigned(items));
+  cfg.gridDim = wide ? dim3(unsigned(items * rows), DIM / 64) : dim3(unsigned(items), (rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, narrow ? attention_combine_kernel<DIM, 64> : attention_combine_kernel<DIM, DIM>, f, C::kRows,
-                                         spread ? rows : 0)) return e;
+  if (cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, attention_combine_wide_kernel<DIM>, f, C::kRows, rows)
+                           : cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM>, f, C::kRows))
+    return e;
   return c.launched("attention_combine");
 }
 
