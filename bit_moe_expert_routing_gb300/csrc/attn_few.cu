@@ -135,10 +135,11 @@ __device__ __forceinline__ Tiles tiles_of(int minpos, int maxpos, int window, in
 }
 
 // An item of at most so many cached elements (keys x dims) is not worth
-// cutting: the combine kernel costs what three of its four warps' share does.
-// (Heads of 64 with a window of 1024 + 4 keys, 256 items: whole 12.9 us, cut
-// 18.4; heads of 256 with 600 keys, 64 items: whole 16.8 us, cut 15.9.)
-constexpr long long kWholeElements = 72 * 1024;
+// cutting: the combine kernel and the parts cost more than the tiles that the
+// CTA would be spared. (Graph replays of 32 sequences: heads of 64, 1100 keys,
+// whole 10.9 us, cut 14.8; 2200 keys 18.4 and 18.8; heads of 128, 1100 keys,
+// 14.0 and 18.0; heads of 256, 600 keys, 11.3 and 17.2.)
+constexpr long long kWholeElements = 144 * 1024;
 constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
 
 struct FewArgs {

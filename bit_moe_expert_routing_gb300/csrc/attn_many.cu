@@ -21,10 +21,19 @@
 // lengths nor few row tiles leave SMs idle. A row tile that falls into several
 // ranges leaves fp32 partial outputs.
 //
+// Two CTAs on neighbouring SMs work as one (cta_group::2): an MMA takes 128
+// rows of each and all of a key tile, of which each SM keeps half (64 keys, or
+// half of the values' dims). A single CTA with the whole key tile is bound by
+// its shared memory: per S tile of 128 rows, 128 keys and 128 dims it reads 64
+// KB for S and 32 KB for O and takes in 32 KB, 1024 cycles at 128 bytes, as
+// long as the products themselves; together they took 1400. The pair reads and
+// takes in 40 KB less.
+//
 // A CTA holds QT row tiles of 128 (two for DIM <= 128; one for 256, whose
 // output fills tensor memory): S tiles alternate between two slots, ordered
 // S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ..., so that the softmax of one
-// tile runs under the products of the other.
+// tile runs under the products of the other. The pair's first CTA issues the
+// MMAs; the other tells it which of its operands have landed.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -34,25 +43,27 @@ namespace moe {
 namespace {
 
 constexpr int kBK = 128;                  // keys per tile
-constexpr uint32_t kUnit = 16384;         // bytes of a ring unit: 128 rows of 128 bytes
+constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
-constexpr int kRing = 9;
 constexpr int kDescs = 4;                 // segment descriptors in flight
 constexpr int kTileCost = 1;              // units added to every row tile: its set-up and output
 
 template <int DIM>
 struct ManyCfg {
   static constexpr int QT = DIM == 256 ? 1 : 2;
-  static constexpr int kRows = 128 * QT;
-  static constexpr int UN = DIM / 64;     // units of a key or value tile
-  static constexpr uint32_t kTileBytes = uint32_t(UN) * kUnit;
+  static constexpr int kRows = 128 * QT;  // of a CTA
+  static constexpr int kPairRows = 2 * kRows;
+  static constexpr int UN = DIM / 64;     // blocks of 64 dims
+  static constexpr uint32_t kSlot = 128u * DIM;  // half a key or value tile: what one CTA of the pair keeps
+  static constexpr uint32_t kTileBytes = 2 * kSlot;
+  static constexpr int kRing = DIM == 64 ? 12 : DIM == 128 ? 9 : 4;
   static constexpr uint32_t kQTile = 128 * DIM * 2;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffRing = QT * kQTile;
-  static constexpr uint32_t kOffEx = kOffRing + kRing * kUnit;  // [2][2][128] floats: row maxima of the halves
+  static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: row maxima of the halves
   static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
-  // full, empty [kRing]; qfull, qempty, ofree, drain; sfull, pready [2]; pvdone [QT]; dfull, dempty [kDescs]
-  static constexpr int kBars = 2 * kRing + 4 + 4 + QT + 2 * kDescs;
+  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready [2]; pvdone [QT]; dfull, dempty [kDescs]
+  static constexpr int kBars = 3 * kRing + 5 + 4 + QT + 2 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 80;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -71,7 +82,7 @@ struct PlanHdr {
   int row_tiles, pad;
 };
 
-struct __align__(16) CtaRange {
+struct __align__(16) PairRange {
   long long begin;  // first unit of all kv heads' units
   int head, rt;     // its kv head and row tile
 };
@@ -87,12 +98,12 @@ struct ManyArgs {
   PlanHdr* plan;
   long long* unit_off;     // [row tiles + 1] first unit of each row tile (kTileCost + its key tiles each)
   RowTile* row_tile;
-  CtaRange* range;         // [ctas + 1] where each CTA's units begin; the last entry ends them
+  PairRange* range;        // [pairs + 1] where each pair's units begin; the last entry ends them
   int max_row_tiles;
-  int ctas;                // of the many kernel
-  int* arrived;            // [ctas] parts written of the row tile whose first part is the CTA's
-  float* part_o;           // [2 ctas][rows][DIM]
-  float* part_lse;         // [2 ctas][rows], base 2
+  int pairs;               // CTA pairs of the many kernel
+  int* arrived;            // [pairs][2] parts written of the row tile whose first part is the pair's, per CTA
+  float* part_o;           // [2 pairs][2][rows][DIM]: two slots per pair, each CTA's rows
+  float* part_lse;         // [2 pairs][2][rows], base 2
   unsigned long long inv_group;  // ceil(2^32 / group): row / group for rows below 2^26
   __device__ __forceinline__ int token(int row) const { return int((unsigned(row) * inv_group) >> 32); }
 };
@@ -204,9 +215,9 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
   }
   __syncthreads();
   const long long all = units * m.nh;
-  for (int c = threadIdx.x; c <= m.ctas; c += kPlanThreads) {
-    const long long begin = all * c / m.ctas;
-    CtaRange r{begin, 0, 0};
+  for (int c = threadIdx.x; c <= m.pairs; c += kPlanThreads) {
+    const long long begin = all * c / m.pairs;
+    PairRange r{begin, 0, 0};
     if (begin < all) {
       r.head = int(begin / units);
       const long long at = begin - r.head * units;
@@ -220,7 +231,7 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
       }
     }
     m.range[c] = r;
-    if (c < m.ctas) m.arrived[c] = 0;
+    if (c < m.pairs) m.arrived[2 * c] = m.arrived[2 * c + 1] = 0;
   }
 }
 
@@ -241,7 +252,7 @@ template <int DIM>
 __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs m) {
   griddep_launch();
   if (blockIdx.x == 0) {
-    make_plan(m, ManyCfg<DIM>::kRows);
+    make_plan(m, ManyCfg<DIM>::kPairRows);
     return;
   }
   __shared__ long long rows16[kBK / 16];  // first cache row of each 16 keys, -1: zeros
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
         const __nv_bfloat16 s16 = __ushort_as_bfloat16(sc[i]), b16 = __ushort_as_bfloat16(bs[i]);
         uint32_t o[4];
         dq8_bf16(c[i], __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
-        *reinterpret_cast<uint4*>(kd + (w / 8) * kUnit + sw128(key, w & 7)) =
+        *reinterpret_cast<uint4*>(kd + (key >> 6) * ManyCfg<DIM>::kSlot + (w / 8) * 8192 + sw128(key & 63, w & 7)) =
             make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
       }
     }
@@ -342,9 +353,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       const int d = 8 * w + n;
-      const uint32_t at = DIM == 64    ? kb * 8192 + sw128(d, ko)
-                          : DIM == 128 ? kb * kUnit + sw128(d, ko)
-                                       : (kb * 2 + d / 128) * kUnit + sw128(d & 127, ko);
+      constexpr int kHalf = DIM / 2;  // dims of a CTA
+      const uint32_t at = d / kHalf * ManyCfg<DIM>::kSlot + kb * (kHalf * 128) + sw128(d % kHalf, ko);
       *reinterpret_cast<uint4*>(vd + at) = make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
     }
   }
@@ -360,9 +370,9 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // and the leading offset; the high half is the same for all.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << (46 - 32)) | (2u << (61 - 32));
-// kind::f16: bf16 A and B, fp32 D, both K-major, M = 128, N = n.
+// kind::f16: bf16 A and B, fp32 D, both K-major, M = 256 (128 rows of each CTA of the pair), N = n.
 constexpr uint32_t idesc_n(int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(256 >> 4) << 24);
 }
 // Four K = 16 steps of a 64-wide K block, by one elected lane of the converged
 // warp: D += A B^T with A in shared memory, or in tensor memory. The first
@@ -378,10 +388,10 @@ __device__ __forceinline__ void umma4_ss(uint32_t d, uint32_t a_lo, uint32_t b_l
       " mov.b64 a0, {%1, %3};\n mov.b64 a1, {x1, %3};\n mov.b64 a2, {x2, %3};\n mov.b64 a3, {x3, %3};\n"
       " mov.b64 b0, {%2, %3};\n mov.b64 b1, {y1, %3};\n mov.b64 b2, {y2, %3};\n mov.b64 b3, {y3, %3};\n"
       " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, %5, %5;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %4, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %4, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %4, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %4, t;\n}" ::"r"(d),
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a0, b0, %4, p;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %4, t;\n}" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -393,19 +403,69 @@ __device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a, uint32_t b_lo, 
       " add.u32 y1, %2, 2;\n add.u32 y2, %2, 4;\n add.u32 y3, %2, 6;\n"
       " mov.b64 b0, {%2, %3};\n mov.b64 b1, {y1, %3};\n mov.b64 b2, {y2, %3};\n mov.b64 b3, {y3, %3};\n"
       " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, %5, %5;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], b1, %4, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], b2, %4, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [x3], b3, %4, t;\n}" ::"r"(d),
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b0, %4, p;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [x1], b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [x2], b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [x3], b3, %4, t;\n}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
 }
-// `bar` receives one arrival when every MMA that the elected lane issued before has completed.
+// `bar` of both CTAs receives one arrival when every MMA that the elected lane issued before has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      "{\n .reg .pred e;\n .reg .b16 both;\n elect.sync _|e, 0xffffffff;\n mov.b16 both, 3;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n}" ::"r"(bar)
       : "memory");
+}
+
+// The same for a barrier of this CTA alone.
+__device__ __forceinline__ void umma_commit_own(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
+}
+
+// Arrives on the first CTA's barrier at this CTA's address `bar`. What it
+// tells of is in tensor memory, or came by TMA, and is ordered by the tcgen05
+// fences and the copies' own barriers; a release of the whole cluster's memory
+// took ~2000 cycles of a softmax warp's time per tile.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+// The same, with this thread's view of memory released to the first CTA.
+__device__ __forceinline__ void arrive_first_release(uint32_t bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+// mbar_wait for such an arrival.
+__device__ __forceinline__ bool mbar_wait_acquire(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr,
+                                                  int site) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kTrySuspendNs)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > kWaitLimit) {
+        *abort_flag = 1;
+        report(hdr, MOE_ERR_DEVICE_TIMEOUT, site);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -481,14 +541,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // ---- the segments of a CTA ------------------------------------------------------------------
 
-// One CTA's part of a row tile: its key tiles [j0, j1) of n. j1 = 0: no more.
+// A CTA's rows of a pair's part of a row tile: key tiles [j0, j1) of n. j1 = 0: no more.
 struct __align__(16) Segment {
   int seq, head, row0, n_rows;   // sequence and kv head (within the pass), first row, rows
   int j0, j1, n, part;           // part: slot of the partial output, -1 if the row tile is whole
   int first, base_pos, last;     // sequence's first step token, position of its token 0, its last row
   int all_sink, all_first;       // Range of the sequence's expanded tiles
   int my_sink, my_first;         // Range of the row tile
-  int parts, c0, c1;             // of a divided row tile: its parts, the first and last CTA with units of it
+  int parts, c0, c1;             // of a divided row tile: its parts, the first and last pair with units of it
   long long u0;                  // its first unit
   __device__ __forceinline__ int tile(int j) const { return j < my_sink ? j : my_first + j - my_sink; }
   __device__ __forceinline__ int index(int j) const {
@@ -504,17 +564,18 @@ __device__ __forceinline__ int tiles_before(long long u, long long u0, int n) {
   return t <= 0 ? 0 : t < n ? int(t) : n;
 }
 
-// Steps through the units [u, end) of a CTA. Every row tile has kTileCost
+// Steps through the units [u, end) of a pair. Every row tile has kTileCost
 // units more than key tiles; a part that holds none of the latter is skipped.
 struct Cursor {
   const ManyArgs& m;
   long long u, end, units;
   int rt, head;
+  const int pair = blockIdx.x >> 1, rank = blockIdx.x & 1;
   __device__ Cursor(const ManyArgs& args) : m(args) {
-    const CtaRange r = m.range[blockIdx.x];
+    const PairRange r = m.range[pair];
     units = m.plan->units;
     u = r.begin;
-    end = m.range[blockIdx.x + 1].begin;
+    end = m.range[pair + 1].begin;
     head = r.head;
     rt = r.rt;
   }
@@ -528,23 +589,23 @@ struct Cursor {
       if (j1 > j0) {
         const RowTile t = m.row_tile[rt];
         const SeqInfo si = t.info();
-        const Range all = seq_range(m, si), mine = rows_range(m, si, t.row0, rows);
+        const Range all = seq_range(m, si), mine = rows_range(m, si, t.row0, 2 * rows);
         s->seq = t.seq - m.b0;
         s->head = head;
-        s->row0 = t.row0;
+        s->row0 = t.row0 + rank * rows;
         s->last = si.n_new * m.a.group - 1;
-        s->n_rows = min(rows, s->last + 1 - t.row0);
+        s->n_rows = max(0, min(rows, s->last + 1 - s->row0));
         s->j0 = j0;
         s->j1 = j1;
         s->n = n;
-        s->part = j0 == 0 && j1 == n ? -1 : 2 * int(blockIdx.x) + (j0 > 0 ? 1 : 0);
+        s->part = j0 == 0 && j1 == n ? -1 : 2 * (2 * pair + (j0 > 0 ? 1 : 0)) + rank;
         s->first = si.first;
         s->base_pos = si.kv - si.n_new;
         s->all_sink = all.n_sink, s->all_first = all.first;
         s->my_sink = mine.n_sink, s->my_first = mine.first;
         if (s->part >= 0) {
           s->u0 = o0;
-          s->c0 = s->c1 = blockIdx.x;
+          s->c0 = s->c1 = pair;
           while (m.range[s->c0].begin > o0) --s->c0;
           while (m.range[s->c1 + 1].begin < o1) ++s->c1;
           s->parts = 0;
@@ -572,7 +633,7 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
 template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
   using C = ManyCfg<DIM>;
-  constexpr int QT = C::QT, UN = C::UN;
+  constexpr int QT = C::QT, UN = C::UN, kRing = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -580,12 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const uint32_t bar0 = base + C::kOffBar;
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kRing + s); };
-  const uint32_t qfull = bar0 + 8u * (2 * kRing), qempty = qfull + 8, ofree = qfull + 16, drain = qfull + 24;
-  auto sfull = [&](uint32_t s) { return qfull + 32 + 8u * s; };
-  auto pready = [&](uint32_t s) { return qfull + 48 + 8u * s; };
-  auto pvdone = [&](uint32_t q) { return qfull + 64 + 8u * q; };
-  auto dfull = [&](uint32_t i) { return qfull + 64 + 8u * (QT + i % kDescs); };
-  auto dempty = [&](uint32_t i) { return qfull + 64 + 8u * (QT + kDescs + i % kDescs); };
+  auto pfull = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + s); };  // first CTA: the other's slot is full
+  const uint32_t qfull = bar0 + 8u * (3 * kRing), qempty = qfull + 8, ofree = qfull + 16, drain = qfull + 24;
+  const uint32_t pq = qfull + 32;  // first CTA: the other's queries are there
+  auto sfull = [&](uint32_t s) { return qfull + 40 + 8u * s; };
+  auto pready = [&](uint32_t s) { return qfull + 56 + 8u * s; };
+  auto pvdone = [&](uint32_t q) { return qfull + 72 + 8u * q; };
+  auto dfull = [&](uint32_t i) { return qfull + 72 + 8u * (QT + i % kDescs); };
+  auto dempty = [&](uint32_t i) { return qfull + 72 + 8u * (QT + kDescs + i % kDescs); };
+  const bool first_cta = (blockIdx.x & 1) == 0;
   Segment* descs = reinterpret_cast<Segment*>(gbase + C::kOffDesc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
@@ -594,24 +658,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (known to be warp-uniform)
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(pfull(s), 1);
+    mbar_init(pq, 1);
     mbar_init(qfull, kLoadWarps * 32);
     mbar_init(qempty, 1);
-    mbar_init(ofree, kSoftWarps);
+    mbar_init(ofree, 2 * kSoftWarps);
     for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps);
-    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), kSoftWarps / QT);  // (row tile q has slot q)
+    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), 2 * kSoftWarps / QT);  // (row tile q has slot q)
     for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == kWarpMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // S slots at columns 0 and 128, O at 256
   griddep_wait();
@@ -648,13 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           // which tile has ring position p
           const bool is_v = QT == 2 ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
           const int i = QT == 2 ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
-          const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + s.index(s.j0 + i)) * C::kTileBytes;
-          for (int u = 0; u < UN; ++u, ++it) {
-            const uint32_t slot = it % kRing;
-            if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
-            mbar_arrive_tx(full(slot), kUnit);
-            bulk_g2s(base + C::kOffRing + slot * kUnit, src + u * kUnit, kUnit, full(slot));
-          }
+          const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + s.index(s.j0 + i)) * C::kTileBytes + (first_cta ? 0 : C::kSlot);
+          const uint32_t slot = it % kRing;
+          if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
+          mbar_arrive_tx(full(slot), C::kSlot);
+          bulk_g2s(base + C::kOffRing + slot * C::kSlot, src, C::kSlot, full(slot));
+          ++it;
         }
       }
       if (!ok) {  // copies in flight land before the CTA leaves (bounded)
@@ -663,70 +728,81 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       }
     }
   } else if (warp == kWarpMma) {
-    // the whole warp, converged; every wait's outcome is made warp-uniform
     Segment s;
-    uint32_t ring = 0, g0 = 0;  // before this segment: ring units, S tiles
     bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity, int site) {
-      ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site));
-      tc_fence_after();
-      return ok;
-    };
-    constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM < 128 ? DIM : 128);
-    for (uint32_t sg = 0;; ++sg) {
-      if (!__all_sync(~0u, descriptor(sg, &s, ok))) break;
-      if (lane == 0) mbar_arrive(dempty(sg));
-      __syncwarp();
-      const int n = s.j1 - s.j0, total = n * QT;
-      if (!wait(qfull, sg & 1u, 222)) break;
-      fence_proxy_async();  // the loader warps' copies, for the tensor core
-      auto wait_unit = [&](uint32_t seq) { return wait(full(seq % kRing), (seq / kRing) & 1u, 223); };
-      auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
-        const int q = x % QT, i = x / QT;
-        const uint32_t sl = (g0 + x) & 1u, d = tmem + sl * 128;
-        for (int u = 0; u < UN; ++u) {
-          const uint32_t seq = ring + k_at(i) * UN + u, slot = seq % kRing;
-          if (q == 0 && !wait_unit(seq)) return;
-          umma4_ss(d, desc_lo(base + C::kOffQ + q * C::kQTile + u * kUnit), desc_lo(base + C::kOffRing + slot * kUnit),
-                   kIdS, u != 0);
-          if (q == QT - 1) umma_commit(empty(slot));
+    uint32_t ring = 0;  // ring slots before this segment
+    if (!first_cta) {
+      // tells the first CTA what has landed here, in the order in which it needs it
+      if (lane == 0) {
+        for (uint32_t sg = 0; descriptor(sg, &s, ok); ++sg) {
+          mbar_arrive(dempty(sg));
+          if (!(ok = mbar_wait(qfull, sg & 1u, abort_flag, hdr, kWaitLimit, false, 233))) break;
+          fence_proxy_async();  // the loader warps' copies, for the tensor cores
+          arrive_first_release(pq);
+          for (int p = 0; p < 2 * (s.j1 - s.j0) && ok; ++p, ++ring) {
+            if (!(ok = mbar_wait(full(ring % kRing), (ring / kRing) & 1u, abort_flag, hdr, kWaitLimit, false, 234))) break;
+            arrive_first(pfull(ring % kRing));
+          }
         }
-        umma_commit(sfull(sl));
-        if (x == total - 1) umma_commit(qempty);
-      };
-      auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
-        const int q = x % QT, i = x / QT;
-        const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
-        for (int u = 0; u < UN; ++u) {
-          const uint32_t seq = ring + v_at(i, n) * UN + u, slot = seq % kRing;
-          if (q == 0 && !wait_unit(seq)) return;
-          const uint32_t vb = base + C::kOffRing + slot * kUnit;
-          // a unit holds both blocks of 64 keys (DIM 64), one block (128), or one block of half the dims (256)
-          const int kb0 = DIM == 64 ? 0 : DIM == 128 ? u : u / 2;
-          const uint32_t od = o + (DIM == 256 ? (u & 1) * 128 : 0);
-#pragma unroll
-          for (int kb = 0; kb < (DIM == 64 ? 2 : 1); ++kb)
-            umma4_ts(od, p + (kb0 + kb) * 32, desc_lo(vb + kb * 8192), kIdO, i > 0 || kb0 + kb > 0);
-          if (q == QT - 1) umma_commit(empty(slot));
-        }
-        umma_commit(pvdone(q));
-      };
-      qk(0);
-      if (ok && total > 1) qk(1);
-      for (int x = 0; x < total && ok; ++x) {
-        const uint32_t g = g0 + x;
-        if (!wait(pready(g & 1u), (g >> 1) & 1u, 224)) break;
-        if (x == 0 && sg > 0 && !wait(ofree, (sg - 1) & 1u, 230)) break;
-        pv(x);
-        if (ok && x + 2 < total) qk(x + 2);
       }
-      g0 += total;
-      ring += 2 * n * UN;
+    } else {
+      // the whole warp, converged; every wait's outcome is made warp-uniform
+      uint32_t g0 = 0;  // S tiles before this segment
+      auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+        ok = __all_sync(~0u, mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site));
+        tc_fence_after();
+        return ok;
+      };
+      constexpr uint32_t kIdS = idesc_n(128), kIdO = idesc_n(DIM);
+      for (uint32_t sg = 0;; ++sg) {
+        if (!__all_sync(~0u, descriptor(sg, &s, ok))) break;
+        if (lane == 0) mbar_arrive(dempty(sg));
+        __syncwarp();
+        const int n = s.j1 - s.j0, total = n * QT;
+        if (!wait(qfull, sg & 1u, 222)) break;
+        if (!(ok = __all_sync(~0u, mbar_wait_acquire(pq, sg & 1u, abort_flag, hdr, 235)))) break;
+        fence_proxy_async();  // the loader warps' copies, for the tensor core
+        auto wait_slot = [&](uint32_t seq) {
+          return wait(full(seq % kRing), (seq / kRing) & 1u, 223) && wait(pfull(seq % kRing), (seq / kRing) & 1u, 236);
+        };
+        auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
+          const int q = x % QT, i = x / QT;
+          const uint32_t sl = (g0 + x) & 1u, seq = ring + k_at(i), kb = base + C::kOffRing + seq % kRing * C::kSlot;
+          if (q == 0 && !wait_slot(seq)) return;
+#pragma unroll
+          for (int u = 0; u < UN; ++u)
+            umma4_ss(tmem + sl * 128, desc_lo(base + C::kOffQ + q * C::kQTile + u * kQBlock), desc_lo(kb + u * 8192), kIdS, u != 0);
+          if (q == QT - 1) umma_commit(empty(seq % kRing));
+          umma_commit(sfull(sl));
+          if (x == total - 1) umma_commit(qempty);
+        };
+        auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
+          const int q = x % QT, i = x / QT;
+          const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
+          const uint32_t seq = ring + v_at(i, n), vb = base + C::kOffRing + seq % kRing * C::kSlot;
+          if (q == 0 && !wait_slot(seq)) return;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) umma4_ts(o, p + kb * 32, desc_lo(vb + kb * (DIM * 64)), kIdO, i > 0 || kb > 0);
+          if (q == QT - 1) umma_commit(empty(seq % kRing));
+          umma_commit(pvdone(q));
+        };
+        qk(0);
+        if (ok && total > 1) qk(1);
+        for (int x = 0; x < total && ok; ++x) {
+          const uint32_t g = g0 + x;
+          if (!wait(pready(g & 1u), (g >> 1) & 1u, 224)) break;
+          if (x == 0 && sg > 0 && !wait(ofree, (sg - 1) & 1u, 230)) break;
+          pv(x);
+          if (ok && x + 2 < total) qk(x + 2);
+        }
+        g0 += total;
+        ring += 2 * n;
+      }
+      // every MMA has completed before the pair leaves (bounded)
+      __syncwarp();
+      umma_commit_own(drain);
+      mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
     }
-    // every MMA has completed before the CTA leaves (bounded)
-    __syncwarp();
-    umma_commit(drain);
-    mbar_wait(drain, 0, abort_flag, hdr, kWaitLimit, true, 225);
   } else {
     // ---------------- segments and query rows: two warps; lane 0 of the first steps through the units ----------
     Cursor cur(m);
@@ -756,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       for (int r = tid / CH; r < C::kRows; r += kLoadWarps * 32 / CH) {
         const int rr = min(mine.row0 + r, mine.last), t = m.token(rr);
         const uint16_t* src = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
-        cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kUnit + sw128(r & 127, c & 7), src,
+        cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kQBlock + sw128(r & 127, c & 7), src,
                    r < mine.n_rows ? 16u : 0u);
       }
       cp_async_arrive_noinc(qfull);
@@ -898,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         if (i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pready(g & 1u));
+        if (lane == 0) arrive_first(pready(g & 1u));
       }
       g0 += n * QT;
       pv0 += n;
@@ -949,13 +1025,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);
+      if (lane == 0) arrive_first(ofree);
       if (s.part >= 0) {
-        // the part is written; whoever completes the count joins all parts, in the order of their CTAs
+        // the part is written; whoever completes the count joins all parts of this CTA's rows, in the order of the pairs
         __threadfence();
         int* last = reinterpret_cast<int*>(gbase + C::kOffMisc + 8);
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
-        if (threadIdx.x == 0) *last = atomicAdd(m.arrived + s.c0, 1) == s.parts - 1;
+        if (threadIdx.x == 0) *last = atomicAdd(m.arrived + 2 * s.c0 + (s.part & 1), 1) == s.parts - 1;
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
         if (*last) {
           __threadfence();
@@ -969,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           auto each_part = [&](auto&& fn) {
             for (int c = s.c0, from = 0; c <= s.c1; ++c) {
               const int to = tiles_before(m.range[c + 1].begin, s.u0, s.n);
-              if (to > from) fn((2ll * c + (from > 0)) * C::kRows);
+              if (to > from) fn((2 * (2ll * c + (from > 0)) + (s.part & 1)) * C::kRows);
               from = to;
             }
           };
@@ -1023,9 +1099,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
+  pair_sync();  // nothing of the other CTA reads or arrives here any more
   if (warp == kWarpMma) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
 
@@ -1038,14 +1116,14 @@ constexpr size_t kPassBytes = size_t(2) << 30;
 size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ManyPlan {
-  int rows, tiles_max, nb, nh, ctas, max_row_tiles;
+  int rows, tiles_max, nb, nh, pairs, max_row_tiles;  // rows: of a row tile, both CTAs'
   size_t kx, vx, bad, plan, unit_off, row_tile, range, arrived, part_o, part_lse, total;
 };
 
 ManyPlan plan(const AttnArgs& a) {
   ManyPlan p{};
   const int dim = a.kv.dim;
-  p.rows = dim == 256 ? 128 : 256;
+  p.rows = dim == 256 ? 256 : 512;
   long long keys = a.kv.max_kv;
   if (a.window > 0)
     keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kBK);
@@ -1054,7 +1132,7 @@ ManyPlan plan(const AttnArgs& a) {
   const size_t fit = std::max<size_t>(1, kPassBytes / head_bytes);
   p.nh = int(std::min<size_t>(a.kv.kv_heads, fit));
   p.nb = int(std::min<size_t>(a.kv.n_seqs, std::max<size_t>(1, fit / p.nh)));
-  p.ctas = num_sms();
+  p.pairs = num_sms() / 2;
   p.max_row_tiles = int(((long long)a.kv.n_tokens * a.group + p.rows - 1) / p.rows + p.nb);
   size_t o = 0;
   auto put = [&](size_t bytes) {
@@ -1068,27 +1146,30 @@ ManyPlan plan(const AttnArgs& a) {
   p.plan = put(sizeof(PlanHdr));
   p.unit_off = put((size_t(p.max_row_tiles) + 1) * 8);
   p.row_tile = put(size_t(p.max_row_tiles) * sizeof(RowTile));
-  p.range = put((size_t(p.ctas) + 1) * sizeof(CtaRange));
-  p.arrived = put(size_t(p.ctas) * 4);
-  p.part_o = put(size_t(2) * p.ctas * p.rows * dim * 4);
-  p.part_lse = put(size_t(2) * p.ctas * p.rows * 4);
+  p.range = put((size_t(p.pairs) + 1) * sizeof(PairRange));
+  p.arrived = put(size_t(p.pairs) * 2 * 4);
+  p.part_o = put(size_t(2) * p.pairs * p.rows * dim * 4);
+  p.part_lse = put(size_t(2) * p.pairs * p.rows * 4);
   p.total = o;
   return p;
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(const KvCall& c, const char* name, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
+cudaError_t launch_pairs(const KvCall& c, const char* name, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
                              Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) return e;
   return c.launched(name);
 }
@@ -1105,7 +1186,7 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
       attention_expand_kernel<DIM><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
       if (cudaError_t e = c.launched("attention_expand")) return e;
-      if (cudaError_t e = launch_dependent(c, "attention_many", attention_many_kernel<DIM>, dim3(p.ctas), kThreads, C::kSmem, m))
+      if (cudaError_t e = launch_pairs(c, "attention_many", attention_many_kernel<DIM>, dim3(2 * p.pairs), kThreads, C::kSmem, m))
         return e;
     }
   return cudaSuccess;
@@ -1128,9 +1209,9 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.plan = reinterpret_cast<PlanHdr*>(w + p.plan);
   m.unit_off = reinterpret_cast<long long*>(w + p.unit_off);
   m.row_tile = reinterpret_cast<RowTile*>(w + p.row_tile);
-  m.range = reinterpret_cast<CtaRange*>(w + p.range);
+  m.range = reinterpret_cast<PairRange*>(w + p.range);
   m.max_row_tiles = p.max_row_tiles;
-  m.ctas = p.ctas;
+  m.pairs = p.pairs;
   m.arrived = reinterpret_cast<int*>(w + p.arrived);
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
