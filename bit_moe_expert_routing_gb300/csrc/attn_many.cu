@@ -32,8 +32,11 @@
 // A CTA holds QT row tiles of 128 (two for DIM <= 128; one for 256, whose
 // output fills tensor memory): S tiles alternate between two slots, ordered
 // S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ..., so that the softmax of one
-// tile runs under the products of the other. The pair's first CTA issues the
-// MMAs; the other tells it which of its operands have landed.
+// tile runs under the products of the other. Heads of 64 leave room for P
+// beside S: there S(x + 2) follows as soon as S(x) has been read, S(0) S(1) |
+// S(2), P(0) V | S(3), P(1) V | ..., and the softmax never waits for a product.
+// The pair's first CTA issues the MMAs; the other tells it which of its
+// operands have landed.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -58,12 +61,15 @@ struct ManyCfg {
   static constexpr uint32_t kTileBytes = 2 * kSlot;
   static constexpr int kRing = DIM == 64 ? 12 : DIM == 128 ? 9 : 4;
   static constexpr uint32_t kQTile = 128 * DIM * 2;
+  // DIM 64: P has tensor memory of its own, and a softmax warpgroup takes a
+  // row tile; else P takes S's place, and both take half of each S tile's keys
+  static constexpr bool kOwnP = DIM == 64;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffRing = QT * kQTile;
   static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: row maxima of the halves
   static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
-  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready [2]; pvdone [QT]; dfull, dempty [kDescs]
-  static constexpr int kBars = 3 * kRing + 5 + 4 + QT + 2 * kDescs;
+  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [QT]; dfull, dempty [kDescs]
+  static constexpr int kBars = 3 * kRing + 5 + 6 + QT + 2 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 80;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
@@ -634,6 +640,8 @@ template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
   using C = ManyCfg<DIM>;
   constexpr int QT = C::QT, UN = C::UN, kRing = C::kRing;
+  constexpr bool kOwnP = C::kOwnP;
+  constexpr int kArrive = kOwnP ? kSoftWarps / 2 : kSoftWarps;  // softmax warps of an S tile, per CTA
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -646,9 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const uint32_t pq = qfull + 32;  // first CTA: the other's queries are there
   auto sfull = [&](uint32_t s) { return qfull + 40 + 8u * s; };
   auto pready = [&](uint32_t s) { return qfull + 56 + 8u * s; };
-  auto pvdone = [&](uint32_t q) { return qfull + 72 + 8u * q; };
-  auto dfull = [&](uint32_t i) { return qfull + 72 + 8u * (QT + i % kDescs); };
-  auto dempty = [&](uint32_t i) { return qfull + 72 + 8u * (QT + kDescs + i % kDescs); };
+  auto sread = [&](uint32_t s) { return qfull + 72 + 8u * s; };  // kOwnP: S has been read
+  auto pvdone = [&](uint32_t q) { return qfull + 88 + 8u * q; };
+  auto dfull = [&](uint32_t i) { return qfull + 88 + 8u * (QT + i % kDescs); };
+  auto dempty = [&](uint32_t i) { return qfull + 88 + 8u * (QT + kDescs + i % kDescs); };
   const bool first_cta = (blockIdx.x & 1) == 0;
   Segment* descs = reinterpret_cast<Segment*>(gbase + C::kOffDesc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
@@ -664,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     mbar_init(qempty, 1);
     mbar_init(ofree, 2 * kSoftWarps);
     for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps);
-    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), 2 * kSoftWarps / QT);  // (row tile q has slot q)
+    for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), 2 * kArrive), mbar_init(sread(s), 2 * kArrive);
     for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -684,10 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   griddep_launch();
 
   // Ring position of key tile i and value tile i of a segment of n tiles, in
-  // the order of their first use: K0 V0 K1 V1 ... with two row tiles, K0 K1
-  // V0 K2 V1 ... with one (its S tiles run two ahead).
-  auto k_at = [](int i) { return QT == 2 ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
-  auto v_at = [](int i, int n) { return QT == 2 ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+  // the order of their first use: K0 V0 K1 V1 ... with two row tiles; K0 K1 V0
+  // K2 V1 ... with one, or where P has its own place (S runs a tile ahead).
+  constexpr bool kKeysAhead = QT == 1 || kOwnP;
+  auto k_at = [](int i) { return !kKeysAhead ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
+  auto v_at = [](int i, int n) { return !kKeysAhead ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
   // Segment i, once its descriptor is there; every reader arrives on dempty(i) when it needs it no more.
   auto descriptor = [&](uint32_t i, Segment* s, bool& ok) {
@@ -712,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const int n = s.j1 - s.j0;
         for (int p = 0; p < 2 * n && ok; ++p) {
           // which tile has ring position p
-          const bool is_v = QT == 2 ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
-          const int i = QT == 2 ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
+          const bool is_v = !kKeysAhead ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
+          const int i = !kKeysAhead ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
           const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + s.index(s.j0 + i)) * C::kTileBytes + (first_cta ? 0 : C::kSlot);
           const uint32_t slot = it % kRing;
           if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
@@ -778,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         };
         auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
           const int q = x % QT, i = x / QT;
-          const uint32_t p = tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
+          const uint32_t p = kOwnP ? tmem + 384 + q * 64 : tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
           const uint32_t seq = ring + v_at(i, n), vb = base + C::kOffRing + seq % kRing * C::kSlot;
           if (q == 0 && !wait_slot(seq)) return;
 #pragma unroll
@@ -790,10 +800,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         if (ok && total > 1) qk(1);
         for (int x = 0; x < total && ok; ++x) {
           const uint32_t g = g0 + x;
+          if (kOwnP) {
+            if (!wait(sread(g & 1u), (g >> 1) & 1u, 237)) break;
+            if (x + 2 < total) qk(x + 2);
+            if (!ok) break;
+          }
           if (!wait(pready(g & 1u), (g >> 1) & 1u, 224)) break;
           if (x == 0 && sg > 0 && !wait(ofree, (sg - 1) & 1u, 230)) break;
           pv(x);
-          if (ok && x + 2 < total) qk(x + 2);
+          if (!kOwnP && ok && x + 2 < total) qk(x + 2);
         }
         g0 += total;
         ring += 2 * n;
@@ -844,13 +859,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: eight warps ----------------
-    // Two row tiles: four warps each, a thread per row with all 128 keys, so that one tile's loads and maxima run
-    // beside the other's exponentials. One row tile: two threads per row with 64 keys each (its products take twice
-    // as long as a tile's softmax, and this halves the softmax's latency); they exchange maxima.
-    constexpr int kCols = 128 / (3 - QT), kOCols = DIM / (3 - QT);  // of a thread: keys of an S tile, dims of O
-    const int wg = warp >> 2, q = QT == 2 ? wg : 0, half = QT == 2 ? 0 : wg, row = (warp & 3) * 32 + lane;
+    // Where P has its own place: four warps per row tile, a thread per row with all 128 keys, so that one tile's loads
+    // and maxima run beside the other's exponentials. Else two threads per row with 64 keys each, which halves the time
+    // between S and P, with the slot's products waiting; they exchange maxima.
+    constexpr bool kHalves = !kOwnP;
+    constexpr int NQ = kHalves ? QT : 1;  // row tiles of a warp
+    constexpr int kCols = kHalves ? 64 : 128, kOCols = kHalves ? DIM / 2 : DIM;  // of a thread: keys of an S tile, dims of O
+    const int wg = warp >> 2, half = kHalves ? wg : 0, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;  // the tensor-memory lanes this warp may access
-    const uint32_t ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
     // |scale| in base 2 (the keys carry the sign; for scale 0 they are zeros)
     const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
@@ -882,10 +898,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           : "memory");
       if (!more) break;
       if (lane == 0) mbar_arrive(dempty(sg));
-      float ref = -INFINITY, sum = 0.f;
-      const int r0 = s.row0 + q * 128;
-      const int pos = s.base_pos + m.token(min(r0 + row, s.last));
-      const int minpos = s.base_pos + m.token(min(r0, s.last)), maxpos = s.base_pos + m.token(min(r0 + 127, s.last));
+      float ref[NQ], sum[NQ];
+      int pos[NQ], minpos[NQ], maxpos[NQ];
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        ref[k] = -INFINITY, sum[k] = 0.f;
+        const int r0 = s.row0 + (kHalves ? k : wg) * 128;
+        pos[k] = s.base_pos + m.token(min(r0 + row, s.last));
+        minpos[k] = s.base_pos + m.token(min(r0, s.last)), maxpos[k] = s.base_pos + m.token(min(r0 + 127, s.last));
+      }
       const int n = s.j1 - s.j0;
       const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
       unsigned bad_next = bad[s.index(s.j0)];
@@ -893,8 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const int k0 = s.tile(s.j0 + i) * kBK;
         const unsigned missing = bad_next;
         if (i + 1 < n) bad_next = bad[s.index(s.j0 + i + 1)];
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+        const int q = kHalves ? k : wg;
         const uint32_t g = g0 + i * QT + q;
         const uint32_t sl = tmem + lanes + (g & 1u) * 128;
+        const uint32_t pl = kOwnP ? tmem + lanes + 384 + q * 64 : sl, ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
         wait(sfull(g & 1u), (g >> 1) & 1u, 226);
         tc_fence_after();
         uint32_t v[kCols];
@@ -902,16 +927,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         for (int c = 0; c < kCols; c += 32) tmem_ld32(sl + half * 64 + c, v + c);
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) tmem_wait_ld32(v + c);
-        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos &&
-                           (a.window == 0 || k0 > maxpos - a.window || k0 + kBK <= a.sinks);
+        if (kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(sread(g & 1u));
+        }
+        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos[k] &&
+                           (a.window == 0 || k0 > maxpos[k] - a.window || k0 + kBK <= a.sinks);
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 64) {
             // bit e: this row sees key kb + e, from the interval (or the sinks) that it sees
-            const int h = QT == 2 ? c / 64 : half, kb = k0 + h * 64;
+            const int h = kHalves ? half : c / 64, kb = k0 + h * 64;
             auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };  // bits under x
-            uint64_t sees = below(pos + 1 - kb);
-            if (a.window > 0) sees &= ~below(pos - a.window + 1 - kb) | below(a.sinks - kb);
+            uint64_t sees = below(pos[k] + 1 - kb);
+            if (a.window > 0) sees &= ~below(pos[k] - a.window + 1 - kb) | below(a.sinks - kb);
 #pragma unroll
             for (int i16 = 0; i16 < 4; ++i16)
               if ((missing >> (h * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
@@ -927,15 +957,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
         for (int e = 0; e < kCols; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (QT == 1) top = fmaxf(top, exchange(top));
+        if (kHalves) top = fmaxf(top, exchange(top));
         top *= c2;
         // the reference maximum moves only when a score passes it by 2^8: probabilities are floating point, so
         // nothing is lost, and the output is hardly ever rescaled
-        if (__any_sync(~0u, top > ref + 8.f)) {
-          const float to = fmaxf(ref, top);
-          const float al = to == -INFINITY ? 1.f : ex2(ref - to);
-          ref = to;
-          sum *= al;
+        if (__any_sync(~0u, top > ref[k] + 8.f)) {
+          const float to = fmaxf(ref[k], top);
+          const float al = to == -INFINITY ? 1.f : ex2(ref[k] - to);
+          ref[k] = to;
+          sum[k] *= al;
           if (i > 0) {
             wait(pvdone(q), (pv0 + i - 1) & 1u, 227);
             tc_fence_after();
@@ -951,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             }
           }
         }
-        const float r = ref == -INFINITY ? 0.f : ref;
+        const float r = ref[k] == -INFINITY ? 0.f : ref[k];
         const float2 c22 = make_float2(c2, c2), r22 = make_float2(-r, -r);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -964,25 +994,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             acc[e & 1] = __fadd2_rn(acc[e & 1], x);
             p[e] = pack2(x.x, x.y);
           }
-          tmem_st32(sl + half * 32 + c / 2, p);
+          // (P's own place is free once the product of the tile before has read it)
+          if (kOwnP && c == 0 && i > 0) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+          tmem_st32(pl + half * 32 + c / 2, p);
           tmem_wait_st();  // (the store reads its registers as it goes)
         }
         acc[0] = __fadd2_rn(acc[0], acc[1]);
-        sum += acc[0].x + acc[0].y;
+        sum[k] += acc[0].x + acc[0].y;
         // A parity wait tells only consecutive phases apart, so the output's wait for the segment's last product has
         // to know that the one before is done, and learns it here: the last one cannot be until this P is there.
-        if (i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+        if (!kOwnP && i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first(pready(g & 1u));
+        }
       }
       g0 += n * QT;
       pv0 += n;
       // output: a row's dims, or half of them
-      {
-        const float tot = QT == 1 ? sum + exchange(sum) : sum;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        const int q = kHalves ? k : wg;
+        const uint32_t ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
+        const float tot = kHalves ? sum[k] + exchange(sum[k]) : sum[k];
         const float inv = tot != 0.f ? 1.f / tot : 0.f;
-        const float lse = tot != 0.f ? ref + log2f(tot) : -INFINITY;
+        const float lse = tot != 0.f ? ref[k] + log2f(tot) : -INFINITY;
         wait(pvdone(q), (pv0 - 1) & 1u, 228);
         tc_fence_after();
         const int r = q * 128 + row;
