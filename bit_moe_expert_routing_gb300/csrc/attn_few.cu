@@ -951,8 +951,9 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   p.nt = rows <= 8 ? 1 : rows <= 16 || a.kv.dim == 256 ? 2 : 4;
   p.row_groups = std::max(1, int((rows + 8 * p.nt - 1) / (8 * p.nt)));
   long long keys = a.kv.max_kv;
+  const long long tokens = std::min<long long>(a.kv.max_new, max_rows / a.group + 1);  // of a sequence taken here
   if (a.window > 0)
-    keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kTile);
+    keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + tokens + 2 * kTile);
   p.whole = keys * a.kv.dim <= kWholeElements;
   const int per_sm = a.kv.dim * p.nt <= 128 ? 4 : 2;  // CTAs that fit (registers and the rings)
   p.ctas = num_sms() * per_sm;

@@ -49,7 +49,8 @@ constexpr int kBK = 128;                  // keys per tile
 constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
 constexpr int kDescs = 4;                 // segment descriptors in flight
-constexpr int kTileCost = 1;              // units added to every row tile: its set-up and output
+constexpr int kTileCost = 3;              // units added to every row tile: its set-up and output (1: 89 us, 3: 84.5 us
+                                          // for a prompt of 4096 tokens)
 
 template <int DIM>
 struct ManyCfg {
@@ -68,10 +69,11 @@ struct ManyCfg {
   static constexpr uint32_t kOffRing = QT * kQTile;
   static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: row maxima of the halves
   static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
-  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [QT]; dfull, dempty [kDescs]
-  static constexpr int kBars = 3 * kRing + 5 + 6 + QT + 2 * kDescs;
+  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [QT]; dfull, dempty, info [kDescs]
+  static constexpr int kBars = 3 * kRing + 5 + 6 + QT + 3 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
-  static constexpr uint32_t kOffMisc = kOffDesc + kDescs * 80;
+  static constexpr uint32_t kOffInfo = kOffDesc + kDescs * 80;
+  static constexpr uint32_t kOffMisc = kOffInfo + kDescs * 16;
   static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -554,8 +556,8 @@ struct __align__(16) Segment {
   int first, base_pos, last;     // sequence's first step token, position of its token 0, its last row
   int all_sink, all_first;       // Range of the sequence's expanded tiles
   int my_sink, my_first;         // Range of the row tile
-  int parts, c0, c1;             // of a divided row tile: its parts, the first and last pair with units of it
-  long long u0;                  // its first unit
+  int pad;
+  long long u0;                  // first unit of the row tile
   __device__ __forceinline__ int tile(int j) const { return j < my_sink ? j : my_first + j - my_sink; }
   __device__ __forceinline__ int index(int j) const {
     const int t = tile(j);
@@ -563,6 +565,11 @@ struct __align__(16) Segment {
   }
 };
 static_assert(sizeof(Segment) == 80, "descriptor size");
+
+// Of a divided row tile: its parts, the first and last pair with units of it.
+struct PartInfo {
+  int parts, c0, c1, pad;
+};
 
 // Key tiles before unit `u` of a row tile of n key tiles that begins at unit u0.
 __device__ __forceinline__ int tiles_before(long long u, long long u0, int n) {
@@ -609,24 +616,28 @@ struct Cursor {
         s->base_pos = si.kv - si.n_new;
         s->all_sink = all.n_sink, s->all_first = all.first;
         s->my_sink = mine.n_sink, s->my_first = mine.first;
-        if (s->part >= 0) {
-          s->u0 = o0;
-          s->c0 = s->c1 = pair;
-          while (m.range[s->c0].begin > o0) --s->c0;
-          while (m.range[s->c1 + 1].begin < o1) ++s->c1;
-          s->parts = 0;
-          for (int c = s->c0, from = 0; c <= s->c1; ++c) {
-            const int to = tiles_before(m.range[c + 1].begin, o0, n);
-            s->parts += to > from;
-            from = to;
-          }
-        }
+        s->u0 = o0;
       }
       u = stop;
       if (stop == o1 && ++rt == m.plan->row_tiles) rt = 0, ++head;
     }
   }
 };
+
+// (apart from the descriptor: it takes loads that depend on one another, and is needed only at the segment's end)
+__device__ __forceinline__ PartInfo part_info(const ManyArgs& m, const Segment& s) {
+  const int pair = s.part >> 2;
+  PartInfo p{0, pair, pair, 0};
+  const long long end = s.u0 + kTileCost + s.n;
+  while (m.range[p.c0].begin > s.u0) --p.c0;
+  while (m.range[p.c1 + 1].begin < end) ++p.c1;
+  for (int c = p.c0, from = 0; c <= p.c1; ++c) {
+    const int to = tiles_before(m.range[c + 1].begin, s.u0, s.n);
+    p.parts += to > from;
+    from = to;
+  }
+  return p;
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -659,7 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   auto dfull = [&](uint32_t i) { return qfull + 88 + 8u * (QT + i % kDescs); };
   auto dempty = [&](uint32_t i) { return qfull + 88 + 8u * (QT + kDescs + i % kDescs); };
   const bool first_cta = (blockIdx.x & 1) == 0;
+  auto info_bar = [&](uint32_t i) { return qfull + 88 + 8u * (QT + 2 * kDescs + i % kDescs); };
   Segment* descs = reinterpret_cast<Segment*>(gbase + C::kOffDesc);
+  PartInfo* infos = reinterpret_cast<PartInfo*>(gbase + C::kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
   const AttnArgs& a = m.a;
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     mbar_init(qfull, kLoadWarps * 32);
     mbar_init(qempty, 1);
     mbar_init(ofree, 2 * kSoftWarps);
-    for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps);
+    for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps), mbar_init(info_bar(i), 1);
     for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), 2 * kArrive), mbar_init(sread(s), 2 * kArrive);
     for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
     mbar_init(drain, 1);
@@ -835,22 +848,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     for (uint32_t sg = 0;; ++sg) {
       if (!__all_sync(~0u, descriptor(sg, &s, ok))) break;
       const Segment mine = s;
-      produce(sg + 1);  // one ahead, before this segment's rows
-      __syncwarp();
       if (sg > 0 && ok) ok = mbar_wait(qempty, (sg - 1) & 1u, abort_flag, hdr, kWaitLimit, false, 232);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       constexpr int CH = DIM / 8;  // 16-byte chunks of a row
       const int tid = threadIdx.x - kWarpLoad * 32, c = tid % CH;
       const uint16_t* qh = a.q + (m.h0 + mine.head) * a.group * DIM + c * 8;
-#pragma unroll 8
-      for (int r = tid / CH; r < C::kRows; r += kLoadWarps * 32 / CH) {
-        const int rr = min(mine.row0 + r, mine.last), t = m.token(rr);
-        const uint16_t* src = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
-        cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kQBlock + sw128(r & 127, c & 7), src,
-                   r < mine.n_rows ? 16u : 0u);
+      constexpr int kStep = kLoadWarps * 32 / CH;  // rows of one instruction of both warps
+      for (int rb = tid / CH; rb < C::kRows; rb += 8 * kStep) {
+        const uint16_t* src[8];  // all addresses first: the copies do not let the compiler interleave their arithmetic
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = min(mine.row0 + rb + k * kStep, mine.last), t = m.token(rr);
+          src[k] = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = rb + k * kStep;
+          cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kQBlock + sw128(r & 127, c & 7), src[k],
+                     r < mine.n_rows ? 16u : 0u);
+        }
       }
       cp_async_arrive_noinc(qfull);
+      produce(sg + 1);  // the next one, while this one's rows are used
+      if (warp == kWarpLoad + 1 && lane == 0) {
+        if (mine.part >= 0) infos[sg % kDescs] = part_info(m, mine);
+        mbar_arrive(info_bar(sg));
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(dempty(sg));
     }
@@ -945,11 +969,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
             for (int i16 = 0; i16 < 4; ++i16)
               if ((missing >> (h * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
-            const uint32_t s0 = uint32_t(sees), s1 = uint32_t(sees >> 32);
+            // 32 keys at a time: most of them are seen by every row of the warp
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!(s0 & (1u << e))) v[c + e] = 0xff800000u;  // -inf
-              if (!(s1 & (1u << e))) v[c + 32 + e] = 0xff800000u;
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t bits = uint32_t(sees >> (32 * w));
+              if (__all_sync(~0u, bits == ~0u)) continue;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits & (1u << e))) v[c + 32 * w + e] = 0xff800000u;  // -inf
             }
           }
         }
@@ -1067,9 +1094,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         __threadfence();
         int* last = reinterpret_cast<int*>(gbase + C::kOffMisc + 8);
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
-        if (threadIdx.x == 0) *last = atomicAdd(m.arrived + 2 * s.c0 + (s.part & 1), 1) == s.parts - 1;
+        if (threadIdx.x == 0) {
+          wait(info_bar(sg), (sg / kDescs) & 1u, 238);
+          const PartInfo i = infos[sg % kDescs];
+          *last = ok && atomicAdd(m.arrived + 2 * i.c0 + (s.part & 1), 1) == i.parts - 1;
+        }
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
         if (*last) {
+          const PartInfo info = infos[sg % kDescs];
           __threadfence();
           // A warp joins rows warp, warp + 8, ..., lane l holding the maximum and sum of row warp + 8 l, and takes the
           // rows' values in batches with all of a part's loads in flight.
@@ -1079,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           const bool has_row = my_row < s.n_rows;
           // parts in order: fn(row of the part buffers at which the part begins)
           auto each_part = [&](auto&& fn) {
-            for (int c = s.c0, from = 0; c <= s.c1; ++c) {
+            for (int c = info.c0, from = 0; c <= info.c1; ++c) {
               const int to = tiles_before(m.range[c + 1].begin, s.u0, s.n);
               if (to > from) fn((2 * (2ll * c + (from > 0)) + (s.part & 1)) * C::kRows);
               from = to;
