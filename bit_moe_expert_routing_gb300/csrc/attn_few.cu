@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     Entry e;
     // (volatile: as an ordinary load the compiler moves it to its use, one iteration on)
     asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e.page) : "l"(table + min(j, last_entry)));
-    const bool unseen = t >= t_end || k0 > gr.maxpos || (a.window > 0 && k0 + 16 <= lo_all && k0 >= a.sinks);
+    // (bit operations: short-circuits would be branches, of which a tile has room for few)
+    const bool unseen = (t >= t_end) | (k0 > gr.maxpos) | ((a.window > 0) & (k0 + 16 <= lo_all) & (k0 >= a.sinks));
     e.state = unseen ? 2 : j >= a.kv.table_stride ? 1 : 0;
     return e;
   };
@@ -389,14 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
       const uint32_t dst = ring_s + s * St::kBytes;
       const int in_page = gr.tiles.key0(t) & page_mask;
       auto row_of = [&](Entry e) { return (((long long)e.page * a.kv.kv_heads + kvh) << a.kv.page_bits) + in_page; };
-      auto valid = [&](Entry e) {
-        const bool ok = e.state == 0 && unsigned(e.page) < unsigned(a.kv.n_pages);
-        if (!ok && e.state != 2) report(a.kv.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
-        return ok;
-      };
-      const bool v0 = valid(e0), v1 = valid(e1);
+      const bool v0 = (e0.state == 0) & (unsigned(e0.page) < unsigned(a.kv.n_pages));
+      const bool v1 = (e1.state == 0) & (unsigned(e1.page) < unsigned(a.kv.n_pages));
+      if ((!v0 & (e0.state != 2)) | (!v1 & (e1.state != 2))) report(a.kv.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
       have = unsigned(v0) | unsigned(v1) << 1;
-      if (v0 && v1 && page_mask >= kTile - 1) {
+      if (v0 & v1 & (page_mask >= kTile - 1)) {
         copy(dst, row_of(e0), 0, 2);
       } else {  // (pages of 16: the second half's page begins where the tile's row 16 is)
         if (v0) copy(dst, row_of(e0), 0, 1);
@@ -477,8 +475,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     const uint8_t* kc = ring + stage * St::kBytes;
     const uint8_t* vc = kc + St::kHalf;
     const int k0 = gr.tiles.key0(t);
-    const bool whole = have == 3 && k0 + kTile - 1 <= gr.minpos &&
-                       (a.window == 0 || k0 > gr.maxpos - a.window || k0 + kTile <= a.sinks);
+    const bool whole = (have == 3) & (k0 + kTile - 1 <= gr.minpos) &
+                       ((a.window == 0) | (k0 > gr.maxpos - a.window) | (k0 + kTile <= a.sinks));
 
     if (!whole) {  // a slot that no row sees may hold anything: its zero probability needs a finite value
       const int key = k0 + lane;
