@@ -141,6 +141,10 @@ __device__ __forceinline__ Tiles tiles_of(int minpos, int maxpos, int window, in
 // 14.0 and 18.0; heads of 256, 600 keys, 11.3 and 17.2.)
 constexpr long long kWholeElements = 144 * 1024;
 constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
+// What beginning, merging and writing an item costs a CTA, in tiles: counted
+// in front of its tiles when units are dealt out. (64 ragged sequences, 512
+// items: CTAs with four items took 143 thousand cycles, with one 112.)
+constexpr int kItemCost = 10;
 
 struct FewArgs {
   AttnArgs a;
@@ -154,13 +158,14 @@ struct FewArgs {
   __device__ __forceinline__ int token(int row) const { return int((unsigned(row) * inv_group) >> 32); }
 };
 
-// A sequence as its items: `groups` per kv head, each with `tiles.n` units
-// (the sequence's tiles; a row group that sees fewer masks the rest).
+// A sequence as its items: `groups` per kv head, each with kItemCost +
+// `tiles.n` units (the sequence's tiles; a row group that sees fewer masks the
+// rest).
 struct SeqItems {
   SeqInfo s;
   int groups, rows;  // row groups of a kv head, rows of all of them
   Tiles tiles;
-  __device__ __forceinline__ long long units(int kv_heads) const { return (long long)groups * kv_heads * tiles.n; }
+  __device__ __forceinline__ long long units(int kv_heads) const { return (long long)groups * kv_heads * (kItemCost + tiles.n); }
 };
 __device__ __forceinline__ SeqItems items_of(const FewArgs& f, int b, int rows_per_group) {
   SeqItems q;
@@ -262,8 +267,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   uint8_t* ring = smem + C::kOffRing + warp * kStages * St::kBytes;
   const uint32_t ring_s = smem_u32(ring);
 
-  // this CTA's units: `left` of them from tile t_begin of item `item` of sequence b on
-  int b, item, t_begin;
+  // this CTA's units: `left` of them from unit `off` of item `item` of sequence b on
+  int b, item, off;
   long long left;
   SeqItems sq;
   if (f.whole) {
@@ -273,8 +278,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     sq = items_of(f, b, C::kRows);
     if (r >= sq.groups) return griddep_wait();
     item = h * sq.groups + r;
-    t_begin = 0;
-    left = sq.tiles.n;
+    off = 0;
+    left = kItemCost + sq.tiles.n;
   } else {
     Cut<kWarps * 32> cut(f, C::kRows, reinterpret_cast<long long*>(smem + C::kOffRing));
     if (int(blockIdx.x) >= cut.ctas) return griddep_wait();
@@ -284,19 +289,26 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     int at;  // (a sequence has at most 8 * 256 * 2^19 units)
     b = cut.find(begin, &at);
     sq = items_of(f, b, C::kRows);
-    item = at / sq.tiles.n;
-    t_begin = at - item * sq.tiles.n;
+    item = at / (kItemCost + sq.tiles.n);
+    off = at - item * (kItemCost + sq.tiles.n);
     __syncthreads();  // the prefix sums' place becomes the ring's
   }
   while (left > 0) {
   if (item >= sq.groups * a.kv.kv_heads) {  // the next sequence that has items (there is one: units are left)
-    item = t_begin = 0;
+    item = off = 0;
     do sq = items_of(f, ++b, C::kRows);
     while (sq.groups == 0);
   }
+  const int span = int(min((long long)(kItemCost + sq.tiles.n - off), left));
+  const int t_begin = max(0, off - kItemCost), t_end = off + span - kItemCost;
+  left -= span;
+  off = 0;
+  if (t_end <= t_begin) {  // none of its tiles
+    ++item;
+    continue;
+  }
   const SeqInfo si = sq.s;
   const int kvh = item / sq.groups, rg = item - kvh * sq.groups;
-  const int t_end = int(min((long long)sq.tiles.n, t_begin + left));
   struct {
     int n_rows, minpos, maxpos;
     Tiles tiles;
@@ -761,8 +773,6 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         }
       }
     }
-  left -= t_end - t_begin;
-  t_begin = 0;
   ++item;
   __syncthreads();  // the merge's place becomes the ring's again
   }
@@ -797,14 +807,14 @@ __device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_
   q.sq = items_of(f, b, rows_per_group);
   q.n_rows = min(q.sq.rows - q.rg * rows_per_group, rows_per_group);
   if (q.n_rows <= 0) return q;
-  // the item's first unit: those of the sequences before, then of the items before
+  // the units of the sequences before, then of the items before
   Cut<256> cut(f, rows_per_group, sums);
   long long u0 = 0;
   for (int c0 = 0; c0 <= b && f.a.kv.n_seqs > 1; c0 += 256) {
     const long long n = f.a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
     u0 += b < c0 + 256 ? (b > c0 ? sums[b - c0 - 1] : 0) : n;
   }
-  u0 += (long long)(q.kvh * q.sq.groups + q.rg) * q.sq.tiles.n;
+  u0 += (long long)(q.kvh * q.sq.groups + q.rg) * (kItemCost + q.sq.tiles.n) + kItemCost;  // its first tile
   q.p0 = cut.cta_of(u0);
   q.n = cut.cta_of(u0 + q.sq.tiles.n - 1) - q.p0 + 1;
   return q;
