@@ -1010,6 +1010,10 @@ size_t attention_few_workspace(const AttnArgs& a, int max_rows) {
   return p.part_rows * (size_t(a.kv.dim) + 1) * 4;
 }
 
+long long attention_few_items(const AttnArgs& a, int max_rows) {
+  return 1ll * plan(a, max_rows).row_groups * a.kv.kv_heads * a.kv.n_seqs;
+}
+
 cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside, const KvCall& c) {
   const FewPlan p = plan(a, max_rows);
   float* part = static_cast<float*>(ws);

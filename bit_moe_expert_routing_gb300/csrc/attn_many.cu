@@ -13,11 +13,13 @@
 //   many     S = Q K^T per 128-row tile and 128 keys into tensor memory, the
 //            softmax warps turn it into P (bf16, in S's place), O += P V with
 //            P read from tensor memory.
-//            The CTA that finishes a row tile's last part joins the parts.
+//            The CTA that finishes a row tile's last part joins the parts, if
+//            there are few; many parts of few row tiles are joined by
+//   combine  over all of the GPU.
 //
 // The cut: a unit is one row tile times one key tile. All units of all
-// sequences and kv heads are numbered row tile by row tile, and one CTA per SM
-// takes an equal, contiguous range, so that neither causal masks, ragged
+// sequences and kv heads are numbered row tile by row tile, and one CTA pair per two
+// SMs takes an equal, contiguous range, so that neither causal masks, ragged
 // lengths nor few row tiles leave SMs idle. A row tile that falls into several
 // ranges leaves fp32 partial outputs.
 //
@@ -49,6 +51,8 @@ constexpr int kBK = 128;                  // keys per tile
 constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
 constexpr int kDescs = 4;                 // segment descriptors in flight
+constexpr int kMinUnits = 4;              // of a pair. (Two kv heads of 128 dims, one sequence, 512 rows, us: 8000 keys
+                                          // 30.3, with at least 1 unit 35.5, 12 units 39.9; 1000 keys 25.5, 22.9, 29.4.)
 constexpr int kTileCost = 3;              // units added to every row tile: its set-up and output (1: 89 us, 3: 84.5 us
                                           // for a prompt of 4096 tokens)
 
@@ -110,6 +114,7 @@ struct ManyArgs {
   int max_row_tiles;
   int pairs;               // CTA pairs of the many kernel
   int* arrived;            // [pairs][2] parts written of the row tile whose first part is the pair's, per CTA
+  bool join;               // the kernel joins the parts (else the combine kernel does)
   float* part_o;           // [2 pairs][2][rows][DIM]: two slots per pair, each CTA's rows
   float* part_lse;         // [2 pairs][2][rows], base 2
   unsigned long long inv_group;  // ceil(2^32 / group): row / group for rows below 2^26
@@ -222,9 +227,10 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
     m.plan->row_tiles = int(n_rt);
   }
   __syncthreads();
-  const long long all = units * m.nh;
+  // Pairs that get units: none fewer than kMinUnits, unless there are fewer in all.
+  const long long all = units * m.nh, used = max(1ll, min((long long)m.pairs, all / kMinUnits));
   for (int c = threadIdx.x; c <= m.pairs; c += kPlanThreads) {
-    const long long begin = all * c / m.pairs;
+    const long long begin = all * min((long long)c, used) / used;
     PairRange r{begin, 0, 0};
     if (begin < all) {
       r.head = int(begin / units);
@@ -872,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       cp_async_arrive_noinc(qfull);
       produce(sg + 1);  // the next one, while this one's rows are used
       if (warp == kWarpLoad + 1 && lane == 0) {
-        if (mine.part >= 0) infos[sg % kDescs] = part_info(m, mine);
+        if (mine.part >= 0 && m.join) infos[sg % kDescs] = part_info(m, mine);
         mbar_arrive(info_bar(sg));
       }
       __syncwarp();
@@ -1089,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(ofree);
-      if (s.part >= 0) {
+      if (s.part >= 0 && m.join) {
         // the part is written; whoever completes the count joins all parts of this CTA's rows, in the order of the pairs
         __threadfence();
         int* last = reinterpret_cast<int*>(gbase + C::kOffMisc + 8);
@@ -1175,6 +1181,86 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   }
 }
 
+// Joins the parts of divided row tiles: out = sum_p 2^(lse_p - max) o_p /
+// sum_p 2^(lse_p - max). CTA (row tile, eight of its rows, kv head), a warp per
+// row, several parts' loads in flight.
+template <int DIM>
+__global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
+  griddep_wait();
+  constexpr int kRows = ManyCfg<DIM>::kRows, kV = DIM / 128 + (DIM < 128);
+  constexpr int kBatch = DIM == 256 ? 4 : 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = blockIdx.x, head = blockIdx.z, pr = blockIdx.y * 8 + warp;  // row of the pair
+  if (rt >= m.plan->row_tiles) return;
+  const RowTile t = m.row_tile[rt];
+  const int last = t.n_new * m.a.group - 1, rr = t.row0 + pr;
+  if (rr > last) return;
+  const long long units = m.plan->units, u0 = head * units + m.unit_off[rt], u1 = head * units + m.unit_off[rt + 1];
+  // the pair that holds the first key tile: the last one whose units begin at or before it
+  int lo = 0, hi = m.pairs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (m.range[mid].begin <= u0 + kTileCost)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int c0 = lo;
+  if (m.range[c0 + 1].begin >= u1) return;  // one pair has all of it, and wrote the output
+  int c1 = c0 + 1;
+  hi = m.pairs - 1;  // the last pair with a unit before u1
+  while (c1 < hi) {
+    const int mid = (c1 + hi + 1) >> 1;
+    if (m.range[mid].begin < u1)
+      c1 = mid;
+    else
+      hi = mid - 1;
+  }
+  const int parts = c1 - c0 + 1, rank = pr / kRows, r = pr % kRows;
+  // part p is pair c0 + p's: in its slot 1 if it begins inside the row tile, as all but the first do
+  auto at = [&](int p) { return (2 * (2ll * (c0 + p) + (p > 0)) + rank) * kRows + r; };
+  float top = -INFINITY;
+  for (int p = lane; p < parts; p += 32) top = fmaxf(top, m.part_lse[at(p)]);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float4 o[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = DIM >= 128 || lane < DIM / 4;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const int some = min(32, parts - p0);
+    const float w = lane < some ? ex2(m.part_lse[at(p0 + lane)] - ref) : 0.f;
+    for (int p = 0; p < some; p += kBatch) {
+      float4 v[kBatch][kV];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+          v[i][k] = mine && p + i < some ? reinterpret_cast<const float4*>(m.part_o + at(p0 + p + i) * DIM)[lane + 32 * k]
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float wi = __shfl_sync(~0u, w, p + i);
+        sum += wi;
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+          o[k].x += wi * v[i][k].x, o[k].y += wi * v[i][k].y, o[k].z += wi * v[i][k].z, o[k].w += wi * v[i][k].w;
+      }
+    }
+  }
+  const int tok = m.token(rr);
+  const long long dst = (long long)(t.first + tok) * m.a.heads + (m.h0 + head) * m.a.group + rr - tok * m.a.group;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  if (mine)
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+      *reinterpret_cast<uint2*>(m.a.out + dst * DIM + 4 * (lane + 32 * k)) =
+          make_uint2(pack2(o[k].x * inv, o[k].y * inv), pack2(o[k].z * inv, o[k].w * inv));
+  if (lane == 0 && m.a.lse) m.a.lse[dst] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
 // ---- host ---------------------------------------------------------------------------------
 
 // Expanded tiles of one pass take at most this, if one sequence's kv head
@@ -1223,8 +1309,8 @@ ManyPlan plan(const AttnArgs& a) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(const KvCall& c, const char* name, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
-                             Args&&... args) {
+cudaError_t launch_beside(const KvCall& c, const char* name, void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
+                          int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
@@ -1234,7 +1320,7 @@ cudaError_t launch_pairs(const KvCall& c, const char* name, void (*kernel)(KArgs
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -1254,8 +1340,13 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
       attention_expand_kernel<DIM><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
       if (cudaError_t e = c.launched("attention_expand")) return e;
-      if (cudaError_t e = launch_pairs(c, "attention_many", attention_many_kernel<DIM>, dim3(2 * p.pairs), kThreads, C::kSmem, m))
+      if (cudaError_t e = launch_beside(c, "attention_many", attention_many_kernel<DIM>, dim3(2 * p.pairs), kThreads,
+                                        C::kSmem, 2, m))
         return e;
+      if (!m.join)
+        if (cudaError_t e = launch_beside(c, "attention_many_combine", attention_many_combine_kernel<DIM>,
+                                          dim3(p.max_row_tiles, C::kPairRows / 8, m.nh), 256, 0, 1, m))
+          return e;
     }
   return cudaSuccess;
 }
@@ -1280,6 +1371,14 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.range = reinterpret_cast<PairRange*>(w + p.range);
   m.max_row_tiles = p.max_row_tiles;
   m.pairs = p.pairs;
+  // Parts of a row tile are about pairs / row tiles. Up to two are joined in
+  // the kernel, by the CTA that writes the last; more of them by the combine
+  // kernel, over all of the GPU. Combined against joined in the kernel, us, 16
+  // heads over 2 kv heads of 128 dims, one sequence: 4 row tiles over 8000 keys
+  // (19 parts each) 33 and 80, 32 of them 77 and 81, 64 of them 140 and 133;
+  // the 128 row tiles of a prompt of 4096 94 and 80.
+  const long long row_tiles = std::max(1ll, (long long)a.kv.n_tokens * a.group / p.rows) * a.kv.kv_heads;
+  m.join = row_tiles * 2 >= p.pairs;
   m.arrived = reinterpret_cast<int*>(w + p.arrived);
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);

@@ -97,6 +97,7 @@ cudaError_t kv_append(const KvArgs& a, const uint16_t* k, long long ks, const ui
 cudaError_t kv_read(const KvArgs& a, uint16_t* k, uint16_t* v, const KvCall& c);
 // Sequences with at most max_rows rows (step tokens x query heads per kv head).
 size_t attention_few_workspace(const AttnArgs& a, int max_rows);
+long long attention_few_items(const AttnArgs& a, int max_rows);  // (sequence, kv head, group of rows), at most
 // `beside`: launched behind the many-row kernels of the same call, on other
 // sequences and another part of the workspace, so it does not wait for them.
 cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside, const KvCall& c);

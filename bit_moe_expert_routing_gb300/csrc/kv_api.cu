@@ -1,5 +1,6 @@
 // C entry points of the 4-bit key/value cache and its attention: argument
 // checks on the host and the choice of kernels.
+#include <algorithm>
 #include <cmath>
 
 #include "kv.cuh"
@@ -56,21 +57,46 @@ moe_status check_attention(const KvArgs& kv, const moe_attention* a) {
 }
 
 // Sequences with at most this many rows (step tokens x query heads per kv
-// head) take the few-row kernel.
-constexpr int kFewRows = 64;
+// head) take the few-row kernel. (One number for a call: the kernels ask it of
+// every sequence.)
+//
+// The few-row kernel expands the codes again for every 32 rows (16 of 256
+// dims); the many-row path expands them once, ahead, and then works in tiles
+// of 512 rows (256), mostly empty below that: measured, 8 query heads per kv
+// head of 128 dims, 2 kv heads, one sequence of 64000 keys, 64 rows 25 us few
+// and 66 many, 128 rows 40 and 67, 256 rows 68 and 67; of 256 dims, 64 rows 57
+// and 83, 128 rows 98 and 86. So 128 rows, 64 of 256 dims.
+//
+// With more rows the few-row kernel still wins as long as its items are at
+// most two CTAs' worth per SM and their products few: the many-row path's
+// launches and set-up take longer than the work. Few against many, us, 128
+// dims: one sequence, 1024 rows over no context 9 and 16, over 1000 keys 19
+// and 26, over 8000 keys (2^31 products) 44 and 33; 8 sequences, 256 rows over
+// 1000 keys (2^29) 19 and 29, over 8000 keys (2^32) 74 and 59. Over 265 sizes
+// this choice is 0.3% slower than the better kernel on average, at most 27%.
+int few_rows(const AttnArgs& a, const Options& o) {
+  constexpr int kAny = 1 << 30;
+  if (o.force_path) return o.force_path == 1 ? kAny : 0;
+  long long keys = a.kv.max_kv;
+  if (a.window > 0) keys = std::min(keys, (long long)a.window + a.sinks + a.kv.max_new);
+  const double products = double(keys) * a.kv.n_tokens * a.heads * a.kv.dim * (a.kv.dim == 256 ? 2 : 1);
+  if (products <= double(1 << 30) && attention_few_items(a, kAny) <= 2 * num_sms()) return kAny;
+  return a.kv.dim == 256 ? 64 : 128;
+}
 
-bool any_many(const AttnArgs& a) { return (long long)a.kv.max_new * a.group > kFewRows; }
+bool any_many(const AttnArgs& a, int few) { return (long long)a.kv.max_new * a.group > few; }
 
 // Whether a sequence may have so few; when the step's tokens are max_new for
 // every sequence, all are alike.
-bool any_few(const AttnArgs& a) {
-  return !any_many(a) || (long long)a.kv.n_seqs * a.kv.max_new != a.kv.n_tokens;
+bool any_few(const AttnArgs& a, int few) {
+  return few > 0 && (!any_many(a, few) || (long long)a.kv.n_seqs * a.kv.max_new != a.kv.n_tokens);
 }
 
 // The few-row kernels' part of the workspace, before the many-row kernels'
-// (both are used when a step has sequences of both kinds).
-size_t few_bytes(const AttnArgs& a) {
-  return any_few(a) ? (attention_few_workspace(a, kFewRows) + 255) & ~size_t(255) : 0;
+// (both are used when a step has sequences of both kinds; always there, so
+// that no smaller step needs more).
+size_t few_bytes(const AttnArgs& a, int few) {
+  return (attention_few_workspace(a, few) + 255) & ~size_t(255);
 }
 
 AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
@@ -122,7 +148,8 @@ size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batc
   KvArgs a;
   if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
   const AttnArgs g = attn_args(a, at);
-  return ((few_bytes(g) + (any_many(g) ? attention_many_workspace(g) : 0)) + 511) & ~size_t(255);
+  const int few = few_rows(g, options_snapshot());
+  return ((few_bytes(g, few) + (any_many(g, few) ? attention_many_workspace(g) : 0)) + 511) & ~size_t(255);
 }
 
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
@@ -143,10 +170,11 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   g.out = out;
   g.lse = lse;
   const KvCall c = begin_call(stream);
-  const bool many = any_many(g);
+  const int few = few_rows(g, c.opt);
+  const bool many = any_many(g, few);
   if (many)
-    if (cudaError_t e = attention_many(g, kFewRows, static_cast<char*>(workspace) + few_bytes(g), c)) return status_of(e);
-  return any_few(g) ? status_of(attention_few(g, kFewRows, workspace, many, c)) : MOE_OK;
+    if (cudaError_t e = attention_many(g, few, static_cast<char*>(workspace) + few_bytes(g, few), c)) return status_of(e);
+  return any_few(g, few) ? status_of(attention_few(g, few, workspace, many, c)) : MOE_OK;
 }
 
 }  // extern "C"

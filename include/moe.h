@@ -122,7 +122,9 @@ typedef enum {
                                 on the D=2048, E=256, k=8, I=512 layer the one-launch
                                 item kernel measured faster than the grouped GEMM at
                                 2, 3 and 4 rows, and slower at 5 and 8) */
-  MOE_OPT_FORCE_PATH = 2,    /* 0 auto by row count, 1 GEMV, 2 grouped GEMM */
+  MOE_OPT_FORCE_PATH = 2,    /* 0 auto by row count, 1 GEMV, 2 grouped GEMM; and of the
+                                attention: 0 auto by the step's sizes, 1 the few-row
+                                kernel, 2 the many-row kernels */
   MOE_OPT_KERNEL_TIMING = 3, /* 1: record CUDA events around each kernel of
                                 the next forwards (read with moe_kernel_times) */
   MOE_OPT_GEMM_IMPL = 4,     /* grouped GEMM used above the GEMV threshold:

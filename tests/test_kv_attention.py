@@ -149,6 +149,13 @@ def test_padding_and_missing_pages():
 
 # --- attention ---------------------------------------------------------------------------------
 
+@pytest.fixture
+def forced():
+    """Sets which kernels take the attention (0: by the sequences' sizes, 1: few rows, 2: many rows)."""
+    yield lambda path: moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, path)
+    moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, 0)
+
+
 def run_attention(heads, kv_heads, dim, page, new, kv, window=0, sinks=0, scale=None, spread=1.0, seed=0, q=None,
                   max_new=None, max_kv=None, outliers=False):
     batch = Batch(new, kv, page, seed=seed)
@@ -157,11 +164,18 @@ def run_attention(heads, kv_heads, dim, page, new, kv, window=0, sinks=0, scale=
     if q is None:
         q = rows(batch.n_tokens, heads, dim, seed + 2)
     dev = batch.device(moe, max_new, max_kv)
-    out, lse = cache.attention(q, dev, scale=scale, window=window, sinks=sinks, lse=True)
-    cache.check()
     s = dim ** -0.5 if scale is None else scale
     s = float(np.float32(s))
-    check_attention(out, lse, attention_reference(q, batch, keys, vals, s, window, sinks))
+    ref = attention_reference(q, batch, keys, vals, s, window, sinks)
+    was = moe.moe_get_option(moe.MOE_OPT_FORCE_PATH)
+    try:
+        for path in [was] if was else [1, 2, 0]:  # each size through both kernels, and as it is dispatched
+            moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, path)
+            out, lse = cache.attention(q, dev, scale=scale, window=window, sinks=sinks, lse=True)
+            cache.check()
+            check_attention(out, lse, ref, path)
+    finally:
+        moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, was)
     return batch, cache, dev, q, out, lse
 
 
@@ -234,10 +248,12 @@ def test_rows_that_see_nothing_give_zero(dim, new, kv):
     assert (lse == -math.inf).any()
 
 
+@pytest.mark.parametrize("path", [0, 1, 2])
 @pytest.mark.parametrize("new,kv", [([1, 1], [100, 37]), ([3, 2], [100, 37]), ([150, 90], [150, 300])])
-def test_masked_places_and_other_rows_do_not_leak(new, kv):
+def test_masked_places_and_other_rows_do_not_leak(new, kv, path, forced):
     """Slots past a sequence's end hold NaN and infinities (junk_cache), a query row of NaN or infinities spoils its
     own output alone, and bounds above the lengths change nothing."""
+    forced(path)
     heads, dim = 8, 128
     batch, cache, dev, q, out, lse = run_attention(heads, 2, dim, 16, new, kv)
     bad = q.clone()
@@ -251,8 +267,10 @@ def test_masked_places_and_other_rows_do_not_leak(new, kv):
     run_attention(heads, 2, dim, 16, new, kv, max_new=max(new) + 1, max_kv=5000)
 
 
+@pytest.mark.parametrize("path", [0, 1, 2])
 @pytest.mark.parametrize("new,kv", [([1, 1], [3000, 37]), ([4], [900]), ([150], [700])])
-def test_attention_is_repeatable_and_takes_strided_queries(new, kv):
+def test_attention_is_repeatable_and_takes_strided_queries(new, kv, path, forced):
+    forced(path)
     batch, cache, dev, q, out, lse = run_attention(8, 2, 128, 32, new, kv)
     for _ in range(3):
         o, l = cache.attention(q, dev, lse=True)
@@ -287,8 +305,10 @@ def test_attention_on_another_stream_and_in_a_graph():
     assert torch.equal(static, out)
 
 
+@pytest.mark.parametrize("path", [0, 1, 2])
 @pytest.mark.parametrize("new,kv", [([1, 1], [100, 300]), ([2], [300]), ([140], [300])])
-def test_a_missing_page_is_recorded_and_left_out(new, kv):
+def test_a_missing_page_is_recorded_and_left_out(new, kv, path, forced):
+    forced(path)
     batch = Batch(new, kv, 16)
     cache = junk_cache(moe, batch.n_pages, 16, 2, 64)
     keys, vals = fill(cache, batch)
