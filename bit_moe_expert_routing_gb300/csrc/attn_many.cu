@@ -58,23 +58,23 @@ constexpr int kTileCost = 3;              // units added to every row tile: its 
 
 template <int DIM>
 struct ManyCfg {
-  static constexpr int QT = DIM == 256 ? 1 : 2;
+  static constexpr int QT = DIM == 64 ? 2 : 1;
   static constexpr int kRows = 128 * QT;  // of a CTA
   static constexpr int kPairRows = 2 * kRows;
   static constexpr int UN = DIM / 64;     // blocks of 64 dims
   static constexpr uint32_t kSlot = 128u * DIM;  // half a key or value tile: what one CTA of the pair keeps
   static constexpr uint32_t kTileBytes = 2 * kSlot;
-  static constexpr int kRing = DIM == 64 ? 12 : DIM == 128 ? 9 : 4;
+  static constexpr int kRing = DIM == 64 ? 12 : DIM == 128 ? 11 : 4;
   static constexpr uint32_t kQTile = 128 * DIM * 2;
-  // DIM 64: P has tensor memory of its own, and a softmax warpgroup takes a
-  // row tile; else P takes S's place, and both take half of each S tile's keys
-  static constexpr bool kOwnP = DIM == 64;
+  static constexpr bool kOwnP = DIM <= 128;    // P has tensor memory of its own; else it takes S's place
+  // The softmax's two warpgroups take: DIM 64 a row tile each; 128 S tiles in turn; 256 half of the keys of each S tile.
+  static constexpr bool kTurns = DIM == 128, kHalves = DIM == 256;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffRing = QT * kQTile;
-  static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: row maxima of the halves
-  static constexpr uint32_t kOffBar = kOffEx + 2 * 2 * 128 * 4;
-  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [QT]; dfull, dempty, info [kDescs]
-  static constexpr int kBars = 3 * kRing + 5 + 6 + QT + 3 * kDescs;
+  static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: exchanged between the warpgroups; [128]: reference maxima
+  static constexpr uint32_t kOffBar = kOffEx + (2 * 2 + 1) * 128 * 4;
+  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [4]; dfull, dempty, info [kDescs]
+  static constexpr int kBars = 3 * kRing + 5 + 10 + 3 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t kOffInfo = kOffDesc + kDescs * 80;
   static constexpr uint32_t kOffMisc = kOffInfo + kDescs * 16;
@@ -645,6 +645,14 @@ __device__ __forceinline__ PartInfo part_info(const ManyArgs& m, const Segment& 
   return p;
 }
 
+// Keeps registers that a store to tensor memory may still be reading.
+__device__ __forceinline__ void keep(const uint32_t (&p)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    asm volatile("" ::"r"(p[e]), "r"(p[e + 1]), "r"(p[e + 2]), "r"(p[e + 3]), "r"(p[e + 4]), "r"(p[e + 5]), "r"(p[e + 6]),
+                 "r"(p[e + 7]));
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
@@ -657,8 +665,8 @@ template <int DIM>
 __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
   using C = ManyCfg<DIM>;
   constexpr int QT = C::QT, UN = C::UN, kRing = C::kRing;
-  constexpr bool kOwnP = C::kOwnP;
-  constexpr int kArrive = kOwnP ? kSoftWarps / 2 : kSoftWarps;  // softmax warps of an S tile, per CTA
+  constexpr bool kOwnP = C::kOwnP, kHalves = C::kHalves, kTurns = C::kTurns;
+  constexpr int kArrive = kHalves ? kSoftWarps : kSoftWarps / 2;  // softmax warps of an S tile, per CTA
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -672,11 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   auto sfull = [&](uint32_t s) { return qfull + 40 + 8u * s; };
   auto pready = [&](uint32_t s) { return qfull + 56 + 8u * s; };
   auto sread = [&](uint32_t s) { return qfull + 72 + 8u * s; };  // kOwnP: S has been read
-  auto pvdone = [&](uint32_t q) { return qfull + 88 + 8u * q; };
-  auto dfull = [&](uint32_t i) { return qfull + 88 + 8u * (QT + i % kDescs); };
-  auto dempty = [&](uint32_t i) { return qfull + 88 + 8u * (QT + kDescs + i % kDescs); };
+  auto pvdone = [&](uint32_t g) { return qfull + 88 + 8u * (g & 3u); };  // of S tile g; phase g / 4
+  auto dfull = [&](uint32_t i) { return qfull + 88 + 8u * (4 + i % kDescs); };
+  auto dempty = [&](uint32_t i) { return qfull + 88 + 8u * (4 + kDescs + i % kDescs); };
   const bool first_cta = (blockIdx.x & 1) == 0;
-  auto info_bar = [&](uint32_t i) { return qfull + 88 + 8u * (QT + 2 * kDescs + i % kDescs); };
+  auto info_bar = [&](uint32_t i) { return qfull + 88 + 8u * (4 + 2 * kDescs + i % kDescs); };
   Segment* descs = reinterpret_cast<Segment*>(gbase + C::kOffDesc);
   PartInfo* infos = reinterpret_cast<PartInfo*>(gbase + C::kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     mbar_init(ofree, 2 * kSoftWarps);
     for (int i = 0; i < kDescs; ++i) mbar_init(dfull(i), 1), mbar_init(dempty(i), kSoftWarps + 2 + kLoadWarps), mbar_init(info_bar(i), 1);
     for (int s = 0; s < 2; ++s) mbar_init(sfull(s), 1), mbar_init(pready(s), 2 * kArrive), mbar_init(sread(s), 2 * kArrive);
-    for (int q = 0; q < QT; ++q) mbar_init(pvdone(q), 1);
+    for (int g = 0; g < 4; ++g) mbar_init(pvdone(g), 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -711,12 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   griddep_wait();
   griddep_launch();
 
-  // Ring position of key tile i and value tile i of a segment of n tiles, in
-  // the order of their first use: K0 V0 K1 V1 ... with two row tiles; K0 K1 V0
-  // K2 V1 ... with one, or where P has its own place (S runs a tile ahead).
-  constexpr bool kKeysAhead = QT == 1 || kOwnP;
-  auto k_at = [](int i) { return !kKeysAhead ? 2 * i : i == 0 ? 0 : 2 * i - 1; };
-  auto v_at = [](int i, int n) { return !kKeysAhead ? 2 * i + 1 : i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+  // Ring position of key tile i and value tile i of a segment of n tiles: K0 K1
+  // V0 K2 V1 ... (S runs a tile ahead, or two).
+  auto k_at = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+  auto v_at = [](int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
 
   // Segment i, once its descriptor is there; every reader arrives on dempty(i) when it needs it no more.
   auto descriptor = [&](uint32_t i, Segment* s, bool& ok) {
@@ -741,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const int n = s.j1 - s.j0;
         for (int p = 0; p < 2 * n && ok; ++p) {
           // which tile has ring position p
-          const bool is_v = !kKeysAhead ? (p & 1) : p == 2 * n - 1 || (p >= 2 && !(p & 1));
-          const int i = !kKeysAhead ? p / 2 : is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
+          const bool is_v = p == 2 * n - 1 || (p >= 2 && !(p & 1));
+          const int i = is_v ? (p == 2 * n - 1 ? n - 1 : p / 2 - 1) : (p + 1) / 2;
           const uint8_t* src = (is_v ? m.vx : m.kx) + (tile0 + s.index(s.j0 + i)) * C::kTileBytes + (first_cta ? 0 : C::kSlot);
           const uint32_t slot = it % kRing;
           if (!(ok = mbar_wait(empty(slot), ((it / kRing) & 1u) ^ 1u, abort_flag, hdr, kWaitLimit, false, 220))) break;
@@ -807,23 +813,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         };
         auto pv = [&](int x) {  // O of row tile x % QT += P(x) V
           const int q = x % QT, i = x / QT;
-          const uint32_t p = kOwnP ? tmem + 384 + q * 64 : tmem + ((g0 + x) & 1u) * 128, o = tmem + 256 + q * DIM;
+          const uint32_t sl = (g0 + x) & 1u, p = kOwnP ? tmem + 384 + sl * 64 : tmem + sl * 128, o = tmem + 256 + q * DIM;
           const uint32_t seq = ring + v_at(i, n), vb = base + C::kOffRing + seq % kRing * C::kSlot;
           if (q == 0 && !wait_slot(seq)) return;
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) umma4_ts(o, p + kb * 32, desc_lo(vb + kb * (DIM * 64)), kIdO, i > 0 || kb > 0);
           if (q == QT - 1) umma_commit(empty(seq % kRing));
-          umma_commit(pvdone(q));
+          umma_commit(pvdone(g0 + x));
         };
         qk(0);
         if (ok && total > 1) qk(1);
+        // kOwnP: once S tile y has been read, S(y + 2) takes its slot. That is before P(y - 1) is there: the warpgroup
+        // that reads S(y) has had P(y - 2) behind it.
+        auto follow = [&](int y) {
+          if (y >= total || !wait(sread((g0 + y) & 1u), ((g0 + y) >> 1) & 1u, 237)) return;
+          if (y + 2 < total) qk(y + 2);
+        };
+        if (kOwnP && ok) follow(0);
         for (int x = 0; x < total && ok; ++x) {
           const uint32_t g = g0 + x;
-          if (kOwnP) {
-            if (!wait(sread(g & 1u), (g >> 1) & 1u, 237)) break;
-            if (x + 2 < total) qk(x + 2);
-            if (!ok) break;
-          }
+          if (kOwnP) follow(x + 1);
+          if (!ok) break;
           if (!wait(pready(g & 1u), (g >> 1) & 1u, 224)) break;
           if (x == 0 && sg > 0 && !wait(ofree, (sg - 1) & 1u, 230)) break;
           pv(x);
@@ -889,34 +899,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: eight warps ----------------
-    // Where P has its own place: four warps per row tile, a thread per row with all 128 keys, so that one tile's loads
-    // and maxima run beside the other's exponentials. Else two threads per row with 64 keys each, which halves the time
-    // between S and P, with the slot's products waiting; they exchange maxima.
-    constexpr bool kHalves = !kOwnP;
-    constexpr int NQ = kHalves ? QT : 1;  // row tiles of a warp
-    constexpr int kCols = kHalves ? 64 : 128, kOCols = kHalves ? DIM / 2 : DIM;  // of a thread: keys of an S tile, dims of O
-    const int wg = warp >> 2, half = kHalves ? wg : 0, row = (warp & 3) * 32 + lane;
+    // Heads of 64 and 128: a thread has a row of an S tile, and one warpgroup's loads and maxima run beside the other's
+    // exponentials. Heads of 64: a row tile each. Heads of 128: the S tiles of one row tile in turn; the reference
+    // maximum is the row's, in shared memory, and handed on from tile to tile. Heads of 256: two threads per row with 64
+    // keys each, which halves the time between S and P, with the slot's products waiting; they exchange maxima.
+    constexpr int kCols = kHalves ? 64 : 128;       // keys of an S tile per thread
+    constexpr int kScale = kHalves ? DIM / 2 : DIM;  // dims of O that a thread rescales
+    constexpr int kOCols = QT == 1 ? DIM / 2 : DIM;  // dims of O that it writes
+    const int wg = warp >> 2, half = kHalves ? wg : 0, ohalf = QT == 1 ? wg : 0, q = QT == 1 ? 0 : wg;
+    const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;  // the tensor-memory lanes this warp may access
     float* ex = reinterpret_cast<float*>(gbase + C::kOffEx);
     // |scale| in base 2 (the keys carry the sign; for scale 0 they are zeros)
     const float c2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;  // rows are multiples of 128 bytes
     Segment s;
-    uint32_t g0 = 0, pv0 = 0, exn = 0;  // before this segment: S tiles, products O += P V per row tile, exchanges
+    uint32_t g0 = 0, exn = 0;  // S tiles before this segment, exchanges
     // After a failed wait a warp keeps going without waiting, so that the
     // others never hang in a barrier; the status says that the output is void.
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, int site) {
       if (ok) ok = mbar_wait(bar, parity, abort_flag, hdr, kWaitLimit, false, site);
     };
-    // the other half's value of this row
+    // the other half's value of this row (the two warps that hold it wait for each other)
     auto exchange = [&](float v) {
       float* e = ex + (exn & 1u) * 256;
       ++exn;
-      e[half * 128 + row] = v;
-      asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
-      return e[(half ^ 1) * 128 + row];
+      e[wg * 128 + row] = v;
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory");
+      return e[(wg ^ 1) * 128 + row];
     };
+    // kTurns: the rows' reference maxima, read and written between take_turn and pass_turn
+    float* refs = ex + 2 * 256;
+    auto take_turn = [&] { asm volatile("bar.sync %0, 64;" ::"r"(6 + (warp ^ 4)) : "memory"); };
+    auto pass_turn = [&] { asm volatile("bar.arrive %0, 64;" ::"r"(6 + warp) : "memory"); };
+    auto wait_product = [&](uint32_t g, int site) { wait(pvdone(g), (g >> 2) & 1u, site); };
     for (uint32_t sg = 0;; ++sg) {
       // The eight warps agree on whether there is a segment: after a failed wait the flag has them all leave here.
       int more = descriptor(sg, &s, ok);
@@ -928,33 +945,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           : "memory");
       if (!more) break;
       if (lane == 0) mbar_arrive(dempty(sg));
-      float ref[NQ], sum[NQ];
-      int pos[NQ], minpos[NQ], maxpos[NQ];
-#pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        ref[k] = -INFINITY, sum[k] = 0.f;
-        const int r0 = s.row0 + (kHalves ? k : wg) * 128;
-        pos[k] = s.base_pos + m.token(min(r0 + row, s.last));
-        minpos[k] = s.base_pos + m.token(min(r0, s.last)), maxpos[k] = s.base_pos + m.token(min(r0 + 127, s.last));
-      }
+      float ref = -INFINITY, sum = 0.f;
+      const int r0 = s.row0 + q * 128;
+      const int pos = s.base_pos + m.token(min(r0 + row, s.last));
+      const int minpos = s.base_pos + m.token(min(r0, s.last)), maxpos = s.base_pos + m.token(min(r0 + 127, s.last));
       const int n = s.j1 - s.j0;
       const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
-      unsigned bad_next = bad[s.index(s.j0)];
-      for (int i = 0; i < n; ++i) {
-        const int k0 = s.tile(s.j0 + i) * kBK;
-        const unsigned missing = bad_next;
-        if (i + 1 < n) bad_next = bad[s.index(s.j0 + i + 1)];
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-        const int q = kHalves ? k : wg;
-        const uint32_t g = g0 + i * QT + q;
-        const uint32_t sl = tmem + lanes + (g & 1u) * 128;
-        const uint32_t pl = kOwnP ? tmem + lanes + 384 + q * 64 : sl, ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
+      const int first = kTurns ? (wg ^ g0) & 1 : 0;  // of this warpgroup's tiles
+      constexpr int kStep = kTurns ? 2 : 1;
+      unsigned bad_next = first < n ? bad[s.index(s.j0 + first)] : 0;
+      // S tile g's scores, on their way when this returns
+      uint32_t v[kCols];
+      auto load = [&](uint32_t g) {
         wait(sfull(g & 1u), (g >> 1) & 1u, 226);
         tc_fence_after();
-        uint32_t v[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) tmem_ld32(sl + half * 64 + c, v + c);
+        for (int c = 0; c < kCols; c += 32) tmem_ld32(tmem + lanes + (g & 1u) * 128 + half * 64 + c, v + c);
+      };
+      for (int i = first; i < n; i += kStep) {
+        const int k0 = s.tile(s.j0 + i) * kBK;
+        const unsigned missing = bad_next;
+        if (i + kStep < n) bad_next = bad[s.index(s.j0 + i + kStep)];
+        const uint32_t g = g0 + i * QT + q, gl = g - QT;  // and the last one before it into the same output
+        const uint32_t pl = tmem + lanes + (kOwnP ? 384 + (g & 1u) * 64 : (g & 1u) * 128);
+        const uint32_t ocol = tmem + lanes + 256 + q * DIM + half * kScale;
+        load(g);
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) tmem_wait_ld32(v + c);
         if (kOwnP) {
@@ -962,16 +977,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           __syncwarp();
           if (lane == 0) arrive_first(sread(g & 1u));
         }
-        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos[k] &&
-                           (a.window == 0 || k0 > maxpos[k] - a.window || k0 + kBK <= a.sinks);
+        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos &&
+                           (a.window == 0 || k0 > maxpos - a.window || k0 + kBK <= a.sinks);
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 64) {
             // bit e: this row sees key kb + e, from the interval (or the sinks) that it sees
             const int h = kHalves ? half : c / 64, kb = k0 + h * 64;
             auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };  // bits under x
-            uint64_t sees = below(pos[k] + 1 - kb);
-            if (a.window > 0) sees &= ~below(pos[k] - a.window + 1 - kb) | below(a.sinks - kb);
+            uint64_t sees = below(pos + 1 - kb);
+            if (a.window > 0) sees &= ~below(pos - a.window + 1 - kb) | below(a.sinks - kb);
 #pragma unroll
             for (int i16 = 0; i16 < 4; ++i16)
               if ((missing >> (h * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));
@@ -990,36 +1005,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
         for (int e = 0; e < kCols; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (kHalves) top = fmaxf(top, exchange(top));
-        top *= c2;
         // the reference maximum moves only when a score passes it by 2^8: probabilities are floating point, so
         // nothing is lost, and the output is hardly ever rescaled
-        if (__any_sync(~0u, top > ref[k] + 8.f)) {
-          const float to = fmaxf(ref[k], top);
-          const float al = to == -INFINITY ? 1.f : ex2(ref[k] - to);
-          ref[k] = to;
-          sum[k] *= al;
-          if (i > 0) {
-            wait(pvdone(q), (pv0 + i - 1) & 1u, 227);
-            tc_fence_after();
+        if (kHalves) top = fmaxf(top, exchange(top));
+        if (kTurns) {
+          if (g > 0) take_turn();
+          const float now = i > 0 ? refs[row] : -INFINITY;
+          if (now != ref) sum *= ex2(ref - now), ref = now;
+        }
+        const bool grew = __any_sync(~0u, top * c2 > ref + 8.f);
+        float al = 1.f;
+        if (grew) {
+          const float to = fmaxf(ref, top * c2);
+          al = to == -INFINITY ? 1.f : ex2(ref - to);
+          ref = to;
+          sum *= al;
+        }
+        if (kTurns) {
+          if (grew || i == 0) refs[row] = ref;
+          __syncwarp();
+          pass_turn();
+        }
+        if (grew && i > 0) {
+          wait_product(gl, 227);
+          tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < kOCols; cc += 16) {
-              uint32_t o[16];
-              tmem_ld16(ocol + cc, o);
-              tmem_wait_ld16(o);
+          for (int cc = 0; cc < kScale; cc += 16) {
+            uint32_t o[16];
+            tmem_ld16(ocol + cc, o);
+            tmem_wait_ld16(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-              tmem_st16(ocol + cc, o);
-              tmem_wait_st();
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            tmem_st16(ocol + cc, o);
+            tmem_wait_st();
           }
         }
-        const float r = ref[k] == -INFINITY ? 0.f : ref[k];
+        const float r = ref == -INFINITY ? 0.f : ref;
         const float2 c22 = make_float2(c2, c2), r22 = make_float2(-r, -r);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t p[32];
 #pragma unroll
         for (int c = 0; c < kCols; c += 64) {
-          uint32_t p[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             float2 x = __ffma2_rn(make_float2(__uint_as_float(v[c + 2 * e]), __uint_as_float(v[c + 2 * e + 1])), c22, r22);
@@ -1027,32 +1053,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             acc[e & 1] = __fadd2_rn(acc[e & 1], x);
             p[e] = pack2(x.x, x.y);
           }
-          // (P's own place is free once the product of the tile before has read it)
-          if (kOwnP && c == 0 && i > 0) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+          if (c == 0) {
+            // P's place is free once the product of S tile g - 2 has read it (P in S's place: as S was there). A parity
+            // wait tells only consecutive phases apart: who waits for a tile's product has to know of the one four tiles
+            // before. So every product up to g - 2 is awaited, in order; none from g on can be done before this P is there.
+            if (kTurns && g >= 3) wait_product(g - 3, 229);
+            if (kOwnP && g >= 2) wait_product(g - 2, 229);
+            if (kOwnP) tc_fence_after();
+          }
           tmem_st32(pl + half * 32 + c / 2, p);
-          tmem_wait_st();  // (the store reads its registers as it goes)
+          if (c + 64 < kCols) tmem_wait_st();  // (the store reads its registers as it goes)
         }
         acc[0] = __fadd2_rn(acc[0], acc[1]);
-        sum[k] += acc[0].x + acc[0].y;
-        // A parity wait tells only consecutive phases apart, so the output's wait for the segment's last product has
-        // to know that the one before is done, and learns it here: the last one cannot be until this P is there.
-        if (!kOwnP && i == n - 1 && n > 1) wait(pvdone(q), (pv0 + i - 1) & 1u, 229);
+        sum += acc[0].x + acc[0].y;
+        tmem_wait_st();
+        keep(p);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first(pready(g & 1u));
-        }
+        if (!kOwnP && g >= 2) wait_product(g - 2, 229);
       }
       g0 += n * QT;
-      pv0 += n;
       // output: a row's dims, or half of them
-#pragma unroll
-      for (int k = 0; k < NQ; ++k) {
-        const int q = kHalves ? k : wg;
-        const uint32_t ocol = tmem + lanes + 256 + q * DIM + half * kOCols;
-        const float tot = kHalves ? sum[k] + exchange(sum[k]) : sum[k];
+      {
+        const uint32_t gl = g0 - QT + q;
+        const uint32_t ocol = tmem + lanes + 256 + q * DIM + ohalf * kOCols;
+        float tot = sum;
+        if (kHalves) tot += exchange(sum);
+        if (kTurns) {
+          const float sum2 = exchange(sum), ref2 = exchange(ref), to = fmaxf(ref, ref2);
+          const float a1 = ref == to ? sum : sum * ex2(ref - to), a2 = ref2 == to ? sum2 : sum2 * ex2(ref2 - to);
+          tot = wg ? a2 + a1 : a1 + a2;
+          ref = to;
+        }
         const float inv = tot != 0.f ? 1.f / tot : 0.f;
-        const float lse = tot != 0.f ? ref[k] + log2f(tot) : -INFINITY;
-        wait(pvdone(q), (pv0 - 1) & 1u, 228);
+        const float lse = tot != 0.f ? ref + log2f(tot) : -INFINITY;
+        wait_product(gl, 228);
         tc_fence_after();
         const int r = q * 128 + row;
         const bool valid = r < s.n_rows, part = s.part >= 0;
@@ -1064,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           uint32_t o[32];
           tmem_ld32(ocol + cc, o);
           tmem_wait_ld32(o);
-          const int d = half * kOCols + cc;
+          const int d = ohalf * kOCols + cc;
           if (part) {
             float* dst = m.part_o + prow * DIM + d;
 #pragma unroll
@@ -1085,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             }
           }
         }
-        if (half == 0) {
+        if (ohalf == 0) {
           if (part)
             m.part_lse[prow] = lse;
           else if (valid && a.lse)
@@ -1277,7 +1313,7 @@ struct ManyPlan {
 ManyPlan plan(const AttnArgs& a) {
   ManyPlan p{};
   const int dim = a.kv.dim;
-  p.rows = dim == 256 ? 256 : 512;
+  p.rows = dim == 64 ? 512 : 256;
   long long keys = a.kv.max_kv;
   if (a.window > 0)
     keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + a.kv.max_new + 2 * kBK);
