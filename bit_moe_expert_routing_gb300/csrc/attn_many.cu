@@ -73,8 +73,8 @@ struct ManyCfg {
   static constexpr uint32_t kOffRing = QT * kQTile;
   static constexpr uint32_t kOffEx = kOffRing + kRing * kSlot;  // [2][2][128] floats: exchanged between the warpgroups; [128]: reference maxima
   static constexpr uint32_t kOffBar = kOffEx + (2 * 2 + 1) * 128 * 4;
-  // full, empty, pfull [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [4]; dfull, dempty, info [kDescs]
-  static constexpr int kBars = 3 * kRing + 5 + 10 + 3 * kDescs;
+  // full, empty [kRing]; qfull, qempty, ofree, drain, pq; sfull, pready, sread [2]; pvdone [4]; dfull, dempty, info [kDescs]
+  static constexpr int kBars = 2 * kRing + 5 + 10 + 3 * kDescs;
   static constexpr uint32_t kOffDesc = (kOffBar + kBars * 8 + 15) & ~15u;
   static constexpr uint32_t kOffInfo = kOffDesc + kDescs * 80;
   static constexpr uint32_t kOffMisc = kOffInfo + kDescs * 16;
@@ -674,8 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const uint32_t bar0 = base + C::kOffBar;
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kRing + s); };
-  auto pfull = [&](uint32_t s) { return bar0 + 8u * (2 * kRing + s); };  // first CTA: the other's slot is full
-  const uint32_t qfull = bar0 + 8u * (3 * kRing), qempty = qfull + 8, ofree = qfull + 16, drain = qfull + 24;
+  const uint32_t qfull = bar0 + 8u * (2 * kRing), qempty = qfull + 8, ofree = qfull + 16, drain = qfull + 24;
   const uint32_t pq = qfull + 32;  // first CTA: the other's queries are there
   auto sfull = [&](uint32_t s) { return qfull + 40 + 8u * s; };
   auto pready = [&](uint32_t s) { return qfull + 56 + 8u * s; };
@@ -694,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (known to be warp-uniform)
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(pfull(s), 1);
+    // (the first CTA's slots are full when the other's are, too)
+    for (int s = 0; s < kRing; ++s) mbar_init(full(s), first_cta ? 2 : 1), mbar_init(empty(s), 1);
     mbar_init(pq, 1);
     mbar_init(qfull, kLoadWarps * 32);
     mbar_init(qempty, 1);
@@ -759,7 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       }
       if (!ok) {  // copies in flight land before the CTA leaves (bounded)
         const uint32_t from = it > kRing ? it - kRing : 0;
-        for (uint32_t i = from; i < it; ++i) mbar_wait(full(i % kRing), (i / kRing) & 1u, abort_flag, hdr, kWaitLimit, true, 221);
+        // (the first CTA's barriers may want for the other's arrivals now: one limit is long enough for any copy)
+        for (uint32_t i = from; i < it; ++i)
+          if (!mbar_wait(full(i % kRing), (i / kRing) & 1u, abort_flag, hdr, kWaitLimit, true, 221)) break;
       }
     }
   } else if (warp == kWarpMma) {
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           arrive_first_release(pq);
           for (int p = 0; p < 2 * (s.j1 - s.j0) && ok; ++p, ++ring) {
             if (!(ok = mbar_wait(full(ring % kRing), (ring / kRing) & 1u, abort_flag, hdr, kWaitLimit, false, 234))) break;
-            arrive_first(pfull(ring % kRing));
+            arrive_first(full(ring % kRing));
           }
         }
       }
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         if (!(ok = __all_sync(~0u, mbar_wait_acquire(pq, sg & 1u, abort_flag, hdr, 235)))) break;
         fence_proxy_async();  // the loader warps' copies, for the tensor core
         auto wait_slot = [&](uint32_t seq) {
-          return wait(full(seq % kRing), (seq / kRing) & 1u, 223) && wait(pfull(seq % kRing), (seq / kRing) & 1u, 236);
+          return wait(full(seq % kRing), (seq / kRing) & 1u, 223);
         };
         auto qk = [&](int x) {  // S tile x: row tile x % QT, key tile x / QT
           const int q = x % QT, i = x / QT;
