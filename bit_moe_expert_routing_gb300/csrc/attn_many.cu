@@ -869,22 +869,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       if (sg > 0 && ok) ok = mbar_wait(qempty, (sg - 1) & 1u, abort_flag, hdr, kWaitLimit, false, 232);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
-      constexpr int CH = DIM / 8;  // 16-byte chunks of a row
-      const int tid = threadIdx.x - kWarpLoad * 32, c = tid % CH;
-      const uint16_t* qh = a.q + (m.h0 + mine.head) * a.group * DIM + c * 8;
-      constexpr int kStep = kLoadWarps * 32 / CH;  // rows of one instruction of both warps
-      for (int rb = tid / CH; rb < C::kRows; rb += 8 * kStep) {
-        const uint16_t* src[8];  // all addresses first: the copies do not let the compiler interleave their arithmetic
+      // A lane looks one row of 32 up, and the warp copies them with the addresses from their lanes: a lookup per chunk
+      // made these copies 3 to 4 thousand cycles long, with the segment's first product behind them.
+      constexpr int CH = DIM / 8, kStep = 32 / CH;  // 16-byte chunks of a row, rows of one instruction
+      const int c = lane % CH, sub = lane / CH;
+      const uint16_t* qh = a.q + (m.h0 + mine.head) * a.group * DIM;
+      for (int r32 = (warp - kWarpLoad) * 32; r32 < C::kRows; r32 += 32 * kLoadWarps) {
+        const int rr = min(mine.row0 + r32 + lane, mine.last), t = m.token(rr);
+        const long long src = reinterpret_cast<long long>(qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM);
+        const uint32_t dst = base + C::kOffQ + (r32 >> 7) * C::kQTile + (c >> 3) * kQBlock + ((r32 & 127) >> 3) * 1024;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = min(mine.row0 + rb + k * kStep, mine.last), t = m.token(rr);
-          src[k] = qh + (mine.first + t) * a.q_stride + (rr - t * a.group) * DIM;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = rb + k * kStep;
-          cp_async16(base + C::kOffQ + (r >> 7) * C::kQTile + (c >> 3) * kQBlock + sw128(r & 127, c & 7), src[k],
-                     r < mine.n_rows ? 16u : 0u);
+        for (int k = 0; k < 32; k += kStep) {
+          const long long from = __shfl_sync(~0u, src, k + sub);
+          cp_async16(dst + sw128(k + sub, c & 7), reinterpret_cast<const uint16_t*>(from) + c * 8,
+                     r32 + k + sub < mine.n_rows ? 16u : 0u);
         }
       }
       cp_async_arrive_noinc(qfull);
