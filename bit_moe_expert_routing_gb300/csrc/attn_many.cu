@@ -31,14 +31,27 @@
 // long as the products themselves; together they took 1400. The pair reads and
 // takes in 40 KB less.
 //
-// A CTA holds QT row tiles of 128 (two for DIM <= 128; one for 256, whose
-// output fills tensor memory): S tiles alternate between two slots, ordered
-// S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ..., so that the softmax of one
-// tile runs under the products of the other. Heads of 64 leave room for P
-// beside S: there S(x + 2) follows as soon as S(x) has been read, S(0) S(1) |
-// S(2), P(0) V | S(3), P(1) V | ..., and the softmax never waits for a product.
+// A CTA holds QT row tiles of 128 (two for heads of 64, else one). S tiles
+// alternate between two slots in tensor memory.
+//   Heads of 64 and 128: P has a place of its own beside S. S(x + 2) is issued
+//   as soon as S(x) has been read, and the softmax's two warpgroups work on two
+//   S tiles at a time, a thread per row: of two row tiles (64), or the same row
+//   tile's in turn (128), with the row's reference maximum handed on.
+//   Heads of 256: the output leaves room for two S slots alone, and P takes its
+//   S's place: S(0) S(1) | P(0) V, S(2) | P(1) V, S(3) | ... Both warpgroups
+//   take half of the keys of every S tile, which halves the time between S and
+//   P, in which the slot's products wait.
 // The pair's first CTA issues the MMAs; the other tells it which of its
 // operands have landed.
+//
+// Measured: 1024 tokens at 32K positions, 16 heads over 2 of 256 dims, 291 us
+// with the 20 of the expansion, 541 GFLOP, 1.9 PFLOP/s while it runs: the tensor
+// cores are busy in 89% of its cycles. A prompt of 4096, 16 heads over 2 of 128
+// dims: 72 us, 69 GFLOP; of that the start and four outputs per pair are about a
+// third (between a segment's last P and the next one's first nothing is
+// multiplied), the rest is bound by the warp that issues the products, at about
+// 1600 cycles per S tile and its product where the tensor cores need 1024.
+// Windowed prompts with heads of 64: 55 us, bound by exponentials and masks.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -51,10 +64,11 @@ constexpr int kBK = 128;                  // keys per tile
 constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
 constexpr int kDescs = 4;                 // segment descriptors in flight
-constexpr int kMinUnits = 4;              // of a pair. (Two kv heads of 128 dims, one sequence, 512 rows, us: 8000 keys
-                                          // 30.3, with at least 1 unit 35.5, 12 units 39.9; 1000 keys 25.5, 22.9, 29.4.)
-constexpr int kTileCost = 3;              // units added to every row tile: its set-up and output (1: 89 us, 3: 84.5 us
-                                          // for a prompt of 4096 tokens)
+constexpr int kMinUnits = 4;              // of a pair. (16 heads over 2 of 128 dims, one sequence, 64 tokens: over 8000
+                                          // keys 25.2 us, with at least 2 units 25.8, 8 units 26.6; over 1000 keys 19.3,
+                                          // 18.7, 22.9.)
+constexpr int kTileCost = 3;              // units added to every row tile: its set-up and output. (A prompt of 4096 with
+                                          // heads of 128: 76 us, with 2 units 79, 5 units 76, 8 units 80.)
 
 template <int DIM>
 struct ManyCfg {
@@ -1410,9 +1424,9 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   // Parts of a row tile are about pairs / row tiles. Up to two are joined in
   // the kernel, by the CTA that writes the last; more of them by the combine
   // kernel, over all of the GPU. Combined against joined in the kernel, us, 16
-  // heads over 2 kv heads of 128 dims, one sequence: 4 row tiles over 8000 keys
-  // (19 parts each) 33 and 80, 32 of them 77 and 81, 64 of them 140 and 133;
-  // the 128 row tiles of a prompt of 4096 94 and 80.
+  // heads over 2 of 128 dims, one sequence over 8000 keys: 8 row tiles 29 and
+  // 41, 32 of them 43 and 46, 64 of them 70 and 67; the 256 row tiles of a
+  // prompt of 4096 86 and 72. Of 256 dims, 8 row tiles 35 and 63.
   const long long row_tiles = std::max(1ll, (long long)a.kv.n_tokens * a.group / p.rows) * a.kv.kv_heads;
   m.join = row_tiles * 2 >= p.pairs;
   m.arrived = reinterpret_cast<int*>(w + p.arrived);
