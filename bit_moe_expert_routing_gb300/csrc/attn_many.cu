@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
     // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
     const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
     constexpr int kBatch = 4;  // loads in flight before the first is used
+    static_assert(kBK * W / kPlanThreads % kBatch == 0, "batches of whole passes");
     const int w = threadIdx.x % W;
     for (int p = 0; p < kBK * W / kPlanThreads; p += kBatch) {
       uint32_t c[kBatch];
