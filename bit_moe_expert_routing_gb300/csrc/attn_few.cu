@@ -32,7 +32,7 @@
 // leaves fp32 partial outputs, which a combine kernel joins. (A grid of
 // fixed-length splits took 107 us for 64 ragged sequences of up to 8191
 // positions, 60 of them in prologues and merges.) When no item has more than
-// kWholeElements, an item is a CTA's whole work and nothing is cut. The four warps
+// whole_keys, an item is a CTA's whole work and nothing is cut. The four warps
 // of a CTA alternate tiles, each with its own ring of asynchronous copies, so
 // that nothing but the merge of an item's end joins them. (cp.async rather than
 // bulk copies: a tile is six runs of one or two pages, and six bulk copies by
@@ -141,12 +141,20 @@ __device__ __forceinline__ Tiles tiles_of(int minpos, int maxpos, int window, in
   return t;
 }
 
-// An item of at most so many cached elements (keys x dims) is not worth
-// cutting: the combine kernel and the parts cost more than the tiles that the
-// CTA would be spared. (Graph replays of 32 sequences: heads of 64, 1100 keys,
-// whole 10.9 us, cut 14.8; 2200 keys 18.4 and 18.8; heads of 128, 1100 keys,
-// 14.0 and 18.0; heads of 256, 600 keys, 11.3 and 17.2.)
-constexpr long long kWholeElements = 144 * 1024;
+// Items of at most so many keys are not worth cutting: the combine kernel and
+// the parts cost more than the tiles that an item's CTA would be spared. With
+// more items less is spared, since the CTAs that would share them have items
+// of their own. (Cut against whole, us, one token per sequence; heads of 64, 4
+// kv heads: 1 sequence 600 keys 7.5 and 6.8, 1000 keys 7.5 and 8.3; 32
+// sequences 1500 keys 11.8 and 10.4, 2200 keys 13.6 and 13.7. Heads of 128, 2
+// kv heads: 8 sequences 600 keys 9.7 and 7.9, 1000 keys 9.9 and 10.1; 64
+// sequences 1500 keys 15.1 and 13.0, 2200 keys 17.9 and 17.1. Heads of 256: 1
+// sequence 256 keys 9.6 and 7.5, 600 keys 9.6 and 10.8; 64 sequences 1500 keys
+// 20.0 and 18.7.) The bound on the lengths is all that is known here, and
+// shorter sequences gain from a cut, so not above 2048.
+long long whole_keys(int dim, long long items) {
+  return std::min(2048ll, std::max(dim == 256 ? 448ll : 896ll, 16 * items));
+}
 constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
 // What beginning, merging and writing an item costs a CTA, in tiles: counted
 // in front of its tiles when units are dealt out. (64 ragged sequences, 512
@@ -956,7 +964,7 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   const long long tokens = std::min<long long>(a.kv.max_new, max_rows / a.group + 1);  // of a sequence taken here
   if (a.window > 0)
     keys = std::min<long long>(keys, (long long)a.window + std::min(a.sinks, a.kv.max_kv) + tokens + 2 * kTile);
-  p.whole = keys * a.kv.dim <= kWholeElements;
+  p.whole = keys <= whole_keys(a.kv.dim, 1ll * p.row_groups * a.kv.kv_heads * a.kv.n_seqs);
   const int per_sm = a.kv.dim * p.nt <= 128 ? 4 : 2;  // CTAs that fit (registers and the rings)
   p.ctas = num_sms() * per_sm;
   p.part_rows = p.whole ? 0 : size_t(2) * p.ctas * 8 * p.nt;

@@ -64,24 +64,24 @@ moe_status check_attention(const KvArgs& kv, const moe_attention* a) {
 // dims); the many-row path expands them once, ahead, and then works in tiles
 // of 256 rows (512 of 64 dims), mostly empty below that: measured, 8 query
 // heads per kv head of 128 dims, 2 kv heads, one sequence of 64000 keys, 64
-// rows 25 us few and 52 many, 128 rows 40 and 53, 256 rows 69 and 54; of 256
-// dims, 64 rows 57 and 83, 128 rows 99 and 87. So 128 rows, 64 of 256 dims.
+// rows 25 us few and 51 many, 128 rows 40 and 52, 256 rows 65 and 54; of 256
+// dims, 64 rows 56 and 84, 128 rows 93 and 86. So 128 rows, 64 of 256 dims.
 //
 // With more rows the few-row kernel still wins as long as its items are at
 // most two CTAs' worth per SM and their products few: the many-row path's
 // launches and set-up take longer than the work. Few against many, us, 128
 // dims: one sequence, 1024 rows over no context 9 and 14, over 1000 keys (2^28
-// products) 19 and 21, over 8000 keys (2^31) 44 and 29; 8 sequences, 256 rows
-// over 1000 keys (2^29) 19 and 22, over 8000 keys (2^32) 74 and 45. Over 360
-// sizes this choice is 0.3% slower than the better kernel on average, at most
-// 35%.
+// products) 17 and 21, over 8000 keys (2^31) 43 and 29; 8 sequences, 256 rows
+// over 1000 keys (2^29) 19 and 22, over 8000 keys (2^32) 72 and 45. Over 360
+// sizes this choice is 0.4% slower than the better kernel on average, at most
+// 33%.
 int few_rows(const AttnArgs& a, const Options& o) {
   constexpr int kAny = 1 << 30;
   if (o.force_path) return o.force_path == 1 ? kAny : 0;
   long long keys = a.kv.max_kv;
   if (a.window > 0) keys = std::min(keys, (long long)a.window + a.sinks + a.kv.max_new);
   const double products = double(keys) * a.kv.n_tokens * a.heads * a.kv.dim * (a.kv.dim == 256 ? 2 : 1);
-  if (products <= double(3 << 28) && attention_few_items(a, kAny) <= 2 * num_sms()) return kAny;
+  if (products <= double(1 << 30) && attention_few_items(a, kAny) <= 2 * num_sms()) return kAny;
   return a.kv.dim == 256 ? 64 : 128;
 }
 
