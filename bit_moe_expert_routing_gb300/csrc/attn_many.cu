@@ -8,20 +8,21 @@
 //   expand   writes the visible keys and values as bf16 tiles of 128 keys into
 //            the workspace, laid out exactly as the MMA reads shared memory
 //            (128-byte-swizzled, keys K-major; values transposed, so K-major
-//            in the second product too), in units of 16 KB. It stays in L2.
+//            in the second product too), each tile as the halves that the two
+//            CTAs of a pair keep. It stays in L2.
 //            One extra CTA cuts the work (below).
 //   many     S = Q K^T per 128-row tile and 128 keys into tensor memory, the
-//            softmax warps turn it into P (bf16, in S's place), O += P V with
+//            softmax warps turn it into P (bf16, there too), O += P V with
 //            P read from tensor memory.
 //            The CTA that finishes a row tile's last part joins the parts, if
 //            there are few; many parts of few row tiles are joined by
 //   combine  over all of the GPU.
 //
 // The cut: a unit is one row tile times one key tile. All units of all
-// sequences and kv heads are numbered row tile by row tile, and one CTA pair per two
-// SMs takes an equal, contiguous range, so that neither causal masks, ragged
-// lengths nor few row tiles leave SMs idle. A row tile that falls into several
-// ranges leaves fp32 partial outputs.
+// sequences and kv heads are numbered row tile by row tile, and each of the CTA
+// pairs, one per two SMs, takes an equal, contiguous range, so that neither
+// causal masks, ragged lengths nor few row tiles leave SMs idle. A row tile that
+// falls into several ranges leaves fp32 partial outputs.
 //
 // Two CTAs on neighbouring SMs work as one (cta_group::2): an MMA takes 128
 // rows of each and all of a key tile, of which each SM keeps half (64 keys, or

@@ -234,6 +234,40 @@ def test_attention_long_context(dim, heads, kv_heads, kv, window, new):
     run_attention(heads, kv_heads, dim, 64, [new], [kv], window=window, sinks=4 if window else 0, seed=3)
 
 
+@pytest.mark.parametrize("dim,max_kv", [(128, 1 << 20), (64, 1 << 22)])
+def test_attention_in_passes(dim, max_kv):
+    """A bound on the lengths whose expanded tiles are more than one pass holds: passes over sequences and kv heads."""
+    run_attention(12, 3, dim, 16, [150, 0, 90, 1], [150, 30, 300, 260], max_kv=max_kv)
+
+
+def test_offsets_past_32_bits(forced):
+    """Pages whose codes lie more than 2^31 words into the arrays."""
+    heads, kv_heads, dim, page = 16, 8, 256, 256
+    batch = Batch([3, 40], [700, 90], page, spare=46000)
+    batch.table = np.where(batch.table < 0, batch.table, batch.n_pages - 1 - batch.table % 7 - 7 * np.arange(batch.table.size)
+                           .reshape(batch.table.shape)).astype(np.int32)
+    used = [p for b in range(2) for p in set(batch.places(b)[0].tolist())]
+    assert len(set(used)) == len(used) and min(used) * kv_heads * page * (dim // 8) > 2 ** 31
+    cache = moe.KVCache.empty(batch.n_pages, page, kv_heads, dim)
+    fill(cache, batch)
+    k, v = rows(batch.n_tokens, kv_heads, dim, 1), rows(batch.n_tokens, kv_heads, dim, 2)
+    dev = batch.device(moe)
+    cache.append(k, v, dev)
+    for got, x in zip(cache.read(dev), (k, v)):
+        assert np.array_equal(got.double().cpu().numpy(), values(*quantise(x.double().cpu().numpy())))
+    # all positions of both sequences, read back, are what the attention sees
+    every = Batch([700, 90], [700, 90], page)
+    every.table = batch.table
+    keys, vals = (t.double().split(every.new) for t in cache.read(every.device(moe)))
+    q = rows(batch.n_tokens, heads, dim, 3)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)))
+    for path in (1, 2):
+        forced(path)
+        out, lse = cache.attention(q, dev, lse=True)
+        cache.check()
+        check_attention(out, lse, ref, path)
+
+
 @pytest.mark.parametrize("new,kv", [([1, 2], [300, 70]), ([200], [260])])
 @pytest.mark.parametrize("scale,spread", [(0.0, 1.0), (-0.3, 1.0), (1.0, 6.0), (1e-4, 1000.0)])
 def test_attention_scales(new, kv, scale, spread):
