@@ -779,7 +779,11 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 
 // Where an item's parts are: parts p = 0 .. n - 1 of CTAs p0 + p. Part 0 ends
 // its CTA's range and is in slot 0; the others begin theirs inside the item,
-// in slot 1.
+// in slot 1. Items that are not cut have nothing to join, and short sequences
+// under a large bound may leave none that is: the combine kernels' threads
+// wait for the kernel before on every way out, or their grid could end before
+// the one that writes the output, with only the combine for what follows on
+// the stream to be ordered behind.
 struct Parts {
   SeqItems sq;
   int kvh, rg, n_rows, p0, n;
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
   constexpr int kV = DIM / 128 + (DIM < 128);  // float4 of a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
   const Parts q = parts_of(f, blockIdx.x, rows_per_group);
-  if (q.n <= 1 || row >= q.n_rows) return;
+  if (q.n <= 1 || row >= q.n_rows) return griddep_wait();  // (see Parts)
   const long long at = q.place(f, rows_per_group, row);
   griddep_wait();
   const bool mine = DIM >= 128 || lane < DIM / 4;
@@ -891,7 +895,7 @@ __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x % rows;
   const Parts q = parts_of(f, blockIdx.x / rows, rows_per_group);
   const int n = q.n;
-  if (n <= 1 || row >= q.n_rows) return;
+  if (n <= 1 || row >= q.n_rows) return griddep_wait();  // (see Parts)
   const long long at = q.place(f, rows_per_group, row);
   const int grp = threadIdx.x / kLanes, d = blockIdx.y * 64 + 4 * (threadIdx.x % kLanes);
   griddep_wait();

@@ -72,7 +72,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // once that kernel has completed and its memory writes are visible (at once
 // for a kernel launched the ordinary way); griddep_launch() lets the next
 // such kernel start. A kernel triggers only after its own wait, so a kernel
-// that starts early can rely on everything before its predecessor.
+// that starts early can rely on everything before its predecessor; but for
+// the down GEMM, whose dependent waits before it reads anything, and the
+// few-row attention kernel, which waits at its end and whose dependent relies
+// until its own wait on what was there before the call alone. Whoever is
+// launched this way waits before its last thread leaves, whether it reads
+// anything or not: what follows it on the stream is ordered behind it, and
+// only through that wait behind its predecessor.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -1,0 +1,60 @@
+"""The cache's attention as a serving loop calls it: bounds above the lengths, a consumer straight behind it on the stream,
+many sequences, and workspaces and settings kept between steps."""
+import math
+
+import numpy as np
+import pytest
+
+import bit_moe_expert_routing_gb300 as moe
+from bit_moe_expert_routing_gb300 import build
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from kv_util import Batch, attention_reference, check_attention, fill, junk_cache  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    moe.lib()
+
+
+def rows(n, heads, dim, seed=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(n, heads, dim, generator=g, device="cuda").to(torch.bfloat16)
+
+
+# Under a bound of 5000 positions items may be cut, but these are short: their units (10 and the tiles of 32 positions)
+# are dealt out in eights at least, and the tiles of each fall to one CTA. In the last one no sequence is the few-row
+# kernel's at all, beside a prompt that is long enough for the many-row kernels.
+@pytest.mark.parametrize("new,kv", [([1], [100]), ([1], [190]), ([1] * 16, [50] * 16), ([1, 1500], [100, 1500]),
+                                    ([1400, 1300], [1400, 1300])])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_kernel_behind_the_call_sees_its_output(dim, new, kv):
+    batch = Batch(new, kv, 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    keys, vals = fill(cache, batch)
+    q = rows(batch.n_tokens, 16, dim)
+    dev = batch.device(moe, max_new=max(new) + 1, max_kv=5000)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)))
+    out, ws = torch.empty_like(q), cache.attention_workspace(16, dev)
+    cache.attention(q, dev, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g, got = torch.cuda.CUDAGraph(), torch.empty_like(out)
+    with torch.cuda.graph(g):
+        out.fill_(math.nan)
+        cache.attention(q, dev, out=out, workspace=ws)
+        got.copy_(out)
+    for _ in range(20):
+        g.replay()
+    torch.cuda.synchronize()
+    check_attention(got, None, ref)
+    for _ in range(20):  # and in a stream
+        out.fill_(math.nan)
+        cache.attention(q, dev, out=out, workspace=ws)
+        got.copy_(out)
+    check_attention(got, None, ref)
+    cache.check()
