@@ -113,8 +113,12 @@ AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
 
 moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-KvCall begin_call(void* stream) {
-  const KvCall c{options_snapshot(), static_cast<cudaStream_t>(stream)};
+size_t workspace_bytes_for(const AttnArgs& a, int few) {
+  return ((few_bytes(a, few) + (any_many(a, few) ? attention_many_workspace(a) : 0)) + 511) & ~size_t(255);
+}
+
+KvCall begin_call(void* stream, const Options& opt = options_snapshot()) {
+  const KvCall c{opt, static_cast<cudaStream_t>(stream)};
   timing_begin(c.opt, c.stream);
   return c;
 }
@@ -149,8 +153,7 @@ size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batc
   KvArgs a;
   if (make_args(cache, batch, &a) || check_attention(a, at)) return 0;
   const AttnArgs g = attn_args(a, at);
-  const int few = few_rows(g, options_snapshot());
-  return ((few_bytes(g, few) + (any_many(g, few) ? attention_many_workspace(g) : 0)) + 511) & ~size_t(255);
+  return workspace_bytes_for(g, few_rows(g, options_snapshot()));
 }
 
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* at,
@@ -163,15 +166,16 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
   if (a.n_tokens == 0) return MOE_OK;
   if (!operand_ok(q, q_stride, at->heads, a.dim) || !out || !aligned(out, 16) || out == q) return MOE_ERR_ARG;
   if (lse && !aligned(lse, 4)) return MOE_ERR_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_attention_workspace_size(cache, batch, at))
-    return MOE_ERR_WORKSPACE;
+  // the options once: the kernels are those that the workspace was checked for, whatever other threads set meanwhile
+  const Options opt = options_snapshot();
   AttnArgs g = attn_args(a, at);
+  const int few = few_rows(g, opt);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_bytes_for(g, few)) return MOE_ERR_WORKSPACE;
   g.q = q;
   g.q_stride = q_stride;
   g.out = out;
   g.lse = lse;
-  const KvCall c = begin_call(stream);
-  const int few = few_rows(g, c.opt);
+  const KvCall c = begin_call(stream, opt);
   const bool many = any_many(g, few);
   if (many)
     if (cudaError_t e = attention_many(g, few, static_cast<char*>(workspace) + few_bytes(g, few), c)) return status_of(e);

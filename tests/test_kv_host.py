@@ -1,0 +1,92 @@
+"""The host side of the attention's entry point without a GPU: kv_api.cu compiled with stand-ins for the kernels' launches,
+which record what they are called with."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import bit_moe_expert_routing_gb300 as moe
+from bit_moe_expert_routing_gb300 import build
+
+P = 1 << 20  # a well-aligned address that nothing reads
+
+HARNESS = r"""
+#include "kv_api.cu"
+
+namespace moe {
+static int paths[2], snapshots, used[2];  // the option's value at the first and at later looks; bytes each kind of kernel uses
+static AttnArgs last;
+Options options_snapshot() {
+  Options o;
+  o.force_path = paths[snapshots++ > 0];
+  return o;
+}
+int num_sms() { return 152; }
+void reset_launch_count() {}
+void timing_begin(const Options&, cudaStream_t) {}
+void launch_done(const Options&, cudaStream_t, const char*) {}
+size_t attention_few_workspace(const AttnArgs&, int) { return 4096; }
+size_t attention_many_workspace(const AttnArgs&) { return 1 << 20; }
+long long attention_few_items(const AttnArgs&, int) { return 1 << 20; }
+cudaError_t attention_few(const AttnArgs& a, int, void*, bool, const KvCall&) {
+  last = a, used[0] = 4096;
+  return cudaSuccess;
+}
+cudaError_t attention_many(const AttnArgs& a, int, void*, const KvCall&) {
+  last = a, used[1] = 1 << 20;
+  return cudaSuccess;
+}
+cudaError_t kv_append(const KvArgs&, const uint16_t*, long long, const uint16_t*, long long, const KvCall&) { return cudaSuccess; }
+cudaError_t kv_read(const KvArgs&, uint16_t*, uint16_t*, const KvCall&) { return cudaSuccess; }
+}  // namespace moe
+
+extern "C" void set_paths(int first, int later) {
+  moe::paths[0] = first, moe::paths[1] = later;
+  moe::snapshots = moe::used[0] = moe::used[1] = 0;
+}
+extern "C" int bytes_used() { return moe::used[0] + moe::used[1]; }
+extern "C" int last_window() { return moe::last.window; }
+extern "C" int last_sinks() { return moe::last.sinks; }
+"""
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    d = tmp_path_factory.mktemp("kv_host")
+    src, so = d / "harness.cu", d / "harness.so"
+    src.write_text(HARNESS)
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-shared",
+                    "-Xlinker", "-Bsymbolic", "-I", build.CSRC, "-I", os.path.join(build.ROOT, "include"), str(src), "-o",
+                    str(so)], check=True, capture_output=True)
+    lib = ctypes.CDLL(str(so))
+    for name in ("moe_attention_workspace_size", "moe_attention_forward"):
+        getattr(lib, name).restype, getattr(lib, name).argtypes = moe.SIGNATURES[name]
+    return lib
+
+
+def step(max_kv=1000, n_tokens=300, window=0, sinks=0):
+    return (moe.moe_kv_cache(10, 16, 2, 128, P, P, P, P, P, P, P), moe.moe_kv_batch(1, n_tokens, n_tokens, max_kv, P, P, P, 64),
+            moe.moe_attention(16, window, sinks, 0.1))
+
+
+def size(host, c, b, a):
+    return host.moe_attention_workspace_size(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a))
+
+
+def forward(host, c, b, a, nbytes):
+    return host.moe_attention_forward(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a), P, 2048, 2 * P, None, P, nbytes, None)
+
+
+@pytest.mark.parametrize("first,later", [(1, 2), (2, 1), (0, 1), (1, 0), (0, 2), (2, 0)])
+def test_an_option_set_during_the_call_does_not_change_its_kernels(host, first, later):
+    """Another thread's change of the path between the workspace's check and the launches."""
+    s = step()
+    host.set_paths(first, first)
+    n = size(host, *s)
+    host.set_paths(first, later)
+    assert forward(host, *s, n) == moe.MOE_OK
+    assert 0 < host.bytes_used() <= n
+    host.set_paths(first, later)
+    assert forward(host, *s, n - 1) == moe.MOE_ERR_WORKSPACE
+    assert host.bytes_used() == 0
