@@ -105,8 +105,10 @@ AttnArgs attn_args(const KvArgs& kv, const moe_attention* at) {
   g.kv = kv;
   g.heads = at->heads;
   g.group = at->heads / kv.kv_heads;
-  g.window = at->window;
-  g.sinks = at->sinks;
+  // A window that covers every position hides none: it is no window, and both numbers stay below 2^24, so that the
+  // kernels' differences from positions (of padding, down to -2^20) stay within 32 bits.
+  g.window = at->window < kv.max_kv ? at->window : 0;
+  g.sinks = g.window ? std::min(at->sinks, kv.max_kv) : 0;
   g.scale = at->scale;
   return g;
 }

@@ -90,3 +90,18 @@ def test_an_option_set_during_the_call_does_not_change_its_kernels(host, first, 
     host.set_paths(first, later)
     assert forward(host, *s, n - 1) == moe.MOE_ERR_WORKSPACE
     assert host.bytes_used() == 0
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("window,sinks,want", [(0, 0, (0, 0)), (0, 7, (0, 0)), (1, 0, (1, 0)), (999, 4, (999, 4)),
+                                               (999, INT_MAX, (999, 1000)), (1000, 4, (0, 0)), (INT_MAX, 0, (0, 0)),
+                                               (INT_MAX, INT_MAX, (0, 0)), (INT_MAX - 2 ** 24, 1, (0, 0))])
+def test_windows_and_sinks_reach_the_kernels_within_the_bound_on_the_lengths(host, window, sinks, want):
+    """Larger ones mean the same, and would pass 32 bits in the kernels' differences."""
+    s = step(max_kv=1000, window=window, sinks=sinks)
+    for path in (0, 1, 2):
+        host.set_paths(path, path)
+        assert forward(host, *s, size(host, *s)) == moe.MOE_OK
+        assert (host.last_window(), host.last_sinks()) == want

@@ -58,3 +58,32 @@ def test_a_kernel_behind_the_call_sees_its_output(dim, new, kv):
         got.copy_(out)
     check_attention(got, None, ref)
     cache.check()
+
+
+@pytest.fixture
+def each_path():
+    """The kernels by turns: by the sequences' sizes, few rows, many rows."""
+    def paths():
+        for path in (0, 1, 2):
+            moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, path)
+            yield path
+    yield paths
+    moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, 0)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 2 ** 20, 4), (300, 0),
+                                          (299, 2 ** 31 - 1), (17, 2 ** 31 - 1)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_windows_past_every_position(dim, window, sinks, each_path):
+    """No limit, as a number, with tokens at negative positions (padding) beside others."""
+    batch = Batch([5, 290, 3, 40, 1], [2, 200, 0, 300, 260], 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    keys, vals = fill(cache, batch)
+    q = rows(batch.n_tokens, 8, dim)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)), window, sinks)
+    for max_kv in (300, 5000):
+        dev = batch.device(moe, max_kv=max_kv)
+        for path in each_path():
+            out, lse = cache.attention(q, dev, window=window, sinks=sinks, lse=True)
+            cache.check()
+            check_attention(out, lse, ref, (path, max_kv))
