@@ -971,7 +971,7 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   p.whole = keys <= whole_keys(a.kv.dim, 1ll * p.row_groups * a.kv.kv_heads * a.kv.n_seqs);
   const int per_sm = a.kv.dim * p.nt <= 128 ? 4 : 2;  // CTAs that fit (registers and the rings)
   p.ctas = num_sms() * per_sm;
-  p.part_rows = p.whole ? 0 : size_t(2) * p.ctas * 8 * p.nt;
+  p.part_rows = size_t(2) * p.ctas * 8 * p.nt;  // (there for whole items, too: fewer of them may be cut)
   return p;
 }
 

@@ -1326,6 +1326,9 @@ struct ManyPlan {
   size_t kx, vx, bad, plan, unit_off, row_tile, range, arrived, part_o, part_lse, total;
 };
 
+// The workspace grows with every bound on the step, so that one sized for a
+// larger step serves a smaller one: what depends on how the passes divide it
+// has the place of the most that any division of a smaller step could use.
 ManyPlan plan(const AttnArgs& a) {
   ManyPlan p{};
   const int dim = a.kv.dim;
@@ -1346,12 +1349,16 @@ ManyPlan plan(const AttnArgs& a) {
     o = al256(o + bytes);
     return at;
   };
-  p.kx = put(size_t(p.nb) * p.nh * head_bytes / 2);
-  p.vx = put(size_t(p.nb) * p.nh * head_bytes / 2);
-  p.bad = put(size_t(p.nb) * p.tiles_max);
+  const size_t tile_bytes = head_bytes / p.tiles_max;
+  const size_t tiles = std::min(size_t(a.kv.n_seqs) * a.kv.kv_heads * p.tiles_max,
+                                std::max<size_t>(p.tiles_max, kPassBytes / tile_bytes));  // of a pass, at least nb nh tiles_max
+  const size_t row_tiles = size_t(p.max_row_tiles - p.nb) + a.kv.n_seqs;
+  p.kx = put(tiles * tile_bytes / 2);
+  p.vx = put(tiles * tile_bytes / 2);
+  p.bad = put(tiles);
   p.plan = put(sizeof(PlanHdr));
-  p.unit_off = put((size_t(p.max_row_tiles) + 1) * 8);
-  p.row_tile = put(size_t(p.max_row_tiles) * sizeof(RowTile));
+  p.unit_off = put((row_tiles + 1) * 8);
+  p.row_tile = put(row_tiles * sizeof(RowTile));
   p.range = put((size_t(p.pairs) + 1) * sizeof(PairRange));
   p.arrived = put(size_t(p.pairs) * 2 * 4);
   p.part_o = put(size_t(2) * p.pairs * p.rows * dim * 4);

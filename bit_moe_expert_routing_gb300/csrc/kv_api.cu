@@ -94,8 +94,8 @@ bool any_few(const AttnArgs& a, int few) {
 }
 
 // The few-row kernels' part of the workspace, before the many-row kernels'
-// (both are used when a step has sequences of both kinds; always there, so
-// that no smaller step needs more).
+// (both are used when a step has sequences of both kinds; always there, and as
+// large whether items are cut or not, so that no smaller step needs more).
 size_t few_bytes(const AttnArgs& a, int few) {
   return (attention_few_workspace(a, few) + 255) & ~size_t(255);
 }

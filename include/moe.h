@@ -407,8 +407,10 @@ typedef struct {
  * device fp32 [n_tokens, heads], the natural logarithm of the row's sum of
  * exp(score), -inf for a row that sees nothing (what merging with attention
  * over other keys needs). workspace: device, 256-byte aligned, at least
- * moe_attention_workspace_size() bytes; no contents kept. Enqueued on
- * `stream`, no host synchronisation. n_tokens = 0 is a no-op. */
+ * moe_attention_workspace_size() bytes; no contents kept. No bound of the
+ * batch (n_seqs, n_tokens, max_new, max_kv) lowers that size as it grows: a
+ * workspace sized for the largest step serves them all. Enqueued on `stream`,
+ * no host synchronisation. n_tokens = 0 is a no-op. */
 size_t moe_attention_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* a);
 moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_attention* a,
                                  const uint16_t* q, long long q_stride, uint16_t* out, float* lse, void* workspace,

@@ -105,3 +105,30 @@ def test_windows_and_sinks_reach_the_kernels_within_the_bound_on_the_lengths(hos
         host.set_paths(path, path)
         assert forward(host, *s, size(host, *s)) == moe.MOE_OK
         assert (host.last_window(), host.last_sinks()) == want
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads,page", [(64, 8, 8, 16), (128, 16, 2, 64), (256, 16, 2, 64), (128, 5, 1, 16),
+                                                    (64, 24, 4, 256), (256, 64, 8, 32)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 1), (512, 4), (5000, 100)])
+def test_a_larger_steps_workspace_serves_a_smaller_one(dim, heads, kv_heads, page, window, sinks):
+    """No bound of the step lowers the size: over the grid, each size against those one bound below it, with the lengths
+    about those up to which items are not cut and those at which the many-row kernels need one pass more."""
+    build.build()
+    c = moe.moe_kv_cache(10, page, kv_heads, dim, P, P, P, P, P, P, P)
+    seqs = [1, 2, 3, 8, 15, 16, 17, 31, 32, 33, 64, 65, 128, 300]
+    tokens = [1, 2, 4, 7, 16, 33, 64, 65, 129, 257, 600, 3000, 40000]
+    new = [1, 2, 3, 4, 8, 9, 17, 129, 257, 600, 3000]
+    tile = 128 * dim * 4  # bytes of an expanded tile of 128 keys and their values
+    passes = [128 * (2 ** 31 // tile // n) for n in (1, 2, 3, 4, 5, 8, 64, 600)]
+    kv = sorted({1, 100, 400, 447, 448, 449, 600, 895, 896, 897, 1100, 1500, 2047, 2048, 2049, 2100, 32768, 1 << 24}
+                | {p + d for p in passes for d in (-129, -1, 0, 1, 128) if 0 < p + d <= 1 << 24})
+    got = {}
+    for i, s in enumerate(seqs):
+        for j, t in enumerate(tokens):
+            for k, m in enumerate(new):
+                for l, v in enumerate(kv):
+                    n = moe.moe_attention_workspace_size(c, moe.moe_kv_batch(s, t, m, v, P, P, P, 64),
+                                                         moe.moe_attention(heads, window, sinks, 0.1))
+                    got[i, j, k, l] = n
+                    for at in ((i - 1, j, k, l), (i, j - 1, k, l), (i, j, k - 1, l), (i, j, k, l - 1)):
+                        assert got.get(at, 1) <= n, (s, t, m, v, at)

@@ -87,3 +87,22 @@ def test_windows_past_every_position(dim, window, sinks, each_path):
             out, lse = cache.attention(q, dev, window=window, sinks=sinks, lse=True)
             cache.check()
             check_attention(out, lse, ref, (path, max_kv))
+
+
+@pytest.mark.parametrize("dim,max_kv", [(128, 1500), (256, 600), (64, 1500)])
+def test_the_largest_steps_workspace_serves_every_step(dim, max_kv):
+    """A loop with one workspace as its sequences end: whole items with many sequences, cut ones with few."""
+    ws = None
+    for n in (64, 32, 3, 1):
+        kv = [max_kv - 7 * i for i in range(n)]
+        batch = Batch([1] * n, kv, 16)
+        cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+        keys, vals = fill(cache, batch)
+        q = rows(n, 16, dim)
+        dev = batch.device(moe, max_kv=max_kv)
+        if ws is None:
+            ws = cache.attention_workspace(16, dev)
+        ws.fill_(0xFF)
+        out, lse = cache.attention(q, dev, lse=True, workspace=ws)
+        cache.check()
+        check_attention(out, lse, attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5))), n)
