@@ -360,7 +360,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       c[i] = sc[i] = bs[i] = 0;
-      if (r16 >= 0 && k0 + key0 + i <= maxpos) {
+      // a slot that no row sees may hold anything: its zero probability needs a finite value
+      const int key = k0 + key0 + i;
+      if (r16 >= 0 && key <= maxpos && (key >= lo || key < m.a.sinks)) {
         const long long row = r16 + (key0 & 15) + i;
         c[i] = kv.codes[1][row * W + w];
         sc[i] = kv.scales[1][row * G + w / 8];

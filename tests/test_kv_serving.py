@@ -106,3 +106,27 @@ def test_the_largest_steps_workspace_serves_every_step(dim, max_kv):
         out, lse = cache.attention(q, dev, lse=True, workspace=ws)
         cache.check()
         check_attention(out, lse, attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5))), n)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,kv,window,sinks", [([1], [700], 100, 0), ([2, 1], [901, 333], 50, 3), ([150], [700], 101, 5),
+                                                 ([150, 40], [1000, 517], 17, 0), ([260], [420], 130, 20), ([1], [40], 7, 33)])
+def test_places_that_no_row_sees_may_hold_anything(dim, new, kv, window, sinks, each_path):
+    """Between the sinks and the first row's window nothing was ever written: NaN scales, infinite biases."""
+    batch = Batch(new, kv, 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    keys, vals = fill(cache, batch)
+    for b, (n, end) in enumerate(zip(new, kv)):
+        pg, sl = batch.places(b)
+        unseen = slice(sinks, max(sinks, end - n - window + 1))
+        pg, sl = torch.from_numpy(pg[unseen].astype(np.int64)).cuda(), torch.from_numpy(sl[unseen]).cuda()
+        for name in ("k", "v"):
+            getattr(cache, name + "_scales")[pg, :, sl] = math.nan
+            getattr(cache, name + "_biases")[pg, :, sl] = math.inf
+    q = rows(batch.n_tokens, 8, dim)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)), window, sinks)
+    dev = batch.device(moe)
+    for path in each_path():
+        out, lse = cache.attention(q, dev, window=window, sinks=sinks, lse=True)
+        cache.check()
+        check_attention(out, lse, ref, path)
