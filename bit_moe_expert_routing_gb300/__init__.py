@@ -319,6 +319,13 @@ def ws_tensor(workspace, ptr: int, shape, dtype):
     return workspace[off:off + n * itemsize].view(dtype).reshape(shape)
 
 
+def _int32(**values):
+    """Refuses what a C int does not hold (ctypes would cut it without a word)."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name}: {v} is not a 32-bit integer")
+
+
 class KVBatch:
     """The sequences of one step (moe_kv_batch): int32 device tensors `q_off`
     [n_seqs + 1], `kv_len` [n_seqs] and `block_table` [n_seqs, pages], and the
@@ -330,6 +337,9 @@ class KVBatch:
         for name, t, nd in (("q_off", q_off, 1), ("kv_len", kv_len, 1), ("block_table", block_table, 2)):
             if t.dtype != torch.int32 or t.dim() != nd or t.device.type != "cuda" or (t.numel() and t.stride(-1) != 1):
                 raise ValueError(f"{name}: a CUDA int32 tensor with {nd} dimension(s), last one contiguous")
+            if t.device != q_off.device:
+                raise ValueError("q_off, kv_len and block_table: on one device")
+        _int32(n_tokens=n_tokens, max_new=max_new, max_kv=max_kv)
         n = kv_len.shape[0]
         if q_off.shape[0] != n + 1 or block_table.shape[0] != n:
             raise ValueError("q_off has n_seqs + 1 entries, kv_len and block_table n_seqs")
@@ -338,7 +348,7 @@ class KVBatch:
         if stride != block_table.shape[1]:
             raise ValueError("block_table: contiguous")
         self._t = (q_off, kv_len, block_table)
-        self.n_tokens = n_tokens
+        self.n_tokens, self.device = n_tokens, q_off.device
         self.c = moe_kv_batch(n, n_tokens, max_new, max_kv, q_off.data_ptr(), kv_len.data_ptr(),
                               block_table.data_ptr(), stride)
         self._ref = ctypes.byref(self.c)
@@ -387,6 +397,12 @@ class KVCache:
             return stream.cuda_stream
         return self._torch._C._cuda_getCurrentRawStream(self.device.index)  # without the stream object's 2 us
 
+    def _batch(self, batch):
+        """The batch, whose pointers go to this cache's device."""
+        if batch.device != self.device:
+            raise ValueError("batch: on the cache's device")
+        return batch._ref
+
     def _rows(self, name, t, n_tokens, heads):
         """Checks a [n_tokens, heads, head dim] operand; its elements between tokens."""
         d = self.head_dim
@@ -403,7 +419,7 @@ class KVCache:
         """Quantises k, v (bf16 [n_tokens, kv heads, head dim]) into the cache."""
         ks = self._rows("k", k, batch.n_tokens, self.kv_heads)
         vs = self._rows("v", v, batch.n_tokens, self.kv_heads)
-        st = lib().moe_kv_append(self._ref, batch._ref, k.data_ptr(), ks, v.data_ptr(), vs, self._stream(stream))
+        st = lib().moe_kv_append(self._ref, self._batch(batch), k.data_ptr(), ks, v.data_ptr(), vs, self._stream(stream))
         if st:
             _check(st, "moe_kv_append")
 
@@ -412,10 +428,11 @@ class KVCache:
         if stream is not None:
             with self._torch.cuda.stream(stream):
                 return self.read(batch)
+        b = self._batch(batch)
         shape = (batch.n_tokens, self.kv_heads, self.head_dim)
         k = self._torch.empty(shape, dtype=self._bf16, device=self.device)
         v = self._torch.empty(shape, dtype=self._bf16, device=self.device)
-        st = lib().moe_kv_read(self._ref, batch._ref, k.data_ptr(), v.data_ptr(), self._stream(None))
+        st = lib().moe_kv_read(self._ref, b, k.data_ptr(), v.data_ptr(), self._stream(None))
         if st:
             _check(st, "moe_kv_read")
         return k, v
@@ -423,6 +440,7 @@ class KVCache:
     def attention_workspace(self, heads: int, batch: KVBatch, window: int = 0, sinks: int = 0):
         """A workspace for attention() with these arguments (a larger batch's serves a smaller one)."""
         import torch
+        _int32(heads=heads, window=window, sinks=sinks)
         n = moe_attention_workspace_size(self.c, batch.c, moe_attention(heads, window, sinks, 1.0))
         if n == 0:
             raise MoEError(MOE_ERR_ARG, "moe_attention_workspace_size")
@@ -439,6 +457,7 @@ class KVCache:
                 return self.attention(q, batch, scale, window, sinks, out, lse, workspace)
         if q.dim() != 3:
             raise ValueError("q: bf16 [n_tokens, heads, head dim]")
+        b = self._batch(batch)
         n, heads, _ = shape = q.shape
         qs = self._rows("q", q, batch.n_tokens, heads)
         if out is None:
@@ -451,14 +470,17 @@ class KVCache:
             lp = l.data_ptr()
         if workspace is None:
             workspace = self.attention_workspace(heads, batch, window, sinks)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous, on the cache's device")
         at = self._settings.get((heads, window, sinks, scale))
         if at is None:
+            _int32(window=window, sinks=sinks)
             if len(self._settings) > 64:
                 self._settings.clear()
             at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
             self._settings[heads, window, sinks, scale] = at = ctypes.byref(at)
-        st = lib().moe_attention_forward(self._ref, batch._ref, at, q.data_ptr(), qs, out.data_ptr(), lp,
-                                         workspace.data_ptr(), workspace.numel(), self._stream(None))
+        st = lib().moe_attention_forward(self._ref, b, at, q.data_ptr(), qs, out.data_ptr(), lp, workspace.data_ptr(),
+                                         workspace.nbytes, self._stream(None))
         if st:
             _check(st, "moe_attention_forward")
         return (out, l) if lse else out

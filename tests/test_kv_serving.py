@@ -130,3 +130,41 @@ def test_places_that_no_row_sees_may_hold_anything(dim, new, kv, window, sinks, 
         out, lse = cache.attention(q, dev, window=window, sinks=sinks, lse=True)
         cache.check()
         check_attention(out, lse, ref, path)
+
+
+def test_handles_refuse_what_the_kernels_cannot_reach():
+    """Tensors elsewhere than the cache, a workspace without memory behind all of it, numbers that a C int would cut."""
+    batch = Batch([1, 2], [40, 30], 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, 64)
+    fill(cache, batch)
+    q, k = rows(3, 8, 64), rows(3, 2, 64)
+    dev = batch.device(moe)
+    n = cache.attention_workspace(8, dev).numel()
+    out = cache.attention(q, dev)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(256, dtype=torch.uint8, device="cuda").expand(n // 256 + 1, 256),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            cache.attention(q, dev, workspace=ws)
+    with pytest.raises(moe.MoEError) as e:
+        cache.attention(q, dev, workspace=torch.empty(n - 256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == moe.MOE_ERR_WORKSPACE
+    assert torch.equal(cache.attention(q, dev, workspace=torch.empty(n // 4 + 1, device="cuda")), out)  # bytes count, of any type
+    away = batch.device(moe)
+    away.device = torch.device("cuda", 1)  # as a batch made on another GPU
+    for call in (lambda: cache.append(k, k, away), lambda: cache.read(away), lambda: cache.attention(q, away)):
+        with pytest.raises(ValueError):
+            call()
+    big = 2 ** 32 + 1
+    for kw in (dict(window=big), dict(sinks=big), dict(window=-big)):
+        with pytest.raises(ValueError):
+            cache.attention(q, dev, **kw)
+        with pytest.raises(ValueError):
+            cache.attention_workspace(8, dev, **kw)
+    t = dev._t
+    for bounds in ((3 + 2 ** 32, 2, 40), (3, big, 40), (3, 2, big)):
+        with pytest.raises(ValueError):
+            moe.KVBatch(*t, *bounds)
+    with pytest.raises(moe.MoEError):  # (in range, and refused by the library)
+        cache.attention(q, dev, window=-1)
+    torch.cuda.synchronize()
+    cache.check()
