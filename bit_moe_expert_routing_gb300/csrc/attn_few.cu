@@ -21,10 +21,12 @@
 // below 256 are, read as a bf16, that integer times 2^-133 (subnormal and
 // first normal binade join). So w & 0x000F000F is the pair (q0, q4) 2^-133, w
 // & 0x00F000F0 is (q1, q5) 2^-129, and one fused multiply-add with scale *
-// 2^113 (2^109) and bias * 2^-20 gives 2^-20 bf16(scale q + bias), rounded
-// once, exactly the cached value. The 2^20 goes into the softmax scale for
-// the keys and into the output for the values. (The cache holds magnitudes
-// up to 2^16, so scale * 2^113 is finite.)
+// 2^110 (2^106) and bias * 2^-23 gives 2^-23 bf16(scale q + bias), rounded
+// once: exactly the cached value, but that a value or bias below 2^-103 is
+// rounded to a multiple of 2^-110. The 2^23 goes into the softmax scale for the keys and
+// into the output for the values. (A smaller power would hold smaller values
+// exactly and overflow on scales below 2^18: a cache's magnitudes of at most
+// 2^16 can come of scales up to 2^17.)
 //
 // Work split: an item is (sequence, kv head, group of 8 NT rows), and its
 // units are its 32-key tiles. One wave of CTAs takes equal, contiguous ranges
@@ -104,10 +106,10 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return r;
 }
 constexpr uint32_t bf16_pow2(int e) { return uint32_t(127 + e) << 7; }
-constexpr uint32_t kMulLo = bf16_pow2(113) * 0x10001u;    // scale of a low nibble: 2^-20 / 2^-133
-constexpr uint32_t kMulHi = bf16_pow2(109) * 0x10001u;    // of a high nibble
-constexpr uint32_t kMulBias = bf16_pow2(-20) * 0x10001u;
-constexpr float kUnscale = 1048576.f;                     // 2^20
+constexpr uint32_t kMulLo = bf16_pow2(110) * 0x10001u;    // scale of a low nibble: 2^-23 / 2^-133
+constexpr uint32_t kMulHi = bf16_pow2(106) * 0x10001u;    // of a high nibble
+constexpr uint32_t kMulBias = bf16_pow2(-23) * 0x10001u;
+constexpr float kUnscale = 8388608.f;                     // 2^23
 
 // Scale and bias of a pair of codes, times the powers above.
 struct Sb {
@@ -714,7 +716,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         const float2 v = ml[w * C::kRows + 8 * n + 2 * c + i];
         sum += ex2(v.x - ref) * v.y;
       }
-      // kUnscale: the values' 2^-20
+      // kUnscale: the values' 2^-23
       fac[i] = sum != 0.f ? ex2(m[n][i] - ref) / sum * kUnscale : 0.f;
       l[n][i] = sum != 0.f ? top + log2f(sum) : -INFINITY;
     }

@@ -323,7 +323,10 @@ moe_status moe_get_device_status_static(void* stream);
  * codes, groups of 64 along the head, one bf16 scale and one bf16 bias per
  * group. A cached value is bf16(scale * code + bias), rounded once to nearest
  * even, the operand value that moe_debug_dequant() shows. Every entry point
- * below sees exactly these values.
+ * below sees exactly these values (but the attention may take a value or bias
+ * below 2^-103 in magnitude for the multiple of 2^-110 next to it). A cache that the caller
+ * fills itself holds scales below 2^18 and values up to 2^16 in magnitude, as
+ * moe_kv_append does.
  *
  * The cache is n_pages pages of page_size token slots that the caller hands
  * out to sequences in any order. All arrays are device memory owned by the

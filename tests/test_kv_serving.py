@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from kv_util import Batch, attention_reference, check_attention, fill, junk_cache  # noqa: E402
+from kv_util import (Batch, attention_reference, bf16_bits, bf16_round, check_attention, fill, junk_cache, pack,  # noqa: E402
+                     values)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -168,3 +169,60 @@ def test_handles_refuse_what_the_kernels_cannot_reach():
         cache.attention(q, dev, window=-1)
     torch.cuda.synchronize()
     cache.check()
+
+
+def coded(cache, batch, which, pick, seed=7):
+    """Puts scales, biases and codes of the caller's own making at every position; returns the values they stand for.
+    pick(r, n) gives the scales, biases and largest codes of n groups."""
+    r = np.random.RandomState(seed)
+    held = []
+    for b in range(len(batch.new)):
+        n, g = batch.kv[b], cache.head_dim // 64
+        s, z, top = (a.reshape(n, cache.kv_heads, g) for a in pick(r, n * cache.kv_heads * g))
+        s, z = bf16_round(s), bf16_round(z)
+        c = r.randint(0, 1 << 30, (n, cache.kv_heads, g, 64)) % (top[..., None] + 1)
+        pg, sl = (torch.from_numpy(a.astype(np.int64)).cuda() for a in batch.places(b))
+        c = c.reshape(n, cache.kv_heads, cache.head_dim)
+        getattr(cache, which + "_codes")[pg, :, sl] = torch.from_numpy(pack(c)).cuda()
+        getattr(cache, which + "_scales")[pg, :, sl] = bf16_bits(s).cuda()
+        getattr(cache, which + "_biases")[pg, :, sl] = bf16_bits(z).cuda()
+        held.append(torch.from_numpy(values(c.astype(np.float64), s, z)).cuda())
+    return held
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,kv", [([1, 3], [700, 77]), ([150], [200])])
+def test_a_cache_of_the_callers_own_making(dim, new, kv, each_path):
+    """Magnitudes up to 2^16 from scales up to 2^17 (append's are below 2^13.2), of either sign."""
+    def pick(r, n):
+        sign = r.choice([-1.0, 1.0], n)
+        e = r.choice([2.0 ** 17, 2.0 ** 16, 40000.0, 2.0 ** 15, 2.0 ** 14, 8000.0, 3.0], n)
+        return sign * e, -sign * 65536.0, np.minimum(15, (131072.0 // e)).astype(np.int64)
+    batch = Batch(new, kv, 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    keys, vals = (coded(cache, batch, w, pick, seed) for w, seed in (("k", 7), ("v", 8)))
+    assert all(t.abs().max() <= 65536 for t in keys + vals)
+    q = rows(batch.n_tokens, 8, dim)
+    scale = float(np.float32(2.0 ** -17))
+    ref = attention_reference(q, batch, keys, vals, scale)
+    dev = batch.device(moe)
+    for path in each_path():
+        out, lse = cache.attention(q, dev, scale=scale, lse=True)
+        cache.check()
+        check_attention(out, lse, ref, path)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_small_values_keep_their_bits(dim, each_path):
+    """Values about 2^-90, in units of which the bounds are as ever."""
+    batch = Batch([2, 150], [300, 200], 16)
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    keys, _ = fill(cache, batch)
+    unit = 2.0 ** -90
+    vals = coded(cache, batch, "v", lambda r, n: (unit * (0.1 + r.rand(n)), -8 * unit * r.rand(n), np.full(n, 15)))
+    q = rows(batch.n_tokens, 8, dim)
+    out, lse, size = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)))
+    dev = batch.device(moe)
+    for path in each_path():
+        got = cache.attention(q, dev)
+        check_attention(got.double() / unit, None, (out / unit, lse, size / unit), path)
