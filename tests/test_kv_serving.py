@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from kv_util import (Batch, attention_reference, bf16_bits, bf16_round, check_attention, fill, junk_cache, pack,  # noqa: E402
-                     values)
+                     quantise, values)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -226,3 +226,56 @@ def test_small_values_keep_their_bits(dim, each_path):
     for path in each_path():
         got = cache.attention(q, dev)
         check_attention(got.double() / unit, None, (out / unit, lse, size / unit), path)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [129, 257, 300])
+@pytest.mark.parametrize("prompt", [False, True])
+def test_many_sequences(dim, n, prompt, each_path):
+    """More sequences than a CTA sums up at a time, some without step tokens at the ends of such a run, lengths that are
+    cut and, with prompt, one of many rows behind the others."""
+    r = np.random.RandomState(n)
+    new = r.choice([0, 1, 1, 1, 3], n)
+    new[120:128], new[-3:-1], new[-1], new[0] = 0, 0, 2, 0
+    kv = new + np.exp(r.uniform(0, np.log(400), n)).astype(int)
+    kv[[5, n // 2, n - 1]] += 1500
+    if prompt:
+        new[n - 2] = kv[n - 2] = 300
+    batch = Batch(new.tolist(), kv.tolist(), 32)
+    cache = junk_cache(moe, batch.n_pages, 32, 2, dim)
+    keys, vals = fill(cache, batch)
+    q = rows(batch.n_tokens, 8, dim)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)))
+    dev = batch.device(moe, max_kv=5000)
+    for path in each_path():
+        out, lse = cache.attention(q, dev, lse=True)
+        cache.check()
+        check_attention(out, lse, ref, path)
+    k = rows(batch.n_tokens, 2, dim, 9)
+    cache.append(k, k, dev)
+    got = cache.read(dev)
+    cache.check()
+    want = values(*quantise(k.double().cpu().numpy()))
+    assert all(np.array_equal(t.double().cpu().numpy(), want) for t in got)
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 8), (128, 16, 2), (256, 16, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1024, 4)])
+def test_a_mixed_step(dim, heads, kv_heads, window, sinks):
+    """Single tokens deep in their contexts, drafted tokens and a later chunk of a prompt in one call, under
+    the bound of a long capacity."""
+    r = np.random.RandomState(dim)
+    new = [1] * 11 + [4, 512, 1, 5]
+    kv = [int(x) for x in np.exp(r.uniform(np.log(200), np.log(4000), 15))]
+    kv[12] = 2300
+    batch = Batch(new, kv, 64)
+    cache = junk_cache(moe, batch.n_pages, 64, kv_heads, dim)
+    keys, vals = fill(cache, batch)
+    q = rows(batch.n_tokens, heads, dim)
+    ref = attention_reference(q, batch, keys, vals, float(np.float32(dim ** -0.5)), window, sinks)
+    dev = batch.device(moe, max_kv=32768)
+    out, lse = cache.attention(q, dev, window=window, sinks=sinks, lse=True)
+    cache.check()
+    check_attention(out, lse, ref)
+    again = cache.attention(q, dev, window=window, sinks=sinks)
+    assert torch.equal(again, out)
