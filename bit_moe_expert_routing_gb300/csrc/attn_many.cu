@@ -1352,12 +1352,12 @@ ManyPlan plan(const AttnArgs& a) {
     return at;
   };
   const size_t tile_bytes = head_bytes / p.tiles_max;
-  const size_t tiles = std::min(size_t(a.kv.n_seqs) * a.kv.kv_heads * p.tiles_max,
-                                std::max<size_t>(p.tiles_max, kPassBytes / tile_bytes));  // of a pass, at least nb nh tiles_max
+  const size_t pass_tiles = std::max<size_t>(p.tiles_max, kPassBytes / tile_bytes);  // at least nb nh tiles_max
+  const size_t seq_tiles = size_t(a.kv.n_seqs) * p.tiles_max, tiles = std::min(seq_tiles * a.kv.kv_heads, pass_tiles);
   const size_t row_tiles = size_t(p.max_row_tiles - p.nb) + a.kv.n_seqs;
   p.kx = put(tiles * tile_bytes / 2);
   p.vx = put(tiles * tile_bytes / 2);
-  p.bad = put(tiles);
+  p.bad = put(std::min(seq_tiles, pass_tiles));  // (with a byte per head, which moves the arrays behind: windowed prompts 1 us slower)
   p.plan = put(sizeof(PlanHdr));
   p.unit_off = put((row_tiles + 1) * 8);
   p.row_tile = put(row_tiles * sizeof(RowTile));
