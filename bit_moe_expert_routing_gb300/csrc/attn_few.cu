@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     const long long begin = cut.begin(blockIdx.x);
     left = cut.begin(blockIdx.x + 1) - begin;
     if (left <= 0) return griddep_wait();
-    int at;  // (a sequence has at most 8 * 256 * 2^19 units)
+    int at;  // (launch() sees to it that a sequence has fewer than 2^31 units)
     b = cut.find(begin, &at);
     sq = items_of(f, b, C::kRows);
     item = at / (kItemCost + sq.tiles.n);
@@ -983,7 +983,10 @@ cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT>);
   if (!ensure_smem_limit(fn, C::kSmem)) return cudaErrorInvalidValue;
   const long long items = 1ll * f.row_groups * f.a.kv.kv_heads * f.a.kv.n_seqs;
-  if (items * C::kRows > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // 32 bits number the items' rows and a sequence's units. (The choice by sizes stays far below, with at most 2^30 of the
+  // latter; with this kernel asked for, a prompt of 2^15 tokens over 2^20 keys may not.)
+  const long long units = 1ll * f.row_groups * f.a.kv.kv_heads * (kItemCost + f.a.kv.max_kv / kTile + 2);
+  if (items * C::kRows > 0x7fffffff || units > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(f.whole ? items : f.max_ctas));
   cfg.blockDim = dim3(kWarps * 32);

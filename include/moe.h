@@ -362,11 +362,13 @@ typedef struct {
  *               are padding: not written, read as zero, attending to nothing.
  *   block_table [n_seqs, table_stride]: page of positions page_size * j ..
  *               page_size * (j + 1) - 1; entries past kv_len are not read
+ *   n_seqs      at most 65535; n_tokens at most 2^20
  *   max_new     upper bound of every sequence's step tokens
  *   max_kv      upper bound of every kv_len, at most 2^24 (bounds chosen by
  *               the caller on the host: no call copies device data back); a
  *               sequence past a bound records MOE_ERR_DEVICE_CHECK and what
- *               lies past it is left out */
+ *               lies past it is left out (of the attention the whole sequence:
+ *               its rows of the output are not written) */
 typedef struct {
   int n_seqs, n_tokens, max_new, max_kv;
   const int32_t* q_off;

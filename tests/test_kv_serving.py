@@ -279,3 +279,20 @@ def test_a_mixed_step(dim, heads, kv_heads, window, sinks):
     check_attention(out, lse, ref)
     again = cache.attention(q, dev, window=window, sinks=sinks)
     assert torch.equal(again, out)
+
+
+def test_more_units_than_32_bits_number_are_refused():
+    """The few-row kernel asked for at a size that it does not number; nothing is launched."""
+    n = 1 << 17
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = moe.KVCache.empty(4, 16, 1, 64)
+    q = torch.empty(n, 64, 64, dtype=torch.bfloat16, device="cuda")
+    batch = moe.KVBatch(i(0, n), i(n), torch.zeros(1, n // 16, dtype=torch.int32, device="cuda"), n, n, 1 << 24)
+    moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, 1)
+    try:
+        ws = cache.attention_workspace(64, batch)
+        with pytest.raises(moe.MoEError) as e:
+            cache.attention(q, batch, workspace=ws)
+        assert e.value.status == moe.MOE_ERR_CUDA and moe.moe_last_launch_count() == 0
+    finally:
+        moe.moe_set_option(moe.MOE_OPT_FORCE_PATH, 0)
