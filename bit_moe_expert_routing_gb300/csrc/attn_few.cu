@@ -46,6 +46,9 @@
 // and 48 multiply. (With the table's entries looked up per tile, not per 32
 // tiles, 75 us.) One sequence at 65537, 16 heads over 2 of 256 dims: 18 us for
 // 37 MB, 3.4 tiles per warp, bound by the chain of its first loads and the join.
+// 32 sequences with a window of 1024, heads of 64, 8 kv heads: 10.5 us for 19 MB in
+// 256 whole items, one or two to an SM, nine tiles per warp one after the other:
+// issue slots 37% of the active cycles, SMs active in 69% of the time.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -601,7 +604,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         }
       }
     }
-    // probabilities; transposed to the B fragments of the value product
+    // probabilities, rounded to the products' type, bf16, after the sums have taken them in fp32 (outputs 0.0020 to 0.0024
+    // off the 64-bit result, relative to its norm, where the output's own rounding makes 0.0017), and transposed to the
+    // B fragments of the value product
     uint2 pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

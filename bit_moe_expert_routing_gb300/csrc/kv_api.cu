@@ -73,8 +73,11 @@ moe_status check_attention(const KvArgs& kv, const moe_attention* a) {
 // dims: one sequence, 1024 rows over no context 9 and 14, over 1000 keys (2^28
 // products) 17 and 21, over 8000 keys (2^31) 43 and 29; 8 sequences, 256 rows
 // over 1000 keys (2^29) 19 and 22, over 8000 keys (2^32) 72 and 45. Over 360
-// sizes this choice is 0.4% slower than the better kernel on average, at most
-// 33%.
+// drawn sizes this choice is 1.1% slower than the better kernel on average and
+// by more than 5% at 16 of them: many sequences of few keys on either side of
+// the switch (46 sequences, 9 tokens over 41 keys, 48 heads over 8 of 256 dims,
+// 64 us for 35; 17 sequences, 136 tokens over 312 keys, 8 heads over 8 of 64
+// dims, 42 for 27).
 int few_rows(const AttnArgs& a, const Options& o) {
   constexpr int kAny = 1 << 30;
   if (o.force_path) return o.force_path == 1 ? kAny : 0;
