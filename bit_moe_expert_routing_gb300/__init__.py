@@ -76,10 +76,29 @@ class moe_attention(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class moe_rotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("axes", ctypes.c_int),
+                ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class moe_kv_pages(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("columns", ctypes.c_int), ("table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("scratch", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class moe_kv_prefix(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int), ("max_tokens", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("max_own", ctypes.c_int), ("seq_off", ctypes.c_void_p), ("length", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes), mirroring include/moe.h
 _VP, _CI, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _W = ctypes.POINTER(moe_weights)
 _KC, _KB, _AT = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch), ctypes.POINTER(moe_attention)
+_RO, _PG, _PX = ctypes.POINTER(moe_rotary), ctypes.POINTER(moe_kv_pages), ctypes.POINTER(moe_kv_prefix)
+_KCS = ctypes.POINTER(_KC)
 _LL = ctypes.c_longlong
 SIGNATURES = {
     "moe_workspace_size": (_SZ, [_W, _CI]),
@@ -99,7 +118,15 @@ SIGNATURES = {
     "moe_expanded_weights_bytes": (_SZ, [_W]),
     "moe_layer_forward_expanded": (_CI, [_W, _VP, _CI, _VP, _VP, _SZ, _VP, _SZ, _VP]),
     "moe_kv_append": (_CI, [_KC, _KB, _VP, _LL, _VP, _LL, _VP]),
+    "moe_kv_append_rotary": (_CI, [_KC, _KB, _RO, _CI, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _VP]),
     "moe_kv_read": (_CI, [_KC, _KB, _VP, _VP, _VP]),
+    "moe_kv_pages_scratch": (_SZ, [_CI, _CI]),
+    "moe_kv_pages_update": (_CI, [_PG, _KB, _KCS, _CI, _VP]),
+    "moe_kv_pages_fork": (_CI, [_PG, _VP, _VP, _CI, _VP]),
+    "moe_kv_pages_compact": (_CI, [_PG, _KCS, _CI, _VP]),
+    "moe_kv_copy_pages": (_CI, [_KCS, _CI, _VP, _VP, _CI, _VP]),
+    "moe_attention_prefix_workspace_size": (_SZ, [_KC, _KB, _PX, _AT]),
+    "moe_attention_prefix_forward": (_CI, [_KC, _KB, _PX, _AT, _VP, _LL, _VP, _VP, _VP, _SZ, _VP]),
     "moe_attention_workspace_size": (_SZ, [_KC, _KB, _AT]),
     "moe_attention_forward": (_CI, [_KC, _KB, _AT, _VP, _LL, _VP, _VP, _VP, _SZ, _VP]),
     "moe_last_launch_count": (_CI, []),
@@ -213,6 +240,12 @@ def moe_kv_append(cache, batch, k_ptr, k_stride, v_ptr, v_stride, stream) -> int
     return lib().moe_kv_append(ctypes.byref(cache), ctypes.byref(batch), k_ptr, k_stride, v_ptr, v_stride, stream)
 
 
+def moe_kv_append_rotary(cache, batch, rotary: moe_rotary, heads, q_ptr, q_stride, q_out_ptr, k_ptr, k_stride, v_ptr, v_stride,
+                         stream) -> int:
+    return lib().moe_kv_append_rotary(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(rotary), heads, q_ptr, q_stride,
+                                      q_out_ptr, k_ptr, k_stride, v_ptr, v_stride, stream)
+
+
 def moe_kv_read(cache, batch, k_ptr, v_ptr, stream) -> int:
     return lib().moe_kv_read(ctypes.byref(cache), ctypes.byref(batch), k_ptr, v_ptr, stream)
 
@@ -224,6 +257,41 @@ def moe_attention_workspace_size(cache, batch, attn: moe_attention) -> int:
 def moe_attention_forward(cache, batch, attn, q_ptr, q_stride, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream) -> int:
     return lib().moe_attention_forward(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(attn), q_ptr, q_stride,
                                        out_ptr, lse_ptr, ws_ptr, ws_bytes, stream)
+
+
+def _caches(caches):
+    """An array of pointers to moe_kv_cache structs."""
+    return (_KC * len(caches))(*(ctypes.pointer(c) for c in caches))
+
+
+def moe_kv_pages_scratch(n_pages: int, n_seqs: int) -> int:
+    return lib().moe_kv_pages_scratch(n_pages, n_seqs)
+
+
+def moe_kv_pages_update(pages: moe_kv_pages, batch, caches, stream) -> int:
+    return lib().moe_kv_pages_update(ctypes.byref(pages), ctypes.byref(batch), _caches(caches), len(caches), stream)
+
+
+def moe_kv_pages_fork(pages: moe_kv_pages, src_ptr, dst_ptr, n, stream) -> int:
+    return lib().moe_kv_pages_fork(ctypes.byref(pages), src_ptr, dst_ptr, n, stream)
+
+
+def moe_kv_pages_compact(pages: moe_kv_pages, caches, stream) -> int:
+    return lib().moe_kv_pages_compact(ctypes.byref(pages), _caches(caches), len(caches), stream)
+
+
+def moe_kv_copy_pages(caches, src_ptr, dst_ptr, n, stream) -> int:
+    return lib().moe_kv_copy_pages(_caches(caches), len(caches), src_ptr, dst_ptr, n, stream)
+
+
+def moe_attention_prefix_workspace_size(cache, batch, prefix: moe_kv_prefix, attn: moe_attention) -> int:
+    return lib().moe_attention_prefix_workspace_size(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(prefix),
+                                                     ctypes.byref(attn))
+
+
+def moe_attention_prefix_forward(cache, batch, prefix, attn, q_ptr, q_stride, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return lib().moe_attention_prefix_forward(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(prefix),
+                                              ctypes.byref(attn), q_ptr, q_stride, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream)
 
 
 def moe_last_launch_count() -> int:
@@ -354,6 +422,58 @@ class KVBatch:
         self._ref = ctypes.byref(self.c)
 
 
+class KVPrefix:
+    """Which sequences of a step share their first positions (moe_kv_prefix): int32 device tensors `seq_off` [n_groups +
+    1] (group g is sequences seq_off[g] .. seq_off[g + 1] - 1) and `length` [n_groups] (positions that a group shares),
+    and the host's bounds: a group's step tokens, the lengths, and a sequence's positions past the shared whole pages.
+    The tensors are kept, not copied."""
+
+    def __init__(self, seq_off, length, max_tokens: int, max_len: int, max_own: int):
+        import torch
+        for name, t in (("seq_off", seq_off), ("length", length)):
+            if t.dtype != torch.int32 or t.dim() != 1 or t.device.type != "cuda" or not t.is_contiguous():
+                raise ValueError(f"{name}: a contiguous CUDA int32 tensor with 1 dimension")
+        if seq_off.device != length.device or seq_off.shape[0] != length.shape[0] + 1:
+            raise ValueError("seq_off has n_groups + 1 entries, length n_groups, on one device")
+        _int32(max_tokens=max_tokens, max_len=max_len, max_own=max_own)
+        self._t, self.device = (seq_off, length), length.device
+        self.c = moe_kv_prefix(length.shape[0], max_tokens, max_len, max_own, seq_off.data_ptr(), length.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+
+class Rotary:
+    """Norms and rotation of a layer's query and key heads (moe_rotary).
+    `inv_freq`: radians per position of each pair of elements (rotary_dim / 2
+    numbers, taken in 64 bits); `axis`: the position axis of each, where there
+    are several (time, height, width); `interleaved`: pairs are neighbours
+    instead of rotary_dim / 2 apart; `q_weight`, `k_weight`: fp32 [head dim]
+    (None: that head is not normed)."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 device="cuda"):
+        import math
+        import torch
+        freq = torch.as_tensor(inv_freq, dtype=torch.float64).flatten().tolist()
+        if len(freq) % 8 or not all(map(math.isfinite, freq)):
+            raise ValueError("inv_freq: finite numbers, a multiple of 8 of them")
+        axis = [0] * len(freq) if axis is None else [int(a) for a in axis]
+        if len(axis) != len(freq) or any(not 0 <= a < 4 for a in axis):
+            raise ValueError("axis: a number from 0 to 3 for every frequency")
+        # turns per position in units of 2^-64: only what is past whole turns counts
+        turns = [int((t - math.floor(t)) * 2 ** 64) % 2 ** 64 for t in (f / (2 * math.pi) for f in freq)]
+        self._turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._axis = torch.tensor(axis, dtype=torch.uint8, device=device)
+        self.device, self.axes, self.rotary_dim = self._turns.device, max(axis, default=0) + 1, 2 * len(freq)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dtype != torch.float32 or w.dim() != 1 or not w.is_contiguous() or w.device != self.device):
+                raise ValueError(f"{name}: contiguous fp32 [head dim] on {self.device}")
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.c = moe_rotary(self.rotary_dim, int(interleaved), self.axes, eps, self._turns.data_ptr(), self._axis.data_ptr(),
+                            None, None if q_weight is None else q_weight.data_ptr(),
+                            None if k_weight is None else k_weight.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+
 class KVCache:
     """A 4-bit key/value cache: the arrays of moe_kv_cache as torch tensors
     (codes int32 [pages, kv heads, page size, head dim / 8]; scales and biases
@@ -423,6 +543,44 @@ class KVCache:
         if st:
             _check(st, "moe_kv_append")
 
+    def append_rotary(self, q, k, v, batch: KVBatch, rotary: Rotary, positions=None, out=None, stream=None):
+        """Norms and turns the heads of q (bf16 [n_tokens, heads, head dim]) and k, v (bf16 [n_tokens, kv heads, head
+        dim]; all may be slices of a fused projection), quantises k and v into the cache and returns q. positions:
+        int32 [n_tokens] or [axes, n_tokens], contiguous; by default each token's position in its sequence."""
+        torch = self._torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.append_rotary(q, k, v, batch, rotary, positions, out)
+        if q.dim() != 3:
+            raise ValueError("q: bf16 [n_tokens, heads, head dim]")
+        b, n = self._batch(batch), batch.n_tokens
+        heads = q.shape[1]
+        qs = self._rows("q", q, n, heads)
+        ks = self._rows("k", k, n, self.kv_heads)
+        vs = self._rows("v", v, n, self.kv_heads)
+        if rotary.device != self.device:
+            raise ValueError("rotary: on the cache's device")
+        for w in (rotary.q_weight, rotary.k_weight):
+            if w is not None and w.shape[0] != self.head_dim:
+                raise ValueError(f"rotary: weights of {self.head_dim} elements")
+        ref = rotary._ref
+        if positions is not None:
+            if positions.dtype != torch.int32 or positions.device != self.device or not positions.is_contiguous() or \
+                    positions.shape not in ((rotary.axes, n), (n,) if rotary.axes == 1 else None):
+                raise ValueError(f"positions: contiguous int32 [{rotary.axes}, {n}] on the cache's device")
+            c = moe_rotary.from_buffer_copy(rotary.c)  # (a handle may be used by two threads)
+            c.positions = positions.data_ptr()
+            ref = ctypes.byref(c)
+        if out is None:
+            out = torch.empty((n, heads, self.head_dim), dtype=self._bf16, device=self.device)
+        elif out.shape != q.shape or out.dtype != self._bf16 or not out.is_contiguous() or out.device != self.device:
+            raise ValueError("out: contiguous, of q's shape, type and device")
+        st = lib().moe_kv_append_rotary(self._ref, b, ref, heads, q.data_ptr(), qs, out.data_ptr(), k.data_ptr(), ks,
+                                        v.data_ptr(), vs, self._stream(None))
+        if st:
+            _check(st, "moe_kv_append_rotary")
+        return out
+
     def read(self, batch: KVBatch, stream=None):
         """The step's tokens as the cache holds them: (k, v) bf16 [n_tokens, kv heads, head dim]."""
         if stream is not None:
@@ -437,24 +595,28 @@ class KVCache:
             _check(st, "moe_kv_read")
         return k, v
 
-    def attention_workspace(self, heads: int, batch: KVBatch, window: int = 0, sinks: int = 0):
+    def attention_workspace(self, heads: int, batch: KVBatch, window: int = 0, sinks: int = 0, prefix: KVPrefix | None = None):
         """A workspace for attention() with these arguments (a larger batch's serves a smaller one)."""
         import torch
         _int32(heads=heads, window=window, sinks=sinks)
-        n = moe_attention_workspace_size(self.c, batch.c, moe_attention(heads, window, sinks, 1.0))
+        at = moe_attention(heads, window, sinks, 1.0)
+        n = moe_attention_workspace_size(self.c, batch.c, at) if prefix is None else \
+            moe_attention_prefix_workspace_size(self.c, batch.c, prefix.c, at)
         if n == 0:
             raise MoEError(MOE_ERR_ARG, "moe_attention_workspace_size")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def attention(self, q, batch: KVBatch, scale: float | None = None, window: int = 0, sinks: int = 0, out=None,
-                  lse: bool = False, workspace=None, stream=None):
+                  lse: bool = False, workspace=None, stream=None, prefix: KVPrefix | None = None):
         """Causal attention of the step's tokens over the cache: q bf16
         [n_tokens, heads, head dim] -> out (the same shape), or (out, lse) with
-        lse fp32 [n_tokens, heads]. scale: 1 / sqrt(head dim) by default."""
+        lse fp32 [n_tokens, heads]. scale: 1 / sqrt(head dim) by default.
+        prefix: what groups of the sequences share at their beginning is
+        attended to once for all of them."""
         torch = self._torch
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.attention(q, batch, scale, window, sinks, out, lse, workspace)
+                return self.attention(q, batch, scale, window, sinks, out, lse, workspace, None, prefix)
         if q.dim() != 3:
             raise ValueError("q: bf16 [n_tokens, heads, head dim]")
         b = self._batch(batch)
@@ -469,7 +631,7 @@ class KVCache:
             l = torch.empty((n, heads), dtype=torch.float32, device=self.device)
             lp = l.data_ptr()
         if workspace is None:
-            workspace = self.attention_workspace(heads, batch, window, sinks)
+            workspace = self.attention_workspace(heads, batch, window, sinks, prefix)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError("workspace: contiguous, on the cache's device")
         at = self._settings.get((heads, window, sinks, scale))
@@ -479,12 +641,98 @@ class KVCache:
                 self._settings.clear()
             at = moe_attention(heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale)
             self._settings[heads, window, sinks, scale] = at = ctypes.byref(at)
-        st = lib().moe_attention_forward(self._ref, b, at, q.data_ptr(), qs, out.data_ptr(), lp, workspace.data_ptr(),
-                                         workspace.nbytes, self._stream(None))
-        if st:
-            _check(st, "moe_attention_forward")
+        if prefix is None:
+            st = lib().moe_attention_forward(self._ref, b, at, q.data_ptr(), qs, out.data_ptr(), lp, workspace.data_ptr(),
+                                             workspace.nbytes, self._stream(None))
+            if st:
+                _check(st, "moe_attention_forward")
+        else:
+            if prefix.device != self.device:
+                raise ValueError("prefix: on the cache's device")
+            st = lib().moe_attention_prefix_forward(self._ref, b, prefix._ref, at, q.data_ptr(), qs, out.data_ptr(), lp,
+                                                    workspace.data_ptr(), workspace.nbytes, self._stream(None))
+            if st:
+                _check(st, "moe_attention_prefix_forward")
         return (out, l) if lse else out
 
     def check(self, stream=None):
         """Synchronises the stream and raises if a call since the last check met a device-side error."""
         _check(moe_get_device_status(ctypes.c_void_p(self.status.data_ptr()), _stream_ptr(stream)), "kv cache")
+
+
+class KVPages:
+    """Which pages of `caches` (KVCaches of one shape, the layers of a model) a set of n_seqs sequences holds
+    (moe_kv_pages), at most `columns` each: int32 device tensors `table` [n_seqs, columns], `held` [n_seqs] and `refs`
+    [n_pages]. All calls are enqueued on `stream` (the current one by default) without host synchronisation; order calls
+    on one set as you would launches on one stream."""
+
+    def __init__(self, caches, n_seqs: int, columns: int):
+        import torch
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("caches: at least one")
+        first = self.caches[0]
+        shape = (first.c.n_pages, first.c.page_size, first.c.kv_heads, first.c.head_dim)
+        for c in self.caches:
+            if (c.c.n_pages, c.c.page_size, c.c.kv_heads, c.c.head_dim) != shape or c.device != first.device:
+                raise ValueError("caches: of one shape, on one device")
+        _int32(n_seqs=n_seqs, columns=columns)
+        n_scratch = moe_kv_pages_scratch(first.c.n_pages, n_seqs)
+        if n_scratch == 0 or not 1 <= columns <= 2 ** 20:
+            raise ValueError("n_seqs: 1 to 65535; columns: 1 to 2^20; at most 2^28 pages")
+        self.n_seqs, self.columns, self.page_size, self.device = n_seqs, columns, first.c.page_size, first.device
+        new = lambda n, v: torch.full(n, v, dtype=torch.int32, device=self.device)  # noqa: E731
+        self.table, self.held, self.refs = new((n_seqs, columns), -1), new((n_seqs,), 0), new((first.c.n_pages,), 0)
+        self._scratch = torch.empty(n_scratch, dtype=torch.int32, device=self.device)
+        self.status = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.c = moe_kv_pages(first.c.n_pages, self.page_size, n_seqs, columns, self.table.data_ptr(), self.held.data_ptr(),
+                              self.refs.data_ptr(), self._scratch.data_ptr(), self.status.data_ptr())
+        self._ref = ctypes.byref(self.c)
+        self._ptrs = _caches([c.c for c in self.caches])
+        self._torch = torch
+
+    def _stream(self, stream):
+        return stream.cuda_stream if stream is not None else self._torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def _numbers(self, name, t, n=None):
+        if t.dtype != self._torch.int32 or t.dim() != 1 or t.device != self.device or not t.is_contiguous() or \
+                (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name}: contiguous int32{'' if n is None else f' [{n}]'} on the caches' device")
+        return t.data_ptr()
+
+    def batch(self, q_off, kv_len, n_tokens: int, max_new: int, max_kv: int) -> KVBatch:
+        """A step of all the sequences, through this set's table."""
+        return KVBatch(q_off, kv_len, self.table, n_tokens, max_new, max_kv)
+
+    def update(self, batch: KVBatch, stream=None):
+        """Gives and takes back pages so that every sequence holds those of the batch's kv_len (0: none), and those that
+        the step's tokens go to alone: shared ones are copied first. `batch` is one of batch()'s."""
+        st = lib().moe_kv_pages_update(self._ref, batch._ref, self._ptrs, len(self.caches), self._stream(stream))
+        if st:
+            _check(st, "moe_kv_pages_update")
+
+    def fork(self, src, dst, stream=None):
+        """Sequences dst (int32 [n] on the device; holding nothing) come to share the pages of sequences src."""
+        n = src.shape[0] if src.dim() == 1 else -1
+        st = lib().moe_kv_pages_fork(self._ref, self._numbers("src", src), self._numbers("dst", dst, n), n, self._stream(stream))
+        if st:
+            _check(st, "moe_kv_pages_fork")
+
+    def compact(self, stream=None):
+        """Moves pages so that those in use come first."""
+        st = lib().moe_kv_pages_compact(self._ref, self._ptrs, len(self.caches), self._stream(stream))
+        if st:
+            _check(st, "moe_kv_pages_compact")
+
+    def copy(self, src, dst, stream=None):
+        """Copies the contents of pages src (int32 [n] on the device) to pages dst, which no other entry names. (Numbers
+        that are no pages are recorded by the first cache.)"""
+        n = src.shape[0] if src.dim() == 1 else -1
+        st = lib().moe_kv_copy_pages(self._ptrs, len(self.caches), self._numbers("src", src), self._numbers("dst", dst, n), n,
+                                     self._stream(stream))
+        if st:
+            _check(st, "moe_kv_copy_pages")
+
+    def check(self, stream=None):
+        """Synchronises the stream and raises if a call since the last check met a device-side error."""
+        _check(moe_get_device_status(ctypes.c_void_p(self.status.data_ptr()), _stream_ptr(stream)), "kv pages")

@@ -273,7 +273,7 @@ struct Cut {
   }
 };
 
-template <int DIM, int NT>
+template <int DIM, int NT, bool PARTS>
 __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attention_few_kernel(const FewArgs f) {
   using C = FewCfg<DIM, NT>;
   using St = Stage<DIM>;
@@ -334,8 +334,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     Tiles tiles;
   } gr;
   gr.n_rows = min(sq.rows - rg * C::kRows, C::kRows);
-  gr.minpos = si.kv - si.n_new + f.token(rg * C::kRows);
-  gr.maxpos = si.kv - si.n_new + f.token(rg * C::kRows + gr.n_rows - 1);
+  const int base = base_pos<PARTS>(a, si);
+  gr.minpos = pos_of<PARTS>(a, base, f.token(rg * C::kRows));
+  gr.maxpos = pos_of<PARTS>(a, base, f.token(rg * C::kRows + gr.n_rows - 1));
   gr.tiles = sq.tiles;
   const int lo_all = a.window > 0 ? max(0, gr.minpos - a.window + 1) : 0;  // first windowed key any row sees
 
@@ -359,15 +360,16 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   // order. Its two halves of 16 keys may lie in different pages. Each lane
   // looks the pages of one of the warp's next 32 tiles up (-1: there is none,
   // recorded, or no row sees a key of that half).
-  const bool has_table = a.kv.table_stride > 0;
-  const int* table = has_table ? a.kv.table + (long long)b * a.kv.table_stride : a.kv.kv_len;
-  const int last_entry = has_table ? a.kv.table_stride - 1 : 0;
+  const KvTable tb = kv_table<PARTS>(a.kv, b);
+  const bool has_table = tb.n > 0;
+  const int* table = has_table ? tb.entry : a.kv.kv_len;
+  const int last_entry = has_table ? tb.n - 1 : 0;
   auto pages_of = [&](int n0, int half) -> int {
     const int t = t_begin + warp + kWarps * (n0 + lane);
     const int k0 = gr.tiles.key0(t) + 16 * half, j = k0 >> a.kv.page_bits;
     const int page = __ldg(table + max(0, min(j, last_entry)));
     const bool unseen = (t >= t_end) | (k0 > gr.maxpos) | ((a.window > 0) & (k0 + 16 <= lo_all) & (k0 >= a.sinks));
-    const bool bad = (j >= a.kv.table_stride) | (unsigned(page) >= unsigned(a.kv.n_pages));
+    const bool bad = (j >= tb.n) | (unsigned(page) >= unsigned(a.kv.n_pages));
     if (bad & !unseen) report(a.kv.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
     return bad | unseen ? -1 : page;
   };
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int pos = si.kv - si.n_new + f.token(rg * C::kRows + 8 * n + 2 * c + i);
+          const int pos = pos_of<PARTS>(a, base, f.token(rg * C::kRows + 8 * n + 2 * c + i));
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -759,15 +761,29 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         if (row >= gr.n_rows) continue;
         const int r = rg * C::kRows + row, t = f.token(r), d = 8 * (VW * g + w);
         const long long at = (long long)(si.first + t) * a.heads + kvh * a.group + r - t * a.group;
-        float v[8];
+        float v[8], lse_out = l[n][i];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[2 * k] = o[n][4 * w + k][i], v[2 * k + 1] = o[n][4 * w + k][2 + i];
-        if (!cut_item) {
+        if (!cut_item && is_first<PARTS>(a)) {
+          float4* dst = reinterpret_cast<float4*>(a.first_o + at * DIM + d);
+          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (g == 0 && w == 0) a.first_lse[at] = l[n][i];
+        } else if (!cut_item) {
+          if (has_first<PARTS>(a, b)) {
+            const Join j = join_of(l[n][i], a.first_lse[at]);
+            const float4* o1 = reinterpret_cast<const float4*>(a.first_o + at * DIM + d);
+            const float4 x = o1[0], y = o1[1];
+            const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = j.own * v[k] + j.first * u[k];
+            if (w == 0) lse_out = j.lse;
+          }
           uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(v[2 * k + 1]), "f"(v[2 * k]));
           *reinterpret_cast<uint4*>(a.out + at * DIM + d) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (g == 0 && w == 0 && a.lse) a.lse[at] = l[n][i] * 0.6931471805599453f;
+          if (g == 0 && w == 0 && a.lse) a.lse[at] = lse_out * 0.6931471805599453f;
         } else {
           float4* dst = reinterpret_cast<float4*>(f.part_o + (size_t(slot) * C::kRows + row) * DIM + d);
           dst[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -793,7 +809,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 // the stream to be ordered behind.
 struct Parts {
   SeqItems sq;
-  int kvh, rg, n_rows, p0, n;
+  int seq, kvh, rg, n_rows, p0, n;
   __device__ __forceinline__ int slot(int p) const { return 2 * (p0 + p) + (p > 0); }
   // place of row `row` of the group in the outputs
   __device__ __forceinline__ long long place(const FewArgs& f, int rows_per_group, int row) const {
@@ -809,6 +825,7 @@ __device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_
   q.n = 0;
   const int per_seq = f.a.kv.kv_heads * f.row_groups;
   const int b = x / per_seq, y = x - b * per_seq;
+  q.seq = b;
   q.kvh = y / f.row_groups;
   q.rg = y - q.kvh * f.row_groups;
   q.sq = items_of(f, b, rows_per_group);
@@ -833,7 +850,7 @@ __device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_
 // in flight, the first eight while the weights are made: bound by this chain of
 // loads. (16 sequences of 4 tokens, 13 parts an item: the call 24.7 us, 26.3
 // with the weights first; the same for few items below gains nothing.)
-template <int DIM>
+template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group) {
   constexpr int kV = DIM / 128 + (DIM < 128);  // float4 of a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
@@ -878,21 +895,42 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
     }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  float lse = sum != 0.f ? top + log2f(sum) : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k].x *= inv, o[k].y *= inv, o[k].z *= inv, o[k].w *= inv;
+  if (is_first<PARTS>(f.a)) {
+    if (mine)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(f.a.first_o + at * DIM)[lane + 32 * k] = o[k];
+    if (lane == 0) f.a.first_lse[at] = lse;
+    return;
+  }
+  if (has_first<PARTS>(f.a, q.seq)) {
+    const Join j = join_of(lse, f.a.first_lse[at]);
+    lse = j.lse;
+    if (mine)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        const float4 u = reinterpret_cast<const float4*>(f.a.first_o + at * DIM)[lane + 32 * k];
+        o[k].x = j.own * o[k].x + j.first * u.x, o[k].y = j.own * o[k].y + j.first * u.y;
+        o[k].z = j.own * o[k].z + j.first * u.z, o[k].w = j.own * o[k].w + j.first * u.w;
+      }
+  }
   if (mine)
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       uint2 h;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(o[k].y * inv), "f"(o[k].x * inv));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(o[k].w * inv), "f"(o[k].z * inv));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(o[k].y), "f"(o[k].x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(o[k].w), "f"(o[k].z));
       *reinterpret_cast<uint2*>(f.a.out + at * DIM + 4 * (lane + 32 * k)) = h;
     }
-  if (lane == 0 && f.a.lse) f.a.lse[at] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (lane == 0 && f.a.lse) f.a.lse[at] = lse * 0.6931471805599453f;
 }
 
 // The same for few items with many parts each, which want all of the GPU: a
 // CTA per (item, row, 64 dims), sixteen threads on the dims and sixteen such
 // groups on the parts, eight loads in flight each.
-template <int DIM>
+template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewArgs f, int rows_per_group, int rows) {
   constexpr int kLanes = 16, kGroups = 16;
   constexpr int kMaxParts = 1024;  // (no item has more parts than there are CTAs)
@@ -951,11 +989,25 @@ __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewAr
       v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
     const float inv = tot != 0.f ? 1.f / tot : 0.f;
+    float lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    if (is_first<PARTS>(f.a)) {
+      *reinterpret_cast<float4*>(f.a.first_o + at * DIM + d) = v;
+      if (d == 0) f.a.first_lse[at] = lse;
+      return;
+    }
+    if (has_first<PARTS>(f.a, q.seq)) {
+      const Join j = join_of(lse, f.a.first_lse[at]);
+      const float4 u = *reinterpret_cast<const float4*>(f.a.first_o + at * DIM + d);
+      lse = j.lse;
+      v.x = j.own * v.x + j.first * u.x, v.y = j.own * v.y + j.first * u.y;
+      v.z = j.own * v.z + j.first * u.z, v.w = j.own * v.w + j.first * u.w;
+    }
     uint2 h;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y * inv), "f"(v.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(v.w * inv), "f"(v.z * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y), "f"(v.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(v.w), "f"(v.z));
     *reinterpret_cast<uint2*>(f.a.out + at * DIM + d) = h;
-    if (d == 0 && f.a.lse) f.a.lse[at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+    if (d == 0 && f.a.lse) f.a.lse[at] = lse * 0.6931471805599453f;
   }
 }
 
@@ -982,10 +1034,10 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
   return p;
 }
 
-template <int DIM, int NT>
+template <int DIM, int NT, bool PARTS>
 cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   using C = FewCfg<DIM, NT>;
-  const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT>);
+  const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT, PARTS>);
   if (!ensure_smem_limit(fn, C::kSmem)) return cudaErrorInvalidValue;
   const long long items = 1ll * f.row_groups * f.a.kv.kv_heads * f.a.kv.n_seqs;
   // 32 bits number the items' rows and a sequence's units. (The choice by sizes stays far below, with at most 2^30 of the
@@ -1002,7 +1054,7 @@ cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = beside ? 1 : 0;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_few_kernel<DIM, NT>, f)) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, attention_few_kernel<DIM, NT, PARTS>, f)) return e;
   if (cudaError_t e = c.launched("attention_few")) return e;
   if (f.whole) return cudaSuccess;
   const int rows = int(std::min<long long>({(long long)f.a.kv.max_new * f.a.group, f.max_rows, C::kRows}));
@@ -1013,10 +1065,24 @@ cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, attention_combine_wide_kernel<DIM>, f, C::kRows, rows)
-                           : cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM>, f, C::kRows))
+  if (cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, attention_combine_wide_kernel<DIM, PARTS>, f, C::kRows, rows)
+                           : cudaLaunchKernelEx(&cfg, attention_combine_kernel<DIM, PARTS>, f, C::kRows))
     return e;
   return c.launched("attention_combine");
+}
+
+template <bool PARTS>
+cudaError_t launch_as(const FewArgs& f, int nt, bool beside, const KvCall& c) {
+  switch (f.a.kv.dim * 8 + nt) {
+    case 64 * 8 + 1: return launch<64, 1, PARTS>(f, beside, c);
+    case 64 * 8 + 2: return launch<64, 2, PARTS>(f, beside, c);
+    case 64 * 8 + 4: return launch<64, 4, PARTS>(f, beside, c);
+    case 128 * 8 + 1: return launch<128, 1, PARTS>(f, beside, c);
+    case 128 * 8 + 2: return launch<128, 2, PARTS>(f, beside, c);
+    case 128 * 8 + 4: return launch<128, 4, PARTS>(f, beside, c);
+    case 256 * 8 + 1: return launch<256, 1, PARTS>(f, beside, c);
+    default: return launch<256, 2, PARTS>(f, beside, c);
+  }
 }
 
 }  // namespace
@@ -1035,16 +1101,7 @@ cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside
   float* part = static_cast<float*>(ws);
   const FewArgs f{a,    max_rows, p.row_groups, p.whole, p.ctas, part, part + p.part_rows * a.kv.dim,
                   ((1ull << 32) + a.group - 1) / a.group};
-  switch (a.kv.dim * 8 + p.nt) {
-    case 64 * 8 + 1: return launch<64, 1>(f, beside, c);
-    case 64 * 8 + 2: return launch<64, 2>(f, beside, c);
-    case 64 * 8 + 4: return launch<64, 4>(f, beside, c);
-    case 128 * 8 + 1: return launch<128, 1>(f, beside, c);
-    case 128 * 8 + 2: return launch<128, 2>(f, beside, c);
-    case 128 * 8 + 4: return launch<128, 4>(f, beside, c);
-    case 256 * 8 + 1: return launch<256, 1>(f, beside, c);
-    default: return launch<256, 2>(f, beside, c);
-  }
+  return a.part == AttnArgs::kWhole ? launch_as<false>(f, p.nt, beside, c) : launch_as<true>(f, p.nt, beside, c);
 }
 
 }  // namespace moe

@@ -169,9 +169,10 @@ __device__ __forceinline__ bool taken(const ManyArgs& m, const SeqInfo& s) { ret
 __device__ __forceinline__ Range seq_range(const ManyArgs& m, const SeqInfo& s) {
   return range_of(s.kv - s.n_new, s.kv - 1, m.a.window, m.a.sinks);
 }
+template <bool PARTS>
 __device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s, int row0, int rows) {
-  const int base = s.kv - s.n_new, last = min(row0 + rows, s.n_new * m.a.group) - 1;
-  return range_of(base + m.token(row0), base + m.token(last), m.a.window, m.a.sinks);
+  const int base = base_pos<PARTS>(m.a, s), last = min(row0 + rows, s.n_new * m.a.group) - 1;
+  return range_of(pos_of<PARTS>(m.a, base, m.token(row0)), pos_of<PARTS>(m.a, base, m.token(last)), m.a.window, m.a.sinks);
 }
 
 // Byte offset of 16-byte chunk c of row r in a 1024-aligned 128-byte-swizzled K-major block.
@@ -203,6 +204,7 @@ __device__ long long block_scan(long long v, long long* total, long long* buf) {
   return v + before;
 }
 
+template <bool PARTS>
 __device__ void make_plan(const ManyArgs& m, int rows) {
   __shared__ long long buf[kPlanThreads / 32];
   __shared__ SeqInfo info[kPlanThreads];
@@ -235,7 +237,7 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
         const SeqInfo q = info[lo];
         const int row0 = (i - (lo ? ends[lo - 1] : 0)) * rows;
         m.row_tile[n_rt + i] = RowTile{m.b0 + base + lo, row0, q.first, q.n_new, q.kv, {}};
-        n = kTileCost + rows_range(m, q, row0, rows).n;
+        n = kTileCost + rows_range<PARTS>(m, q, row0, rows).n;
       }
       long long sum;
       const long long end = block_scan(n, &sum, buf);
@@ -287,11 +289,11 @@ __device__ __forceinline__ uint32_t dq_pair(uint32_t p, __nv_bfloat162 s2, __nv_
 // CTA 0 makes the plan; the others expand the keys or the values of one key
 // tile of one (sequence, kv head): the keys row by row, the values eight keys of eight dims at a time,
 // which leaves the transposed 16-byte chunks in registers.
-template <int DIM>
+template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs m) {
   griddep_launch();
   if (blockIdx.x == 0) {
-    make_plan(m, ManyCfg<DIM>::kPairRows);
+    make_plan<PARTS>(m, ManyCfg<DIM>::kPairRows);
     return;
   }
   __shared__ long long rows16[kBK / 16];  // first cache row of each 16 keys, -1: zeros
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
       const int k = k0 + 16 * threadIdx.x;
       long long row = -1;
       if (k <= maxpos && (k + 16 > lo || k < m.a.sinks)) {
-        row = kv_page_row(kv, b, k >> kv.page_bits, m.h0 + h);
+        row = kv_page_row<PARTS>(kv, b, k >> kv.page_bits, m.h0 + h);
         missing = row < 0;
         if (row >= 0) row += k & ((1 << kv.page_bits) - 1);
       }
@@ -613,6 +615,7 @@ __device__ __forceinline__ int tiles_before(long long u, long long u0, int n) {
 
 // Steps through the units [u, end) of a pair. Every row tile has kTileCost
 // units more than key tiles; a part that holds none of the latter is skipped.
+template <bool PARTS>
 struct Cursor {
   const ManyArgs& m;
   long long u, end, units;
@@ -636,7 +639,7 @@ struct Cursor {
       if (j1 > j0) {
         const RowTile t = m.row_tile[rt];
         const SeqInfo si = t.info();
-        const Range all = seq_range(m, si), mine = rows_range(m, si, t.row0, 2 * rows);
+        const Range all = seq_range(m, si), mine = rows_range<PARTS>(m, si, t.row0, 2 * rows);
         s->seq = t.seq - m.b0;
         s->head = head;
         s->row0 = t.row0 + rank * rows;
@@ -647,7 +650,7 @@ struct Cursor {
         s->n = n;
         s->part = j0 == 0 && j1 == n ? -1 : 2 * (2 * pair + (j0 > 0 ? 1 : 0)) + rank;
         s->first = si.first;
-        s->base_pos = si.kv - si.n_new;
+        s->base_pos = base_pos<PARTS>(m.a, si);
         s->all_sink = all.n_sink, s->all_first = all.first;
         s->my_sink = mine.n_sink, s->my_first = mine.first;
         s->u0 = o0;
@@ -689,7 +692,7 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int DIM>
+template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
   using C = ManyCfg<DIM>;
   constexpr int QT = C::QT, UN = C::UN, kRing = C::kRing;
@@ -879,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
     }
   } else {
     // ---------------- segments and query rows: two warps; lane 0 of the first steps through the units ----------
-    Cursor cur(m);
+    Cursor<PARTS> cur(m);
     Segment s;
     bool ok = true;
     auto produce = [&](uint32_t i) {
@@ -975,8 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       if (lane == 0) mbar_arrive(dempty(sg));
       float ref = -INFINITY, sum = 0.f;
       const int r0 = s.row0 + q * 128;
-      const int pos = s.base_pos + m.token(min(r0 + row, s.last));
-      const int minpos = s.base_pos + m.token(min(r0, s.last)), maxpos = s.base_pos + m.token(min(r0 + 127, s.last));
+      const int pos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + row, s.last)));
+      const int minpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0, s.last)));
+      const int maxpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + 127, s.last)));
       const int n = s.j1 - s.j0;
       const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
       const int first = kTurns ? (wg ^ g0) & 1 : 0;  // of this warpgroup's tiles
@@ -1114,32 +1118,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           tot = wg ? a2 + a1 : a1 + a2;
           ref = to;
         }
-        const float inv = tot != 0.f ? 1.f / tot : 0.f;
-        const float lse = tot != 0.f ? ref + log2f(tot) : -INFINITY;
+        float inv = tot != 0.f ? 1.f / tot : 0.f;
+        float lse = tot != 0.f ? ref + log2f(tot) : -INFINITY;
         wait_product(gl, 228);
         tc_fence_after();
         const int r = q * 128 + row;
-        const bool valid = r < s.n_rows, part = s.part >= 0;
+        const bool valid = r < s.n_rows, part = s.part >= 0, first = is_first<PARTS>(a);
         const int rr = min(s.row0 + r, s.last), t = m.token(rr);
         const long long at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
         const long long prow = (long long)s.part * C::kRows + r;
+        float with = 0.f;  // weight of the row's first part, if this is the second
+        if (!part && valid && has_first<PARTS>(a, m.b0 + s.seq)) {
+          const Join j = join_of(lse, a.first_lse[at]);
+          inv *= j.own, with = j.first, lse = j.lse;
+        }
+        float* dst32 = part ? m.part_o + prow * DIM : a.first_o + at * DIM;
 #pragma unroll 1
         for (int cc = 0; cc < kOCols; cc += 32) {
           uint32_t o[32];
           tmem_ld32(ocol + cc, o);
           tmem_wait_ld32(o);
           const int d = ohalf * kOCols + cc;
-          if (part) {
-            float* dst = m.part_o + prow * DIM + d;
+          if (part || (first && valid)) {
+            float* dst = dst32 + d;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) st_v8(dst + e, o + e);
           } else if (valid) {
             uint16_t* dst = a.out + at * DIM + d;
+            if (with != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              o[e / 2] = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              for (int e = 0; e < 32; e += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(a.first_o + at * DIM + d + e);
+                const float x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[e + k] = __float_as_uint(__uint_as_float(o[e + k]) * inv + with * x[k]);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) o[e / 2] = pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                o[e / 2] = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+            }
             if (wide) {
               st_v8(dst, o), st_v8(dst + 16, o + 8);
             } else {
@@ -1152,6 +1174,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         if (ohalf == 0) {
           if (part)
             m.part_lse[prow] = lse;
+          else if (valid && first)
+            a.first_lse[at] = lse;
           else if (valid && a.lse)
             a.lse[at] = lse * 0.6931471805599453f;
         }
@@ -1194,7 +1218,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           const float inv = tot != 0.f ? 1.f / tot : 0.f;
           const int rr = min(s.row0 + my_row, s.last), t = m.token(rr);
           const long long my_at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
-          if (has_row && a.lse) a.lse[my_at] = tot != 0.f ? (top + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+          const bool first = is_first<PARTS>(a);
+          float my_own = 1.f, my_first = 0.f, my_lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
+          if (has_row && has_first<PARTS>(a, m.b0 + s.seq)) {
+            const Join j = join_of(my_lse, a.first_lse[my_at]);
+            my_own = j.own, my_first = j.first, my_lse = j.lse;
+          }
+          if (has_row && first) a.first_lse[my_at] = my_lse;
+          if (has_row && !first && a.lse) a.lse[my_at] = my_lse * 0.6931471805599453f;
           for (int b0 = 0; warp + kSoftWarps * b0 < s.n_rows; b0 += kBatch) {
             float4 o[kBatch][kV];
 #pragma unroll
@@ -1202,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
               for (int k = 0; k < kV; ++k) o[b][k] = make_float4(0.f, 0.f, 0.f, 0.f);
             each_part([&](long long at) {
-              const float w = has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) * inv : 0.f;
+              const float w = has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) * inv * my_own : 0.f;
               float4 v[kBatch][kV];
 #pragma unroll
               for (int b = 0; b < kBatch; ++b) {
@@ -1223,7 +1254,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
               const long long at = __shfl_sync(~0u, my_at, (b0 + b) & 31);
-              if (mine && warp + kSoftWarps * (b0 + b) < s.n_rows)
+              const float with = __shfl_sync(~0u, my_first, (b0 + b) & 31);
+              if (!mine || warp + kSoftWarps * (b0 + b) >= s.n_rows) continue;
+              if (first) {
+#pragma unroll
+                for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(a.first_o + at * DIM)[lane + 32 * k] = o[b][k];
+                continue;
+              }
+              if (with != 0.f)
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                  const float4 u = reinterpret_cast<const float4*>(a.first_o + at * DIM)[lane + 32 * k];
+                  o[b][k].x += with * u.x, o[b][k].y += with * u.y, o[b][k].z += with * u.z, o[b][k].w += with * u.w;
+                }
 #pragma unroll
                 for (int k = 0; k < kV; ++k)
                   *reinterpret_cast<uint2*>(a.out + at * DIM + 4 * (lane + 32 * k)) =
@@ -1248,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 // Joins the parts of divided row tiles: out = sum_p 2^(lse_p - max) o_p /
 // sum_p 2^(lse_p - max). CTA (row tile, eight of its rows, kv head), a warp per
 // row, several parts' loads in flight.
-template <int DIM>
+template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
   griddep_wait();
   constexpr int kRows = ManyCfg<DIM>::kRows, kV = DIM / 128 + (DIM < 128);
@@ -1317,12 +1360,33 @@ __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyA
   const int tok = m.token(rr);
   const long long dst = (long long)(t.first + tok) * m.a.heads + (m.h0 + head) * m.a.group + rr - tok * m.a.group;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  float lse = sum != 0.f ? top + log2f(sum) : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k].x *= inv, o[k].y *= inv, o[k].z *= inv, o[k].w *= inv;
+  if (is_first<PARTS>(m.a)) {
+    if (mine)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(m.a.first_o + dst * DIM)[lane + 32 * k] = o[k];
+    if (lane == 0) m.a.first_lse[dst] = lse;
+    return;
+  }
+  if (has_first<PARTS>(m.a, t.seq)) {
+    const Join j = join_of(lse, m.a.first_lse[dst]);
+    lse = j.lse;
+    if (mine)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        const float4 u = reinterpret_cast<const float4*>(m.a.first_o + dst * DIM)[lane + 32 * k];
+        o[k].x = j.own * o[k].x + j.first * u.x, o[k].y = j.own * o[k].y + j.first * u.y;
+        o[k].z = j.own * o[k].z + j.first * u.z, o[k].w = j.own * o[k].w + j.first * u.w;
+      }
+  }
   if (mine)
 #pragma unroll
     for (int k = 0; k < kV; ++k)
       *reinterpret_cast<uint2*>(m.a.out + dst * DIM + 4 * (lane + 32 * k)) =
-          make_uint2(pack2(o[k].x * inv, o[k].y * inv), pack2(o[k].z * inv, o[k].w * inv));
-  if (lane == 0 && m.a.lse) m.a.lse[dst] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          make_uint2(pack2(o[k].x, o[k].y), pack2(o[k].z, o[k].w));
+  if (lane == 0 && m.a.lse) m.a.lse[dst] = lse * 0.6931471805599453f;
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -1399,27 +1463,33 @@ cudaError_t launch_beside(const KvCall& c, const char* name, void (*kernel)(KArg
   return c.launched(name);
 }
 
-template <int DIM>
+template <int DIM, bool PARTS>
 cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
   using C = ManyCfg<DIM>;
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(&attention_many_kernel<DIM>), C::kSmem)) return cudaErrorInvalidValue;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(&attention_many_kernel<DIM, PARTS>), C::kSmem)) return cudaErrorInvalidValue;
   for (m.b0 = 0; m.b0 < m.a.kv.n_seqs; m.b0 += p.nb)
     for (m.h0 = 0; m.h0 < m.a.kv.kv_heads; m.h0 += p.nh) {
       m.nb = std::min(p.nb, m.a.kv.n_seqs - m.b0);
       m.nh = std::min(p.nh, m.a.kv.kv_heads - m.h0);
       const long long grid = 1 + 2ll * m.nb * m.nh * p.tiles_max;
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-      attention_expand_kernel<DIM><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
+      attention_expand_kernel<DIM, PARTS><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
       if (cudaError_t e = c.launched("attention_expand")) return e;
-      if (cudaError_t e = launch_beside(c, "attention_many", attention_many_kernel<DIM>, dim3(2 * p.pairs), kThreads,
+      if (cudaError_t e = launch_beside(c, "attention_many", attention_many_kernel<DIM, PARTS>, dim3(2 * p.pairs), kThreads,
                                         C::kSmem, 2, m))
         return e;
       if (!m.join)
-        if (cudaError_t e = launch_beside(c, "attention_many_combine", attention_many_combine_kernel<DIM>,
+        if (cudaError_t e = launch_beside(c, "attention_many_combine", attention_many_combine_kernel<DIM, PARTS>,
                                           dim3(p.max_row_tiles, C::kPairRows / 8, m.nh), 256, 0, 1, m))
           return e;
     }
   return cudaSuccess;
+}
+
+template <bool PARTS>
+cudaError_t launch_as(const ManyArgs& m, const ManyPlan& p, const KvCall& c) {
+  const int dim = m.a.kv.dim;
+  return dim == 64 ? launch<64, PARTS>(m, p, c) : dim == 128 ? launch<128, PARTS>(m, p, c) : launch<256, PARTS>(m, p, c);
 }
 
 }  // namespace
@@ -1454,7 +1524,7 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
   m.inv_group = ((1ull << 32) + a.group - 1) / a.group;
-  return a.kv.dim == 64 ? launch<64>(m, p, c) : a.kv.dim == 128 ? launch<128>(m, p, c) : launch<256>(m, p, c);
+  return a.part == AttnArgs::kWhole ? launch_as<false>(m, p, c) : launch_as<true>(m, p, c);
 }
 
 }  // namespace moe

@@ -1,0 +1,192 @@
+// Attention of sequences that share their first positions, group by group.
+//
+// A row's softmax over all of its keys is that over the shared ones joined
+// with that over its own: with m = max(l1, l2), o = (2^(l1 - m) o1 + 2^(l2 - m)
+// o2) / (2^(l1 - m) + 2^(l2 - m)), l the base-2 log-sum-exps. Both are the step
+// as other steps of the same kernels:
+//
+//   first    groups as sequences: all step tokens of a group are rows that see
+//            all of its shared positions. Outputs in fp32.
+//   second   the step itself over what lies past the shared positions; where a
+//            row's output is written it is joined with the first part.
+//
+// The shared keys are read (and, for the tensor cores, expanded) once per
+// group instead of once per sequence, and a group's rows together fill the
+// products' tiles. A small kernel makes both steps' lengths and offsets on the
+// device. What it costs is that kernel, the second set of launches and the
+// rows' fp32 outputs, written and read once.
+#include "kv_host.cuh"
+
+namespace moe {
+namespace {
+
+struct PrefixArgs {
+  KvArgs kv;
+  int n_groups, max_tokens, max_len;
+  const int32_t* seq_off;
+  const int32_t* length;
+  // for the kernels
+  int32_t* group_off;  // [n_groups + 1] first step token
+  int32_t* group_len;  // [n_groups] shared positions, whole pages
+  int32_t* group_row;  // [n_groups] row of the table
+  int32_t* own_len;    // [n_seqs] positions past the shared ones
+  int32_t* skip;       // [n_seqs] shared positions
+};
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBadGroups = 204;  // detail in the status word
+
+// One CTA: groups first, then sequences. Nothing is shared unless all groups
+// are in order, so that the kernels may go by the sums of their sizes.
+__global__ void __launch_bounds__(kPlanThreads) attention_prefix_plan_kernel(const PrefixArgs p) {
+  const KvArgs& a = p.kv;
+  bool bad = p.seq_off[0] != 0 || p.seq_off[p.n_groups] != a.n_seqs || a.q_off[0] != 0 || a.q_off[a.n_seqs] != a.n_tokens;
+  for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+    const int s0 = p.seq_off[g], s1 = p.seq_off[g + 1], len = p.length[g];
+    bool ok = s0 >= 0 && s0 <= s1 && s1 <= a.n_seqs && len >= 0 && len <= p.max_len;
+    const int q0 = ok ? a.q_off[s0] : 0, q1 = ok ? a.q_off[s1] : 0;
+    ok &= q0 >= 0 && q0 <= q1 && q1 <= a.n_tokens && q1 - q0 <= p.max_tokens;
+    bad |= !ok;
+    p.group_off[g] = q0;
+    if (g == p.n_groups - 1) p.group_off[g + 1] = q1;
+    p.group_len[g] = ok ? len >> a.page_bits << a.page_bits : -1;
+    p.group_row[g] = ok ? min(s0, a.n_seqs - 1) : 0;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kBadGroups);
+  for (int b = threadIdx.x; b < a.n_seqs; b += kPlanThreads) {
+    const int q0 = a.q_off[b], n = a.q_off[b + 1] - q0, kv = a.kv_len[b];
+    int skip = 0;
+    if (!bad) {
+      int lo = 0, hi = p.n_groups - 1;  // the last group that begins at or before b
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.seq_off[mid] <= b)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int len = p.length[lo] >> a.page_bits << a.page_bits;
+      // (its rows are among the group's: offsets that do not ascend within one leave them out)
+      const bool inside = n >= 0 && q0 >= a.q_off[p.seq_off[lo]] && q0 + n <= a.q_off[p.seq_off[lo + 1]];
+      if (inside && kv <= a.max_kv && kv - n >= len) skip = len;
+    }
+    p.skip[b] = skip;
+    p.own_len[b] = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
+  }
+}
+
+struct PrefixPlan {
+  AttnArgs first, second;
+  int few_first, few_second;
+  size_t group_off, group_len, group_row, own_len, skip, lse, o, attend, total;
+};
+
+moe_status check_prefix(const KvArgs& kv, const moe_kv_prefix* x) {
+  if (!x || x->n_groups < 0 || x->n_groups > 65535 || x->max_tokens < 0 || x->max_len < 0 || x->max_len > (1 << 24) ||
+      x->max_own < 0 || x->max_own > (1 << 24))
+    return MOE_ERR_ARG;
+  if (x->n_groups && kv.n_tokens &&
+      (!x->seq_off || !x->length || !aligned(x->seq_off, 4) || !aligned(x->length, 4)))
+    return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+// Whether the step is taken in two parts. (One with a window reads what is near each sequence's end.)
+bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x) {
+  return at.window == 0 && x.n_groups > 0 && x.n_groups < a.kv.n_seqs && x.max_tokens > 0 &&
+         x.max_len >= (1 << a.kv.page_bits);
+}
+
+PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
+  PrefixPlan p{a, a};
+  p.first.kv.n_seqs = x.n_groups;
+  p.first.kv.max_new = std::min(x.max_tokens, a.kv.n_tokens);
+  p.first.kv.max_kv = x.max_len;
+  p.first.part = AttnArgs::kFirst;
+  p.second.kv.max_kv = std::min(x.max_own, a.kv.max_kv);
+  p.second.part = AttnArgs::kSecond;
+  p.few_first = few_rows(p.first, opt);
+  p.few_second = few_rows(p.second, opt);
+  size_t o = 0;
+  auto put = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) & ~size_t(255);
+    return at;
+  };
+  p.group_off = put((size_t(x.n_groups) + 1) * 4);
+  p.group_len = put(size_t(x.n_groups) * 4);
+  p.group_row = put(size_t(x.n_groups) * 4);
+  p.own_len = put(size_t(a.kv.n_seqs) * 4);
+  p.skip = put(size_t(a.kv.n_seqs) * 4);
+  p.lse = put(size_t(a.kv.n_tokens) * a.heads * 4);
+  p.o = put(size_t(a.kv.n_tokens) * a.heads * a.kv.dim * 4);
+  p.attend = put(std::max(workspace_bytes_for(p.first, p.few_first), workspace_bytes_for(p.second, p.few_second)));
+  p.total = o;
+  return p;
+}
+
+// Workspace of a call: for either way of taking the step, since a larger one in two parts may be followed by a smaller
+// one in one. (Windows are never taken in two.)
+size_t bytes_for(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x, const Options& opt) {
+  const size_t whole = workspace_bytes_for(a, few_rows(a, opt));
+  return at.window ? whole : std::max(whole, plan(a, x, opt).total);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_attention_prefix_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_kv_prefix* x,
+                                           const moe_attention* at) {
+  KvArgs a;
+  if (make_args(cache, batch, &a) || check_attention(a, at) || check_prefix(a, x)) return 0;
+  const AttnArgs g = attn_args(a, at);
+  const Options opt = options_snapshot();
+  return bytes_for(g, *at, *x, opt);
+}
+
+moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_kv_prefix* x,
+                                        const moe_attention* at, const uint16_t* q, long long q_stride, uint16_t* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  KvArgs a;
+  reset_launch_count();
+  if (moe_status s = make_args(cache, batch, &a)) return s;
+  if (moe_status s = check_attention(a, at)) return s;
+  if (moe_status s = check_prefix(a, x)) return s;
+  if (a.n_tokens == 0) return MOE_OK;
+  if (!operand_ok(q, q_stride, at->heads, a.dim) || !out || !aligned(out, 16) || out == q) return MOE_ERR_ARG;
+  if (lse && !aligned(lse, 4)) return MOE_ERR_ARG;
+  const Options opt = options_snapshot();
+  AttnArgs g = attn_args(a, at);
+  g.q = q;
+  g.q_stride = q_stride;
+  g.out = out;
+  g.lse = lse;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < bytes_for(g, *at, *x, opt)) return MOE_ERR_WORKSPACE;
+  const KvCall c = begin_call(stream, opt);
+  if (!shares(g, *at, *x)) return status_of(attend(g, few_rows(g, opt), workspace, c));
+  PrefixPlan p = plan(g, *x, opt);
+  char* w = static_cast<char*>(workspace);
+  auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };
+  const PrefixArgs args{a, x->n_groups, x->max_tokens, x->max_len, x->seq_off, x->length, ints(p.group_off),
+                        ints(p.group_len), ints(p.group_row), ints(p.own_len), ints(p.skip)};
+  attention_prefix_plan_kernel<<<1, kPlanThreads, 0, c.stream>>>(args);
+  if (cudaError_t e = c.launched("attention_prefix_plan")) return status_of(e);
+  for (AttnArgs* part : {&p.first, &p.second}) {
+    part->first_o = reinterpret_cast<float*>(w + p.o);
+    part->first_lse = reinterpret_cast<float*>(w + p.lse);
+  }
+  p.first.kv.q_off = args.group_off;
+  p.first.kv.kv_len = args.group_len;
+  p.first.kv.rows = args.group_row;
+  p.second.kv.kv_len = args.own_len;
+  p.second.kv.skip = args.skip;
+  if (cudaError_t e = attend(p.first, p.few_first, w + p.attend, c)) return status_of(e);
+  return status_of(attend(p.second, p.few_second, w + p.attend, c));
+}
+
+}  // extern "C"

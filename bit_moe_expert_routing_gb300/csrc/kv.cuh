@@ -20,16 +20,33 @@ struct KvArgs {
   int table_stride;
   int n_seqs, n_tokens, max_new, max_kv;
   int n_pages, page_bits, kv_heads, dim;
+  // A part of every sequence (set by the kernels' callers within the library):
+  const int32_t* rows;  // [n_seqs] its row of the table; NULL: its own number
+  const int32_t* skip;  // [n_seqs] positions before the part's first, whole pages; NULL: none
 };
+
+// A sequence's entries of the table, from its position 0 on.
+struct KvTable {
+  const int32_t* entry;
+  int n;
+};
+template <bool PARTS = false>
+__device__ __forceinline__ KvTable kv_table(const KvArgs& a, int seq) {
+  if (!PARTS) return KvTable{a.table + (long long)seq * a.table_stride, a.table_stride};
+  const int row = a.rows ? a.rows[seq] : seq, before = a.skip ? a.skip[seq] >> a.page_bits : 0;
+  return KvTable{a.table + (long long)row * a.table_stride + before, a.table_stride - before};
+}
 
 // Device-side checks recorded in the cache's status word (its detail).
 constexpr int kKvBadPage = 200, kKvBadNumber = 201, kKvBadBatch = 202;
 
 // First page row (row = one head of one slot) of a sequence's page `j`, or -1
 // (recorded) when the table has no valid entry for it.
+template <bool PARTS = false>
 __device__ __forceinline__ long long kv_page_row(const KvArgs& a, int seq, int j, int head) {
   int p = -1;
-  if (j < a.table_stride) p = a.table[(long long)seq * a.table_stride + j];
+  const KvTable t = kv_table<PARTS>(a, seq);
+  if (j < t.n) p = t.entry[j];
   if (p < 0 || p >= a.n_pages) {
     report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
     return -1;
@@ -90,7 +107,45 @@ struct AttnArgs {
   int heads, group;  // query heads, query heads per kv head
   int window, sinks;
   float scale;
+  // Attention in two parts. kFirst: every row sees all positions, and its
+  // output goes to first_o, first_lse as fp32 (lse in base 2). kSecond: causal
+  // as ever, over the positions from kv.skip on; the rows of sequences that
+  // skip any are joined with what kFirst left.
+  enum Part { kWhole, kFirst, kSecond };
+  int part;
+  float* first_o;    // [n_tokens, heads, dim]
+  float* first_lse;  // [n_tokens, heads]
 };
+
+// (The kernels are compiled for whole calls and for PARTS apart: what the latter need cost the former registers.)
+// Position of a sequence's step token 0, and of its step token t.
+template <bool PARTS>
+__device__ __forceinline__ int base_pos(const AttnArgs& a, const SeqInfo& s) {
+  return PARTS && a.part == AttnArgs::kFirst ? s.kv - 1 : s.kv - s.n_new;
+}
+template <bool PARTS>
+__device__ __forceinline__ int pos_of(const AttnArgs& a, int base, int t) {
+  return PARTS && a.part == AttnArgs::kFirst ? base : base + t;
+}
+// Whether outputs are the first part's, and whether a sequence's rows have a first part to be joined with.
+template <bool PARTS>
+__device__ __forceinline__ bool is_first(const AttnArgs& a) {
+  return PARTS && a.part == AttnArgs::kFirst;
+}
+template <bool PARTS>
+__device__ __forceinline__ bool has_first(const AttnArgs& a, int seq) {
+  return PARTS && a.part == AttnArgs::kSecond && a.kv.skip[seq] > 0;
+}
+// Weights of a row's two parts, both normalised, in the whole, from their log-sum-exps (base 2; -inf: it saw nothing).
+struct Join {
+  float own, first, lse;
+};
+__device__ __forceinline__ Join join_of(float own, float first) {
+  const float top = fmaxf(own, first), ref = top == -INFINITY ? 0.f : top;
+  const float a = exp2f(own - ref), b = exp2f(first - ref), sum = a + b;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  return Join{a * inv, b * inv, sum != 0.f ? ref + log2f(sum) : -INFINITY};
+}
 
 cudaError_t kv_append(const KvArgs& a, const uint16_t* k, long long ks, const uint16_t* v, long long vs,
                       const KvCall& c);

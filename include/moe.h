@@ -421,6 +421,154 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
                                  const uint16_t* q, long long q_stride, uint16_t* out, float* lse, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* ---- rotated append ----
+ *
+ * What a layer does to a step's queries and keys between its projection and
+ * its attention, with the append in the same pass: every head is normed,
+ * turned to its position, and the keys and values are quantised into the cache.
+ *
+ *   y = x                                       without a weight
+ *   y = x / sqrt(mean(x^2) + eps) * weight      over the head_dim elements of the head
+ *   (y[a], y[b]) turned by the angle 2 pi position turns[i] / 2^64, i = 0 ..
+ *               rotary_dim / 2 - 1: y[a] cos - y[b] sin, y[b] cos + y[a] sin,
+ *               where (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) if
+ *               interleaved; elements from rotary_dim on are not turned
+ *
+ * in fp32, rounded once to bf16: that is q_out, and the keys that
+ * moe_kv_append's rule then quantises. (Angles are exact to 2^-25 turns at any
+ * position: whole turns fall out of a 64-bit product.)
+ *   rotary_dim   a multiple of 16, 0 to head_dim (0: nothing is turned, turns
+ *                may be NULL)
+ *   axes         1 to 4 position axes; axis[i] is frequency i's
+ *   turns        device uint64 [rotary_dim / 2], 8-byte aligned: turns per
+ *                position in units of 2^-64, the two's complement of a negative one
+ *   axis         device uint8 [rotary_dim / 2], or NULL: all 0; a number that is
+ *                no axis is taken for 0
+ *   positions    device int32 [axes, n_tokens], or NULL: a token's position in
+ *                its sequence, on every axis. They turn the heads only; where a
+ *                token is cached goes by the batch.
+ *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL: no norm
+ *   eps          at least 2^-64, finite; used with a weight only
+ * Squares may pass fp32. A NaN makes every normed element of its head NaN, an
+ * infinity makes itself NaN and the others 0; keys are then stored as by moe_kv_append. */
+typedef struct {
+  int rotary_dim, interleaved, axes;
+  float eps;
+  const uint64_t* turns;
+  const uint8_t* axis;
+  const int32_t* positions;
+  const float* q_weight;
+  const float* k_weight;
+} moe_rotary;
+
+/* q: device bf16 [n_tokens, heads, head_dim], strided as k and v are (see
+ * moe_kv_append); q_out: device bf16, contiguous, 16-byte aligned, not
+ * overlapping q, k or v. heads: 1 to 16384. Padding tokens (negative positions) get their
+ * q_out, turned to that position, and are not cached. n_tokens = 0 is a no-op. */
+moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rotary* rotary, int heads,
+                                const uint16_t* q, long long q_stride, uint16_t* q_out, const uint16_t* k,
+                                long long k_stride, const uint16_t* v, long long v_stride, void* stream);
+
+/* ---- pages of a cache ----
+ *
+ * Which pages a set of sequences holds, kept on the device, so that giving
+ * pages, taking them back, forking sequences and moving pages need no host
+ * synchronisation and can be part of a CUDA graph. Several caches (the layers
+ * of a model) share one set: a page number means the same place in each.
+ * All arrays are device memory owned by the caller, 16-byte aligned:
+ *   table    int32 [n_seqs, columns] page of positions page_size * j ..; -1
+ *            past the pages held. The block_table of the steps' batches.
+ *   held     int32 [n_seqs] pages that each sequence holds
+ *   refs     int32 [n_pages] table entries that name each page; 0: it is free
+ *   scratch  int32 [moe_kv_pages_scratch(n_pages, n_seqs)], no contents kept
+ *   status   as moe_kv_cache's (it may be a cache's)
+ * To start with, table is all -1, held and refs 0. Calls on one set are ordered
+ * by the caller, as the launches on one stream are. Every call is
+ * deterministic: where there is a choice, the lowest number goes first. */
+typedef struct {
+  int n_pages, page_size, n_seqs, columns;
+  int32_t* table;
+  int32_t* held;
+  int32_t* refs;
+  int32_t* scratch;
+  void* status;
+} moe_kv_pages;
+
+size_t moe_kv_pages_scratch(int n_pages, int n_seqs); /* in int32 elements; 0 on bad arguments */
+
+/* Fits every sequence's pages to the step `batch` (whose block_table is the
+ * set's table, n_seqs its sequences and table_stride its columns):
+ *   1. pages past the batch's kv_len go back (a kv_len of 0 frees a sequence);
+ *   2. then pages are given, the lowest free ones, sequence by sequence and
+ *      position by position: for positions below kv_len that have none, and for
+ *      held pages with positions of the step's tokens (which will be written)
+ *      that another sequence holds too. These are copied first, in all of the
+ *      caches.
+ * A sequence whose kv_len is negative or passes max_kv or the table, or that
+ * has a negative number of step tokens or more than max_new, records
+ * MOE_ERR_DEVICE_CHECK and keeps what it has. When the free pages run out, that
+ * sequence and the later ones that want any record it and get none; a page
+ * that would have been copied leaves the sequence (entry -1, its positions are
+ * lost), since writing it would change the others.
+ * caches: n_caches pointers (read during the call), each of the set's n_pages and
+ * page_size, all of one kv_heads and head_dim; at least one. */
+moe_status moe_kv_pages_update(const moe_kv_pages* pages, const moe_kv_batch* batch, const moe_kv_cache* const* caches,
+                               int n_caches, void* stream);
+
+/* Sequence dst[i] comes to hold the pages of sequence src[i], for i < n (int32
+ * device arrays). The pages are shared, not copied; the next
+ * moe_kv_pages_update copies those that a holder writes. A source may be
+ * forked any number of times. A pair with a number that is no sequence, a
+ * destination that holds pages, is named earlier in the call or is
+ * a source of the call (any pair's), records MOE_ERR_DEVICE_CHECK and is left
+ * out. 0 <= n <= n_seqs. */
+moe_status moe_kv_pages_fork(const moe_kv_pages* pages, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Moves pages so that those in use are 0 .. m - 1: in ascending order, the
+ * ones at m and past it go to the free places below. Contents (in all caches),
+ * tables and references go with them. */
+moe_status moe_kv_pages_compact(const moe_kv_pages* pages, const moe_kv_cache* const* caches, int n_caches, void* stream);
+
+/* Copies the contents of page src[i] to page dst[i] in all caches, for i < n (int32
+ * device arrays), tables and references aside. No page may be named by two
+ * entries of dst, or by dst and src (but a pair of equal numbers is left out); a
+ * number that is no page records MOE_ERR_DEVICE_CHECK in the first cache's
+ * status, and its pair is left out. */
+moe_status moe_kv_copy_pages(const moe_kv_cache* const* caches, int n_caches, const int32_t* src, const int32_t* dst,
+                             int n, void* stream);
+
+/* ---- attention of sequences that share their first positions ----
+ *
+ * moe_attention_forward for a step whose sequences, group by group, hold the
+ * same keys and values at their first positions (forked from one prompt, or
+ * given the same pages): a group's shared part is read and multiplied once, with the
+ * rows of all its sequences together, and each sequence's own part is joined to
+ * it in fp32. The result is moe_attention_forward's but for roundings.
+ *   seq_off  device int32 [n_groups + 1]: group g is the sequences seq_off[g]
+ *            .. seq_off[g + 1] - 1; ascending, from 0 to n_seqs
+ *   length   device int32 [n_groups]: how many first positions the group shares;
+ *            of these the whole pages count. They are read through the table
+ *            of the group's first sequence.
+ *   max_tokens  upper bound of a group's step tokens
+ *   max_len     upper bound of the lengths
+ *   max_own     upper bound of kv_len less its group's shared positions in whole pages
+ * A sequence whose step tokens begin before its group's shared positions end
+ * shares nothing. Groups that are not as said here, or past their bounds, record
+ * MOE_ERR_DEVICE_CHECK, and no sequence of the step shares anything; a sequence
+ * past max_own records it, and its rows of the output are not written. With a
+ * window (which reads near positions only) the call is moe_attention_forward. */
+typedef struct {
+  int n_groups, max_tokens, max_len, max_own;
+  const int32_t* seq_off;
+  const int32_t* length;
+} moe_kv_prefix;
+
+size_t moe_attention_prefix_workspace_size(const moe_kv_cache* cache, const moe_kv_batch* batch,
+                                           const moe_kv_prefix* prefix, const moe_attention* a);
+moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_kv_prefix* prefix,
+                                        const moe_attention* a, const uint16_t* q, long long q_stride, uint16_t* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of this library's kernels the last forward call on this thread
  * launched (all of its passes). */
 int moe_last_launch_count(void);
