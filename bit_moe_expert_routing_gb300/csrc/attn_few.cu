@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   }
   __syncthreads();
   const bool cut_item = t_begin > 0 || t_end < sq.tiles.n;
+  if (is_shared<PARTS>(a) && !cut_item) griddep_wait();  // the rows' own parts are there
   const int slot = 2 * blockIdx.x + (t_begin > 0);  // a CTA's parts: one that begins in an item, one that ends in one
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -764,19 +765,20 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
         float v[8], lse_out = l[n][i];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[2 * k] = o[n][4 * w + k][i], v[2 * k + 1] = o[n][4 * w + k][2 + i];
-        if (!cut_item && is_first<PARTS>(a)) {
-          float4* dst = reinterpret_cast<float4*>(a.first_o + at * DIM + d);
+        if (!cut_item && to_own<PARTS>(a, b)) {
+          float4* dst = reinterpret_cast<float4*>(a.own_o + at * DIM + d);
           dst[0] = make_float4(v[0], v[1], v[2], v[3]);
           dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (g == 0 && w == 0) a.first_lse[at] = l[n][i];
+          if (g == 0 && w == 0) a.own_lse[at] = l[n][i];
         } else if (!cut_item) {
-          if (has_first<PARTS>(a, b)) {
-            const Join j = join_of(l[n][i], a.first_lse[at]);
-            const float4* o1 = reinterpret_cast<const float4*>(a.first_o + at * DIM + d);
+          if (!is_written<PARTS>(a, si.first + t)) continue;
+          if (is_shared<PARTS>(a)) {
+            const Join j = join_of(l[n][i], a.own_lse[at]);
+            const float4* o1 = reinterpret_cast<const float4*>(a.own_o + at * DIM + d);
             const float4 x = o1[0], y = o1[1];
             const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = j.own * v[k] + j.first * u[k];
+            for (int k = 0; k < 8; ++k) v[k] = j.shared * v[k] + j.own * u[k];
             if (w == 0) lse_out = j.lse;
           }
           uint32_t h[4];
@@ -811,6 +813,9 @@ struct Parts {
   SeqItems sq;
   int seq, kvh, rg, n_rows, p0, n;
   __device__ __forceinline__ int slot(int p) const { return 2 * (p0 + p) + (p > 0); }
+  __device__ __forceinline__ int token(const FewArgs& f, int rows_per_group, int row) const {
+    return sq.s.first + f.token(rg * rows_per_group + row);
+  }
   // place of row `row` of the group in the outputs
   __device__ __forceinline__ long long place(const FewArgs& f, int rows_per_group, int row) const {
     const int r = rg * rows_per_group + row, t = f.token(r);
@@ -854,8 +859,9 @@ template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group) {
   constexpr int kV = DIM / 128 + (DIM < 128);  // float4 of a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
+  if (PARTS && f.a.part == AttnArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
   const Parts q = parts_of(f, blockIdx.x, rows_per_group);
-  if (q.n <= 1 || row >= q.n_rows) return griddep_wait();  // (see Parts)
+  if (q.n <= 1 || row >= q.n_rows || !is_written<PARTS>(f.a, q.token(f, rows_per_group, row))) return griddep_wait();  // (see Parts)
   const long long at = q.place(f, rows_per_group, row);
   griddep_wait();
   const bool mine = DIM >= 128 || lane < DIM / 4;
@@ -898,22 +904,22 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
   float lse = sum != 0.f ? top + log2f(sum) : -INFINITY;
 #pragma unroll
   for (int k = 0; k < kV; ++k) o[k].x *= inv, o[k].y *= inv, o[k].z *= inv, o[k].w *= inv;
-  if (is_first<PARTS>(f.a)) {
+  if (to_own<PARTS>(f.a, q.seq)) {
     if (mine)
 #pragma unroll
-      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(f.a.first_o + at * DIM)[lane + 32 * k] = o[k];
-    if (lane == 0) f.a.first_lse[at] = lse;
+      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(f.a.own_o + at * DIM)[lane + 32 * k] = o[k];
+    if (lane == 0) f.a.own_lse[at] = lse;
     return;
   }
-  if (has_first<PARTS>(f.a, q.seq)) {
-    const Join j = join_of(lse, f.a.first_lse[at]);
+  if (is_shared<PARTS>(f.a)) {
+    const Join j = join_of(lse, f.a.own_lse[at]);
     lse = j.lse;
     if (mine)
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        const float4 u = reinterpret_cast<const float4*>(f.a.first_o + at * DIM)[lane + 32 * k];
-        o[k].x = j.own * o[k].x + j.first * u.x, o[k].y = j.own * o[k].y + j.first * u.y;
-        o[k].z = j.own * o[k].z + j.first * u.z, o[k].w = j.own * o[k].w + j.first * u.w;
+        const float4 u = reinterpret_cast<const float4*>(f.a.own_o + at * DIM)[lane + 32 * k];
+        o[k].x = j.shared * o[k].x + j.own * u.x, o[k].y = j.shared * o[k].y + j.own * u.y;
+        o[k].z = j.shared * o[k].z + j.own * u.z, o[k].w = j.shared * o[k].w + j.own * u.w;
       }
   }
   if (mine)
@@ -938,9 +944,10 @@ __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewAr
   __shared__ float4 acc[kGroups][kLanes];
   __shared__ float red[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x % rows;
+  if (PARTS && f.a.part == AttnArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
   const Parts q = parts_of(f, blockIdx.x / rows, rows_per_group);
   const int n = q.n;
-  if (n <= 1 || row >= q.n_rows) return griddep_wait();  // (see Parts)
+  if (n <= 1 || row >= q.n_rows || !is_written<PARTS>(f.a, q.token(f, rows_per_group, row))) return griddep_wait();  // (see Parts)
   const long long at = q.place(f, rows_per_group, row);
   const int grp = threadIdx.x / kLanes, d = blockIdx.y * 64 + 4 * (threadIdx.x % kLanes);
   griddep_wait();
@@ -991,17 +998,17 @@ __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewAr
     const float inv = tot != 0.f ? 1.f / tot : 0.f;
     float lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
     v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-    if (is_first<PARTS>(f.a)) {
-      *reinterpret_cast<float4*>(f.a.first_o + at * DIM + d) = v;
-      if (d == 0) f.a.first_lse[at] = lse;
+    if (to_own<PARTS>(f.a, q.seq)) {
+      *reinterpret_cast<float4*>(f.a.own_o + at * DIM + d) = v;
+      if (d == 0) f.a.own_lse[at] = lse;
       return;
     }
-    if (has_first<PARTS>(f.a, q.seq)) {
-      const Join j = join_of(lse, f.a.first_lse[at]);
-      const float4 u = *reinterpret_cast<const float4*>(f.a.first_o + at * DIM + d);
+    if (is_shared<PARTS>(f.a)) {
+      const Join j = join_of(lse, f.a.own_lse[at]);
+      const float4 u = *reinterpret_cast<const float4*>(f.a.own_o + at * DIM + d);
       lse = j.lse;
-      v.x = j.own * v.x + j.first * u.x, v.y = j.own * v.y + j.first * u.y;
-      v.z = j.own * v.z + j.first * u.z, v.w = j.own * v.w + j.first * u.w;
+      v.x = j.shared * v.x + j.own * u.x, v.y = j.shared * v.y + j.own * u.y;
+      v.z = j.shared * v.z + j.own * u.z, v.w = j.shared * v.w + j.own * u.w;
     }
     uint2 h;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y), "f"(v.x));

@@ -74,6 +74,7 @@ namespace {
 constexpr int kBK = 128;                  // keys per tile
 constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
+constexpr int kMaxPairs = 256;            // CTA pairs, at most (this GPU has 76)
 constexpr int kDescs = 4;                 // segment descriptors in flight
 constexpr int kMinUnits = 4;              // of a pair. (16 heads over 2 of 128 dims, one sequence, 64 tokens: over 8000
                                           // keys 25.2 us, with at least 2 units 25.8, 8 units 26.6; over 1000 keys 19.3,
@@ -91,6 +92,7 @@ struct ManyCfg {
   static constexpr uint32_t kTileBytes = 2 * kSlot;
   static constexpr int kRing = DIM == 64 ? 12 : DIM == 128 ? 11 : 4;
   static constexpr uint32_t kQTile = 128 * DIM * 2;
+  static constexpr int kCombineSplit = DIM == 256 ? 2 : 1;  // warps of a row in the combine kernel
   static constexpr bool kOwnP = DIM <= 128;    // P has tensor memory of its own; else it takes S's place
   // The softmax's two warpgroups take: DIM 64 a row tile each; 128 S tiles in turn; 256 half of the keys of each S tile.
   static constexpr bool kTurns = DIM == 128, kHalves = DIM == 256;
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   griddep_launch();
   if (blockIdx.x == 0) {
     make_plan<PARTS>(m, ManyCfg<DIM>::kPairRows);
+    if (is_shared<PARTS>(m.a)) griddep_wait();  // launched beside the sequences' own part, it does not end before that
     return;
   }
   __shared__ long long rows16[kBK / 16];  // first cache row of each 16 keys, -1: zeros
@@ -1123,23 +1126,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         wait_product(gl, 228);
         tc_fence_after();
         const int r = q * 128 + row;
-        const bool valid = r < s.n_rows, part = s.part >= 0, first = is_first<PARTS>(a);
         const int rr = min(s.row0 + r, s.last), t = m.token(rr);
+        const bool valid = r < s.n_rows && is_written<PARTS>(a, s.first + t), part = s.part >= 0;
+        const bool own = to_own<PARTS>(a, m.b0 + s.seq);
         const long long at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
         const long long prow = (long long)s.part * C::kRows + r;
-        float with = 0.f;  // weight of the row's first part, if this is the second
-        if (!part && valid && has_first<PARTS>(a, m.b0 + s.seq)) {
-          const Join j = join_of(lse, a.first_lse[at]);
-          inv *= j.own, with = j.first, lse = j.lse;
+        float with = 0.f;  // weight of the row's own part, if this is the shared one
+        if (!part && valid && is_shared<PARTS>(a)) {
+          const Join j = join_of(lse, a.own_lse[at]);
+          inv *= j.shared, with = j.own, lse = j.lse;
         }
-        float* dst32 = part ? m.part_o + prow * DIM : a.first_o + at * DIM;
+        float* dst32 = part ? m.part_o + prow * DIM : a.own_o + at * DIM;
 #pragma unroll 1
         for (int cc = 0; cc < kOCols; cc += 32) {
           uint32_t o[32];
           tmem_ld32(ocol + cc, o);
           tmem_wait_ld32(o);
           const int d = ohalf * kOCols + cc;
-          if (part || (first && valid)) {
+          if (part || (own && valid)) {
             float* dst = dst32 + d;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
@@ -1150,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             if (with != 0.f) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(a.first_o + at * DIM + d + e);
+                const float4 u = *reinterpret_cast<const float4*>(a.own_o + at * DIM + d + e);
                 const float x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[e + k] = __float_as_uint(__uint_as_float(o[e + k]) * inv + with * x[k]);
@@ -1174,8 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         if (ohalf == 0) {
           if (part)
             m.part_lse[prow] = lse;
-          else if (valid && first)
-            a.first_lse[at] = lse;
+          else if (valid && own)
+            a.own_lse[at] = lse;
           else if (valid && a.lse)
             a.lse[at] = lse * 0.6931471805599453f;
         }
@@ -1202,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           constexpr int kV = DIM / 128 + (DIM < 128), kBatch = DIM == 256 ? 4 : 8;
           const bool mine = DIM >= 128 || lane < DIM / 4;  // DIM 64: half of the lanes hold a row
           const int my_row = warp + kSoftWarps * lane;
-          const bool has_row = my_row < s.n_rows;
+          const bool has_row = my_row < s.n_rows && is_written<PARTS>(a, s.first + m.token(min(s.row0 + my_row, s.last)));
           // parts in order: fn(row of the part buffers at which the part begins)
           auto each_part = [&](auto&& fn) {
             for (int c = info.c0, from = 0; c <= info.c1; ++c) {
@@ -1218,14 +1222,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           const float inv = tot != 0.f ? 1.f / tot : 0.f;
           const int rr = min(s.row0 + my_row, s.last), t = m.token(rr);
           const long long my_at = (long long)(s.first + t) * a.heads + (m.h0 + s.head) * a.group + rr - t * a.group;
-          const bool first = is_first<PARTS>(a);
-          float my_own = 1.f, my_first = 0.f, my_lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
-          if (has_row && has_first<PARTS>(a, m.b0 + s.seq)) {
-            const Join j = join_of(my_lse, a.first_lse[my_at]);
-            my_own = j.own, my_first = j.first, my_lse = j.lse;
+          const bool own = to_own<PARTS>(a, m.b0 + s.seq);
+          float my_shared = 1.f, my_own = 0.f, my_lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
+          if (has_row && is_shared<PARTS>(a)) {
+            const Join j = join_of(my_lse, a.own_lse[my_at]);
+            my_shared = j.shared, my_own = j.own, my_lse = j.lse;
           }
-          if (has_row && first) a.first_lse[my_at] = my_lse;
-          if (has_row && !first && a.lse) a.lse[my_at] = my_lse * 0.6931471805599453f;
+          if (has_row && own) a.own_lse[my_at] = my_lse;
+          if (has_row && !own && a.lse) a.lse[my_at] = my_lse * 0.6931471805599453f;
           for (int b0 = 0; warp + kSoftWarps * b0 < s.n_rows; b0 += kBatch) {
             float4 o[kBatch][kV];
 #pragma unroll
@@ -1233,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
               for (int k = 0; k < kV; ++k) o[b][k] = make_float4(0.f, 0.f, 0.f, 0.f);
             each_part([&](long long at) {
-              const float w = has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) * inv * my_own : 0.f;
+              const float w = has_row ? ex2(__ldcg(m.part_lse + at + my_row) - r0) * inv * my_shared : 0.f;
               float4 v[kBatch][kV];
 #pragma unroll
               for (int b = 0; b < kBatch; ++b) {
@@ -1254,17 +1258,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
               const long long at = __shfl_sync(~0u, my_at, (b0 + b) & 31);
-              const float with = __shfl_sync(~0u, my_first, (b0 + b) & 31);
-              if (!mine || warp + kSoftWarps * (b0 + b) >= s.n_rows) continue;
-              if (first) {
+              const float with = __shfl_sync(~0u, my_own, (b0 + b) & 31);
+              const bool there = __shfl_sync(~0u, int(has_row), (b0 + b) & 31);
+              if (!mine || !there) continue;
+              if (own) {
 #pragma unroll
-                for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(a.first_o + at * DIM)[lane + 32 * k] = o[b][k];
+                for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(a.own_o + at * DIM)[lane + 32 * k] = o[b][k];
                 continue;
               }
               if (with != 0.f)
 #pragma unroll
                 for (int k = 0; k < kV; ++k) {
-                  const float4 u = reinterpret_cast<const float4*>(a.first_o + at * DIM)[lane + 32 * k];
+                  const float4 u = reinterpret_cast<const float4*>(a.own_o + at * DIM)[lane + 32 * k];
                   o[b][k].x += with * u.x, o[b][k].y += with * u.y, o[b][k].z += with * u.z, o[b][k].w += with * u.w;
                 }
 #pragma unroll
@@ -1289,36 +1294,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 }
 
 // Joins the parts of divided row tiles: out = sum_p 2^(lse_p - max) o_p /
-// sum_p 2^(lse_p - max). CTA (row tile, eight of its rows, kv head), a warp per
-// row, several parts' loads in flight.
+// sum_p 2^(lse_p - max). A warp per row (two for 256 dims, 128 each), a CTA per
+// eight warps, several parts' loads in flight, the first of them while the
+// weights are made. Which parts there are is looked up before the parts are
+// awaited: the ranges are older than the kernel that writes these.
 template <int DIM, bool PARTS>
 __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
-  griddep_wait();
-  constexpr int kRows = ManyCfg<DIM>::kRows, kV = DIM / 128 + (DIM < 128);
-  constexpr int kBatch = DIM == 256 ? 4 : 8;
+  constexpr int kRows = ManyCfg<DIM>::kRows, kSplit = ManyCfg<DIM>::kCombineSplit, kBatch = 8;
+  __shared__ long long begins[kMaxPairs + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rt = blockIdx.x, head = blockIdx.z, pr = blockIdx.y * 8 + warp;  // row of the pair
-  if (rt >= m.plan->row_tiles) return;
+  const int rt = blockIdx.x, head = blockIdx.z, pr = blockIdx.y * (8 / kSplit) + warp / kSplit;  // row of the pair
+  for (int c = threadIdx.x; c <= m.pairs; c += 256) begins[c] = m.range[c].begin;
+  __syncthreads();
+  if (rt >= m.plan->row_tiles) return griddep_wait();
   const RowTile t = m.row_tile[rt];
   const int last = t.n_new * m.a.group - 1, rr = t.row0 + pr;
-  if (rr > last) return;
+  if (rr > last || !is_written<PARTS>(m.a, t.first + m.token(rr))) return griddep_wait();
   const long long units = m.plan->units, u0 = head * units + m.unit_off[rt], u1 = head * units + m.unit_off[rt + 1];
   // the pair that holds the first key tile: the last one whose units begin at or before it
   int lo = 0, hi = m.pairs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (m.range[mid].begin <= u0 + kTileCost)
+    if (begins[mid] <= u0 + kTileCost)
       lo = mid;
     else
       hi = mid - 1;
   }
   const int c0 = lo;
-  if (m.range[c0 + 1].begin >= u1) return;  // one pair has all of it, and wrote the output
+  if (begins[c0 + 1] >= u1) return griddep_wait();  // one pair has all of it, and wrote the output
   int c1 = c0 + 1;
   hi = m.pairs - 1;  // the last pair with a unit before u1
   while (c1 < hi) {
     const int mid = (c1 + hi + 1) >> 1;
-    if (m.range[mid].begin < u1)
+    if (begins[mid] < u1)
       c1 = mid;
     else
       hi = mid - 1;
@@ -1326,67 +1334,58 @@ __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyA
   const int parts = c1 - c0 + 1, rank = pr / kRows, r = pr % kRows;
   // part p is pair c0 + p's: in its slot 1 if it begins inside the row tile, as all but the first do
   auto at = [&](int p) { return (2 * (2ll * (c0 + p) + (p > 0)) + rank) * kRows + r; };
+  const int tok = m.token(rr);
+  const long long dst = (long long)(t.first + tok) * m.a.heads + (m.h0 + head) * m.a.group + rr - tok * m.a.group;
+  const int d = DIM >= 128 ? warp % kSplit * 128 + 4 * lane : 4 * lane;  // this lane's four dims
+  const bool mine = DIM >= 128 || lane < DIM / 4;
+  griddep_wait();
+  float4 v[kBatch];
+  auto load = [&](int p) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      v[i] = mine && p + i < parts ? *reinterpret_cast<const float4*>(m.part_o + at(p + i) * DIM + d)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(0);
   float top = -INFINITY;
   for (int p = lane; p < parts; p += 32) top = fmaxf(top, m.part_lse[at(p)]);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
   const float ref = top == -INFINITY ? 0.f : top;
   float sum = 0.f;
-  float4 o[kV];
-#pragma unroll
-  for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool mine = DIM >= 128 || lane < DIM / 4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p0 = 0; p0 < parts; p0 += 32) {
     const int some = min(32, parts - p0);
     const float w = lane < some ? ex2(m.part_lse[at(p0 + lane)] - ref) : 0.f;
     for (int p = 0; p < some; p += kBatch) {
-      float4 v[kBatch][kV];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int k = 0; k < kV; ++k)
-          v[i][k] = mine && p + i < some ? reinterpret_cast<const float4*>(m.part_o + at(p0 + p + i) * DIM)[lane + 32 * k]
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p0 + p) load(p0 + p);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const float wi = __shfl_sync(~0u, w, p + i);
         sum += wi;
-#pragma unroll
-        for (int k = 0; k < kV; ++k)
-          o[k].x += wi * v[i][k].x, o[k].y += wi * v[i][k].y, o[k].z += wi * v[i][k].z, o[k].w += wi * v[i][k].w;
+        o.x += wi * v[i].x, o.y += wi * v[i].y, o.z += wi * v[i].z, o.w += wi * v[i].w;
       }
     }
   }
-  const int tok = m.token(rr);
-  const long long dst = (long long)(t.first + tok) * m.a.heads + (m.h0 + head) * m.a.group + rr - tok * m.a.group;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   float lse = sum != 0.f ? top + log2f(sum) : -INFINITY;
-#pragma unroll
-  for (int k = 0; k < kV; ++k) o[k].x *= inv, o[k].y *= inv, o[k].z *= inv, o[k].w *= inv;
-  if (is_first<PARTS>(m.a)) {
-    if (mine)
-#pragma unroll
-      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(m.a.first_o + dst * DIM)[lane + 32 * k] = o[k];
-    if (lane == 0) m.a.first_lse[dst] = lse;
+  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  if (to_own<PARTS>(m.a, t.seq)) {
+    if (mine) *reinterpret_cast<float4*>(m.a.own_o + dst * DIM + d) = o;
+    if (d == 0) m.a.own_lse[dst] = lse;
     return;
   }
-  if (has_first<PARTS>(m.a, t.seq)) {
-    const Join j = join_of(lse, m.a.first_lse[dst]);
+  if (is_shared<PARTS>(m.a)) {
+    const Join j = join_of(lse, m.a.own_lse[dst]);
     lse = j.lse;
-    if (mine)
-#pragma unroll
-      for (int k = 0; k < kV; ++k) {
-        const float4 u = reinterpret_cast<const float4*>(m.a.first_o + dst * DIM)[lane + 32 * k];
-        o[k].x = j.own * o[k].x + j.first * u.x, o[k].y = j.own * o[k].y + j.first * u.y;
-        o[k].z = j.own * o[k].z + j.first * u.z, o[k].w = j.own * o[k].w + j.first * u.w;
-      }
+    if (mine) {
+      const float4 u = *reinterpret_cast<const float4*>(m.a.own_o + dst * DIM + d);
+      o.x = j.shared * o.x + j.own * u.x, o.y = j.shared * o.y + j.own * u.y;
+      o.z = j.shared * o.z + j.own * u.z, o.w = j.shared * o.w + j.own * u.w;
+    }
   }
-  if (mine)
-#pragma unroll
-    for (int k = 0; k < kV; ++k)
-      *reinterpret_cast<uint2*>(m.a.out + dst * DIM + 4 * (lane + 32 * k)) =
-          make_uint2(pack2(o[k].x, o[k].y), pack2(o[k].z, o[k].w));
-  if (lane == 0 && m.a.lse) m.a.lse[dst] = lse * 0.6931471805599453f;
+  if (mine) *reinterpret_cast<uint2*>(m.a.out + dst * DIM + d) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+  if (d == 0 && m.a.lse) m.a.lse[dst] = lse * 0.6931471805599453f;
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -1417,7 +1416,7 @@ ManyPlan plan(const AttnArgs& a) {
   const size_t fit = std::max<size_t>(1, kPassBytes / head_bytes);
   p.nh = int(std::min<size_t>(a.kv.kv_heads, fit));
   p.nb = int(std::min<size_t>(a.kv.n_seqs, std::max<size_t>(1, fit / p.nh)));
-  p.pairs = num_sms() / 2;
+  p.pairs = std::min(num_sms() / 2, kMaxPairs);
   p.max_row_tiles = int(((long long)a.kv.n_tokens * a.group + p.rows - 1) / p.rows + p.nb);
   size_t o = 0;
   auto put = [&](size_t bytes) {
@@ -1473,14 +1472,21 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
       m.nh = std::min(p.nh, m.a.kv.kv_heads - m.h0);
       const long long grid = 1 + 2ll * m.nb * m.nh * p.tiles_max;
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-      attention_expand_kernel<DIM, PARTS><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
-      if (cudaError_t e = c.launched("attention_expand")) return e;
+      // the shared part's first expansion runs beside the own part's last kernel; it touches nothing of that
+      if (PARTS && m.a.part == AttnArgs::kShared && m.b0 == 0 && m.h0 == 0) {
+        if (cudaError_t e = launch_beside(c, "attention_expand", attention_expand_kernel<DIM, PARTS>, dim3(unsigned(grid)),
+                                          kPlanThreads, 0, 1, m))
+          return e;
+      } else {
+        attention_expand_kernel<DIM, PARTS><<<unsigned(grid), kPlanThreads, 0, c.stream>>>(m);
+        if (cudaError_t e = c.launched("attention_expand")) return e;
+      }
       if (cudaError_t e = launch_beside(c, "attention_many", attention_many_kernel<DIM, PARTS>, dim3(2 * p.pairs), kThreads,
                                         C::kSmem, 2, m))
         return e;
       if (!m.join)
         if (cudaError_t e = launch_beside(c, "attention_many_combine", attention_many_combine_kernel<DIM, PARTS>,
-                                          dim3(p.max_row_tiles, C::kPairRows / 8, m.nh), 256, 0, 1, m))
+                                          dim3(p.max_row_tiles, C::kPairRows * C::kCombineSplit / 8, m.nh), 256, 0, 1, m))
           return e;
     }
   return cudaSuccess;

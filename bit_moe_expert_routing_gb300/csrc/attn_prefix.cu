@@ -5,16 +5,19 @@
 // o2) / (2^(l1 - m) + 2^(l2 - m)), l the base-2 log-sum-exps. Both are the step
 // as other steps of the same kernels:
 //
-//   first    groups as sequences: all step tokens of a group are rows that see
-//            all of its shared positions. Outputs in fp32.
-//   second   the step itself over what lies past the shared positions; where a
-//            row's output is written it is joined with the first part.
+//   own      the step itself over what lies past the shared positions; outputs
+//            in fp32
+//   shared   groups as sequences: all step tokens of a group are rows that see
+//            all of its shared positions; where an output is written it is
+//            joined with the row's own part
 //
 // The shared keys are read (and, for the tensor cores, expanded) once per
 // group instead of once per sequence, and a group's rows together fill the
 // products' tiles. A small kernel makes both steps' lengths and offsets on the
 // device. What it costs is that kernel, the second set of launches and the
-// rows' fp32 outputs, written and read once.
+// rows' fp32 outputs, written and read once. The own part comes first because
+// it is short: the shared part's kernels start beside it, and wait for it only
+// where they join.
 #include "kv_host.cuh"
 
 namespace moe {
@@ -31,55 +34,81 @@ struct PrefixArgs {
   int32_t* group_row;  // [n_groups] row of the table
   int32_t* own_len;    // [n_seqs] positions past the shared ones
   int32_t* skip;       // [n_seqs] shared positions
+  uint8_t* shares;     // [n_tokens] whether the token's sequence shares any
+  int max_own;
 };
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBadGroups = 204;  // detail in the status word
 
 // One CTA: groups first, then sequences. Nothing is shared unless all groups
-// are in order, so that the kernels may go by the sums of their sizes.
-__global__ void __launch_bounds__(kPlanThreads) attention_prefix_plan_kernel(const PrefixArgs p) {
+// and offsets are in order, so that the kernels may go by the sums of their
+// sizes, and every token is some sequence's.
+__global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(const PrefixArgs p) {
   const KvArgs& a = p.kv;
+  const int b0 = threadIdx.x, lane = threadIdx.x & 31;
+  // (a thread's first sequence, asked for beside the groups)
+  int q0 = 0, q1 = 0, kv = 0;
+  if (b0 < a.n_seqs) q0 = a.q_off[b0], q1 = a.q_off[b0 + 1], kv = a.kv_len[b0];
   bool bad = p.seq_off[0] != 0 || p.seq_off[p.n_groups] != a.n_seqs || a.q_off[0] != 0 || a.q_off[a.n_seqs] != a.n_tokens;
   for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
     const int s0 = p.seq_off[g], s1 = p.seq_off[g + 1], len = p.length[g];
     bool ok = s0 >= 0 && s0 <= s1 && s1 <= a.n_seqs && len >= 0 && len <= p.max_len;
-    const int q0 = ok ? a.q_off[s0] : 0, q1 = ok ? a.q_off[s1] : 0;
-    ok &= q0 >= 0 && q0 <= q1 && q1 <= a.n_tokens && q1 - q0 <= p.max_tokens;
+    const int t0 = ok ? a.q_off[s0] : 0, t1 = ok ? a.q_off[s1] : 0;
+    ok &= t0 >= 0 && t0 <= t1 && t1 <= a.n_tokens && t1 - t0 <= p.max_tokens;
     bad |= !ok;
-    p.group_off[g] = q0;
-    if (g == p.n_groups - 1) p.group_off[g + 1] = q1;
-    p.group_len[g] = ok ? len >> a.page_bits << a.page_bits : -1;
+    p.group_off[g] = t0;
+    if (g == p.n_groups - 1) p.group_off[g + 1] = t1;
+    p.group_len[g] = len >> a.page_bits << a.page_bits;
     p.group_row[g] = ok ? min(s0, a.n_seqs - 1) : 0;
   }
+  bad |= q1 < q0;
+  for (int b = b0 + kPlanThreads; b < a.n_seqs; b += kPlanThreads) bad |= a.q_off[b + 1] < a.q_off[b];
   bad = __syncthreads_or(bad);
-  if (bad && threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kBadGroups);
-  for (int b = threadIdx.x; b < a.n_seqs; b += kPlanThreads) {
-    const int q0 = a.q_off[b], n = a.q_off[b + 1] - q0, kv = a.kv_len[b];
-    int skip = 0;
-    if (!bad) {
-      int lo = 0, hi = p.n_groups - 1;  // the last group that begins at or before b
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.seq_off[mid] <= b)
-          lo = mid;
-        else
-          hi = mid - 1;
+  if (bad) {
+    if (threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kBadGroups);
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) p.group_len[g] = -1;  // the kernels leave it out
+  }
+  for (int c0 = 0; c0 < a.n_seqs; c0 += kPlanThreads) {
+    const int b = c0 + b0;
+    bool shares = false;
+    int n = 0;
+    if (b < a.n_seqs) {
+      if (c0 > 0) q0 = a.q_off[b], q1 = a.q_off[b + 1], kv = a.kv_len[b];
+      n = q1 - q0;
+      int skip = 0;
+      if (!bad && kv <= a.max_kv) {
+        int lo = 0, hi = p.n_groups - 1;  // the last group that begins at or before b
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.seq_off[mid] <= b)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        const int len = p.length[lo] >> a.page_bits << a.page_bits;
+        if (kv - n >= len) skip = len;
       }
-      const int len = p.length[lo] >> a.page_bits << a.page_bits;
-      // (its rows are among the group's: offsets that do not ascend within one leave them out)
-      const bool inside = n >= 0 && q0 >= a.q_off[p.seq_off[lo]] && q0 + n <= a.q_off[p.seq_off[lo + 1]];
-      if (inside && kv <= a.max_kv && kv - n >= len) skip = len;
+      const int own = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
+      p.skip[b] = skip;
+      p.own_len[b] = own;
+      // (as the kernels look at a sequence: one that they leave out has no own part to be joined)
+      shares = skip > 0 && own >= 0 && own <= p.max_own && n <= a.max_new;
     }
-    p.skip[b] = skip;
-    p.own_len[b] = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
+    if (bad) continue;  // (no token is looked at)
+    // the tokens of the warp's sequences, one sequence after the other
+    for (int l = 0; l < 32; ++l) {
+      const int first = __shfl_sync(~0u, q0, l), count = __shfl_sync(~0u, n, l);
+      const uint8_t flag = __shfl_sync(~0u, int(shares), l);
+      for (int i = lane; i < count; i += 32) p.shares[first + i] = flag;
+    }
   }
 }
 
 struct PrefixPlan {
-  AttnArgs first, second;
-  int few_first, few_second;
-  size_t group_off, group_len, group_row, own_len, skip, lse, o, attend, total;
+  AttnArgs own, shared;
+  int few_own, few_shared;
+  size_t group_off, group_len, group_row, own_len, skip, shares, lse, o, attend_own, attend_shared, total;
 };
 
 moe_status check_prefix(const KvArgs& kv, const moe_kv_prefix* x) {
@@ -100,14 +129,14 @@ bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x) 
 
 PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
   PrefixPlan p{a, a};
-  p.first.kv.n_seqs = x.n_groups;
-  p.first.kv.max_new = std::min(x.max_tokens, a.kv.n_tokens);
-  p.first.kv.max_kv = x.max_len;
-  p.first.part = AttnArgs::kFirst;
-  p.second.kv.max_kv = std::min(x.max_own, a.kv.max_kv);
-  p.second.part = AttnArgs::kSecond;
-  p.few_first = few_rows(p.first, opt);
-  p.few_second = few_rows(p.second, opt);
+  p.own.kv.max_kv = std::min(x.max_own, a.kv.max_kv);
+  p.own.part = AttnArgs::kOwn;
+  p.shared.kv.n_seqs = x.n_groups;
+  p.shared.kv.max_new = std::min(x.max_tokens, a.kv.n_tokens);
+  p.shared.kv.max_kv = x.max_len;
+  p.shared.part = AttnArgs::kShared;
+  p.few_own = few_rows(p.own, opt);
+  p.few_shared = few_rows(p.shared, opt);
   size_t o = 0;
   auto put = [&](size_t bytes) {
     const size_t at = o;
@@ -119,9 +148,11 @@ PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
   p.group_row = put(size_t(x.n_groups) * 4);
   p.own_len = put(size_t(a.kv.n_seqs) * 4);
   p.skip = put(size_t(a.kv.n_seqs) * 4);
+  p.shares = put(size_t(a.kv.n_tokens));
   p.lse = put(size_t(a.kv.n_tokens) * a.heads * 4);
   p.o = put(size_t(a.kv.n_tokens) * a.heads * a.kv.dim * 4);
-  p.attend = put(std::max(workspace_bytes_for(p.first, p.few_first), workspace_bytes_for(p.second, p.few_second)));
+  p.attend_own = put(workspace_bytes_for(p.own, p.few_own));
+  p.attend_shared = put(workspace_bytes_for(p.shared, p.few_shared));  // (a place of its own: they run side by side)
   p.total = o;
   return p;
 }
@@ -172,21 +203,33 @@ moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_
   PrefixPlan p = plan(g, *x, opt);
   char* w = static_cast<char*>(workspace);
   auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };
-  const PrefixArgs args{a, x->n_groups, x->max_tokens, x->max_len, x->seq_off, x->length, ints(p.group_off),
-                        ints(p.group_len), ints(p.group_row), ints(p.own_len), ints(p.skip)};
+  const PrefixArgs args{a,
+                        x->n_groups,
+                        x->max_tokens,
+                        x->max_len,
+                        x->seq_off,
+                        x->length,
+                        ints(p.group_off),
+                        ints(p.group_len),
+                        ints(p.group_row),
+                        ints(p.own_len),
+                        ints(p.skip),
+                        reinterpret_cast<uint8_t*>(w + p.shares),
+                        p.own.kv.max_kv};
   attention_prefix_plan_kernel<<<1, kPlanThreads, 0, c.stream>>>(args);
   if (cudaError_t e = c.launched("attention_prefix_plan")) return status_of(e);
-  for (AttnArgs* part : {&p.first, &p.second}) {
-    part->first_o = reinterpret_cast<float*>(w + p.o);
-    part->first_lse = reinterpret_cast<float*>(w + p.lse);
+  for (AttnArgs* part : {&p.own, &p.shared}) {
+    part->own_o = reinterpret_cast<float*>(w + p.o);
+    part->own_lse = reinterpret_cast<float*>(w + p.lse);
+    part->shares = args.shares;
   }
-  p.first.kv.q_off = args.group_off;
-  p.first.kv.kv_len = args.group_len;
-  p.first.kv.rows = args.group_row;
-  p.second.kv.kv_len = args.own_len;
-  p.second.kv.skip = args.skip;
-  if (cudaError_t e = attend(p.first, p.few_first, w + p.attend, c)) return status_of(e);
-  return status_of(attend(p.second, p.few_second, w + p.attend, c));
+  p.own.kv.kv_len = args.own_len;
+  p.own.kv.skip = args.skip;
+  p.shared.kv.q_off = args.group_off;
+  p.shared.kv.kv_len = args.group_len;
+  p.shared.kv.rows = args.group_row;
+  if (cudaError_t e = attend(p.own, p.few_own, w + p.attend_own, c)) return status_of(e);
+  return status_of(attend(p.shared, p.few_shared, w + p.attend_shared, c));
 }
 
 }  // extern "C"

@@ -107,42 +107,49 @@ struct AttnArgs {
   int heads, group;  // query heads, query heads per kv head
   int window, sinks;
   float scale;
-  // Attention in two parts. kFirst: every row sees all positions, and its
-  // output goes to first_o, first_lse as fp32 (lse in base 2). kSecond: causal
-  // as ever, over the positions from kv.skip on; the rows of sequences that
-  // skip any are joined with what kFirst left.
-  enum Part { kWhole, kFirst, kSecond };
+  // Attention in two parts. kOwn: causal as ever, over the positions from
+  // kv.skip on; outputs of sequences that skip any go to own_o, own_lse (fp32,
+  // the lse in base 2). kShared, behind it: every row sees all positions, and
+  // the rows of tokens that `shares` marks are joined with what kOwn left and
+  // written; no others are.
+  enum Part { kWhole, kOwn, kShared };
   int part;
-  float* first_o;    // [n_tokens, heads, dim]
-  float* first_lse;  // [n_tokens, heads]
+  float* own_o;           // [n_tokens, heads, dim]
+  float* own_lse;         // [n_tokens, heads]
+  const uint8_t* shares;  // [n_tokens]
 };
 
 // (The kernels are compiled for whole calls and for PARTS apart: what the latter need cost the former registers.)
+template <bool PARTS>
+__device__ __forceinline__ bool is_shared(const AttnArgs& a) {
+  return PARTS && a.part == AttnArgs::kShared;
+}
 // Position of a sequence's step token 0, and of its step token t.
 template <bool PARTS>
 __device__ __forceinline__ int base_pos(const AttnArgs& a, const SeqInfo& s) {
-  return PARTS && a.part == AttnArgs::kFirst ? s.kv - 1 : s.kv - s.n_new;
+  return is_shared<PARTS>(a) ? s.kv - 1 : s.kv - s.n_new;
 }
 template <bool PARTS>
 __device__ __forceinline__ int pos_of(const AttnArgs& a, int base, int t) {
-  return PARTS && a.part == AttnArgs::kFirst ? base : base + t;
+  return is_shared<PARTS>(a) ? base : base + t;
 }
-// Whether outputs are the first part's, and whether a sequence's rows have a first part to be joined with.
+// Whether a sequence's outputs are to be joined with a shared part.
 template <bool PARTS>
-__device__ __forceinline__ bool is_first(const AttnArgs& a) {
-  return PARTS && a.part == AttnArgs::kFirst;
+__device__ __forceinline__ bool to_own(const AttnArgs& a, int seq) {
+  return PARTS && a.part == AttnArgs::kOwn && a.kv.skip[seq] > 0;
 }
+// Whether a step token's rows are written.
 template <bool PARTS>
-__device__ __forceinline__ bool has_first(const AttnArgs& a, int seq) {
-  return PARTS && a.part == AttnArgs::kSecond && a.kv.skip[seq] > 0;
+__device__ __forceinline__ bool is_written(const AttnArgs& a, int token) {
+  return !is_shared<PARTS>(a) || a.shares[token];
 }
 // Weights of a row's two parts, both normalised, in the whole, from their log-sum-exps (base 2; -inf: it saw nothing).
 struct Join {
-  float own, first, lse;
+  float shared, own, lse;
 };
-__device__ __forceinline__ Join join_of(float own, float first) {
-  const float top = fmaxf(own, first), ref = top == -INFINITY ? 0.f : top;
-  const float a = exp2f(own - ref), b = exp2f(first - ref), sum = a + b;
+__device__ __forceinline__ Join join_of(float shared, float own) {
+  const float top = fmaxf(shared, own), ref = top == -INFINITY ? 0.f : top;
+  const float a = exp2f(shared - ref), b = exp2f(own - ref), sum = a + b;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   return Join{a * inv, b * inv, sum != 0.f ? ref + log2f(sum) : -INFINITY};
 }

@@ -5,7 +5,14 @@
 // what counts is that no host waits for it); the pages that it moves are then
 // copied by a grid of the size of the GPU, in all caches that share the set,
 // which finds their number on the device.
+//
+// An update is a chain: lengths, table entries, references, and then the
+// places of what is given, by prefix sums. It works on a copy of the references
+// in shared memory, which answers at once; what changes goes to memory beside
+// that and nobody waits for it. (From 24000 pages on the copy is in the scratch
+// memory.)
 #include "kv_host.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -27,7 +34,8 @@ struct PagesArgs {
   int32_t* src;    // [n_pages] moves
   int32_t* dst;    // [n_pages]
   int32_t* list;   // [n_pages] free pages; new places (compaction)
-  int32_t* want;   // [n_seqs] pages that a sequence wants
+  int32_t* snap;   // [n_pages] copy of the references
+  int32_t* seqs;   // [4 n_seqs] need, first, held, want
 };
 
 // The step's part of an update.
@@ -65,64 +73,107 @@ __device__ __forceinline__ int scan_before(int v, int* total, int* buf) {
 }
 
 // References of pages p .. p + 3 (p a multiple of 4); past the last page: in use.
-__device__ __forceinline__ int4 refs4(const PagesArgs& a, int p) {
-  if (p + 4 <= a.n_pages) return __ldcg(reinterpret_cast<const int4*>(a.refs + p));
+template <bool CACHED>
+__device__ __forceinline__ int4 refs4(const int32_t* refs, int n_pages, int p) {
+  auto at = [&](int q) { return CACHED ? refs[q] : __ldcg(refs + q); };
+  if (p + 4 <= n_pages) return CACHED ? *reinterpret_cast<const int4*>(refs + p) : __ldcg(reinterpret_cast<const int4*>(refs + p));
   int4 r = make_int4(1, 1, 1, 1);
-  if (p < a.n_pages) r.x = __ldcg(a.refs + p);
-  if (p + 1 < a.n_pages) r.y = __ldcg(a.refs + p + 1);
-  if (p + 2 < a.n_pages) r.z = __ldcg(a.refs + p + 2);
+  if (p < n_pages) r.x = at(p);
+  if (p + 1 < n_pages) r.y = at(p + 1);
+  if (p + 2 < n_pages) r.z = at(p + 2);
   return r;
 }
 
-// What a step wants of sequence b: pages that it needs, the first one that it writes. False: it is not to be touched.
-__device__ __forceinline__ bool wants(const PagesArgs& a, const StepArgs& s, int b, int* need, int* first) {
-  const int kv = s.kv_len[b], n = s.q_off[b + 1] - s.q_off[b];
-  const int size = 1 << a.page_bits;
-  if (kv < 0 || kv > s.max_kv || n < 0 || n > s.max_new || (kv + size - 1) >> a.page_bits > a.columns) return false;
-  *need = (kv + size - 1) >> a.page_bits;
-  *first = n > 0 ? max(kv - n, 0) >> a.page_bits : a.columns;
-  return true;
-}
+constexpr int kAbreast = 2;  // sequences whose entries a warp asks for together
 
-// One CTA. A page that is to be copied is marked in the table as -2 - page
-// between the count of what is wanted and the giving.
-__global__ void __launch_bounds__(kPlanThreads) pages_update_kernel(const PagesArgs a, const StepArgs s) {
+// One CTA. LOCAL: the copy of the references, the list of free pages and the
+// sequences' numbers are in shared memory, else in the scratch memory.
+//
+// The copy is as the references are once pages have gone back, and stays so:
+// whether a page is shared is asked twice, when what is wanted is counted and
+// when it is given.
+template <bool LOCAL>
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_update_kernel(const PagesArgs a, const StepArgs s) {
+  extern __shared__ int4 local[];
   __shared__ int buf[kPlanWarps];
-  __shared__ int n_free_s, n_moves;
+  __shared__ int n_moves;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int padded = (a.n_pages + 3) & ~3;
+  int32_t* snap = LOCAL ? reinterpret_cast<int32_t*>(local) : a.snap;
+  int32_t* list = LOCAL ? snap + padded : a.list;
+  int32_t* need_s = LOCAL ? list + padded : a.seqs;
+  int32_t *first_s = need_s + a.n_seqs, *held_s = first_s + a.n_seqs, *want_s = held_s + a.n_seqs;
+  auto get = [](const int32_t* p) { return LOCAL ? *p : __ldcg(p); };
+  griddep_wait();
+  griddep_launch();
   if (threadIdx.x == 0) n_moves = 0;
 
-  // pages go back
-  for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-    int need, first;
-    if (!wants(a, s, b, &need, &first)) {
-      if (lane == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
-      continue;
-    }
-    int32_t* row = a.table + (long long)b * a.columns;
-    const int held = min(a.held[b], a.columns);
-    for (int j = need + lane; j < held; j += 32) {
-      const int p = row[j];
-      if (is_page(a, p)) atomicAdd(a.refs + p, -1);
-      row[j] = -1;
-    }
-    __syncwarp();  // every lane has read held
-    if (lane == 0 && need < held) a.held[b] = need;
+  for (int p = 4 * threadIdx.x; p < a.n_pages; p += kChunk) {
+    const int4 r = refs4<false>(a.refs, a.n_pages, p);
+    *reinterpret_cast<int4*>(snap + p) = r;  // (padded)
+  }
+  // what the step wants of each sequence: pages, the first one written; what it holds of them. need -1: not to be touched
+  for (int b = threadIdx.x; b < a.n_seqs; b += kPlanThreads) {
+    const int kv = s.kv_len[b], n = s.q_off[b + 1] - s.q_off[b], held = max(0, min(a.held[b], a.columns));
+    const int need = int((kv + (1ll << a.page_bits) - 1) >> a.page_bits);
+    const bool ok = kv >= 0 && kv <= s.max_kv && n >= 0 && n <= s.max_new && need <= a.columns;
+    if (!ok) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
+    need_s[b] = ok ? need : -1;
+    first_s[b] = ok && n > 0 ? max(kv - n, 0) >> a.page_bits : a.columns;
+    held_s[b] = held;
   }
   __syncthreads();
-  // what every sequence wants
-  for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-    int need, first, n = 0;
-    if (wants(a, s, b, &need, &first)) {
-      int32_t* row = a.table + (long long)b * a.columns;
-      const int held = max(0, min(__ldcg(a.held + b), a.columns));
-      for (int j = first + lane; j < held; j += 32) {
-        const int p = row[j];
-        if (is_page(a, p) && __ldcg(a.refs + p) > 1) row[j] = -2 - p, ++n;
+  // pages go back
+  for (int b0 = warp * kAbreast; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast) {
+    int p[kAbreast];
+    auto each = [&](auto&& fn) {
+#pragma unroll
+      for (int i = 0; i < kAbreast; ++i) {
+        const int b = b0 + i;
+        if (b >= a.n_seqs) break;
+        const int need = get(need_s + b), held = get(held_s + b);
+        if (need >= 0 && need < held) fn(i, b, need, held);
       }
-      n = __reduce_add_sync(~0u, n) + max(0, need - held);
+    };
+    each([&](int i, int b, int need, int held) {
+      p[i] = need + lane < held ? a.table[(long long)b * a.columns + need + lane] : -1;
+    });
+    each([&](int i, int b, int need, int held) {
+      int32_t* row = a.table + (long long)b * a.columns;
+      for (int j = need + lane; j < held; j += 32) {
+        const int q = j < need + 32 ? p[i] : row[j];
+        row[j] = -1;
+        if (!is_page(a, q)) continue;
+        atomicAdd(a.refs + q, -1);
+        atomicAdd(snap + q, -1);
+      }
+      if (lane == 0) a.held[b] = need;
+    });
+  }
+  __syncthreads();
+  // what every sequence wants: pages that it shares and writes, and pages that it has not
+  for (int b0 = warp * kAbreast; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast) {
+    int n[kAbreast];
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      const int b = b0 + i;
+      n[i] = 0;
+      if (b >= a.n_seqs) break;
+      const int need = get(need_s + b), held = min(get(held_s + b), need);
+      const int32_t* row = a.table + (long long)b * a.columns;
+      for (int j = get(first_s + b) + lane; j < held; j += 32) {
+        const int p = row[j];
+        n[i] += is_page(a, p) && get(snap + p) > 1;
+      }
     }
-    if (lane == 0) a.want[b] = n;
+#pragma unroll
+    for (int i = 0; i < kAbreast; ++i) {
+      const int b = b0 + i;
+      if (b >= a.n_seqs) break;
+      const int need = get(need_s + b), more = need < 0 ? 0 : max(0, need - get(held_s + b));
+      const int sum = __reduce_add_sync(~0u, n[i]) + more;
+      if (lane == 0) want_s[b] = sum;
+    }
   }
   __syncthreads();
   // where each sequence's pages begin among those given
@@ -130,8 +181,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_update_kernel(const PagesA
   for (int b0 = 0; b0 < a.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     int sum;
-    const int before = scan_before(b < a.n_seqs ? a.want[b] : 0, &sum, buf);
-    if (b < a.n_seqs) a.want[b] = total + before;
+    const int before = scan_before(b < a.n_seqs ? get(want_s + b) : 0, &sum, buf);
+    if (b < a.n_seqs) want_s[b] = total + before;
     total += sum;
     __syncthreads();
   }
@@ -139,39 +190,35 @@ __global__ void __launch_bounds__(kPlanThreads) pages_update_kernel(const PagesA
   int n_free = 0;
   for (int p0 = 0; p0 < a.n_pages && n_free < total; p0 += kChunk) {
     const int p = p0 + 4 * threadIdx.x;
-    const int4 r = refs4(a, p);
+    const int4 r = refs4<LOCAL>(snap, a.n_pages, p);
     const int n = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     int sum;
     int at = n_free + scan_before(n, &sum, buf);
-    if (r.x == 0) a.list[at++] = p;
-    if (r.y == 0) a.list[at++] = p + 1;
-    if (r.z == 0) a.list[at++] = p + 2;
-    if (r.w == 0) a.list[at++] = p + 3;
+    if (r.x == 0) list[at++] = p;
+    if (r.y == 0) list[at++] = p + 1;
+    if (r.z == 0) list[at++] = p + 2;
+    if (r.w == 0) list[at++] = p + 3;
     n_free += sum;
     __syncthreads();
   }
-  if (threadIdx.x == 0) n_free_s = n_free;
-  __syncthreads();
   // the giving
-  for (int b = warp; b < a.n_seqs; b += kPlanWarps) {
-    const int at0 = __ldcg(a.want + b), at1 = b + 1 < a.n_seqs ? __ldcg(a.want + b + 1) : total;
+  for (int b = warp; b < a.n_seqs && total > 0; b += kPlanWarps) {
+    const int at0 = get(want_s + b), at1 = b + 1 < a.n_seqs ? get(want_s + b + 1) : total;
     if (at0 == at1) continue;  // (a sequence that is not to be touched wants nothing)
-    int need, first;
-    wants(a, s, b, &need, &first);
+    const int need = get(need_s + b), first = get(first_s + b), held = min(get(held_s + b), need);
     int32_t* row = a.table + (long long)b * a.columns;
-    const int held = max(0, min(__ldcg(a.held + b), a.columns));
-    const bool fits = at1 <= n_free_s;
+    const bool fits = at1 <= n_free;
     if (!fits && lane == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
     int at = at0;
-    for (int j0 = min(first, held); j0 < held; j0 += 32) {
-      const int j = j0 + lane, p = j < held ? -2 - __ldcg(row + j) : -1;
-      const bool marked = p >= 0 && is_page(a, p);
-      const unsigned m = __ballot_sync(~0u, marked);
-      if (marked) {
+    for (int j0 = first; j0 < held; j0 += 32) {
+      const int j = j0 + lane, p = j < held ? row[j] : -1;
+      const bool shared = is_page(a, p) && get(snap + p) > 1;
+      const unsigned m = __ballot_sync(~0u, shared);
+      if (shared) {
         atomicAdd(a.refs + p, -1);
         int to = -1;
         if (fits) {
-          to = __ldcg(a.list + at + __popc(m & ((1u << lane) - 1)));
+          to = get(list + at + __popc(m & ((1u << lane) - 1)));
           a.refs[to] = 1;
           const int i = atomicAdd(&n_moves, 1);
           a.src[i] = p;
@@ -183,11 +230,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_update_kernel(const PagesA
     }
     if (!fits) continue;
     for (int j = held + lane; j < need; j += 32) {
-      const int to = __ldcg(a.list + at + j - held);
+      const int to = get(list + at + j - held);
       row[j] = to;
       a.refs[to] = 1;
     }
-    __syncwarp();  // every lane has read held
     if (lane == 0 && need > held) a.held[b] = need;
   }
   __syncthreads();
@@ -195,11 +241,13 @@ __global__ void __launch_bounds__(kPlanThreads) pages_update_kernel(const PagesA
 }
 
 // One CTA: which pages move where.
-__global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const PagesArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_kernel(const PagesArgs a) {
   __shared__ int buf[kPlanWarps];
+  griddep_wait();
+  griddep_launch();
   int live = 0;
   for (int p0 = 0; p0 < a.n_pages; p0 += kChunk) {
-    const int4 r = refs4(a, p0 + 4 * threadIdx.x);
+    const int4 r = refs4<false>(a.refs, a.n_pages, p0 + 4 * threadIdx.x);
     live += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
   }
   // (past the last page refs4 says 1)
@@ -211,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const Pages
   int n_src = 0, n_dst = 0;
   for (int p0 = 0; p0 < a.n_pages; p0 += kChunk) {
     const int p = p0 + 4 * threadIdx.x;
-    const int4 r = refs4(a, p);
+    const int4 r = refs4<false>(a.refs, a.n_pages, p);
     const int v[4] = {r.x, r.y, r.z, r.w};
     int n = 0;  // sources in the high half, destinations in the low
 #pragma unroll
@@ -273,6 +321,8 @@ __device__ __forceinline__ uint4* word_of(const CopyArgs& c, int cache, int page
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyArgs c) {
   constexpr int kWords = 4;  // of a thread, in flight together
+  griddep_wait();
+  griddep_launch();
   if (c.table) {
     const int from = c.count[1];
     for (long long i = blockIdx.x * kCopyThreads + threadIdx.x; i < c.entries; i += (long long)gridDim.x * kCopyThreads) {
@@ -308,19 +358,17 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 constexpr int kForkThreads = 128;
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const PagesArgs a, const int32_t* src, const int32_t* dst,
                                                                   int n) {
+  griddep_wait();
+  griddep_launch();
   const int i = blockIdx.x, from = src[i], to = dst[i];
   bool bad = unsigned(from) >= unsigned(a.n_seqs) || unsigned(to) >= unsigned(a.n_seqs);
+  // (no pair that goes through changes a source, and this pair's destination is another's only if it does not)
+  const int held = bad ? 0 : max(0, min(a.held[from], a.columns)), holds = bad ? 0 : __ldcg(a.held + to);
   for (int j = threadIdx.x; j < n; j += kForkThreads) bad |= (j < i && dst[j] == to) || src[j] == to;
-  if (__syncthreads_or(bad)) {
+  if (__syncthreads_or(bad || holds != 0)) {
     if (threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
     return;
   }
-  // (nothing else in this launch changes either sequence: `to` is this pair's alone, `from` no pair's destination)
-  if (a.held[to] != 0) {
-    if (threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
-    return;
-  }
-  const int held = max(0, min(a.held[from], a.columns));
   for (int j = threadIdx.x; j < held; j += kForkThreads) {
     const int p = a.table[(long long)from * a.columns + j];
     a.table[(long long)to * a.columns + j] = p;
@@ -346,9 +394,10 @@ moe_status make_pages(const moe_kv_pages* p, PagesArgs* a) {
                  static_cast<WsHeader*>(p->status)};
   a->count = p->scratch;
   a->src = a->count + 4;
-  a->dst = a->src + p->n_pages;
-  a->list = a->dst + p->n_pages;
-  a->want = a->list + p->n_pages;
+  a->dst = a->src + ((p->n_pages + 3) & ~3);
+  a->list = a->dst + ((p->n_pages + 3) & ~3);
+  a->snap = a->list + ((p->n_pages + 3) & ~3);
+  a->seqs = a->snap + ((p->n_pages + 3) & ~3);
   return MOE_OK;
 }
 
@@ -367,6 +416,24 @@ moe_status check_caches(const moe_kv_cache* const* caches, int n, int n_pages, i
   return MOE_OK;
 }
 
+// A launch that may begin while the kernel before it on the stream ends (each of these waits for it first).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_early(const KvCall& c, const char* name, void (*kernel)(KArgs...), int grid, int block, size_t smem,
+                         Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) return e;
+  return c.launched(name);
+}
+
 cudaError_t copy_pages(CopyArgs c, const moe_kv_cache* const* caches, int n_caches, const KvCall& call) {
   const moe_kv_cache& f = *caches[0];
   c.n_pages = f.n_pages;
@@ -380,11 +447,18 @@ cudaError_t copy_pages(CopyArgs c, const moe_kv_cache* const* caches, int n_cach
       c.scales[i][0] = k.k_scales, c.scales[i][1] = k.v_scales;
       c.biases[i][0] = k.k_biases, c.biases[i][1] = k.v_biases;
     }
-    pages_copy_kernel<<<8 * num_sms(), kCopyThreads, 0, call.stream>>>(c);
-    if (cudaError_t e = call.launched("pages_copy")) return e;
+    if (cudaError_t e = launch_early(call, "pages_copy", pages_copy_kernel, 4 * num_sms(), kCopyThreads, 0, c)) return e;
     c.table = nullptr;  // (renamed by the first launch)
   }
   return cudaSuccess;
+}
+
+cudaError_t plan_update(const PagesArgs& a, const StepArgs& s, const KvCall& c) {
+  constexpr size_t kLocal = 200 << 10;
+  const size_t bytes = (2 * size_t((a.n_pages + 3) & ~3) + 4 * size_t(a.n_seqs)) * 4;
+  if (bytes > kLocal) return launch_early(c, "pages_update", pages_update_kernel<false>, 1, kPlanThreads, 0, a, s);
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(&pages_update_kernel<true>), kLocal)) return cudaErrorInvalidValue;
+  return launch_early(c, "pages_update", pages_update_kernel<true>, 1, kPlanThreads, bytes, a, s);
 }
 
 }  // namespace
@@ -396,7 +470,7 @@ extern "C" {
 
 size_t moe_kv_pages_scratch(int n_pages, int n_seqs) {
   if (n_pages < 1 || n_pages > kMaxPages || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
-  return 4 + size_t(3) * n_pages + n_seqs;
+  return 4 + size_t(4) * ((n_pages + 3) & ~3) + size_t(4) * n_seqs;
 }
 
 moe_status moe_kv_pages_update(const moe_kv_pages* pages, const moe_kv_batch* b, const moe_kv_cache* const* caches,
@@ -409,8 +483,7 @@ moe_status moe_kv_pages_update(const moe_kv_pages* pages, const moe_kv_batch* b,
   if (!b->q_off || !b->kv_len || !aligned(b->q_off, 4) || !aligned(b->kv_len, 4)) return MOE_ERR_ARG;
   if (b->max_new < 0 || b->max_kv < 0 || b->max_kv > (1 << 24)) return MOE_ERR_ARG;
   const KvCall c = begin_call(stream);
-  pages_update_kernel<<<1, kPlanThreads, 0, c.stream>>>(a, StepArgs{b->q_off, b->kv_len, b->max_new, b->max_kv});
-  if (cudaError_t e = c.launched("pages_update")) return status_of(e);
+  if (cudaError_t e = plan_update(a, StepArgs{b->q_off, b->kv_len, b->max_new, b->max_kv}, c)) return status_of(e);
   CopyArgs y{};
   y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
   return status_of(copy_pages(y, caches, n_caches, c));
@@ -424,8 +497,7 @@ moe_status moe_kv_pages_fork(const moe_kv_pages* pages, const int32_t* src, cons
   if (n == 0) return MOE_OK;
   if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return MOE_ERR_ARG;
   const KvCall c = begin_call(stream);
-  pages_fork_kernel<<<n, kForkThreads, 0, c.stream>>>(a, src, dst, n);
-  return status_of(c.launched("pages_fork"));
+  return status_of(launch_early(c, "pages_fork", pages_fork_kernel, n, kForkThreads, 0, a, src, dst, n));
 }
 
 moe_status moe_kv_pages_compact(const moe_kv_pages* pages, const moe_kv_cache* const* caches, int n_caches, void* stream) {
@@ -434,8 +506,7 @@ moe_status moe_kv_pages_compact(const moe_kv_pages* pages, const moe_kv_cache* c
   if (moe_status s = make_pages(pages, &a)) return s;
   if (moe_status s = check_caches(caches, n_caches, a.n_pages, pages->page_size)) return s;
   const KvCall c = begin_call(stream);
-  pages_compact_kernel<<<1, kPlanThreads, 0, c.stream>>>(a);
-  if (cudaError_t e = c.launched("pages_compact")) return status_of(e);
+  if (cudaError_t e = launch_early(c, "pages_compact", pages_compact_kernel, 1, kPlanThreads, 0, a)) return status_of(e);
   CopyArgs y{};
   y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
   y.table = a.table, y.list = a.list, y.entries = (long long)a.n_seqs * a.columns;

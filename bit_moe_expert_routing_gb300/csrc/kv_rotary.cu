@@ -7,8 +7,9 @@
 // key's or value's read (2) and stored (0.5625). So a thread holds sixteen
 // elements of a head, the two chunks of eight whose elements are turned
 // together, and nothing but a norm's sum and a key's re-ordering leaves its
-// registers; the angles, which all heads of a token share, are made once per
-// CTA.
+// registers. A thread stays with one token and steps through its heads: the
+// angles are made once per token, by all of the CTA, and then kept in
+// registers, as is the token's place in the cache.
 #include "kv_host.cuh"
 #include "kv_quant.cuh"
 
@@ -16,7 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRun = 16;  // step tokens of a CTA, at most
+constexpr int kBatch = 4;  // query heads of a thread whose loads are in flight together
 
 struct RotaryArgs {
   KvArgs kv;
@@ -30,7 +31,8 @@ struct RotaryArgs {
   const uint16_t* src[3];  // queries, keys, values
   long long stride[3];
   uint16_t* q_out;
-  int run, part;  // step tokens of a CTA; of their heads + 2 kv_heads heads
+  int lanes_log;  // log2 of a token's threads per 16 elements: heads taken side by side
+  int part;       // of the heads + kv_heads heads (a kv head: key and value), a CTA's
 };
 
 // cos and sin of `pos` times `turns` / 2^64 turns: whole turns fall out of the
@@ -42,61 +44,130 @@ __device__ __forceinline__ float2 turned_by(uint64_t turns, int pos) {
   return cs;
 }
 
-// A thread's sixteen elements as fp32.
-struct Sixteen {
-  float v[2][8];
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ uint32_t narrow(float2 v) {
+  uint32_t h;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v.y), "f"(v.x));
+  return h;
+}
+
+// A thread's chunks of eight elements, as stored, and as pairs of fp32.
+struct Chunks {
+  uint4 c[2];
 };
-__device__ __forceinline__ Sixteen widen(const uint4 (&x)[2]) {
-  Sixteen y;
+struct Wide {
+  float2 v[2][4];
+};
+__device__ __forceinline__ Wide widen(const Chunks& x) {
+  Wide y;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y.v[i][2 * j] = bf16lo(w[j]), y.v[i][2 * j + 1] = bf16hi(w[j]);
+    for (int j = 0; j < 4; ++j) y.v[i][j] = make_float2(bf16lo(w[j]), bf16hi(w[j]));
   }
   return y;
-}
-__device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
-  uint32_t h[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // 1 / sqrt(mean of the head's squares + eps); W neighbouring lanes hold a head.
 template <int W>
-__device__ __forceinline__ float inverse_norm(const Sixteen& x, float eps, unsigned lanes) {
+__device__ __forceinline__ float inverse_norm(const Wide& x, float eps, unsigned lanes) {
   auto sum = [&](float scale) {
-    float s = 0.f;
+    float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(x.v[i][j] * scale, x.v[i][j] * scale, s);
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = scale == 1.f ? x.v[i][j] : mul(x.v[i][j], both(scale));
+        s = fma(v, v, s);
+      }
+    float t = s.x + s.y;
 #pragma unroll
-    for (int off = W / 2; off; off >>= 1) s += __shfl_xor_sync(lanes, s, off);
-    return s;
+    for (int off = W / 2; off; off >>= 1) t += __shfl_xor_sync(lanes, t, off);
+    return t;
   };
   const float s = sum(1.f);
   if (s < INFINITY) return rsqrtf(s * (1.f / (16 * W)) + eps);
   return rsqrtf(sum(0x1p-70f) * (1.f / (16 * W))) * 0x1p-70f;  // squares past fp32: eps is nothing beside them
 }
 
-// CTA (run of step tokens, part of their heads): the queries', the keys', the
-// values' heads in turn, W threads to a head.
+// The turning of a thread's sixteen elements: cosines and sines of its eight
+// angles, where it has any.
+struct Turn {
+  float2 cos[4], sin[4];
+  bool on, interleaved;
+};
+
+// Norms (given a weight) and turns a head's elements.
+template <int W>
+__device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, const Wide& weight, float eps, const Turn& t,
+                                         unsigned lanes) {
+  Wide y = widen(x);
+  if (norm) {
+    const float2 inv = both(inverse_norm<W>(y, eps, lanes));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y.v[i][j] = mul(mul(y.v[i][j], inv), weight.v[i][j]);
+  }
+  if (t.on) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // angles 2 j and 2 j + 1
+      // halves: elements j of both chunks; neighbours: two pairs of one chunk
+      float2 &u = t.interleaved ? y.v[j / 2][2 * (j % 2)] : y.v[0][j], &v = t.interleaved ? y.v[j / 2][2 * (j % 2) + 1] : y.v[1][j];
+      const float2 p = t.interleaved ? make_float2(u.x, v.x) : u, q = t.interleaved ? make_float2(u.y, v.y) : v;
+      const float2 minus = make_float2(-t.sin[j].x, -t.sin[j].y);
+      const float2 a = fma(p, t.cos[j], mul(q, minus)), b = fma(q, t.cos[j], mul(p, t.sin[j]));
+      u = t.interleaved ? make_float2(a.x, b.x) : a;
+      v = t.interleaved ? make_float2(a.y, b.y) : b;
+    }
+  }
+  Chunks z;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    z.c[i] = make_uint4(narrow(y.v[i][0]), narrow(y.v[i][1]), narrow(y.v[i][2]), narrow(y.v[i][3]));
+  return z;
+}
+
+// CTA (tokens, part of their heads): W threads to a head, 2^lanes_log heads of
+// a token side by side.
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv_append_rotary_kernel(const RotaryArgs r) {
+__global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const RotaryArgs r) {
   constexpr int W = DIM / 16, kRows = kThreads / W;
-  extern __shared__ float2 cs[];  // [run][half]
-  __shared__ int pos[kMaxRun], page[kMaxRun];
+  extern __shared__ float4 cs[];  // [token][4][pairs]: cosines and sines of a lane's angles 2 j, 2 j + 1
+  __shared__ int pos_s[kRows], page_s[kRows];
   const KvArgs& a = r.kv;
-  const int i0 = blockIdx.x * r.run, n = min(r.run, a.n_tokens - i0);
-  const int h0 = blockIdx.y * r.part, h1 = min(h0 + r.part, r.heads + 2 * a.kv_heads);
-  const int w = threadIdx.x % W, row = threadIdx.x / W;
-  const unsigned lanes = (W == 32 ? ~0u : (1u << W) - 1u) << (threadIdx.x & 31 & ~(W - 1));
+  const int tokens = kRows >> r.lanes_log, side = 1 << r.lanes_log;
+  const int i0 = blockIdx.x * tokens, n = min(tokens, a.n_tokens - i0);
+  const int h0 = blockIdx.y * r.part, h1 = min(h0 + r.part, r.heads + a.kv_heads);
+  const int w = threadIdx.x % W, row = threadIdx.x / W, t = row >> r.lanes_log, g = row & (side - 1);
+  const unsigned lanes = ((1u << W) - 1u) << (threadIdx.x & 31 & ~(W - 1));
+  const int i = i0 + min(t, n - 1);
+  // this thread's chunks of eight elements: those turned together (halves apart, or neighbours)
+  const int pairs = r.half / 8;  // lanes that turn theirs
+  const bool apart = !r.interleaved && w < pairs;
+  const int c0 = apart ? w : 2 * w, c1 = apart ? w + pairs : 2 * w + 1;
+
+  // the first queries, asked for before the token is looked up
+  const int q_end = t < n ? min(h1, r.heads) : 0;
+  const uint16_t* src = r.src[0] + i * r.stride[0];
+  Chunks x[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (h + u * side < q_end) {
+        const uint16_t* p = src + (h + u * side) * DIM;
+        x[u].c[0] = *reinterpret_cast<const uint4*>(p + 8 * c0);
+        x[u].c[1] = *reinterpret_cast<const uint4*>(p + 8 * c1);
+      }
+  };
+  load(h0 + g);
 
   if (threadIdx.x < n) {
-    const int i = i0 + threadIdx.x, b = kv_seq_of(a, i);
-    const int p = a.kv_len[b] - (a.q_off[b + 1] - i);
+    const int b = kv_seq_of(a, i0 + threadIdx.x);
+    const int p = a.kv_len[b] - (a.q_off[b + 1] - (i0 + int(threadIdx.x)));
     int pg = -1;
     if (p >= a.max_kv) {
       report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadBatch);
@@ -104,112 +175,119 @@ __global__ void __launch_bounds__(kThreads) kv_append_rotary_kernel(const Rotary
       const long long first = kv_page_row(a, b, p >> a.page_bits, 0);
       if (first >= 0) pg = int((first >> a.page_bits) / a.kv_heads);
     }
-    pos[threadIdx.x] = p;
-    page[threadIdx.x] = pg;
+    pos_s[threadIdx.x] = p;
+    page_s[threadIdx.x] = pg;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < n * r.half; e += kThreads) {
-    const int t = e / r.half, f = e - t * r.half;
-    int p = pos[t];
+    const int tt = e / r.half, f = e - tt * r.half;
+    int p = pos_s[tt];
     if (r.positions) {
       const int ax = r.axis ? r.axis[f] : 0;
-      p = r.positions[(long long)(ax < r.axes ? ax : 0) * a.n_tokens + i0 + t];
+      p = r.positions[(long long)(ax < r.axes ? ax : 0) * a.n_tokens + i0 + tt];
     }
-    cs[e] = turned_by(r.turns[f], p);
+    // lane f / 8's angle f % 8: its float4 (f % 8) / 2, so that neighbouring lanes read neighbouring words
+    const float2 v = turned_by(r.turns[f], p);
+    float* at = reinterpret_cast<float*>(cs + (tt * 4 + (f % 8) / 2) * pairs + f / 8) + (f & 1);
+    at[0] = v.x;
+    at[2] = v.y;
   }
   __syncthreads();
+  if (t >= n) return;
+  Turn turn;
+  turn.on = w < pairs;
+  turn.interleaved = r.interleaved;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (turn.on) {
+      const float4 v = cs[(t * 4 + j) * pairs + w];
+      turn.cos[j] = make_float2(v.x, v.y);
+      turn.sin[j] = make_float2(v.z, v.w);
+    }
+  auto weights = [&](const float* p) {
+    Wide y;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y.v[k][j] = p ? *reinterpret_cast<const float2*>(p + 8 * (k ? c1 : c0) + 2 * j) : both(0.f);
+    return y;
+  };
 
-  // this thread's chunks of eight elements: those turned together (halves apart, or neighbours)
-  const int pairs = r.half / 8;  // lanes that turn theirs
-  const int c0 = r.interleaved || w >= pairs ? 2 * w : w, c1 = r.interleaved || w >= pairs ? 2 * w + 1 : w + pairs;
+  {
+    const Wide weight = weights(r.weight[0]);
+    uint16_t* dst = r.q_out + (long long)i * r.heads * DIM;
+    for (int h = h0 + g; h < q_end; h += kBatch * side) {
+      if (h != h0 + g) load(h);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (h + u * side >= q_end) break;
+        const Chunks y = turned<W>(x[u], r.weight[0], weight, r.eps, turn, lanes);
+        uint16_t* p = dst + (h + u * side) * DIM;
+        *reinterpret_cast<uint4*>(p + 8 * c0) = y.c[0];
+        *reinterpret_cast<uint4*>(p + 8 * c1) = y.c[1];
+      }
+    }
+  }
+
+  const int page = page_s[t], slot = pos_s[t] & ((1 << a.page_bits) - 1);
+  if (page < 0) return;
   bool bad = false;
+  const Wide weight = weights(r.weight[1]);
+  for (int h = max(h0, r.heads) - r.heads + g; h < h1 - r.heads; h += side) {
+    const uint16_t *k = r.src[1] + i * r.stride[1] + h * DIM, *v = r.src[2] + i * r.stride[2] + h * DIM;
+    Chunks kx, vx;
+    kx.c[0] = *reinterpret_cast<const uint4*>(k + 8 * c0);
+    kx.c[1] = *reinterpret_cast<const uint4*>(k + 8 * c1);
+    vx.c[0] = *reinterpret_cast<const uint4*>(v + 16 * w);
+    vx.c[1] = *reinterpret_cast<const uint4*>(v + 16 * w + 8);
+    kx = turned<W>(kx, r.weight[1], weight, r.eps, turn, lanes);
+    if (!r.interleaved) {
+      // the quantisation takes a head's elements in order: chunks 2 w and 2 w + 1, from where they are
+      Chunks z;
 #pragma unroll
-  for (int kind = 0; kind < 3; ++kind) {
-    const int first = kind == 0 ? 0 : r.heads + (kind - 1) * a.kv_heads;  // of the kind's heads
-    const int lo = max(h0 - first, 0), hi = min(h1 - first, kind == 0 ? r.heads : a.kv_heads);
-    const int per = hi - lo;
-    if (per <= 0) continue;
-    const float* weight = kind < 2 ? r.weight[kind] : nullptr;
-    float wt[2][8];
-    if (weight)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wt[0][j] = weight[8 * c0 + j], wt[1][j] = weight[8 * c1 + j];
-    for (int e = row; e < n * per; e += kRows) {
-      const int t = e / per, h = lo + e - t * per;
-      const uint16_t* src = r.src[kind] + (i0 + t) * r.stride[kind] + h * DIM;
-      uint4 x[2];
-      if (kind == 2) {
-        x[0] = *reinterpret_cast<const uint4*>(src + 16 * w);
-        x[1] = *reinterpret_cast<const uint4*>(src + 16 * w + 8);
-      } else {
-        x[0] = *reinterpret_cast<const uint4*>(src + 8 * c0);
-        x[1] = *reinterpret_cast<const uint4*>(src + 8 * c1);
-        Sixteen y = widen(x);
-        if (weight) {
-          const float inv = inverse_norm<W>(y, r.eps, lanes);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y.v[i][j] = y.v[i][j] * inv * wt[i][j];
-        }
-        if (w < pairs) {
-          const float2* at = cs + t * r.half + 8 * w;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 c = at[j];
-            float& p = r.interleaved ? y.v[j / 4][2 * (j % 4)] : y.v[0][j];
-            float& q = r.interleaved ? y.v[j / 4][2 * (j % 4) + 1] : y.v[1][j];
-            const float u = p * c.x - q * c.y;
-            q = q * c.x + p * c.y;
-            p = u;
-          }
-        }
-        x[0] = narrow(y.v[0]);
-        x[1] = narrow(y.v[1]);
+      for (int e = 0; e < 2; ++e) {
+        const int c = 2 * w + e;
+        const int from = c < pairs ? c : c < 2 * pairs ? c - pairs : c / 2;
+        const bool second = c < pairs ? false : c < 2 * pairs ? true : c & 1;
+        auto take = [&](uint32_t u0, uint32_t u1) {
+          const uint32_t v0 = __shfl_sync(lanes, u0, from, W), v1 = __shfl_sync(lanes, u1, from, W);
+          return second ? v1 : v0;
+        };
+        z.c[e] = make_uint4(take(kx.c[0].x, kx.c[1].x), take(kx.c[0].y, kx.c[1].y), take(kx.c[0].z, kx.c[1].z),
+                            take(kx.c[0].w, kx.c[1].w));
       }
-      if (kind == 0) {
-        uint16_t* dst = r.q_out + ((long long)(i0 + t) * r.heads + h) * DIM;
-        *reinterpret_cast<uint4*>(dst + 8 * c0) = x[0];
-        *reinterpret_cast<uint4*>(dst + 8 * c1) = x[1];
-        continue;
-      }
-      if (kind == 1 && !r.interleaved) {
-        // the quantisation takes a head's elements in order: chunks 2 w and 2 w + 1, from where they are
-        uint4 z[2];
+      kx = z;
+    }
+    const long long at = (((long long)page * a.kv_heads + h) << a.page_bits) + slot;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = 2 * w + i;
-          const int from = c < pairs ? c : c < 2 * pairs ? c - pairs : c / 2;
-          const bool second = c < pairs ? false : c < 2 * pairs ? true : c & 1;
-          auto take = [&](uint32_t u0, uint32_t u1) {
-            const uint32_t v0 = __shfl_sync(lanes, u0, from, W), v1 = __shfl_sync(lanes, u1, from, W);
-            return second ? v1 : v0;
-          };
-          z[i] = make_uint4(take(x[0].x, x[1].x), take(x[0].y, x[1].y), take(x[0].z, x[1].z), take(x[0].w, x[1].w));
-        }
-        x[0] = z[0], x[1] = z[1];
-      }
-      if (page[t] < 0) continue;
-      const long long at = (((long long)page[t] * a.kv_heads + h) << a.page_bits) + (pos[t] & ((1 << a.page_bits) - 1));
+    for (int which = 0; which < 2; ++which) {
       uint16_t s, b;
-      const uint2 word = quantise16(x, &s, &b, &bad);
-      *reinterpret_cast<uint2*>(a.codes[kind - 1] + at * (DIM / 8) + 2 * w) = word;
+      const uint2 word = quantise16(which ? vx.c : kx.c, &s, &b, &bad);
+      *reinterpret_cast<uint2*>(a.codes[which] + at * (DIM / 8) + 2 * w) = word;
       if ((w & 3) == 0) {
-        a.scales[kind - 1][at * (DIM / 64) + w / 4] = s;
-        a.biases[kind - 1][at * (DIM / 64) + w / 4] = b;
+        a.scales[which][at * (DIM / 64) + w / 4] = s;
+        a.biases[which][at * (DIM / 64) + w / 4] = b;
       }
     }
   }
   if (bad) report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadNumber);
 }
 
+// Heads side by side: four, so that a thread makes the most of its token's
+// angles, or more where that leaves SMs without CTAs; then the heads are
+// divided, too.
 template <int DIM>
 cudaError_t launch(RotaryArgs r, const KvCall& c) {
-  const int heads = r.heads + 2 * r.kv.kv_heads;
-  r.run = kMaxRun;
+  constexpr int kRows = kThreads / (DIM / 16);
+  const int heads = r.heads + r.kv.kv_heads, want = 4 * num_sms();
+  auto ctas = [&] { return (r.kv.n_tokens + (kRows >> r.lanes_log) - 1) / (kRows >> r.lanes_log); };
+  r.lanes_log = 2;
+  while ((1 << r.lanes_log) < kRows && (1 << r.lanes_log) < heads && ctas() < want) ++r.lanes_log;
   r.part = heads;
-  const dim3 grid((r.kv.n_tokens + r.run - 1) / r.run, (heads + r.part - 1) / r.part);
-  kv_append_rotary_kernel<DIM><<<grid, kThreads, r.run * r.half * sizeof(float2), c.stream>>>(r);
+  if (ctas() < want) r.part = std::max(1 << r.lanes_log, (heads + want / ctas() - 1) / (want / ctas()));
+  const int tokens = kRows >> r.lanes_log;
+  const dim3 grid(ctas(), (heads + r.part - 1) / r.part);
+  kv_append_rotary_kernel<DIM><<<grid, kThreads, tokens * r.half * sizeof(float2), c.stream>>>(r);
   return c.launched("kv_append_rotary");
 }
 
