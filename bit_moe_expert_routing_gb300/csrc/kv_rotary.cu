@@ -16,7 +16,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // (CTAs of 256 threads are 4% slower, of 64 the same)
 constexpr int kBatch = 4;  // query heads of a thread whose loads are in flight together
 
 struct RotaryArgs {
@@ -93,36 +93,55 @@ __device__ __forceinline__ float inverse_norm(const Wide& x, float eps, unsigned
   return rsqrtf(sum(0x1p-70f) * (1.f / (16 * W))) * 0x1p-70f;  // squares past fp32: eps is nothing beside them
 }
 
-// The turning of a thread's sixteen elements: cosines and sines of its eight
-// angles, where it has any.
+// What a thread's elements are multiplied with once they are normed: weights
+// (1 without a norm) times cosines and sines of its eight angles, where it has
+// any. For chunks p and q of elements that are turned together:
+//   p' = p pc - q qs,  q' = q qc + p ps
 struct Turn {
-  float2 cos[4], sin[4];
-  bool on, interleaved;
+  float2 pc[4], qc[4], ps[4], qs[4];
 };
+template <bool INTERLEAVED>
+__device__ __forceinline__ Turn turn_of(const Wide& weight, const float2 (&cos)[4], const float2 (&sin)[4]) {
+  Turn t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 p, q;
+    if (INTERLEAVED) {  // angles 2 j, 2 j + 1 turn the pairs of elements 4 j .. 4 j + 3
+      const float2 u = weight.v[j / 2][2 * (j % 2)], v = weight.v[j / 2][2 * (j % 2) + 1];
+      p = make_float2(u.x, v.x), q = make_float2(u.y, v.y);
+    } else {
+      p = weight.v[0][j], q = weight.v[1][j];
+    }
+    t.pc[j] = mul(p, cos[j]), t.ps[j] = mul(p, sin[j]);
+    t.qc[j] = mul(q, cos[j]), t.qs[j] = mul(q, make_float2(-sin[j].x, -sin[j].y));
+  }
+  return t;
+}
 
-// Norms (given a weight) and turns a head's elements.
-template <int W>
-__device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, const Wide& weight, float eps, const Turn& t,
-                                         unsigned lanes) {
+// Norms (if asked) and turns a head's elements. `on`: this thread's are turned; else they meet their weights alone, in
+// t.pc and t.qc.
+template <int W, bool INTERLEAVED>
+__device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, float eps, bool on, const Turn& t, unsigned lanes) {
   Wide y = widen(x);
   if (norm) {
     const float2 inv = both(inverse_norm<W>(y, eps, lanes));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y.v[i][j] = mul(mul(y.v[i][j], inv), weight.v[i][j]);
+      for (int j = 0; j < 4; ++j) y.v[i][j] = mul(y.v[i][j], inv);
   }
-  if (t.on) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // angles 2 j and 2 j + 1
-      // halves: elements j of both chunks; neighbours: two pairs of one chunk
-      float2 &u = t.interleaved ? y.v[j / 2][2 * (j % 2)] : y.v[0][j], &v = t.interleaved ? y.v[j / 2][2 * (j % 2) + 1] : y.v[1][j];
-      const float2 p = t.interleaved ? make_float2(u.x, v.x) : u, q = t.interleaved ? make_float2(u.y, v.y) : v;
-      const float2 minus = make_float2(-t.sin[j].x, -t.sin[j].y);
-      const float2 a = fma(p, t.cos[j], mul(q, minus)), b = fma(q, t.cos[j], mul(p, t.sin[j]));
-      u = t.interleaved ? make_float2(a.x, b.x) : a;
-      v = t.interleaved ? make_float2(a.y, b.y) : b;
+  for (int j = 0; j < 4; ++j) {
+    float2 &u = INTERLEAVED ? y.v[j / 2][2 * (j % 2)] : y.v[0][j], &v = INTERLEAVED ? y.v[j / 2][2 * (j % 2) + 1] : y.v[1][j];
+    const float2 p = INTERLEAVED ? make_float2(u.x, v.x) : u, q = INTERLEAVED ? make_float2(u.y, v.y) : v;
+    float2 a, b;
+    if (on) {
+      a = fma(p, t.pc[j], mul(q, t.qs[j])), b = fma(q, t.qc[j], mul(p, t.ps[j]));
+    } else {
+      a = mul(p, t.pc[j]), b = mul(q, t.qc[j]);
     }
+    u = INTERLEAVED ? make_float2(a.x, b.x) : a;
+    v = INTERLEAVED ? make_float2(a.y, b.y) : b;
   }
   Chunks z;
 #pragma unroll
@@ -133,8 +152,8 @@ __device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, const Wide&
 
 // CTA (tokens, part of their heads): W threads to a head, 2^lanes_log heads of
 // a token side by side.
-template <int DIM>
-__global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const RotaryArgs r) {
+template <int DIM, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const RotaryArgs r) {
   constexpr int W = DIM / 16, kRows = kThreads / W;
   extern __shared__ float4 cs[];  // [token][4][pairs]: cosines and sines of a lane's angles 2 j, 2 j + 1
   __shared__ int pos_s[kRows], page_s[kRows];
@@ -147,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const Rot
   const int i = i0 + min(t, n - 1);
   // this thread's chunks of eight elements: those turned together (halves apart, or neighbours)
   const int pairs = r.half / 8;  // lanes that turn theirs
-  const bool apart = !r.interleaved && w < pairs;
+  const bool on = w < pairs, apart = !INTERLEAVED && on;
   const int c0 = apart ? w : 2 * w, c1 = apart ? w + pairs : 2 * w + 1;
 
   // the first queries, asked for before the token is looked up
@@ -194,34 +213,34 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const Rot
   }
   __syncthreads();
   if (t >= n) return;
-  Turn turn;
-  turn.on = w < pairs;
-  turn.interleaved = r.interleaved;
+  float2 cos[4], sin[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (turn.on) {
+  for (int j = 0; j < 4; ++j) {
+    cos[j] = both(1.f), sin[j] = both(0.f);
+    if (on) {
       const float4 v = cs[(t * 4 + j) * pairs + w];
-      turn.cos[j] = make_float2(v.x, v.y);
-      turn.sin[j] = make_float2(v.z, v.w);
+      cos[j] = make_float2(v.x, v.y);
+      sin[j] = make_float2(v.z, v.w);
     }
+  }
   auto weights = [&](const float* p) {
     Wide y;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y.v[k][j] = p ? *reinterpret_cast<const float2*>(p + 8 * (k ? c1 : c0) + 2 * j) : both(0.f);
+      for (int j = 0; j < 4; ++j) y.v[k][j] = p ? *reinterpret_cast<const float2*>(p + 8 * (k ? c1 : c0) + 2 * j) : both(1.f);
     return y;
   };
 
   {
-    const Wide weight = weights(r.weight[0]);
+    const Turn turn = turn_of<INTERLEAVED>(weights(r.weight[0]), cos, sin);
     uint16_t* dst = r.q_out + (long long)i * r.heads * DIM;
     for (int h = h0 + g; h < q_end; h += kBatch * side) {
       if (h != h0 + g) load(h);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (h + u * side >= q_end) break;
-        const Chunks y = turned<W>(x[u], r.weight[0], weight, r.eps, turn, lanes);
+        const Chunks y = turned<W, INTERLEAVED>(x[u], r.weight[0], r.eps, on, turn, lanes);
         uint16_t* p = dst + (h + u * side) * DIM;
         *reinterpret_cast<uint4*>(p + 8 * c0) = y.c[0];
         *reinterpret_cast<uint4*>(p + 8 * c1) = y.c[1];
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const Rot
   const int page = page_s[t], slot = pos_s[t] & ((1 << a.page_bits) - 1);
   if (page < 0) return;
   bool bad = false;
-  const Wide weight = weights(r.weight[1]);
+  const Turn turn = turn_of<INTERLEAVED>(weights(r.weight[1]), cos, sin);
   for (int h = max(h0, r.heads) - r.heads + g; h < h1 - r.heads; h += side) {
     const uint16_t *k = r.src[1] + i * r.stride[1] + h * DIM, *v = r.src[2] + i * r.stride[2] + h * DIM;
     Chunks kx, vx;
@@ -240,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const Rot
     kx.c[1] = *reinterpret_cast<const uint4*>(k + 8 * c1);
     vx.c[0] = *reinterpret_cast<const uint4*>(v + 16 * w);
     vx.c[1] = *reinterpret_cast<const uint4*>(v + 16 * w + 8);
-    kx = turned<W>(kx, r.weight[1], weight, r.eps, turn, lanes);
-    if (!r.interleaved) {
+    kx = turned<W, INTERLEAVED>(kx, r.weight[1], r.eps, on, turn, lanes);
+    if (!INTERLEAVED) {
       // the quantisation takes a head's elements in order: chunks 2 w and 2 w + 1, from where they are
       Chunks z;
 #pragma unroll
@@ -273,21 +292,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_rotary_kernel(const Rot
   if (bad) report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadNumber);
 }
 
-// Heads side by side: four, so that a thread makes the most of its token's
-// angles, or more where that leaves SMs without CTAs; then the heads are
-// divided, too.
+// Heads side by side: what makes 512 bytes of a token, so that a thread makes
+// the most of its token's angles and loads stay long, or more where that leaves
+// SMs without CTAs; then the heads are divided, too. (Measured, us: 4096 tokens
+// of 16 heads over 2 of 256 dims, one side by side 16.9, two 18.1, four 22.0;
+// 14593 tokens of 32 over 8 of 128, one 79, two 67, four 68, eight 73; 3282
+// tokens of 8 over 4 of 64, two 7.7, four 5.8, eight 8.1.)
 template <int DIM>
 cudaError_t launch(RotaryArgs r, const KvCall& c) {
   constexpr int kRows = kThreads / (DIM / 16);
-  const int heads = r.heads + r.kv.kv_heads, want = 4 * num_sms();
+  const int heads = r.heads + r.kv.kv_heads, want = 2 * num_sms();
   auto ctas = [&] { return (r.kv.n_tokens + (kRows >> r.lanes_log) - 1) / (kRows >> r.lanes_log); };
-  r.lanes_log = 2;
+  r.lanes_log = DIM == 256 ? 0 : DIM == 128 ? 1 : 2;
   while ((1 << r.lanes_log) < kRows && (1 << r.lanes_log) < heads && ctas() < want) ++r.lanes_log;
   r.part = heads;
   if (ctas() < want) r.part = std::max(1 << r.lanes_log, (heads + want / ctas() - 1) / (want / ctas()));
   const int tokens = kRows >> r.lanes_log;
   const dim3 grid(ctas(), (heads + r.part - 1) / r.part);
-  kv_append_rotary_kernel<DIM><<<grid, kThreads, tokens * r.half * sizeof(float2), c.stream>>>(r);
+  (r.interleaved ? kv_append_rotary_kernel<DIM, true> : kv_append_rotary_kernel<DIM, false>)<<<
+      grid, kThreads, tokens * r.half * sizeof(float2), c.stream>>>(r);
   return c.launched("kv_append_rotary");
 }
 
