@@ -38,7 +38,8 @@ struct PrefixArgs {
   int max_own;
 };
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kFew = 8;
 constexpr int kBadGroups = 204;  // detail in the status word
 
 // One CTA: groups first, then sequences. Nothing is shared unless all groups
@@ -96,11 +97,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
       shares = skip > 0 && own >= 0 && own <= p.max_own && n <= a.max_new;
     }
     if (bad) continue;  // (no token is looked at)
-    // the tokens of the warp's sequences, one sequence after the other
-    for (int l = 0; l < 32; ++l) {
-      const int first = __shfl_sync(~0u, q0, l), count = __shfl_sync(~0u, n, l);
-      const uint8_t flag = __shfl_sync(~0u, int(shares), l);
-      for (int i = lane; i < count; i += 32) p.shares[first + i] = flag;
+    // its tokens' marks: a few at once, more of them by the warp, one sequence after the other
+    const bool flag = shares;
+    if (n <= kFew)
+      for (int i = 0; i < n; ++i) p.shares[q0 + i] = flag;
+    for (unsigned long_ones = __ballot_sync(~0u, n > kFew); long_ones; long_ones &= long_ones - 1) {
+      const int l = __ffs(long_ones) - 1, first = __shfl_sync(~0u, q0, l), count = __shfl_sync(~0u, n, l);
+      const uint8_t mark = __shfl_sync(~0u, int(flag), l);
+      for (int i = lane; i < count; i += 32) p.shares[first + i] = mark;
     }
   }
 }
