@@ -278,6 +278,11 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
   }
 }
 
+// Copies 16 bytes to shared memory: the first src_bytes of them, then zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
 // ---- expand -------------------------------------------------------------------------------
 
 // Pairs (codes in bits 0..3 of both halves of p) -> bf16 scale * code + bias, rounded once.
@@ -287,6 +292,14 @@ __device__ __forceinline__ uint32_t dq_pair(uint32_t p, __nv_bfloat162 s2, __nv_
   const __nv_bfloat162 r = __hfma2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), k128), s2, b2);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// Shared memory of a tile's codes, scales and biases, with 16 bytes of padding after eight keys.
+template <int DIM>
+struct ExpandStage {
+  static constexpr int kScales = kBK / 8 * (DIM * 4 + 16);
+  static constexpr int kBiases = kScales + kBK / 8 * (DIM / 64 * 16 + 16);
+  static constexpr int kBytes = kBiases + kBK / 8 * (DIM / 64 * 16 + 16);
+};
 
 // CTA 0 makes the plan; the others expand the keys or the values of one key
 // tile of one (sequence, kv head): the keys row by row, the values eight keys of eight dims at a time,
@@ -330,37 +343,46 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   __syncthreads();
   const long long tile = ((long long)bi * m.nh + h) * m.tiles_max + t;
   constexpr int W = DIM / 8, G = DIM / 64;
+  // the tile's codes, scales and biases, all asked for at once: eight keys' rows, then 16 bytes of padding, so that the
+  // eight chunks of keys that neighbouring lanes take are in different banks
+  using St = ExpandStage<DIM>;
+  __shared__ __align__(16) uint8_t stage[St::kBytes];
+  const uint32_t stage_s = smem_u32(stage);
+  constexpr int kCodeChunks = kBK * DIM / 32, kSbChunks = kBK * G / 8;  // of 16 bytes; of the scales, or the biases
+  for (int e = threadIdx.x; e < kCodeChunks + 2 * kSbChunks; e += kPlanThreads) {
+    const bool codes = e < kCodeChunks;
+    const int x = codes ? e : (e - kCodeChunks) % kSbChunks, which = codes ? 0 : 1 + (e - kCodeChunks) / kSbChunks;
+    const int per8 = codes ? DIM / 4 : G, key8 = x / per8, in8 = x % per8;  // chunks of eight keys, and the place in them
+    const long long row = rows16[key8 >> 1] + (key8 & 1) * 8;
+    const uint8_t* p = codes ? reinterpret_cast<const uint8_t*>(kv.codes[values]) + row * (DIM / 2)
+                             : reinterpret_cast<const uint8_t*>(which == 1 ? kv.scales[values] : kv.biases[values]) + row * (2 * G);
+    const uint32_t dst = stage_s + (which == 0 ? 0 : which == 1 ? St::kScales : St::kBiases) + key8 * (per8 * 16 + 16) + in8 * 16;
+    const bool there = rows16[key8 >> 1] >= 0;  // (else zeros)
+    cp_async16(dst, there ? p + in8 * 16 : reinterpret_cast<const uint8_t*>(kv.codes[values]), there ? 16u : 0u);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  auto code_of = [&](int key, int w) {
+    return *reinterpret_cast<const uint32_t*>(stage + (key >> 3) * (DIM * 4 + 16) + (key & 7) * (DIM / 2) + w * 4);
+  };
+  auto sb_of = [&](int key, int w, int at) {
+    return *reinterpret_cast<const uint16_t*>(stage + at + (key >> 3) * (G * 16 + 16) + ((key & 7) * G + w / 8) * 2);
+  };
   if (!values) {
     uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
     // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
     const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
-    constexpr int kBatch = 4;  // loads in flight before the first is used
-    static_assert(kBK * W / kPlanThreads % kBatch == 0, "batches of whole passes");
     const int w = threadIdx.x % W;
-    for (int p = 0; p < kBK * W / kPlanThreads; p += kBatch) {
-      uint32_t c[kBatch];
-      uint16_t sc[kBatch], bs[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int key = (p + i) * (kPlanThreads / W) + threadIdx.x / W;
-        const long long r16 = rows16[key >> 4];
-        c[i] = sc[i] = bs[i] = 0;
-        if (r16 >= 0 && k0 + key <= maxpos) {
-          const long long row = r16 + (key & 15);
-          c[i] = kv.codes[0][row * W + w];
-          sc[i] = kv.scales[0][row * G + w / 8];
-          bs[i] = kv.biases[0][row * G + w / 8];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int key = (p + i) * (kPlanThreads / W) + threadIdx.x / W;
-        const __nv_bfloat16 s16 = __ushort_as_bfloat16(sc[i]), b16 = __ushort_as_bfloat16(bs[i]);
-        uint32_t o[4];
-        dq8_bf16(c[i], __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
-        *reinterpret_cast<uint4*>(kd + (key >> 6) * ManyCfg<DIM>::kSlot + (w / 8) * 8192 + sw128(key & 63, w & 7)) =
-            make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
-      }
+#pragma unroll 4
+    for (int key = threadIdx.x / W; key < kBK; key += kPlanThreads / W) {
+      const bool in = k0 + key <= maxpos;
+      const uint32_t c = in ? code_of(key, w) : 0u;
+      const __nv_bfloat16 s16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kScales) : 0);
+      const __nv_bfloat16 b16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kBiases) : 0);
+      uint32_t o[4];
+      dq8_bf16(c, __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
+      *reinterpret_cast<uint4*>(kd + (key >> 6) * ManyCfg<DIM>::kSlot + (w / 8) * 8192 + sw128(key & 63, w & 7)) =
+          make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
     }
     return;
   }
@@ -369,28 +391,23 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   for (int e = threadIdx.x; e < (kBK / 8) * W; e += kPlanThreads) {
     const int ko = e & 7, w = (e >> 3) % W, kb = (e >> 3) / W;  // 8-key chunk in its block, word, block of 64 keys
     const int key0 = kb * 64 + ko * 8;
-    uint32_t c[8];
-    uint32_t sc[8], bs[8];
-    const long long r16 = rows16[key0 >> 4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = sc[i] = bs[i] = 0;
-      // a slot that no row sees may hold anything: its zero probability needs a finite value
-      const int key = k0 + key0 + i;
-      if (r16 >= 0 && key <= maxpos && (key >= lo || key < m.a.sinks)) {
-        const long long row = r16 + (key0 & 15) + i;
-        c[i] = kv.codes[1][row * W + w];
-        sc[i] = kv.scales[1][row * G + w / 8];
-        bs[i] = kv.biases[1][row * G + w / 8];
-      }
-    }
     uint32_t o[8][4];  // [dim][pair of keys]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t s2 = sc[2 * i] | sc[2 * i + 1] << 16, b2 = bs[2 * i] | bs[2 * i + 1] << 16;
+      uint32_t c[2], sc[2], bs[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // a slot that no row sees may hold anything: its zero probability needs a finite value
+        const int key = key0 + 2 * i + j, at = k0 + key;
+        const bool in = at <= maxpos && (at >= lo || at < m.a.sinks);
+        c[j] = in ? code_of(key, w) : 0u;
+        sc[j] = in ? sb_of(key, w, St::kScales) : 0u;
+        bs[j] = in ? sb_of(key, w, St::kBiases) : 0u;
+      }
+      const uint32_t s2 = sc[0] | sc[1] << 16, b2 = bs[0] | bs[1] << 16;
       const __nv_bfloat162 sp = *reinterpret_cast<const __nv_bfloat162*>(&s2);
       const __nv_bfloat162 bp = *reinterpret_cast<const __nv_bfloat162*>(&b2);
-      const uint32_t lo2 = __byte_perm(c[2 * i], c[2 * i + 1], 0x5410), hi2 = __byte_perm(c[2 * i], c[2 * i + 1], 0x7632);
+      const uint32_t lo2 = __byte_perm(c[0], c[1], 0x5410), hi2 = __byte_perm(c[0], c[1], 0x7632);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         o[n][i] = dq_pair(lo2 >> (4 * n), sp, bp);
@@ -687,9 +704,6 @@ __device__ __forceinline__ void keep(const uint32_t (&p)[32]) {
                  "r"(p[e + 7]));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
 // Arrives on `bar` once every cp.async of this thread has landed (counted in the barrier's arrivals).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");

@@ -84,16 +84,73 @@ __device__ __forceinline__ int4 refs4(const int32_t* refs, int n_pages, int p) {
   return r;
 }
 
+struct CopyArgs {
+  uint32_t* codes[kMaxCaches][2];
+  uint16_t* scales[kMaxCaches][2];
+  uint16_t* biases[kMaxCaches][2];
+  int n_caches, n_pages;
+  int codes16, sb16;       // 16-byte words of a page's codes; of its scales, or biases (keys' or values')
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;    // on the device; NULL: n
+  int n;
+  WsHeader* hdr;
+  int32_t* table;          // compaction: entries past count[1] become list's; NULL: none
+  const int32_t* list;
+  long long entries;
+};
+
+// A thread's 16 bytes of a page of a cache, at word `x` of the page's six arrays.
+__device__ __forceinline__ uint4* word_of(const CopyArgs& c, int cache, int page, int x) {
+  const int half = c.codes16 + 2 * c.sb16, kv = x >= half;
+  x -= kv ? half : 0;
+  if (x < c.codes16) return reinterpret_cast<uint4*>(c.codes[cache][kv]) + (long long)page * c.codes16 + x;
+  x -= c.codes16;
+  uint16_t* p = x < c.sb16 ? c.scales[cache][kv] : c.biases[cache][kv];
+  return reinterpret_cast<uint4*>(p) + (long long)page * c.sb16 + (x < c.sb16 ? x : x - c.sb16);
+}
+
+// The moves, by `ctas` CTAs of THREADS threads of which this is number `cta`.
+template <int THREADS>
+__device__ __forceinline__ void copy_moves(const CopyArgs& c, int n, int cta, int ctas) {
+  constexpr int kWords = 4;  // of a thread, in flight together
+  const int words = 2 * (c.codes16 + 2 * c.sb16), pieces = (words + kWords * THREADS - 1) / (kWords * THREADS);
+  const long long units = (long long)n * c.n_caches * pieces;
+  for (long long u = cta; u < units; u += ctas) {
+    const int piece = int(u % pieces);
+    const long long v = u / pieces;
+    const int cache = int(v % c.n_caches), move = int(v / c.n_caches);
+    const int from = c.src[move], to = c.dst[move];
+    if (unsigned(from) >= unsigned(c.n_pages) || unsigned(to) >= unsigned(c.n_pages)) {
+      if (threadIdx.x == 0) report(c.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
+      continue;
+    }
+    if (from == to) continue;
+    uint4 x[kWords];
+    const int x0 = piece * kWords * THREADS + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (x0 + i * THREADS < words) x[i] = *word_of(c, cache, from, x0 + i * THREADS);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (x0 + i * THREADS < words) *word_of(c, cache, to, x0 + i * THREADS) = x[i];
+  }
+}
+
 constexpr int kAbreast = 2;  // sequences whose entries a warp asks for together
 
-// One CTA. LOCAL: the copy of the references, the list of free pages and the
+// One CTA, or a cluster of them (COPY): the first one plans, then all of them
+// copy what has to be. (Two launches that overlap copy more at once; a step's
+// few pages, and the many steps that copy none, are done sooner in one.)
+//
+// LOCAL: the copy of the references, the list of free pages and the
 // sequences' numbers are in shared memory, else in the scratch memory.
 //
 // The copy is as the references are once pages have gone back, and stays so:
 // whether a page is shared is asked twice, when what is wanted is counted and
 // when it is given.
 template <bool LOCAL>
-__global__ void __launch_bounds__(kPlanThreads, 1) pages_update_kernel(const PagesArgs a, const StepArgs s) {
+__device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s) {
   extern __shared__ int4 local[];
   __shared__ int buf[kPlanWarps];
   __shared__ int n_moves;
@@ -104,8 +161,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_update_kernel(const Pag
   int32_t* need_s = LOCAL ? list + padded : a.seqs;
   int32_t *first_s = need_s + a.n_seqs, *held_s = first_s + a.n_seqs, *want_s = held_s + a.n_seqs;
   auto get = [](const int32_t* p) { return LOCAL ? *p : __ldcg(p); };
-  griddep_wait();
-  griddep_launch();
   if (threadIdx.x == 0) n_moves = 0;
 
   for (int p = 4 * threadIdx.x; p < a.n_pages; p += kChunk) {
@@ -238,6 +293,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_update_kernel(const Pag
   }
   __syncthreads();
   if (threadIdx.x == 0) a.count[0] = n_moves, a.count[1] = a.n_pages;
+  __syncthreads();
+}
+
+constexpr int kCluster = 8;
+
+template <bool LOCAL, bool COPY>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    pages_update_kernel(const PagesArgs a, const StepArgs s, const __grid_constant__ CopyArgs c) {
+  griddep_wait();
+  griddep_launch();
+  if (!COPY || blockIdx.x == 0) plan_step<LOCAL>(a, s);
+  if (!COPY) return;
+  // the plan, to the cluster's other CTAs
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  copy_moves<kPlanThreads>(c, __ldcg(a.count), blockIdx.x, kCluster);
 }
 
 // One CTA: which pages move where.
@@ -293,34 +363,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_kernel(const Pa
   if (threadIdx.x == 0) a.count[0] = n_src, a.count[1] = live;
 }
 
-struct CopyArgs {
-  uint32_t* codes[kMaxCaches][2];
-  uint16_t* scales[kMaxCaches][2];
-  uint16_t* biases[kMaxCaches][2];
-  int n_caches, n_pages;
-  int codes16, sb16;       // 16-byte words of a page's codes; of its scales, or biases (keys' or values')
-  const int32_t* src;
-  const int32_t* dst;
-  const int32_t* count;    // on the device; NULL: n
-  int n;
-  WsHeader* hdr;
-  int32_t* table;          // compaction: entries past count[1] become list's; NULL: none
-  const int32_t* list;
-  long long entries;
-};
-
-// A thread's 16 bytes of a page of a cache, at word `x` of the page's six arrays.
-__device__ __forceinline__ uint4* word_of(const CopyArgs& c, int cache, int page, int x) {
-  const int half = c.codes16 + 2 * c.sb16, kv = x >= half;
-  x -= kv ? half : 0;
-  if (x < c.codes16) return reinterpret_cast<uint4*>(c.codes[cache][kv]) + (long long)page * c.codes16 + x;
-  x -= c.codes16;
-  uint16_t* p = x < c.sb16 ? c.scales[cache][kv] : c.biases[cache][kv];
-  return reinterpret_cast<uint4*>(p) + (long long)page * c.sb16 + (x < c.sb16 ? x : x - c.sb16);
-}
-
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyArgs c) {
-  constexpr int kWords = 4;  // of a thread, in flight together
   griddep_wait();
   griddep_launch();
   if (c.table) {
@@ -330,28 +373,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
       if (p >= from && p < c.n_pages) c.table[i] = c.list[p];
     }
   }
-  const int n = c.count ? c.count[0] : c.n;
-  const int words = 2 * (c.codes16 + 2 * c.sb16), pieces = (words + kWords * kCopyThreads - 1) / (kWords * kCopyThreads);
-  const long long units = (long long)n * c.n_caches * pieces;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int piece = int(u % pieces);
-    const long long v = u / pieces;
-    const int cache = int(v % c.n_caches), move = int(v / c.n_caches);
-    const int from = c.src[move], to = c.dst[move];
-    if (unsigned(from) >= unsigned(c.n_pages) || unsigned(to) >= unsigned(c.n_pages)) {
-      if (threadIdx.x == 0) report(c.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
-      continue;
-    }
-    if (from == to) continue;
-    uint4 x[kWords];
-    const int x0 = piece * kWords * kCopyThreads + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      if (x0 + i * kCopyThreads < words) x[i] = *word_of(c, cache, from, x0 + i * kCopyThreads);
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      if (x0 + i * kCopyThreads < words) *word_of(c, cache, to, x0 + i * kCopyThreads) = x[i];
-  }
+  copy_moves<kCopyThreads>(c, c.count ? c.count[0] : c.n, blockIdx.x, gridDim.x);
 }
 
 // CTA per pair.
@@ -378,6 +400,10 @@ __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const PagesArg
   if (threadIdx.x == 0) a.held[to] = held;
 }
 
+constexpr size_t kLocalBytes = 200 << 10;  // shared memory of the plan
+// Bytes, at most, that a step may copy for the planning cluster to do it. (A step of 64 sequences that copies none, us a
+// call and replayed: 9 and 6.1 in one launch, 11.3 and 6.6 in two; one that copies 4.7 MB: 10 more and 21 more.)
+constexpr double kInPlan = 2 << 20;
 constexpr int kMaxPages = 1 << 28, kMaxSeqs = 65535;
 
 moe_status make_pages(const moe_kv_pages* p, PagesArgs* a) {
@@ -419,46 +445,72 @@ moe_status check_caches(const moe_kv_cache* const* caches, int n, int n_pages, i
 // A launch that may begin while the kernel before it on the stream ends (each of these waits for it first).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_early(const KvCall& c, const char* name, void (*kernel)(KArgs...), int grid, int block, size_t smem,
-                         Args&&... args) {
+                         int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...)) return e;
   return c.launched(name);
 }
 
-cudaError_t copy_pages(CopyArgs c, const moe_kv_cache* const* caches, int n_caches, const KvCall& call) {
+// The caches [i0, i0 + n) as the copy's.
+void set_caches(CopyArgs* c, const moe_kv_cache* const* caches, int i0, int n) {
   const moe_kv_cache& f = *caches[0];
-  c.n_pages = f.n_pages;
-  c.codes16 = f.kv_heads * f.page_size * f.head_dim / 32;
-  c.sb16 = f.kv_heads * f.page_size * f.head_dim / 512;
+  c->n_pages = f.n_pages;
+  c->codes16 = f.kv_heads * f.page_size * f.head_dim / 32;
+  c->sb16 = f.kv_heads * f.page_size * f.head_dim / 512;
+  c->n_caches = n;
+  for (int i = 0; i < n; ++i) {
+    const moe_kv_cache& k = *caches[i0 + i];
+    c->codes[i][0] = k.k_codes, c->codes[i][1] = k.v_codes;
+    c->scales[i][0] = k.k_scales, c->scales[i][1] = k.v_scales;
+    c->biases[i][0] = k.k_biases, c->biases[i][1] = k.v_biases;
+  }
+}
+
+cudaError_t copy_pages(CopyArgs c, const moe_kv_cache* const* caches, int n_caches, const KvCall& call) {
   for (int i0 = 0; i0 < n_caches; i0 += kMaxCaches) {
-    c.n_caches = std::min(kMaxCaches, n_caches - i0);
-    for (int i = 0; i < c.n_caches; ++i) {
-      const moe_kv_cache& k = *caches[i0 + i];
-      c.codes[i][0] = k.k_codes, c.codes[i][1] = k.v_codes;
-      c.scales[i][0] = k.k_scales, c.scales[i][1] = k.v_scales;
-      c.biases[i][0] = k.k_biases, c.biases[i][1] = k.v_biases;
-    }
-    if (cudaError_t e = launch_early(call, "pages_copy", pages_copy_kernel, 4 * num_sms(), kCopyThreads, 0, c)) return e;
+    set_caches(&c, caches, i0, std::min(kMaxCaches, n_caches - i0));
+    if (cudaError_t e = launch_early(call, "pages_copy", pages_copy_kernel, 4 * num_sms(), kCopyThreads, 0, 1, c)) return e;
     c.table = nullptr;  // (renamed by the first launch)
   }
   return cudaSuccess;
 }
 
-cudaError_t plan_update(const PagesArgs& a, const StepArgs& s, const KvCall& c) {
-  constexpr size_t kLocal = 200 << 10;
+// Bytes that a step copies at most: of every sequence with step tokens, the pages that these go to and that were there.
+double most_copied(const PagesArgs& a, const moe_kv_batch& b, const moe_kv_cache& c, int n_caches) {
+  const double pages = 2.0 * std::min(a.n_seqs, b.n_tokens) + (b.n_tokens >> a.page_bits);
+  return pages * n_caches * c.kv_heads * c.page_size * c.head_dim * 1.125;
+}
+
+template <bool LOCAL>
+cudaError_t launch_update(const PagesArgs& a, const StepArgs& s, size_t bytes, const CopyArgs& y, bool copy, const KvCall& c) {
+  auto kernel = copy ? pages_update_kernel<LOCAL, true> : pages_update_kernel<LOCAL, false>;
+  if (bytes && !ensure_smem_limit(reinterpret_cast<const void*>(kernel), kLocalBytes)) return cudaErrorInvalidValue;
+  return launch_early(c, "pages_update", kernel, copy ? kCluster : 1, kPlanThreads, bytes, copy ? kCluster : 1, a, s, y);
+}
+
+cudaError_t update_pages(const PagesArgs& a, const moe_kv_batch& b, const moe_kv_cache* const* caches, int n_caches,
+                         const KvCall& c) {
+  const StepArgs s{b.q_off, b.kv_len, b.max_new, b.max_kv};
   const size_t bytes = (2 * size_t((a.n_pages + 3) & ~3) + 4 * size_t(a.n_seqs)) * 4;
-  if (bytes > kLocal) return launch_early(c, "pages_update", pages_update_kernel<false>, 1, kPlanThreads, 0, a, s);
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(&pages_update_kernel<true>), kLocal)) return cudaErrorInvalidValue;
-  return launch_early(c, "pages_update", pages_update_kernel<true>, 1, kPlanThreads, bytes, a, s);
+  const bool copy = n_caches <= kMaxCaches && most_copied(a, b, *caches[0], n_caches) <= kInPlan;
+  CopyArgs y{};
+  y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
+  if (copy) set_caches(&y, caches, 0, n_caches);
+  if (cudaError_t e = bytes <= kLocalBytes ? launch_update<true>(a, s, bytes, y, copy, c) : launch_update<false>(a, s, 0, y, copy, c))
+    return e;
+  return copy ? cudaSuccess : copy_pages(y, caches, n_caches, c);
 }
 
 }  // namespace
@@ -481,12 +533,8 @@ moe_status moe_kv_pages_update(const moe_kv_pages* pages, const moe_kv_batch* b,
   if (moe_status s = check_caches(caches, n_caches, a.n_pages, pages->page_size)) return s;
   if (!b || b->n_seqs != a.n_seqs || b->block_table != a.table || b->table_stride != a.columns) return MOE_ERR_ARG;
   if (!b->q_off || !b->kv_len || !aligned(b->q_off, 4) || !aligned(b->kv_len, 4)) return MOE_ERR_ARG;
-  if (b->max_new < 0 || b->max_kv < 0 || b->max_kv > (1 << 24)) return MOE_ERR_ARG;
-  const KvCall c = begin_call(stream);
-  if (cudaError_t e = plan_update(a, StepArgs{b->q_off, b->kv_len, b->max_new, b->max_kv}, c)) return status_of(e);
-  CopyArgs y{};
-  y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
-  return status_of(copy_pages(y, caches, n_caches, c));
+  if (b->n_tokens < 0 || b->max_new < 0 || b->max_kv < 0 || b->max_kv > (1 << 24)) return MOE_ERR_ARG;
+  return status_of(update_pages(a, *b, caches, n_caches, begin_call(stream)));
 }
 
 moe_status moe_kv_pages_fork(const moe_kv_pages* pages, const int32_t* src, const int32_t* dst, int n, void* stream) {
@@ -497,7 +545,7 @@ moe_status moe_kv_pages_fork(const moe_kv_pages* pages, const int32_t* src, cons
   if (n == 0) return MOE_OK;
   if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return MOE_ERR_ARG;
   const KvCall c = begin_call(stream);
-  return status_of(launch_early(c, "pages_fork", pages_fork_kernel, n, kForkThreads, 0, a, src, dst, n));
+  return status_of(launch_early(c, "pages_fork", pages_fork_kernel, n, kForkThreads, 0, 1, a, src, dst, n));
 }
 
 moe_status moe_kv_pages_compact(const moe_kv_pages* pages, const moe_kv_cache* const* caches, int n_caches, void* stream) {
@@ -506,7 +554,7 @@ moe_status moe_kv_pages_compact(const moe_kv_pages* pages, const moe_kv_cache* c
   if (moe_status s = make_pages(pages, &a)) return s;
   if (moe_status s = check_caches(caches, n_caches, a.n_pages, pages->page_size)) return s;
   const KvCall c = begin_call(stream);
-  if (cudaError_t e = launch_early(c, "pages_compact", pages_compact_kernel, 1, kPlanThreads, 0, a)) return status_of(e);
+  if (cudaError_t e = launch_early(c, "pages_compact", pages_compact_kernel, 1, kPlanThreads, 0, 1, a)) return status_of(e);
   CopyArgs y{};
   y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
   y.table = a.table, y.list = a.list, y.entries = (long long)a.n_seqs * a.columns;
