@@ -71,7 +71,7 @@
 namespace moe {
 namespace {
 
-constexpr int kBK = 128;                  // keys per tile
+constexpr int kBK = kKeyTile;             // keys per tile
 constexpr uint32_t kQBlock = 16384;       // 128 query rows of 64 dims
 constexpr int kSoftWarps = 8, kWarpTma = 8, kWarpMma = 9, kWarpLoad = 10, kLoadWarps = 2, kThreads = 384;
 constexpr int kMaxPairs = 256;            // CTA pairs, at most (this GPU has 76)
@@ -112,7 +112,7 @@ struct ManyCfg {
 struct __align__(16) RowTile {
   int seq, row0;        // sequence, first row within it
   int first, n_new, kv;  // of the sequence
-  int pad[3];
+  int sink, tile, n;     // kTogether: its Range
   __device__ __forceinline__ SeqInfo info() const { return SeqInfo{first, n_new, kv}; }
 };
 
@@ -177,6 +177,40 @@ __device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s,
   return range_of(pos_of<PARTS>(m.a, base, m.token(row0)), pos_of<PARTS>(m.a, base, m.token(last)), m.a.window, m.a.sinks);
 }
 
+// kTogether: a row's sequence, and what it sees: positions below `sink`, and
+// lo .. pos.
+struct RowView {
+  int seq, sink, lo, pos;
+};
+__device__ __forceinline__ RowView row_view(const AttnArgs& a, int group, int token) {
+  int lo = a.seq_off[group], hi = a.seq_off[group + 1] - 1;  // the last sequence that begins at or before the token
+  const int tile0 = a.own_tile[lo], shared = (a.shared_len[group] + kBK - 1) / kBK;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.step_off[mid] <= token)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  RowView v;
+  v.seq = lo;
+  v.sink = a.skip[lo];
+  v.lo = (shared + a.own_tile[lo] - tile0) * kBK;
+  v.pos = v.lo + a.own_len[lo] - max(1, a.step_off[lo + 1] - token);
+  return v;
+}
+// Key tiles that a row tile's rows see: the shared ones, then those of the own positions of its sequences.
+__device__ __forceinline__ Range together_range(const ManyArgs& m, int group, const SeqInfo& s, int row0, int rows) {
+  const int last = min(row0 + rows, s.n_new * m.a.group) - 1;
+  const RowView v0 = row_view(m.a, group, s.first + m.token(row0)), v1 = row_view(m.a, group, s.first + m.token(last));
+  Range r;
+  r.n_sink = (m.a.shared_len[group] + kBK - 1) / kBK;
+  r.first = v0.lo / kBK;
+  const int end = v1.pos >= v1.lo ? v1.pos / kBK + 1 : v1.lo / kBK;
+  r.n = max(1, r.n_sink + max(0, end - r.first));
+  return r;
+}
+
 // Byte offset of 16-byte chunk c of row r in a 1024-aligned 128-byte-swizzled K-major block.
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return uint32_t((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
@@ -238,8 +272,10 @@ __device__ void make_plan(const ManyArgs& m, int rows) {
         }
         const SeqInfo q = info[lo];
         const int row0 = (i - (lo ? ends[lo - 1] : 0)) * rows;
-        m.row_tile[n_rt + i] = RowTile{m.b0 + base + lo, row0, q.first, q.n_new, q.kv, {}};
-        n = kTileCost + rows_range<PARTS>(m, q, row0, rows).n;
+        const Range r = is_together<PARTS>(m.a) ? together_range(m, m.b0 + base + lo, q, row0, rows)
+                                                : rows_range<PARTS>(m, q, row0, rows);
+        m.row_tile[n_rt + i] = RowTile{m.b0 + base + lo, row0, q.first, q.n_new, q.kv, r.n_sink, r.first, r.n};
+        n = kTileCost + r.n;
       }
       long long sum;
       const long long end = block_scan(n, &sum, buf);
@@ -321,17 +357,40 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   const KvArgs& kv = m.a.kv;
   const SeqInfo s = kv_seq(kv, b);
   if (!taken(m, s)) return;
-  const Range r = seq_range(m, s);
-  if (t >= r.n) return;
-  const int k0 = r.tile(t) * kBK, minpos = s.kv - s.n_new, maxpos = s.kv - 1;
-  const int lo = m.a.window > 0 ? max(0, minpos - m.a.window + 1) : 0;
+  // the tile's keys: the first `keys` of them, from position k0 on of the sequence in the table's row `at`
+  int k0, keys, at = b;
+  if (is_together<PARTS>(m.a)) {
+    if (t >= s.kv / kBK) return;
+    const int shared = (m.a.shared_len[b] + kBK - 1) / kBK;
+    if (t < shared) {
+      k0 = t * kBK, keys = m.a.shared_len[b] - k0, at = kv.rows[b];
+    } else {
+      int lo = m.a.seq_off[b], hi = m.a.seq_off[b + 1] - 1;  // the last sequence whose own tiles begin at or before it
+      const int x = t - shared + m.a.own_tile[lo];
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (m.a.own_tile[mid] <= x)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      k0 = (x - m.a.own_tile[lo]) * kBK, keys = m.a.own_len[lo] - k0, k0 += m.a.skip[lo], at = lo;
+    }
+  } else {
+    const Range r = seq_range(m, s);
+    if (t >= r.n) return;
+    k0 = r.tile(t) * kBK;
+    keys = s.kv - k0;
+  }
+  const int minpos = s.kv - s.n_new, lo = m.a.window > 0 ? max(0, minpos - m.a.window + 1) : 0;
   if (threadIdx.x < 32) {
     bool missing = false;
     if (threadIdx.x < kBK / 16) {
       const int k = k0 + 16 * threadIdx.x;
       long long row = -1;
-      if (k <= maxpos && (k + 16 > lo || k < m.a.sinks)) {
-        row = kv_page_row<PARTS>(kv, b, k >> kv.page_bits, m.h0 + h);
+      if (16 * int(threadIdx.x) < keys && (k + 16 > lo || k < m.a.sinks)) {
+        row = is_together<PARTS>(m.a) ? kv_page_row(kv, at, k >> kv.page_bits, m.h0 + h)
+                                      : kv_page_row<PARTS>(kv, b, k >> kv.page_bits, m.h0 + h);
         missing = row < 0;
         if (row >= 0) row += k & ((1 << kv.page_bits) - 1);
       }
@@ -375,7 +434,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
     const int w = threadIdx.x % W;
 #pragma unroll 4
     for (int key = threadIdx.x / W; key < kBK; key += kPlanThreads / W) {
-      const bool in = k0 + key <= maxpos;
+      const bool in = key < keys;
       const uint32_t c = in ? code_of(key, w) : 0u;
       const __nv_bfloat16 s16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kScales) : 0);
       const __nv_bfloat16 b16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kBiases) : 0);
@@ -398,8 +457,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         // a slot that no row sees may hold anything: its zero probability needs a finite value
-        const int key = key0 + 2 * i + j, at = k0 + key;
-        const bool in = at <= maxpos && (at >= lo || at < m.a.sinks);
+        const int key = key0 + 2 * i + j, pos = k0 + key;
+        const bool in = key < keys && (pos >= lo || pos < m.a.sinks);
         c[j] = in ? code_of(key, w) : 0u;
         sc[j] = in ? sb_of(key, w, St::kScales) : 0u;
         bs[j] = in ? sb_of(key, w, St::kBiases) : 0u;
@@ -659,7 +718,9 @@ struct Cursor {
       if (j1 > j0) {
         const RowTile t = m.row_tile[rt];
         const SeqInfo si = t.info();
-        const Range all = seq_range(m, si), mine = rows_range<PARTS>(m, si, t.row0, 2 * rows);
+        const bool together = is_together<PARTS>(m.a);
+        const Range all = together ? Range{0, 0, 0} : seq_range(m, si);  // (all of a group's tiles are expanded, in order)
+        const Range mine = together ? Range{t.sink, t.tile, t.n} : rows_range<PARTS>(m, si, t.row0, 2 * rows);
         s->seq = t.seq - m.b0;
         s->head = head;
         s->row0 = t.row0 + rank * rows;
@@ -995,9 +1056,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       if (lane == 0) mbar_arrive(dempty(sg));
       float ref = -INFINITY, sum = 0.f;
       const int r0 = s.row0 + q * 128;
-      const int pos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + row, s.last)));
-      const int minpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0, s.last)));
-      const int maxpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + 127, s.last)));
+      int pos, minpos, maxpos, low = 0, sink = 0;  // (low, sink: kTogether's)
+      if (is_together<PARTS>(a)) {
+        const RowView v = row_view(a, m.b0 + s.seq, s.first + m.token(min(r0 + row, s.last)));
+        pos = v.pos, low = v.lo, sink = v.sink;
+        minpos = maxpos = 0;
+      } else {
+        pos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + row, s.last)));
+        minpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0, s.last)));
+        maxpos = pos_of<PARTS>(a, s.base_pos, m.token(min(r0 + 127, s.last)));
+      }
       const int n = s.j1 - s.j0;
       const uint8_t* bad = m.bad + (long long)s.seq * m.tiles_max;
       const int first = kTurns ? (wg ^ g0) & 1 : 0;  // of this warpgroup's tiles
@@ -1026,8 +1094,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           __syncwarp();
           if (lane == 0) arrive_first(sread(g & 1u));
         }
-        const bool whole = missing == 0 && k0 + kBK - 1 <= minpos &&
-                           (a.window == 0 || k0 > maxpos - a.window || k0 + kBK <= a.sinks);
+        const bool whole = is_together<PARTS>(a)
+                               ? missing == 0 && __all_sync(~0u, k0 + kBK <= sink)
+                               : missing == 0 && k0 + kBK - 1 <= minpos &&
+                                     (a.window == 0 || k0 > maxpos - a.window || k0 + kBK <= a.sinks);
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < kCols; c += 64) {
@@ -1035,7 +1105,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             const int h = kHalves ? half : c / 64, kb = k0 + h * 64;
             auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };  // bits under x
             uint64_t sees = below(pos + 1 - kb);
-            if (a.window > 0) sees &= ~below(pos - a.window + 1 - kb) | below(a.sinks - kb);
+            if (is_together<PARTS>(a))
+              sees = (sees & ~below(low - kb)) | below(sink - kb);
+            else if (a.window > 0)
+              sees &= ~below(pos - a.window + 1 - kb) | below(a.sinks - kb);
 #pragma unroll
             for (int i16 = 0; i16 < 4; ++i16)
               if ((missing >> (h * 4 + i16)) & 1u) sees &= ~(0xFFFFull << (16 * i16));

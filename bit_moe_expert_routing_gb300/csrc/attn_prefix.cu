@@ -18,6 +18,13 @@
 // rows' fp32 outputs, written and read once. The own part comes first because
 // it is short: the shared part's kernels start beside it, and wait for it only
 // where they join.
+//
+// Sequences of many rows each (prompts behind a shared one) are taken in one
+// go instead: in the many-row kernels a group is one sequence, whose positions
+// are the shared ones and then each sequence's own, and a row sees two ranges of
+// them, as it does with a window and sinks. A tile of rows then meets the own
+// positions of its few sequences besides the shared ones, and nothing has to be
+// joined.
 #include "kv_host.cuh"
 
 namespace moe {
@@ -34,7 +41,10 @@ struct PrefixArgs {
   int32_t* group_row;  // [n_groups] row of the table
   int32_t* own_len;    // [n_seqs] positions past the shared ones
   int32_t* skip;       // [n_seqs] shared positions
-  uint8_t* shares;     // [n_tokens] whether the token's sequence shares any
+  uint8_t* shares;     // [n_tokens] whether the token's sequence shares any; together: whether it is written
+  int32_t* own_tile;   // together: [n_seqs + 1] key tiles of the own positions of the sequences before
+  int32_t* shared_len; // together: [n_groups] shared positions; group_len is that of all positions, in whole tiles
+  int32_t* seqs;       // together: [n_groups + 1] seq_off, or one group of all sequences if that is not in order
   int max_own;
 };
 
@@ -42,16 +52,44 @@ constexpr int kPlanThreads = 256;
 constexpr int kFew = 8;
 constexpr int kBadGroups = 204;  // detail in the status word
 
+// Marks the tokens of the warp's sequences (one per lane: n tokens from q0 on): a few at once, more of them by the warp,
+// one sequence after the other.
+__device__ __forceinline__ void mark(uint8_t* shares, int q0, int n, bool flag) {
+  const int lane = threadIdx.x & 31;
+  if (n <= kFew)
+    for (int i = 0; i < n; ++i) shares[q0 + i] = flag;
+  for (unsigned many = __ballot_sync(~0u, n > kFew); many; many &= many - 1) {
+    const int l = __ffs(many) - 1, first = __shfl_sync(~0u, q0, l), count = __shfl_sync(~0u, n, l);
+    const uint8_t of = __shfl_sync(~0u, int(flag), l);
+    for (int i = lane; i < count; i += 32) shares[first + i] = of;
+  }
+}
+
+// The group of sequence b (all groups in order): the last that begins at or before it.
+__device__ __forceinline__ int group_of(const PrefixArgs& p, int b) {
+  int lo = 0, hi = p.n_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.seq_off[mid] <= b)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 // One CTA: groups first, then sequences. Nothing is shared unless all groups
 // and offsets are in order, so that the kernels may go by the sums of their
 // sizes, and every token is some sequence's.
+template <bool TOGETHER>
 __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(const PrefixArgs p) {
   const KvArgs& a = p.kv;
-  const int b0 = threadIdx.x, lane = threadIdx.x & 31;
+  const int b0 = threadIdx.x;
+  auto whole_pages = [&](int len) { return len >> a.page_bits << a.page_bits; };
   // (a thread's first sequence, asked for beside the groups)
   int q0 = 0, q1 = 0, kv = 0;
   if (b0 < a.n_seqs) q0 = a.q_off[b0], q1 = a.q_off[b0 + 1], kv = a.kv_len[b0];
-  bool bad = p.seq_off[0] != 0 || p.seq_off[p.n_groups] != a.n_seqs || a.q_off[0] != 0 || a.q_off[a.n_seqs] != a.n_tokens;
+  bool bad = p.seq_off[0] != 0 || p.seq_off[p.n_groups] != a.n_seqs;
   for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
     const int s0 = p.seq_off[g], s1 = p.seq_off[g + 1], len = p.length[g];
     bool ok = s0 >= 0 && s0 <= s1 && s1 <= a.n_seqs && len >= 0 && len <= p.max_len;
@@ -60,59 +98,98 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
     bad |= !ok;
     p.group_off[g] = t0;
     if (g == p.n_groups - 1) p.group_off[g + 1] = t1;
-    p.group_len[g] = len >> a.page_bits << a.page_bits;
+    (TOGETHER ? p.shared_len : p.group_len)[g] = whole_pages(len);
     p.group_row[g] = ok ? min(s0, a.n_seqs - 1) : 0;
+    if (TOGETHER) {
+      p.seqs[g] = s0;
+      if (g == p.n_groups - 1) p.seqs[g + 1] = s1;
+    }
   }
-  bad |= q1 < q0;
-  for (int b = b0 + kPlanThreads; b < a.n_seqs; b += kPlanThreads) bad |= a.q_off[b + 1] < a.q_off[b];
-  bad = __syncthreads_or(bad);
+  bool off = a.q_off[0] != 0 || a.q_off[a.n_seqs] != a.n_tokens || q1 < q0;
+  for (int b = b0 + kPlanThreads; b < a.n_seqs; b += kPlanThreads) off |= a.q_off[b + 1] < a.q_off[b];
+  off = __syncthreads_or(off);
+  bad = __syncthreads_or(bad || off);
   if (bad) {
     if (threadIdx.x == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kBadGroups);
-    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) p.group_len[g] = -1;  // the kernels leave it out
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+      if (!TOGETHER) {
+        p.group_len[g] = -1;  // the kernels leave it out
+      } else {  // one group of all sequences, and empty ones (offsets out of order: nothing is done)
+        p.shared_len[g] = p.group_row[g] = 0;
+        p.group_off[g + 1] = off ? 0 : a.n_tokens;
+        p.seqs[g + 1] = a.n_seqs;
+        if (g == 0) p.group_off[0] = p.seqs[0] = 0;
+      }
+    }
   }
+  __shared__ int sums[kPlanThreads / 32];
+  int tiles_before = 0;
   for (int c0 = 0; c0 < a.n_seqs; c0 += kPlanThreads) {
     const int b = c0 + b0;
-    bool shares = false;
-    int n = 0;
+    bool flag = false;
+    int n = 0, tiles = 0;
     if (b < a.n_seqs) {
       if (c0 > 0) q0 = a.q_off[b], q1 = a.q_off[b + 1], kv = a.kv_len[b];
       n = q1 - q0;
       int skip = 0;
       if (!bad && kv <= a.max_kv) {
-        int lo = 0, hi = p.n_groups - 1;  // the last group that begins at or before b
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (p.seq_off[mid] <= b)
-            lo = mid;
-          else
-            hi = mid - 1;
-        }
-        const int len = p.length[lo] >> a.page_bits << a.page_bits;
+        const int len = whole_pages(p.length[group_of(p, b)]);
         if (kv - n >= len) skip = len;
       }
-      const int own = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
+      int own = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
+      // (as the kernels look at a sequence: one that they leave out has no own part to be joined)
+      const bool in = own >= 0 && own <= p.max_own && n >= 0 && n <= a.max_new;
+      if (TOGETHER) {
+        if (!in) report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadBatch);
+        if (!in) own = -1;
+        flag = in;
+        tiles = in && !off && n > 0 ? (own + kKeyTile - 1) / kKeyTile : 0;
+      } else {
+        flag = in && skip > 0;
+      }
       p.skip[b] = skip;
       p.own_len[b] = own;
-      // (as the kernels look at a sequence: one that they leave out has no own part to be joined)
-      shares = skip > 0 && own >= 0 && own <= p.max_own && n <= a.max_new;
     }
-    if (bad) continue;  // (no token is looked at)
-    // its tokens' marks: a few at once, more of them by the warp, one sequence after the other
-    const bool flag = shares;
-    if (n <= kFew)
-      for (int i = 0; i < n; ++i) p.shares[q0 + i] = flag;
-    for (unsigned long_ones = __ballot_sync(~0u, n > kFew); long_ones; long_ones &= long_ones - 1) {
-      const int l = __ffs(long_ones) - 1, first = __shfl_sync(~0u, q0, l), count = __shfl_sync(~0u, n, l);
-      const uint8_t mark = __shfl_sync(~0u, int(flag), l);
-      for (int i = lane; i < count; i += 32) p.shares[first + i] = mark;
+    if (TOGETHER) {
+      int s = tiles;
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(~0u, s, d);
+        if (lane >= d) s += u;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = s;
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kPlanThreads / 32; ++w) before += w < warp ? sums[w] : 0, all += sums[w];
+      if (b < a.n_seqs) p.own_tile[b + 1] = tiles_before + before + s;
+      if (b == 0) p.own_tile[0] = 0;
+      tiles_before += all;
+    }
+    if (TOGETHER ? !off : !bad) mark(p.shares, q0, n, flag);  // (else no token is looked at)
+  }
+  if (TOGETHER) {
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+      const int s0 = __ldcg(p.seqs + g), s1 = __ldcg(p.seqs + g + 1);
+      const int shared = (__ldcg(p.shared_len + g) + kKeyTile - 1) / kKeyTile;
+      p.group_len[g] = off ? -1 : (shared + __ldcg(p.own_tile + s1) - __ldcg(p.own_tile + s0)) * kKeyTile;
     }
   }
 }
 
+// From so many rows per sequence (step tokens x query heads per kv head) on,
+// on average, shared and own positions are attended to in one go.
+constexpr long long kTogetherRows = 128;
+
 struct PrefixPlan {
-  AttnArgs own, shared;
+  AttnArgs own, shared, together;
   int few_own, few_shared;
+  bool is_together;
   size_t group_off, group_len, group_row, own_len, skip, shares, lse, o, attend_own, attend_shared, total;
+  size_t own_tile, shared_len, seqs, attend_together;
 };
 
 moe_status check_prefix(const KvArgs& kv, const moe_kv_prefix* x) {
@@ -132,7 +209,7 @@ bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x) 
 }
 
 PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
-  PrefixPlan p{a, a};
+  PrefixPlan p{a, a, a};
   p.own.kv.max_kv = std::min(x.max_own, a.kv.max_kv);
   p.own.part = AttnArgs::kOwn;
   p.shared.kv.n_seqs = x.n_groups;
@@ -158,6 +235,23 @@ PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
   p.attend_own = put(workspace_bytes_for(p.own, p.few_own));
   p.attend_shared = put(workspace_bytes_for(p.shared, p.few_shared));  // (a place of its own: they run side by side)
   p.total = o;
+  // The same for the whole of it in one go, if it has a place in that: what is there for the parts is not needed then.
+  const long long tile = kKeyTile, rows = (long long)a.kv.n_tokens * a.group;
+  const long long tiles = (x.max_len + tile - 1) / tile + a.kv.n_seqs * ((p.own.kv.max_kv + tile - 1) / tile);
+  p.together.part = AttnArgs::kTogether;
+  p.together.kv.n_seqs = x.n_groups;
+  p.together.kv.max_new = a.kv.n_tokens;
+  p.together.kv.max_kv = int(std::min(tiles * tile, 1ll << 24));
+  p.is_together = x.n_groups > 0 && a.kv.n_tokens > 0 && rows >= kTogetherRows * a.kv.n_seqs && opt.force_path != 1 &&
+                  tiles * tile <= (1 << 24);
+  if (p.is_together) {
+    o = p.lse;
+    p.own_tile = put((size_t(a.kv.n_seqs) + 1) * 4);
+    p.shared_len = put(size_t(x.n_groups) * 4);
+    p.seqs = put((size_t(x.n_groups) + 1) * 4);
+    p.attend_together = put(workspace_bytes_for(p.together, 0));
+    p.is_together = o <= p.total;
+  }
   return p;
 }
 
@@ -219,9 +313,27 @@ moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_
                         ints(p.own_len),
                         ints(p.skip),
                         reinterpret_cast<uint8_t*>(w + p.shares),
+                        ints(p.own_tile),
+                        ints(p.shared_len),
+                        ints(p.seqs),
                         p.own.kv.max_kv};
-  attention_prefix_plan_kernel<<<1, kPlanThreads, 0, c.stream>>>(args);
+  (p.is_together ? attention_prefix_plan_kernel<true> : attention_prefix_plan_kernel<false>)<<<1, kPlanThreads, 0, c.stream>>>(
+      args);
   if (cudaError_t e = c.launched("attention_prefix_plan")) return status_of(e);
+  if (p.is_together) {
+    AttnArgs& t = p.together;
+    t.kv.q_off = args.group_off;
+    t.kv.kv_len = args.group_len;
+    t.kv.rows = args.group_row;
+    t.shares = args.shares;
+    t.seq_off = args.seqs;
+    t.step_off = a.q_off;
+    t.skip = args.skip;
+    t.own_len = args.own_len;
+    t.own_tile = args.own_tile;
+    t.shared_len = args.shared_len;
+    return status_of(attention_many(t, 0, w + p.attend_together, c));
+  }
   for (AttnArgs* part : {&p.own, &p.shared}) {
     part->own_o = reinterpret_cast<float*>(w + p.o);
     part->own_lse = reinterpret_cast<float*>(w + p.lse);

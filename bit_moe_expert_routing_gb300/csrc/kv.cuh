@@ -98,6 +98,8 @@ struct KvCall {
   }
 };
 
+constexpr int kKeyTile = 128;  // keys of a tile of the many-row kernels
+
 struct AttnArgs {
   KvArgs kv;
   const uint16_t* q;
@@ -112,11 +114,24 @@ struct AttnArgs {
   // the lse in base 2). kShared, behind it: every row sees all positions, and
   // the rows of tokens that `shares` marks are joined with what kOwn left and
   // written; no others are.
-  enum Part { kWhole, kOwn, kShared };
+  //
+  // kTogether: groups as sequences in one go, over the positions of all of a
+  // group's sequences laid out one behind the other: the shared ones, then each
+  // sequence's own, every part beginning on a key tile of the many-row kernels
+  // (the only ones that take it). A row sees the first skip[its sequence], and
+  // its sequence's own up to itself.
+  enum Part { kWhole, kOwn, kShared, kTogether };
   int part;
   float* own_o;           // [n_tokens, heads, dim]
   float* own_lse;         // [n_tokens, heads]
-  const uint8_t* shares;  // [n_tokens]
+  const uint8_t* shares;  // [n_tokens]; kTogether: whether the token is to be written
+  // kTogether, besides kv.rows:
+  const int32_t* seq_off;     // [groups + 1] sequences of each group
+  const int32_t* step_off;    // [sequences + 1] step tokens of each sequence
+  const int32_t* skip;        // [sequences] shared positions
+  const int32_t* own_len;     // [sequences] positions past them
+  const int32_t* own_tile;    // [sequences + 1] key tiles of the own positions of the sequences before
+  const int32_t* shared_len;  // [groups] shared positions
 };
 
 // (The kernels are compiled for whole calls and for PARTS apart: what the latter need cost the former registers.)
@@ -141,7 +156,11 @@ __device__ __forceinline__ bool to_own(const AttnArgs& a, int seq) {
 // Whether a step token's rows are written.
 template <bool PARTS>
 __device__ __forceinline__ bool is_written(const AttnArgs& a, int token) {
-  return !is_shared<PARTS>(a) || a.shares[token];
+  return !PARTS || a.part < AttnArgs::kShared || a.shares[token];
+}
+template <bool PARTS>
+__device__ __forceinline__ bool is_together(const AttnArgs& a) {
+  return PARTS && a.part == AttnArgs::kTogether;
 }
 // Weights of a row's two parts, both normalised, in the whole, from their log-sum-exps (base 2; -inf: it saw nothing).
 struct Join {

@@ -138,6 +138,8 @@ GROUPS = [
     [(257, [(40, 40), (1, 2), (130, 160), (17, 17)])],
     [(1200, [(0, 3), (1, 10), (0, 0), (1, 1)]), (50, [(0, 0), (0, 1)])],
     [(2500, [(1, 1 + 13 * i) for i in range(20)])],
+    [(130, [(70, 70), (33, 64), (0, 5), (90, 300)]), (16, [(129, 200), (128, 128), (1, 1)]), (0, [(40, 41)])],
+    [(1000, [(256, 256)] * 3 + [(1, 129)] + [(300, 512)])],
 ]
 
 
@@ -211,13 +213,14 @@ def test_a_window_reads_near_positions_only(each_path):
 
 
 @pytest.mark.gpu
-def test_sequences_that_begin_inside_the_shared_part_are_on_their_own(each_path):
+@pytest.mark.parametrize("heads,new", [(8, [1, 3, 1]), (16, [40, 30, 60])])
+def test_sequences_that_begin_inside_the_shared_part_are_on_their_own(heads, new, each_path):
     """Lengths larger than what a sequence has behind its step tokens: it is attended to whole; the others share."""
-    batch = Shared([(160, [(1, 9), (3, 3), (1, 40)])], 16)
+    batch = Shared([(160, [(n, n + 8) for n in new])], 16)
     batch.kv[1] = 90  # within the shared pages
     cache = junk_cache(moe, batch.n_pages, 16, 2, 64)
     held = share(cache, batch, fill(cache, batch))
-    q = rows(batch.n_tokens, 8, 64)
+    q = rows(batch.n_tokens, heads, 64)
     ref = attention_reference(q, batch, *held, 0.125)
     for path in each_path():
         out, lse = cache.attention(q, batch.device(moe), lse=True, prefix=batch.prefix(max_own=100))
@@ -226,36 +229,39 @@ def test_sequences_that_begin_inside_the_shared_part_are_on_their_own(each_path)
 
 
 @pytest.mark.gpu
-def test_groups_out_of_order_or_past_their_bounds_share_nothing(each_path):
-    batch = Shared([(160, [(1, 9), (3, 3)]), (64, [(1, 40)])], 16)
+@pytest.mark.parametrize("heads,new", [(8, [1, 3, 1]), (16, [40, 30, 60])])
+def test_groups_out_of_order_or_past_their_bounds_share_nothing(heads, new, each_path):
+    batch = Shared([(160, [(new[0], new[0] + 8), (new[1], new[1])]), (64, [(new[2], 99)])], 16)
     cache = junk_cache(moe, batch.n_pages, 16, 2, 64)
     held = share(cache, batch, fill(cache, batch))
-    q = rows(batch.n_tokens, 8, 64)
+    q = rows(batch.n_tokens, heads, 64)
     ref = attention_reference(q, batch, *held, 0.125)
     dev = batch.device(moe)
     i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
-    good = dict(max_tokens=4, max_len=160, max_own=200)
+    good = dict(max_tokens=max(new[0] + new[1], new[2]), max_len=160, max_own=260)
     for path in each_path():
         for seq_off, length, over in ((i(0, 2, 4), i(160, 64), {}), (i(1, 2, 3), i(160, 64), {}), (i(0, 4, 3), i(160, 64), {}),
                                       (i(0, -1, 3), i(160, 64), {}), (i(0, 2, 2), i(160, 64), {}), (i(0, 2, 3), i(161, 64), {}),
-                                      (i(0, 2, 3), i(-1, 64), {}), (i(0, 2, 3), i(160, 64), dict(max_tokens=3))):
+                                      (i(0, 2, 3), i(-1, 64), {}), (i(0, 2, 3), i(160, 64), dict(max_tokens=new[0]))):
             out, lse = cache.attention(q, dev, lse=True, prefix=moe.KVPrefix(seq_off, length, **dict(good, **over)))
             with pytest.raises(moe.MoEError):
                 cache.check()
             check_attention(out, lse, ref, (path, seq_off.tolist(), length.tolist()))
         # one past max_own: recorded, and its rows stay as they are
         out = torch.full_like(q, 7.0)
-        cache.attention(q, dev, out=out, prefix=batch.prefix(max_own=20))
+        cache.attention(q, dev, out=out, prefix=batch.prefix(max_own=50))
         with pytest.raises(moe.MoEError):
             cache.check()
-        assert (out[4] == 7.0).all()
-        check_attention(out[:4], None, tuple(r[:4] for r in ref), path)
+        n = new[0] + new[1]
+        assert (out[n:] == 7.0).all()
+        check_attention(out[:n], None, tuple(r[:n] for r in ref), path)
 
 
 @pytest.mark.gpu
-def test_missing_pages_are_left_out(each_path):
+@pytest.mark.parametrize("new", [(1, 3), (50, 20)])
+def test_missing_pages_are_left_out(new, each_path):
     """A page of the shared part that is missing: its positions are seen by none of the group, and that is recorded."""
-    batch = Shared([(160, [(1, 9), (3, 30)])], 16)
+    batch = Shared([(160, [(new[0], new[0] + 8), (new[1], 30)])], 16)
     cache = junk_cache(moe, batch.n_pages, 16, 2, 64)
     held = share(cache, batch, fill(cache, batch))
     dev = batch.device(moe)
