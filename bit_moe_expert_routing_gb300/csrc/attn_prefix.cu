@@ -181,8 +181,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
 }
 
 // From so many rows per sequence (step tokens x query heads per kv head) on,
-// on average, shared and own positions are attended to in one go.
-constexpr long long kTogetherRows = 128;
+// on average, shared and own positions are attended to in one go. (288 sizes,
+// one group of 4 or 24 sequences behind 1500 or 16000 positions, time in one go
+// against in parts: 64 rows, 64 dims 0.83 to 1.08, wider heads 0.60 to 1.01; 128
+// rows 0.87 to 1.08 and 0.62 to 1.0; 256 rows 0.69 to 0.88 and 0.73 to 0.96; 32
+// rows 1.0 to 1.07 and 0.93 to 1.0.)
+long long together_rows(int dim) { return dim == 64 ? 192 : 64; }
 
 struct PrefixPlan {
   AttnArgs own, shared, together;
@@ -202,10 +206,36 @@ moe_status check_prefix(const KvArgs& kv, const moe_kv_prefix* x) {
   return MOE_OK;
 }
 
-// Whether the step is taken in two parts. (One with a window reads what is near each sequence's end.)
-bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x) {
-  return at.window == 0 && x.n_groups > 0 && x.n_groups < a.kv.n_seqs && x.max_tokens > 0 &&
-         x.max_len >= (1 << a.kv.page_bits);
+// What attending to a position costs a (sequence, kv head) with so many rows,
+// in passes of the few-row kernel with eight of them: its wider passes cost
+// more each; many rows cost the expansion, then products by tiles of rows.
+double passes(long long rows, int dim) {
+  if (rows > (dim == 256 ? 64 : 128)) return 4.7 + 2.65 * double((rows + 255) / 256);
+  if (rows <= 8) return 1.;
+  if (rows <= 16 || dim == 256) return 1.3 * double((rows + 15) / 16);
+  return 2.1 * double((rows + 31) / 32);
+}
+
+// Whether the step is taken with its shared part apart. One with a window reads
+// what is near each sequence's end. Else, if that spares enough passes over the
+// shared positions: it costs a small kernel, a second set of launches (or tiles
+// of several sequences' own positions) and a join, 8 to 15 us in all, and a pass
+// of eight rows reads some 4 million elements of keys (and as many of values)
+// per us. (Measured over 144 sizes, 2 to 16 sequences of 1 to 64 tokens behind
+// 64 to 3968 positions, us with sharing and without: 16 sequences of 1 token, 8
+// heads over 8 of 64 dims, 3968 positions, 28 million elements spared, 16 and 18,
+// of 128 dims 19 and 23, of 256 dims 25 and 35; 16 of 8 tokens, 128 dims, 31
+// million, 36 and 24, 256 dims, 70 million, 38 and 36; 16 of 64 tokens, 128 dims,
+// 200 million, 47 and 78; 16 of 64 tokens behind 960, 50 million, 42 and 24.)
+constexpr double kSpared = 5.6e7;
+bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x, const Options& opt) {
+  if (at.window != 0 || x.n_groups < 1 || x.n_groups >= a.kv.n_seqs || x.max_tokens < 1 || x.max_len < (1 << a.kv.page_bits))
+    return false;
+  if (opt.force_path) return true;
+  const long long rows = (long long)a.kv.n_tokens * a.group;
+  const double spared = a.kv.n_seqs * passes((rows + a.kv.n_seqs - 1) / a.kv.n_seqs, a.kv.dim) -
+                        x.n_groups * passes((rows + x.n_groups - 1) / x.n_groups, a.kv.dim);
+  return spared * x.max_len * a.kv.kv_heads * a.kv.dim >= kSpared;
 }
 
 PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
@@ -242,7 +272,7 @@ PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
   p.together.kv.n_seqs = x.n_groups;
   p.together.kv.max_new = a.kv.n_tokens;
   p.together.kv.max_kv = int(std::min(tiles * tile, 1ll << 24));
-  p.is_together = x.n_groups > 0 && a.kv.n_tokens > 0 && rows >= kTogetherRows * a.kv.n_seqs && opt.force_path != 1 &&
+  p.is_together = x.n_groups > 0 && a.kv.n_tokens > 0 && rows >= together_rows(a.kv.dim) * a.kv.n_seqs && opt.force_path != 1 &&
                   tiles * tile <= (1 << 24);
   if (p.is_together) {
     o = p.lse;
@@ -297,7 +327,7 @@ moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_
   g.lse = lse;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < bytes_for(g, *at, *x, opt)) return MOE_ERR_WORKSPACE;
   const KvCall c = begin_call(stream, opt);
-  if (!shares(g, *at, *x)) return status_of(attend(g, few_rows(g, opt), workspace, c));
+  if (!shares(g, *at, *x, opt)) return status_of(attend(g, few_rows(g, opt), workspace, c));
   PrefixPlan p = plan(g, *x, opt);
   char* w = static_cast<char*>(workspace);
   auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };

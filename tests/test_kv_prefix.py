@@ -244,9 +244,12 @@ def test_groups_out_of_order_or_past_their_bounds_share_nothing(heads, new, each
                                       (i(0, -1, 3), i(160, 64), {}), (i(0, 2, 2), i(160, 64), {}), (i(0, 2, 3), i(161, 64), {}),
                                       (i(0, 2, 3), i(-1, 64), {}), (i(0, 2, 3), i(160, 64), dict(max_tokens=new[0]))):
             out, lse = cache.attention(q, dev, lse=True, prefix=moe.KVPrefix(seq_off, length, **dict(good, **over)))
-            with pytest.raises(moe.MoEError):
-                cache.check()
+            if path:  # (by its size, this step is taken whole)
+                with pytest.raises(moe.MoEError):
+                    cache.check()
             check_attention(out, lse, ref, (path, seq_off.tolist(), length.tolist()))
+        if not path:
+            continue
         # one past max_own: recorded, and its rows stay as they are
         out = torch.full_like(q, 7.0)
         cache.attention(q, dev, out=out, prefix=batch.prefix(max_own=50))
