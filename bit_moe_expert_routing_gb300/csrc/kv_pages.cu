@@ -35,7 +35,7 @@ struct PagesArgs {
   int32_t* dst;    // [n_pages]
   int32_t* list;   // [n_pages] free pages; new places (compaction)
   int32_t* snap;   // [n_pages] copy of the references
-  int32_t* seqs;   // [4 n_seqs] need, first, held, want
+  int32_t* seqs;   // [5 n_seqs] want (64 bits), need, first, held
 };
 
 // The step's part of an update.
@@ -48,28 +48,27 @@ struct StepArgs {
 __device__ __forceinline__ bool is_page(const PagesArgs& a, int p) { return unsigned(p) < unsigned(a.n_pages); }
 
 // Sum over the CTA of the values before this thread's; *total gets the sum of
-// all. (buf: kPlanWarps ints; the CTA is together before and after.)
-__device__ __forceinline__ int scan_before(int v, int* total, int* buf) {
+// all. (buf: kPlanWarps values; the CTA is together before and after.)
+template <typename T>
+__device__ __forceinline__ T scan_before(T v, T* total, T* buf) {
+  static_assert(kPlanWarps == 32, "a lane per warp");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int s = v;
+  auto inclusive = [&](T s) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(~0u, s, off);
-    if (lane >= off) s += u;
-  }
+    for (int off = 1; off < 32; off <<= 1) {
+      const T u = __shfl_up_sync(~0u, s, off);
+      if (lane >= off) s += u;
+    }
+    return s;
+  };
+  const T s = inclusive(v);
   __syncthreads();
   if (lane == 31) buf[warp] = s;
   __syncthreads();
-  static_assert(kPlanWarps == 32, "a lane per warp");
-  int w = buf[lane];  // sums of the warps up to each
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int u = __shfl_up_sync(~0u, w, off);
-    if (lane >= off) w += u;
-  }
+  const T w = inclusive(buf[lane]);  // sums of the warps up to each
   *total = __shfl_sync(~0u, w, 31);
-  const int before = __shfl_sync(~0u, w, max(warp, 1) - 1);
-  return (warp ? before : 0) + s - v;
+  const T before = __shfl_sync(~0u, w, max(warp, 1) - 1);
+  return (warp ? before : T(0)) + s - v;
 }
 
 // References of pages p .. p + 3 (p a multiple of 4); past the last page: in use.
@@ -153,14 +152,17 @@ template <bool LOCAL>
 __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s) {
   extern __shared__ int4 local[];
   __shared__ int buf[kPlanWarps];
+  __shared__ long long wide[kPlanWarps];
   __shared__ int n_moves;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = (a.n_pages + 3) & ~3;
   int32_t* snap = LOCAL ? reinterpret_cast<int32_t*>(local) : a.snap;
   int32_t* list = LOCAL ? snap + padded : a.list;
-  int32_t* need_s = LOCAL ? list + padded : a.seqs;
-  int32_t *first_s = need_s + a.n_seqs, *held_s = first_s + a.n_seqs, *want_s = held_s + a.n_seqs;
-  auto get = [](const int32_t* p) { return LOCAL ? *p : __ldcg(p); };
+  // (what all sequences want may pass 32 bits, long before it could be given)
+  long long* want_s = reinterpret_cast<long long*>(LOCAL ? list + padded : a.seqs);
+  int32_t* need_s = reinterpret_cast<int32_t*>(want_s + a.n_seqs);
+  int32_t *first_s = need_s + a.n_seqs, *held_s = first_s + a.n_seqs;
+  auto get = [](const auto* p) { return LOCAL ? *p : __ldcg(p); };
   if (threadIdx.x == 0) n_moves = 0;
 
   for (int p = 4 * threadIdx.x; p < a.n_pages; p += kChunk) {
@@ -232,11 +234,11 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
   }
   __syncthreads();
   // where each sequence's pages begin among those given
-  int total = 0;
+  long long total = 0;
   for (int b0 = 0; b0 < a.n_seqs; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int sum;
-    const int before = scan_before(b < a.n_seqs ? get(want_s + b) : 0, &sum, buf);
+    long long sum;
+    const long long before = scan_before(b < a.n_seqs ? get(want_s + b) : 0ll, &sum, wide);
     if (b < a.n_seqs) want_s[b] = total + before;
     total += sum;
     __syncthreads();
@@ -258,13 +260,13 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
   }
   // the giving
   for (int b = warp; b < a.n_seqs && total > 0; b += kPlanWarps) {
-    const int at0 = get(want_s + b), at1 = b + 1 < a.n_seqs ? get(want_s + b + 1) : total;
+    const long long at0 = get(want_s + b), at1 = b + 1 < a.n_seqs ? get(want_s + b + 1) : total;
     if (at0 == at1) continue;  // (a sequence that is not to be touched wants nothing)
     const int need = get(need_s + b), first = get(first_s + b), held = min(get(held_s + b), need);
     int32_t* row = a.table + (long long)b * a.columns;
     const bool fits = at1 <= n_free;
     if (!fits && lane == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
-    int at = at0;
+    int at = int(at0);  // (used where all of them fit)
     for (int j0 = first; j0 < held; j0 += 32) {
       const int j = j0 + lane, p = j < held ? row[j] : -1;
       const bool shared = is_page(a, p) && get(snap + p) > 1;
@@ -503,7 +505,7 @@ cudaError_t launch_update(const PagesArgs& a, const StepArgs& s, size_t bytes, c
 cudaError_t update_pages(const PagesArgs& a, const moe_kv_batch& b, const moe_kv_cache* const* caches, int n_caches,
                          const KvCall& c) {
   const StepArgs s{b.q_off, b.kv_len, b.max_new, b.max_kv};
-  const size_t bytes = (2 * size_t((a.n_pages + 3) & ~3) + 4 * size_t(a.n_seqs)) * 4;
+  const size_t bytes = (2 * size_t((a.n_pages + 3) & ~3) + 5 * size_t(a.n_seqs)) * 4;
   const bool copy = n_caches <= kMaxCaches && most_copied(a, b, *caches[0], n_caches) <= kInPlan;
   CopyArgs y{};
   y.src = a.src, y.dst = a.dst, y.count = a.count, y.hdr = a.hdr;
@@ -522,7 +524,7 @@ extern "C" {
 
 size_t moe_kv_pages_scratch(int n_pages, int n_seqs) {
   if (n_pages < 1 || n_pages > kMaxPages || n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
-  return 4 + size_t(4) * ((n_pages + 3) & ~3) + size_t(4) * n_seqs;
+  return 4 + size_t(4) * ((n_pages + 3) & ~3) + size_t(5) * n_seqs;
 }
 
 moe_status moe_kv_pages_update(const moe_kv_pages* pages, const moe_kv_batch* b, const moe_kv_cache* const* caches,

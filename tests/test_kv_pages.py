@@ -214,7 +214,8 @@ def step(pages, kv, new, max_new=None, max_kv=None):
 @pytest.mark.gpu
 @pytest.mark.parametrize("n_pages,size,n_seqs,columns,kv_heads,dim,layers", [
     (40, 16, 5, 9, 1, 64, 1), (97, 32, 40, 12, 3, 128, 2), (1, 16, 2, 1, 2, 256, 1), (5003, 16, 130, 50, 1, 64, 1),
-    (300, 256, 33, 40, 2, 128, 1), (200, 64, 7, 33, 8, 128, 3)])
+    (300, 256, 33, 40, 2, 128, 1), (200, 64, 7, 33, 8, 128, 3),
+    (30001, 16, 9, 4000, 1, 64, 1)])
 def test_a_long_random_run(n_pages, size, n_seqs, columns, kv_heads, dim, layers):
     """Steps that grow, shrink, end and fork sequences, with too few pages and bad numbers now and then."""
     r = np.random.RandomState(n_pages + n_seqs)
@@ -298,6 +299,24 @@ def test_no_page_of_another_sequence_is_written_when_pages_run_out():
     pages.update(step(pages, kv, new)), m.update(kv, new, 1, 64)
     assert m.bad
     check_same(pages, m)
+
+
+@pytest.mark.gpu
+def test_wishes_past_32_bits():
+    """2100 sequences that want 2^20 pages each, of eight: none gets any, and the last one, which wants one, neither."""
+    pages = moe.KVPages(caches(1, 8, 16, 1, 64), 2100, 2 ** 20)
+    q_off = torch.zeros(2101, dtype=torch.int32, device="cuda")
+    kv = torch.full((2100,), 2 ** 24, dtype=torch.int32, device="cuda")
+    kv[-1] = 5
+    pages.update(pages.batch(q_off, kv, 0, 0, 2 ** 24))
+    with pytest.raises(moe.MoEError):
+        pages.check()
+    assert pages.held.sum() == 0 and pages.refs.sum() == 0 and (pages.table == -1).all()
+    kv[:-1] = 3
+    kv[7:-1] = 0
+    pages.update(pages.batch(q_off, kv, 0, 0, 2 ** 24))
+    pages.check()
+    assert pages.table[:7, 0].tolist() == list(range(7)) and pages.table[-1, 0] == 7
 
 
 @pytest.mark.gpu
