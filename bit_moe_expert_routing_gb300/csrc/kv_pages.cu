@@ -180,22 +180,26 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
     held_s[b] = held;
   }
   __syncthreads();
-  // pages go back
-  for (int b0 = warp * kAbreast; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast) {
-    int p[kAbreast];
-    auto each = [&](auto&& fn) {
+  // A warp's sequences, kAbreast at a time; of the first ones, the entries that the step may write are kept from here on.
+  auto each = [&](int b0, auto&& fn) {
 #pragma unroll
-      for (int i = 0; i < kAbreast; ++i) {
-        const int b = b0 + i;
-        if (b >= a.n_seqs) break;
-        const int need = get(need_s + b), held = get(held_s + b);
-        if (need >= 0 && need < held) fn(i, b, need, held);
-      }
-    };
-    each([&](int i, int b, int need, int held) {
-      p[i] = need + lane < held ? a.table[(long long)b * a.columns + need + lane] : -1;
+    for (int i = 0; i < kAbreast; ++i) {
+      const int b = b0 + i;
+      if (b < a.n_seqs) fn(i, b, get(need_s + b), get(first_s + b), get(held_s + b));
+    }
+  };
+  const int mine = warp * kAbreast;
+  int kept[kAbreast];
+  // pages go back
+  for (int b0 = mine; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast) {
+    int p[kAbreast];
+    each(b0, [&](int i, int b, int need, int first, int held) {
+      const int32_t* row = a.table + (long long)b * a.columns;
+      p[i] = need >= 0 && need + lane < held ? row[need + lane] : -1;
+      if (b0 == mine) kept[i] = first + lane < min(need, held) ? row[first + lane] : -1;
     });
-    each([&](int i, int b, int need, int held) {
+    each(b0, [&](int i, int b, int need, int first, int held) {
+      if (need < 0 || need >= held) return;
       int32_t* row = a.table + (long long)b * a.columns;
       for (int j = need + lane; j < held; j += 32) {
         const int q = j < need + 32 ? p[i] : row[j];
@@ -209,29 +213,17 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
   }
   __syncthreads();
   // what every sequence wants: pages that it shares and writes, and pages that it has not
-  for (int b0 = warp * kAbreast; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast) {
-    int n[kAbreast];
-#pragma unroll
-    for (int i = 0; i < kAbreast; ++i) {
-      const int b = b0 + i;
-      n[i] = 0;
-      if (b >= a.n_seqs) break;
-      const int need = get(need_s + b), held = min(get(held_s + b), need);
+  for (int b0 = mine; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast)
+    each(b0, [&](int i, int b, int need, int first, int held) {
       const int32_t* row = a.table + (long long)b * a.columns;
-      for (int j = get(first_s + b) + lane; j < held; j += 32) {
-        const int p = row[j];
-        n[i] += is_page(a, p) && get(snap + p) > 1;
+      int n = 0;
+      for (int j = first + lane; j < min(need, held); j += 32) {
+        const int p = b0 == mine && j < first + 32 ? kept[i] : row[j];
+        n += is_page(a, p) && get(snap + p) > 1;
       }
-    }
-#pragma unroll
-    for (int i = 0; i < kAbreast; ++i) {
-      const int b = b0 + i;
-      if (b >= a.n_seqs) break;
-      const int need = get(need_s + b), more = need < 0 ? 0 : max(0, need - get(held_s + b));
-      const int sum = __reduce_add_sync(~0u, n[i]) + more;
-      if (lane == 0) want_s[b] = sum;
-    }
-  }
+      n = __reduce_add_sync(~0u, n) + (need < 0 ? 0 : max(0, need - held));
+      if (lane == 0) want_s[b] = n;
+    });
   __syncthreads();
   // where each sequence's pages begin among those given
   long long total = 0;
@@ -259,40 +251,41 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
     __syncthreads();
   }
   // the giving
-  for (int b = warp; b < a.n_seqs && total > 0; b += kPlanWarps) {
-    const long long at0 = get(want_s + b), at1 = b + 1 < a.n_seqs ? get(want_s + b + 1) : total;
-    if (at0 == at1) continue;  // (a sequence that is not to be touched wants nothing)
-    const int need = get(need_s + b), first = get(first_s + b), held = min(get(held_s + b), need);
-    int32_t* row = a.table + (long long)b * a.columns;
-    const bool fits = at1 <= n_free;
-    if (!fits && lane == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
-    int at = int(at0);  // (used where all of them fit)
-    for (int j0 = first; j0 < held; j0 += 32) {
-      const int j = j0 + lane, p = j < held ? row[j] : -1;
-      const bool shared = is_page(a, p) && get(snap + p) > 1;
-      const unsigned m = __ballot_sync(~0u, shared);
-      if (shared) {
-        atomicAdd(a.refs + p, -1);
-        int to = -1;
-        if (fits) {
-          to = get(list + at + __popc(m & ((1u << lane) - 1)));
-          a.refs[to] = 1;
-          const int i = atomicAdd(&n_moves, 1);
-          a.src[i] = p;
-          a.dst[i] = to;
+  for (int b0 = mine; b0 < a.n_seqs && total > 0; b0 += kPlanWarps * kAbreast)
+    each(b0, [&](int i, int b, int need, int first, int holds) {
+      const long long at0 = get(want_s + b), at1 = b + 1 < a.n_seqs ? get(want_s + b + 1) : total;
+      if (at0 == at1) return;  // (a sequence that is not to be touched wants nothing)
+      const int held = min(holds, need);
+      int32_t* row = a.table + (long long)b * a.columns;
+      const bool fits = at1 <= n_free;
+      if (!fits && lane == 0) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
+      int at = int(at0);  // (used where all of them fit)
+      for (int j0 = first; j0 < held; j0 += 32) {
+        const int j = j0 + lane, p = j >= held ? -1 : b0 == mine && j0 == first ? kept[i] : row[j];
+        const bool shared = is_page(a, p) && get(snap + p) > 1;
+        const unsigned m = __ballot_sync(~0u, shared);
+        if (shared) {
+          atomicAdd(a.refs + p, -1);
+          int to = -1;
+          if (fits) {
+            to = get(list + at + __popc(m & ((1u << lane) - 1)));
+            a.refs[to] = 1;
+            const int k = atomicAdd(&n_moves, 1);
+            a.src[k] = p;
+            a.dst[k] = to;
+          }
+          row[j] = to;
         }
-        row[j] = to;
+        at += __popc(m);
       }
-      at += __popc(m);
-    }
-    if (!fits) continue;
-    for (int j = held + lane; j < need; j += 32) {
-      const int to = get(list + at + j - held);
-      row[j] = to;
-      a.refs[to] = 1;
-    }
-    if (lane == 0 && need > held) a.held[b] = need;
-  }
+      if (!fits) return;
+      for (int j = held + lane; j < need; j += 32) {
+        const int to = get(list + at + j - held);
+        row[j] = to;
+        a.refs[to] = 1;
+      }
+      if (lane == 0 && need > held) a.held[b] = need;
+    });
   __syncthreads();
   if (threadIdx.x == 0) a.count[0] = n_moves, a.count[1] = a.n_pages;
   __syncthreads();
