@@ -215,7 +215,7 @@ def step(pages, kv, new, max_new=None, max_kv=None):
 @pytest.mark.parametrize("n_pages,size,n_seqs,columns,kv_heads,dim,layers", [
     (40, 16, 5, 9, 1, 64, 1), (97, 32, 40, 12, 3, 128, 2), (1, 16, 2, 1, 2, 256, 1), (5003, 16, 130, 50, 1, 64, 1),
     (300, 256, 33, 40, 2, 128, 1), (200, 64, 7, 33, 8, 128, 3),
-    (30001, 16, 9, 4000, 1, 64, 1)])
+    (30001, 16, 9, 4000, 1, 64, 1), (70003, 16, 300, 300, 1, 64, 1)])
 def test_a_long_random_run(n_pages, size, n_seqs, columns, kv_heads, dim, layers):
     """Steps that grow, shrink, end and fork sequences, with too few pages and bad numbers now and then."""
     r = np.random.RandomState(n_pages + n_seqs)
