@@ -64,6 +64,7 @@
 // has taken it in fp32: outputs 0.0021 to 0.0024 off the 64-bit result, relative
 // to its norm, where fp32 probabilities and the output's own rounding make 0.0017.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.cuh"
 #include "ptx.cuh"
@@ -427,60 +428,68 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   auto sb_of = [&](int key, int w, int at) {
     return *reinterpret_cast<const uint16_t*>(stage + at + (key >> 3) * (G * 16 + 16) + ((key & 7) * G + w / 8) * 2);
   };
-  if (!values) {
-    uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
-    // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
-    const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
-    const int w = threadIdx.x % W;
+  // FULL: every key of the tile is some row's (a missing page's are zeros)
+  auto expand = [&](auto is_full) {
+    constexpr bool FULL = decltype(is_full)::value;
+    if (!values) {
+      uint8_t* kd = m.kx + tile * ManyCfg<DIM>::kTileBytes;
+      // the softmax multiplies by |scale|: a negative scale flips the keys' signs, scale 0 clears them
+      const uint32_t flip = m.a.scale < 0.f ? 0x80008000u : 0u, keep = m.a.scale == 0.f ? 0u : 0xFFFFFFFFu;
+      const int w = threadIdx.x % W;
 #pragma unroll 4
-    for (int key = threadIdx.x / W; key < kBK; key += kPlanThreads / W) {
-      const bool in = key < keys;
-      const uint32_t c = in ? code_of(key, w) : 0u;
-      const __nv_bfloat16 s16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kScales) : 0);
-      const __nv_bfloat16 b16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kBiases) : 0);
-      uint32_t o[4];
-      dq8_bf16(c, __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
-      *reinterpret_cast<uint4*>(kd + (key >> 6) * ManyCfg<DIM>::kSlot + (w / 8) * 8192 + sw128(key & 63, w & 7)) =
-          make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
-    }
-    return;
-  }
-  uint8_t* vd = m.vx + tile * ManyCfg<DIM>::kTileBytes;
-  // lanes: eight 8-key chunks (one 128-byte row of 64 keys) by four words
-  for (int e = threadIdx.x; e < (kBK / 8) * W; e += kPlanThreads) {
-    const int ko = e & 7, w = (e >> 3) % W, kb = (e >> 3) / W;  // 8-key chunk in its block, word, block of 64 keys
-    const int key0 = kb * 64 + ko * 8;
-    uint32_t o[8][4];  // [dim][pair of keys]
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t c[2], sc[2], bs[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        // a slot that no row sees may hold anything: its zero probability needs a finite value
-        const int key = key0 + 2 * i + j, pos = k0 + key;
-        const bool in = key < keys && (pos >= lo || pos < m.a.sinks);
-        c[j] = in ? code_of(key, w) : 0u;
-        sc[j] = in ? sb_of(key, w, St::kScales) : 0u;
-        bs[j] = in ? sb_of(key, w, St::kBiases) : 0u;
+      for (int key = threadIdx.x / W; key < kBK; key += kPlanThreads / W) {
+        const bool in = FULL || key < keys;
+        const uint32_t c = in ? code_of(key, w) : 0u;
+        const __nv_bfloat16 s16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kScales) : 0);
+        const __nv_bfloat16 b16 = __ushort_as_bfloat16(in ? sb_of(key, w, St::kBiases) : 0);
+        uint32_t o[4];
+        dq8_bf16(c, __halves2bfloat162(s16, s16), __halves2bfloat162(b16, b16), o);
+        *reinterpret_cast<uint4*>(kd + (key >> 6) * ManyCfg<DIM>::kSlot + (w / 8) * 8192 + sw128(key & 63, w & 7)) =
+            make_uint4((o[0] ^ flip) & keep, (o[1] ^ flip) & keep, (o[2] ^ flip) & keep, (o[3] ^ flip) & keep);
       }
-      const uint32_t s2 = sc[0] | sc[1] << 16, b2 = bs[0] | bs[1] << 16;
-      const __nv_bfloat162 sp = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-      const __nv_bfloat162 bp = *reinterpret_cast<const __nv_bfloat162*>(&b2);
-      const uint32_t lo2 = __byte_perm(c[0], c[1], 0x5410), hi2 = __byte_perm(c[0], c[1], 0x7632);
+      return;
+    }
+    uint8_t* vd = m.vx + tile * ManyCfg<DIM>::kTileBytes;
+    // lanes: eight 8-key chunks (one 128-byte row of 64 keys) by four words
+    for (int e = threadIdx.x; e < (kBK / 8) * W; e += kPlanThreads) {
+      const int ko = e & 7, w = (e >> 3) % W, kb = (e >> 3) / W;  // 8-key chunk in its block, word, block of 64 keys
+      const int key0 = kb * 64 + ko * 8;
+      uint32_t o[8][4];  // [dim][pair of keys]
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        o[n][i] = dq_pair(lo2 >> (4 * n), sp, bp);
-        o[n + 4][i] = dq_pair(hi2 >> (4 * n), sp, bp);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t c[2], sc[2], bs[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // a slot that no row sees may hold anything: its zero probability needs a finite value
+          const int key = key0 + 2 * i + j, pos = k0 + key;
+          const bool in = FULL || (key < keys && (pos >= lo || pos < m.a.sinks));
+          c[j] = in ? code_of(key, w) : 0u;
+          sc[j] = in ? sb_of(key, w, St::kScales) : 0u;
+          bs[j] = in ? sb_of(key, w, St::kBiases) : 0u;
+        }
+        const uint32_t s2 = __byte_perm(sc[0], sc[1], 0x5410), b2 = __byte_perm(bs[0], bs[1], 0x5410);
+        const __nv_bfloat162 sp = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+        const __nv_bfloat162 bp = *reinterpret_cast<const __nv_bfloat162*>(&b2);
+        const uint32_t lo2 = __byte_perm(c[0], c[1], 0x5410), hi2 = __byte_perm(c[0], c[1], 0x7632);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          o[n][i] = dq_pair(lo2 >> (4 * n), sp, bp);
+          o[n + 4][i] = dq_pair(hi2 >> (4 * n), sp, bp);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int d = 8 * w + n;
+        constexpr int kHalf = DIM / 2;  // dims of a CTA
+        const uint32_t at = d / kHalf * ManyCfg<DIM>::kSlot + kb * (kHalf * 128) + sw128(d % kHalf, ko);
+        *reinterpret_cast<uint4*>(vd + at) = make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
       }
     }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int d = 8 * w + n;
-      constexpr int kHalf = DIM / 2;  // dims of a CTA
-      const uint32_t at = d / kHalf * ManyCfg<DIM>::kSlot + kb * (kHalf * 128) + sw128(d % kHalf, ko);
-      *reinterpret_cast<uint4*>(vd + at) = make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
-    }
-  }
+  };
+  if (keys >= kBK && m.a.window == 0)
+    expand(std::true_type{});
+  else
+    expand(std::false_type{});
 }
 
 // ---- tcgen05 ------------------------------------------------------------------------------
