@@ -79,7 +79,7 @@ class moe_attention(ctypes.Structure):
 class moe_rotary(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("axes", ctypes.c_int),
                 ("eps", ctypes.c_float), ("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p),
-                ("positions", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
 
 
 class moe_kv_pages(ctypes.Structure):
@@ -118,7 +118,7 @@ SIGNATURES = {
     "moe_expanded_weights_bytes": (_SZ, [_W]),
     "moe_layer_forward_expanded": (_CI, [_W, _VP, _CI, _VP, _VP, _SZ, _VP, _SZ, _VP]),
     "moe_kv_append": (_CI, [_KC, _KB, _VP, _LL, _VP, _LL, _VP]),
-    "moe_kv_append_rotary": (_CI, [_KC, _KB, _RO, _CI, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _VP]),
+    "moe_kv_append_rotary": (_CI, [_KC, _KB, _RO, _VP, _CI, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _VP]),
     "moe_kv_read": (_CI, [_KC, _KB, _VP, _VP, _VP]),
     "moe_kv_pages_scratch": (_SZ, [_CI, _CI]),
     "moe_kv_pages_update": (_CI, [_PG, _KB, _KCS, _CI, _VP]),
@@ -240,10 +240,10 @@ def moe_kv_append(cache, batch, k_ptr, k_stride, v_ptr, v_stride, stream) -> int
     return lib().moe_kv_append(ctypes.byref(cache), ctypes.byref(batch), k_ptr, k_stride, v_ptr, v_stride, stream)
 
 
-def moe_kv_append_rotary(cache, batch, rotary: moe_rotary, heads, q_ptr, q_stride, q_out_ptr, k_ptr, k_stride, v_ptr, v_stride,
-                         stream) -> int:
-    return lib().moe_kv_append_rotary(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(rotary), heads, q_ptr, q_stride,
-                                      q_out_ptr, k_ptr, k_stride, v_ptr, v_stride, stream)
+def moe_kv_append_rotary(cache, batch, rotary: moe_rotary, positions_ptr, heads, q_ptr, q_stride, q_out_ptr, k_ptr, k_stride,
+                         v_ptr, v_stride, stream) -> int:
+    return lib().moe_kv_append_rotary(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(rotary), positions_ptr, heads,
+                                      q_ptr, q_stride, q_out_ptr, k_ptr, k_stride, v_ptr, v_stride, stream)
 
 
 def moe_kv_read(cache, batch, k_ptr, v_ptr, stream) -> int:
@@ -468,8 +468,9 @@ class Rotary:
             if w is not None and (w.dtype != torch.float32 or w.dim() != 1 or not w.is_contiguous() or w.device != self.device):
                 raise ValueError(f"{name}: contiguous fp32 [head dim] on {self.device}")
         self.q_weight, self.k_weight = q_weight, k_weight
+        self._dims = {w.shape[0] for w in (q_weight, k_weight) if w is not None}
         self.c = moe_rotary(self.rotary_dim, int(interleaved), self.axes, eps, self._turns.data_ptr(), self._axis.data_ptr(),
-                            None, None if q_weight is None else q_weight.data_ptr(),
+                            None if q_weight is None else q_weight.data_ptr(),
                             None if k_weight is None else k_weight.data_ptr())
         self._ref = ctypes.byref(self.c)
 
@@ -558,24 +559,19 @@ class KVCache:
         qs = self._rows("q", q, n, heads)
         ks = self._rows("k", k, n, self.kv_heads)
         vs = self._rows("v", v, n, self.kv_heads)
-        if rotary.device != self.device:
-            raise ValueError("rotary: on the cache's device")
-        for w in (rotary.q_weight, rotary.k_weight):
-            if w is not None and w.shape[0] != self.head_dim:
-                raise ValueError(f"rotary: weights of {self.head_dim} elements")
-        ref = rotary._ref
+        if rotary.device != self.device or rotary._dims - {self.head_dim}:
+            raise ValueError(f"rotary: on the cache's device, with weights of {self.head_dim} elements")
+        at = None
         if positions is not None:
             if positions.dtype != torch.int32 or positions.device != self.device or not positions.is_contiguous() or \
                     positions.shape not in ((rotary.axes, n), (n,) if rotary.axes == 1 else None):
                 raise ValueError(f"positions: contiguous int32 [{rotary.axes}, {n}] on the cache's device")
-            c = moe_rotary.from_buffer_copy(rotary.c)  # (a handle may be used by two threads)
-            c.positions = positions.data_ptr()
-            ref = ctypes.byref(c)
+            at = positions.data_ptr()
         if out is None:
             out = torch.empty((n, heads, self.head_dim), dtype=self._bf16, device=self.device)
         elif out.shape != q.shape or out.dtype != self._bf16 or not out.is_contiguous() or out.device != self.device:
             raise ValueError("out: contiguous, of q's shape, type and device")
-        st = lib().moe_kv_append_rotary(self._ref, b, ref, heads, q.data_ptr(), qs, out.data_ptr(), k.data_ptr(), ks,
+        st = lib().moe_kv_append_rotary(self._ref, b, rotary._ref, at, heads, q.data_ptr(), qs, out.data_ptr(), k.data_ptr(), ks,
                                         v.data_ptr(), vs, self._stream(None))
         if st:
             _check(st, "moe_kv_append_rotary")

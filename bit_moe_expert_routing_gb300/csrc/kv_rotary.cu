@@ -320,7 +320,7 @@ cudaError_t launch(RotaryArgs r, const KvCall& c) {
 using namespace moe;
 
 extern "C" moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rotary* rot,
-                                           int heads, const uint16_t* q, long long q_stride, uint16_t* q_out,
+                                           const int32_t* positions, int heads, const uint16_t* q, long long q_stride, uint16_t* q_out,
                                            const uint16_t* k, long long k_stride, const uint16_t* v, long long v_stride,
                                            void* stream) {
   RotaryArgs r{};
@@ -330,7 +330,7 @@ extern "C" moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_
   if (rot->rotary_dim < 0 || rot->rotary_dim > r.kv.dim || rot->rotary_dim % 16) return MOE_ERR_SHAPE;
   if (heads < 1 || heads > 16384 || rot->axes < 1 || rot->axes > 4) return MOE_ERR_SHAPE;
   if (rot->rotary_dim && (!rot->turns || !aligned(rot->turns, 8))) return MOE_ERR_ARG;
-  if (!aligned(rot->positions, 4) || !aligned(rot->q_weight, 16) || !aligned(rot->k_weight, 16)) return MOE_ERR_ARG;
+  if (!aligned(positions, 4) || !aligned(rot->q_weight, 16) || !aligned(rot->k_weight, 16)) return MOE_ERR_ARG;
   if ((rot->q_weight || rot->k_weight) && !(rot->eps >= 0x1p-64f && std::isfinite(rot->eps))) return MOE_ERR_ARG;
   if (r.kv.n_tokens == 0) return MOE_OK;
   if (!operand_ok(q, q_stride, heads, r.kv.dim) || !operand_ok(k, k_stride, r.kv.kv_heads, r.kv.dim) ||
@@ -339,7 +339,7 @@ extern "C" moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_
   if (!q_out || !aligned(q_out, 16) || q_out == q || q_out == k || q_out == v) return MOE_ERR_ARG;
   r.turns = rot->turns;
   r.axis = rot->axis;
-  r.positions = rot->positions;
+  r.positions = positions;
   r.weight[0] = rot->q_weight;
   r.weight[1] = rot->k_weight;
   r.eps = rot->eps;

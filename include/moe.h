@@ -124,7 +124,8 @@ typedef enum {
                                 2, 3 and 4 rows, and slower at 5 and 8) */
   MOE_OPT_FORCE_PATH = 2,    /* 0 auto by row count, 1 GEMV, 2 grouped GEMM; and of the
                                 attention: 0 auto by the step's sizes, 1 the few-row
-                                kernel, 2 the many-row kernels */
+                                kernel, 2 the many-row kernels (either also shares
+                                prefixes whatever they spare) */
   MOE_OPT_KERNEL_TIMING = 3, /* 1: record CUDA events around each kernel of
                                 the next forwards (read with moe_kernel_times) */
   MOE_OPT_GEMM_IMPL = 4,     /* grouped GEMM used above the GEMV threshold:
@@ -444,9 +445,6 @@ moe_status moe_attention_forward(const moe_kv_cache* cache, const moe_kv_batch* 
  *                position in units of 2^-64, the two's complement of a negative one
  *   axis         device uint8 [rotary_dim / 2], or NULL: all 0; a number that is
  *                no axis is taken for 0
- *   positions    device int32 [axes, n_tokens], or NULL: a token's position in
- *                its sequence, on every axis. They turn the heads only; where a
- *                token is cached goes by the batch.
  *   q_weight, k_weight  device fp32 [head_dim], 16-byte aligned, or NULL: no norm
  *   eps          at least 2^-64, finite; used with a weight only
  * Squares may pass fp32. A NaN makes every normed element of its head NaN, an
@@ -456,18 +454,21 @@ typedef struct {
   float eps;
   const uint64_t* turns;
   const uint8_t* axis;
-  const int32_t* positions;
   const float* q_weight;
   const float* k_weight;
 } moe_rotary;
 
-/* q: device bf16 [n_tokens, heads, head_dim], strided as k and v are (see
- * moe_kv_append); q_out: device bf16, contiguous, 16-byte aligned, not
- * overlapping q, k or v. heads: 1 to 16384. Padding tokens (negative positions) get their
- * q_out, turned to that position, and are not cached. n_tokens = 0 is a no-op. */
-moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rotary* rotary, int heads,
-                                const uint16_t* q, long long q_stride, uint16_t* q_out, const uint16_t* k,
-                                long long k_stride, const uint16_t* v, long long v_stride, void* stream);
+/* positions: device int32 [axes, n_tokens], or NULL: a token's position in its
+ * sequence, on every axis. They turn the heads only; where a token is cached
+ * goes by the batch. q: device bf16 [n_tokens, heads, head_dim], strided as k
+ * and v are (see moe_kv_append); q_out: device bf16, contiguous, 16-byte
+ * aligned, not overlapping q, k or v. heads: 1 to 16384. Padding tokens
+ * (negative positions) get their q_out, turned to that position, and are not
+ * cached. n_tokens = 0 is a no-op. */
+moe_status moe_kv_append_rotary(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rotary* rotary,
+                                const int32_t* positions, int heads, const uint16_t* q, long long q_stride,
+                                uint16_t* q_out, const uint16_t* k, long long k_stride, const uint16_t* v,
+                                long long v_stride, void* stream);
 
 /* ---- pages of a cache ----
  *
@@ -541,9 +542,9 @@ moe_status moe_kv_copy_pages(const moe_kv_cache* const* caches, int n_caches, co
  *
  * moe_attention_forward for a step whose sequences, group by group, hold the
  * same keys and values at their first positions (forked from one prompt, or
- * given the same pages): a group's shared part is read and multiplied once, with the
- * rows of all its sequences together, and each sequence's own part is joined to
- * it in fp32. The result is moe_attention_forward's but for roundings.
+ * given the same pages): a group's shared part is read (and expanded for the
+ * tensor cores) once, and meets the rows of all its sequences together. The
+ * result is moe_attention_forward's but for roundings.
  *   seq_off  device int32 [n_groups + 1]: group g is the sequences seq_off[g]
  *            .. seq_off[g + 1] - 1; ascending, from 0 to n_seqs
  *   length   device int32 [n_groups]: how many first positions the group shares;
@@ -555,10 +556,11 @@ moe_status moe_kv_copy_pages(const moe_kv_cache* const* caches, int n_caches, co
  * A sequence whose step tokens begin before its group's shared positions end
  * shares nothing. The call is moe_attention_forward where sharing would not
  * pay: with a window (which reads near positions only), and where few passes
- * over few positions are spared. Where it shares, groups that are not as said here, or past
- * their bounds, record MOE_ERR_DEVICE_CHECK, and no sequence of the step shares
- * anything; a sequence past max_own records it, and its rows of the output are
- * not written. (MOE_OPT_FORCE_PATH other than 0 shares wherever there is no window.) */
+ * over few positions are spared. Where it shares, groups that are not as said
+ * here, or past their bounds, record MOE_ERR_DEVICE_CHECK, and no sequence of
+ * the step shares anything; a sequence past max_own records it, and its rows of
+ * the output are not written. (MOE_OPT_FORCE_PATH other than 0 shares wherever
+ * there is no window.) */
 typedef struct {
   int n_groups, max_tokens, max_len, max_own;
   const int32_t* seq_off;

@@ -26,21 +26,21 @@ def _built():
 def c_args(cache=None, batch=None, **rotary):
     c = moe.moe_kv_cache(10, 16, 2, 128, P, P, P, P, P, P, P)
     b = moe.moe_kv_batch(2, 2, 1, 100, P, P, P, 8)
-    r = moe.moe_rotary(64, 0, 1, 1e-6, P, P, None, P, P)
+    r = moe.moe_rotary(64, 0, 1, 1e-6, P, P, P, P)
     for s, kw in ((c, cache or {}), (b, batch or {}), (r, rotary)):
         for name, v in kw.items():
             setattr(s, name, v)
     return c, b, r
 
 
-def call(c, b, r, heads=8, q=P, qs=1024, out=2 * P, k=P, ks=256, v=P, vs=256):
-    return moe.moe_kv_append_rotary(c, b, r, heads, q, qs, out, k, ks, v, vs, None)
+def call(c, b, r, positions=None, heads=8, q=P, qs=1024, out=2 * P, k=P, ks=256, v=P, vs=256):
+    return moe.moe_kv_append_rotary(c, b, r, positions, heads, q, qs, out, k, ks, v, vs, None)
 
 
 @pytest.mark.parametrize("rotary,want", [
     (dict(rotary_dim=-16), moe.MOE_ERR_SHAPE), (dict(rotary_dim=144), moe.MOE_ERR_SHAPE), (dict(rotary_dim=24), moe.MOE_ERR_SHAPE),
     (dict(axes=0), moe.MOE_ERR_SHAPE), (dict(axes=5), moe.MOE_ERR_SHAPE), (dict(turns=None), moe.MOE_ERR_ARG),
-    (dict(turns=P + 4), moe.MOE_ERR_ARG), (dict(positions=P + 2), moe.MOE_ERR_ARG), (dict(q_weight=P + 8), moe.MOE_ERR_ARG),
+    (dict(turns=P + 4), moe.MOE_ERR_ARG), (dict(q_weight=P + 8), moe.MOE_ERR_ARG),
     (dict(k_weight=P + 8), moe.MOE_ERR_ARG), (dict(eps=0.0), moe.MOE_ERR_ARG), (dict(eps=-1e-6), moe.MOE_ERR_ARG),
     (dict(eps=math.inf), moe.MOE_ERR_ARG), (dict(eps=math.nan), moe.MOE_ERR_ARG)])
 def test_bad_rotations_are_refused(rotary, want):
@@ -52,11 +52,11 @@ def test_bad_rotations_are_refused(rotary, want):
 def test_bad_caches_and_operands_are_refused():
     assert call(*c_args(cache=dict(head_dim=96))) == moe.MOE_ERR_SHAPE
     assert call(*c_args(batch=dict(max_kv=-1))) == moe.MOE_ERR_ARG
-    assert moe.lib().moe_kv_append_rotary(*(ctypes.byref(x) for x in c_args()[:2]), None, 8, P, 1024, 2 * P, P, 256, P, 256,
+    assert moe.lib().moe_kv_append_rotary(*(ctypes.byref(x) for x in c_args()[:2]), None, None, 8, P, 1024, 2 * P, P, 256, P, 256,
                                           None) == moe.MOE_ERR_ARG
     for kw in (dict(heads=0), dict(heads=16385)):
         assert call(*c_args(), **kw) == moe.MOE_ERR_SHAPE
-    for kw in (dict(q=None), dict(q=P + 2), dict(qs=1016), dict(qs=1028), dict(out=None), dict(out=2 * P + 8), dict(out=P),
+    for kw in (dict(positions=P + 2), dict(q=None), dict(q=P + 2), dict(qs=1016), dict(qs=1028), dict(out=None), dict(out=2 * P + 8), dict(out=P),
                dict(k=None), dict(ks=248), dict(v=P + 8), dict(vs=-256), dict(k=2 * P), dict(v=2 * P)):
         assert call(*c_args(), **kw) == moe.MOE_ERR_ARG, kw
     assert call(*c_args(batch=dict(n_tokens=0)), q=None, k=None, v=None, out=None) == moe.MOE_OK
