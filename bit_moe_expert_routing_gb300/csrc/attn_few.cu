@@ -166,8 +166,9 @@ constexpr int kMinTiles = 8;  // of a CTA, when items are cut: two per warp
 // items: CTAs with four items took 143 thousand cycles, with one 112.)
 constexpr int kItemCost = 10;
 
+template <bool PARTS>
 struct FewArgs {
-  AttnArgs a;
+  Attn<PARTS> a;
   int max_rows;      // sequences with more rows than this are left to the other kernels
   int row_groups;    // groups of 8 NT rows per (sequence, kv head), at most
   int whole;         // every CTA takes one item, whole
@@ -187,7 +188,8 @@ struct SeqItems {
   Tiles tiles;
   __device__ __forceinline__ long long units(int kv_heads) const { return (long long)groups * kv_heads * (kItemCost + tiles.n); }
 };
-__device__ __forceinline__ SeqItems items_of(const FewArgs& f, int b, int rows_per_group) {
+template <typename F>
+__device__ __forceinline__ SeqItems items_of(const F& f, int b, int rows_per_group) {
   SeqItems q;
   q.s = kv_seq(f.a.kv, b);
   q.rows = q.s.n_new * f.a.group;
@@ -200,9 +202,9 @@ __device__ __forceinline__ SeqItems items_of(const FewArgs& f, int b, int rows_p
 
 // The units of all sequences, and where unit ranges begin. One CTA computes
 // it, kScanThreads sequences at a time.
-template <int THREADS>
+template <int THREADS, typename F>
 struct Cut {
-  const FewArgs& f;
+  const F& f;
   const int rows;
   long long* sums;  // [THREADS] shared memory
   long long total, each;
@@ -228,7 +230,7 @@ struct Cut {
     __syncthreads();
     return sums[THREADS - 1];
   }
-  __device__ Cut(const FewArgs& args, int rows_per_group, long long* shared) : f(args), rows(rows_per_group), sums(shared) {
+  __device__ Cut(const F& args, int rows_per_group, long long* shared) : f(args), rows(rows_per_group), sums(shared) {
     total = 0;
     if (f.a.kv.n_seqs == 1) {  // one request: no sums to make
       total = items_of(f, 0, rows).units(f.a.kv.kv_heads);
@@ -274,14 +276,14 @@ struct Cut {
 };
 
 template <int DIM, int NT, bool PARTS>
-__global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attention_few_kernel(const FewArgs f) {
+__global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attention_few_kernel(const FewArgs<PARTS> f) {
   using C = FewCfg<DIM, NT>;
   using St = Stage<DIM>;
   constexpr int kSteps = C::kSteps, kStages = C::kStages;
   constexpr int KW = DIM / 32;  // words of a key row that one lane expands (four lanes share a row)
   constexpr int VW = DIM / 64;  // words of a value row per lane (eight lanes share a row)
   extern __shared__ __align__(128) uint8_t smem[];
-  const AttnArgs& a = f.a;
+  const Attn<PARTS>& a = f.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   griddep_launch();
   uint8_t* ring = smem + C::kOffRing + warp * kStages * St::kBytes;
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
     off = 0;
     left = kItemCost + sq.tiles.n;
   } else {
-    Cut<kWarps * 32> cut(f, C::kRows, reinterpret_cast<long long*>(smem + C::kOffRing));
+    Cut<kWarps * 32, FewArgs<PARTS>> cut(f, C::kRows, reinterpret_cast<long long*>(smem + C::kOffRing));
     if (int(blockIdx.x) >= cut.ctas) return griddep_wait();
     const long long begin = cut.begin(blockIdx.x);
     left = cut.begin(blockIdx.x + 1) - begin;
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
   // order. Its two halves of 16 keys may lie in different pages. Each lane
   // looks the pages of one of the warp's next 32 tiles up (-1: there is none,
   // recorded, or no row sees a key of that half).
-  const KvTable tb = kv_table<PARTS>(a.kv, b);
+  const KvTable tb = kv_table<PARTS>(a, b);
   const bool has_table = tb.n > 0;
   const int* table = has_table ? tb.entry : a.kv.kv_len;
   const int last_entry = has_table ? tb.n - 1 : 0;
@@ -766,15 +768,15 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<DIM, NT>::kMinCtas) attent
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[2 * k] = o[n][4 * w + k][i], v[2 * k + 1] = o[n][4 * w + k][2 + i];
         if (!cut_item && to_own<PARTS>(a, b)) {
-          float4* dst = reinterpret_cast<float4*>(a.own_o + at * DIM + d);
+          float4* dst = reinterpret_cast<float4*>(as_part(a).own_o + at * DIM + d);
           dst[0] = make_float4(v[0], v[1], v[2], v[3]);
           dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (g == 0 && w == 0) a.own_lse[at] = l[n][i];
+          if (g == 0 && w == 0) as_part(a).own_lse[at] = l[n][i];
         } else if (!cut_item) {
           if (!is_written<PARTS>(a, si.first + t)) continue;
           if (is_shared<PARTS>(a)) {
-            const Join j = join_of(l[n][i], a.own_lse[at]);
-            const float4* o1 = reinterpret_cast<const float4*>(a.own_o + at * DIM + d);
+            const Join j = join_of(l[n][i], as_part(a).own_lse[at]);
+            const float4* o1 = reinterpret_cast<const float4*>(as_part(a).own_o + at * DIM + d);
             const float4 x = o1[0], y = o1[1];
             const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -813,18 +815,21 @@ struct Parts {
   SeqItems sq;
   int seq, kvh, rg, n_rows, p0, n;
   __device__ __forceinline__ int slot(int p) const { return 2 * (p0 + p) + (p > 0); }
-  __device__ __forceinline__ int token(const FewArgs& f, int rows_per_group, int row) const {
+  template <typename F>
+  __device__ __forceinline__ int token(const F& f, int rows_per_group, int row) const {
     return sq.s.first + f.token(rg * rows_per_group + row);
   }
   // place of row `row` of the group in the outputs
-  __device__ __forceinline__ long long place(const FewArgs& f, int rows_per_group, int row) const {
+  template <typename F>
+  __device__ __forceinline__ long long place(const F& f, int rows_per_group, int row) const {
     const int r = rg * rows_per_group + row, t = f.token(r);
     return (long long)(sq.s.first + t) * f.a.heads + kvh * f.a.group + r - t * f.a.group;
   }
 };
 // The parts of item x of the grid's items (by one CTA of 256 threads; what
 // they are counted from is input, so this runs beside the kernel before).
-__device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_group) {
+template <typename F>
+__device__ __forceinline__ Parts parts_of(const F& f, int x, int rows_per_group) {
   __shared__ long long sums[256];
   Parts q;
   q.n = 0;
@@ -837,7 +842,7 @@ __device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_
   q.n_rows = min(q.sq.rows - q.rg * rows_per_group, rows_per_group);
   if (q.n_rows <= 0) return q;
   // the units of the sequences before, then of the items before
-  Cut<256> cut(f, rows_per_group, sums);
+  Cut<256, F> cut(f, rows_per_group, sums);
   long long u0 = 0;
   for (int c0 = 0; c0 <= b && f.a.kv.n_seqs > 1; c0 += 256) {
     const long long n = f.a.kv.n_seqs <= 256 ? cut.total : cut.chunk(c0);
@@ -856,10 +861,10 @@ __device__ __forceinline__ Parts parts_of(const FewArgs& f, int x, int rows_per_
 // loads. (16 sequences of 4 tokens, 13 parts an item: the call 24.7 us, 26.3
 // with the weights first; the same for few items below gains nothing.)
 template <int DIM, bool PARTS>
-__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f, int rows_per_group) {
+__global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs<PARTS> f, int rows_per_group) {
   constexpr int kV = DIM / 128 + (DIM < 128);  // float4 of a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 8 + warp;
-  if (PARTS && f.a.part == AttnArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
+  if (PARTS && as_part(f.a).part == PartArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
   const Parts q = parts_of(f, blockIdx.x, rows_per_group);
   if (q.n <= 1 || row >= q.n_rows || !is_written<PARTS>(f.a, q.token(f, rows_per_group, row))) return griddep_wait();  // (see Parts)
   const long long at = q.place(f, rows_per_group, row);
@@ -907,17 +912,17 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
   if (to_own<PARTS>(f.a, q.seq)) {
     if (mine)
 #pragma unroll
-      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(f.a.own_o + at * DIM)[lane + 32 * k] = o[k];
-    if (lane == 0) f.a.own_lse[at] = lse;
+      for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(as_part(f.a).own_o + at * DIM)[lane + 32 * k] = o[k];
+    if (lane == 0) as_part(f.a).own_lse[at] = lse;
     return;
   }
   if (is_shared<PARTS>(f.a)) {
-    const Join j = join_of(lse, f.a.own_lse[at]);
+    const Join j = join_of(lse, as_part(f.a).own_lse[at]);
     lse = j.lse;
     if (mine)
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        const float4 u = reinterpret_cast<const float4*>(f.a.own_o + at * DIM)[lane + 32 * k];
+        const float4 u = reinterpret_cast<const float4*>(as_part(f.a).own_o + at * DIM)[lane + 32 * k];
         o[k].x = j.shared * o[k].x + j.own * u.x, o[k].y = j.shared * o[k].y + j.own * u.y;
         o[k].z = j.shared * o[k].z + j.own * u.z, o[k].w = j.shared * o[k].w + j.own * u.w;
       }
@@ -937,14 +942,14 @@ __global__ void __launch_bounds__(256) attention_combine_kernel(const FewArgs f,
 // CTA per (item, row, 64 dims), sixteen threads on the dims and sixteen such
 // groups on the parts, eight loads in flight each.
 template <int DIM, bool PARTS>
-__global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewArgs f, int rows_per_group, int rows) {
+__global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewArgs<PARTS> f, int rows_per_group, int rows) {
   constexpr int kLanes = 16, kGroups = 16;
   constexpr int kMaxParts = 1024;  // (no item has more parts than there are CTAs)
   __shared__ float weight[kMaxParts];
   __shared__ float4 acc[kGroups][kLanes];
   __shared__ float red[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x % rows;
-  if (PARTS && f.a.part == AttnArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
+  if (PARTS && as_part(f.a).part == PartArgs::kOwn) griddep_launch();  // (the shared part's kernels, which wait for this one)
   const Parts q = parts_of(f, blockIdx.x / rows, rows_per_group);
   const int n = q.n;
   if (n <= 1 || row >= q.n_rows || !is_written<PARTS>(f.a, q.token(f, rows_per_group, row))) return griddep_wait();  // (see Parts)
@@ -999,13 +1004,13 @@ __global__ void __launch_bounds__(256) attention_combine_wide_kernel(const FewAr
     float lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
     v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
     if (to_own<PARTS>(f.a, q.seq)) {
-      *reinterpret_cast<float4*>(f.a.own_o + at * DIM + d) = v;
-      if (d == 0) f.a.own_lse[at] = lse;
+      *reinterpret_cast<float4*>(as_part(f.a).own_o + at * DIM + d) = v;
+      if (d == 0) as_part(f.a).own_lse[at] = lse;
       return;
     }
     if (is_shared<PARTS>(f.a)) {
-      const Join j = join_of(lse, f.a.own_lse[at]);
-      const float4 u = *reinterpret_cast<const float4*>(f.a.own_o + at * DIM + d);
+      const Join j = join_of(lse, as_part(f.a).own_lse[at]);
+      const float4 u = *reinterpret_cast<const float4*>(as_part(f.a).own_o + at * DIM + d);
       lse = j.lse;
       v.x = j.shared * v.x + j.own * u.x, v.y = j.shared * v.y + j.own * u.y;
       v.z = j.shared * v.z + j.own * u.z, v.w = j.shared * v.w + j.own * u.w;
@@ -1042,7 +1047,7 @@ FewPlan plan(const AttnArgs& a, int max_rows) {
 }
 
 template <int DIM, int NT, bool PARTS>
-cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
+cudaError_t launch(const FewArgs<PARTS>& f, bool beside, const KvCall& c) {
   using C = FewCfg<DIM, NT>;
   const void* fn = reinterpret_cast<const void*>(&attention_few_kernel<DIM, NT, PARTS>);
   if (!ensure_smem_limit(fn, C::kSmem)) return cudaErrorInvalidValue;
@@ -1079,7 +1084,7 @@ cudaError_t launch(const FewArgs& f, bool beside, const KvCall& c) {
 }
 
 template <bool PARTS>
-cudaError_t launch_as(const FewArgs& f, int nt, bool beside, const KvCall& c) {
+cudaError_t launch_as(const FewArgs<PARTS>& f, int nt, bool beside, const KvCall& c) {
   switch (f.a.kv.dim * 8 + nt) {
     case 64 * 8 + 1: return launch<64, 1, PARTS>(f, beside, c);
     case 64 * 8 + 2: return launch<64, 2, PARTS>(f, beside, c);
@@ -1090,6 +1095,15 @@ cudaError_t launch_as(const FewArgs& f, int nt, bool beside, const KvCall& c) {
     case 256 * 8 + 1: return launch<256, 1, PARTS>(f, beside, c);
     default: return launch<256, 2, PARTS>(f, beside, c);
   }
+}
+
+template <bool PARTS>
+cudaError_t start(const Attn<PARTS>& a, int max_rows, void* ws, bool beside, const KvCall& c) {
+  const FewPlan p = plan(a, max_rows);
+  float* part = static_cast<float*>(ws);
+  const FewArgs<PARTS> f{a,    max_rows, p.row_groups, p.whole, p.ctas, part, part + p.part_rows * a.kv.dim,
+                         ((1ull << 32) + a.group - 1) / a.group};
+  return launch_as<PARTS>(f, p.nt, beside, c);
 }
 
 }  // namespace
@@ -1104,11 +1118,10 @@ long long attention_few_items(const AttnArgs& a, int max_rows) {
 }
 
 cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside, const KvCall& c) {
-  const FewPlan p = plan(a, max_rows);
-  float* part = static_cast<float*>(ws);
-  const FewArgs f{a,    max_rows, p.row_groups, p.whole, p.ctas, part, part + p.part_rows * a.kv.dim,
-                  ((1ull << 32) + a.group - 1) / a.group};
-  return a.part == AttnArgs::kWhole ? launch_as<false>(f, p.nt, beside, c) : launch_as<true>(f, p.nt, beside, c);
+  return start<false>(a, max_rows, ws, beside, c);
+}
+cudaError_t attention_few_part(const PartArgs& a, int max_rows, void* ws, bool beside, const KvCall& c) {
+  return start<true>(a, max_rows, ws, beside, c);
 }
 
 }  // namespace moe

@@ -127,8 +127,9 @@ struct __align__(16) PairRange {
   int head, rt;     // its kv head and row tile
 };
 
+template <bool PARTS>
 struct ManyArgs {
-  AttnArgs a;
+  Attn<PARTS> a;
   int max_few;             // sequences with at most this many rows are not taken
   int b0, nb, h0, nh;      // sequences and kv heads of this pass
   int tiles_max;           // key tiles per (sequence, kv head) in the expanded arrays
@@ -167,13 +168,15 @@ __device__ __forceinline__ Range range_of(int minpos, int maxpos, int window, in
   return r;
 }
 
-__device__ __forceinline__ bool taken(const ManyArgs& m, const SeqInfo& s) { return s.n_new * m.a.group > m.max_few; }
+template <typename M>
+__device__ __forceinline__ bool taken(const M& m, const SeqInfo& s) { return s.n_new * m.a.group > m.max_few; }
 
-__device__ __forceinline__ Range seq_range(const ManyArgs& m, const SeqInfo& s) {
+template <typename M>
+__device__ __forceinline__ Range seq_range(const M& m, const SeqInfo& s) {
   return range_of(s.kv - s.n_new, s.kv - 1, m.a.window, m.a.sinks);
 }
 template <bool PARTS>
-__device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s, int row0, int rows) {
+__device__ __forceinline__ Range rows_range(const ManyArgs<PARTS>& m, const SeqInfo& s, int row0, int rows) {
   const int base = base_pos<PARTS>(m.a, s), last = min(row0 + rows, s.n_new * m.a.group) - 1;
   return range_of(pos_of<PARTS>(m.a, base, m.token(row0)), pos_of<PARTS>(m.a, base, m.token(last)), m.a.window, m.a.sinks);
 }
@@ -183,7 +186,7 @@ __device__ __forceinline__ Range rows_range(const ManyArgs& m, const SeqInfo& s,
 struct RowView {
   int seq, sink, lo, pos;
 };
-__device__ __forceinline__ RowView row_view(const AttnArgs& a, int group, int token) {
+__device__ __forceinline__ RowView row_view(const PartArgs& a, int group, int token) {
   int lo = a.seq_off[group], hi = a.seq_off[group + 1] - 1;  // the last sequence that begins at or before the token
   const int tile0 = a.own_tile[lo], shared = (a.shared_len[group] + kBK - 1) / kBK;
   while (lo < hi) {
@@ -201,11 +204,13 @@ __device__ __forceinline__ RowView row_view(const AttnArgs& a, int group, int to
   return v;
 }
 // Key tiles that a row tile's rows see: the shared ones, then those of the own positions of its sequences.
-__device__ __forceinline__ Range together_range(const ManyArgs& m, int group, const SeqInfo& s, int row0, int rows) {
+template <typename M>
+__device__ __forceinline__ Range together_range(const M& m, int group, const SeqInfo& s, int row0, int rows) {
   const int last = min(row0 + rows, s.n_new * m.a.group) - 1;
-  const RowView v0 = row_view(m.a, group, s.first + m.token(row0)), v1 = row_view(m.a, group, s.first + m.token(last));
+  const RowView v0 = row_view(as_part(m.a), group, s.first + m.token(row0));
+  const RowView v1 = row_view(as_part(m.a), group, s.first + m.token(last));
   Range r;
-  r.n_sink = (m.a.shared_len[group] + kBK - 1) / kBK;
+  r.n_sink = (as_part(m.a).shared_len[group] + kBK - 1) / kBK;
   r.first = v0.lo / kBK;
   const int end = v1.pos >= v1.lo ? v1.pos / kBK + 1 : v1.lo / kBK;
   r.n = max(1, r.n_sink + max(0, end - r.first));
@@ -242,7 +247,7 @@ __device__ long long block_scan(long long v, long long* total, long long* buf) {
 }
 
 template <bool PARTS>
-__device__ void make_plan(const ManyArgs& m, int rows) {
+__device__ void make_plan(const ManyArgs<PARTS>& m, int rows) {
   __shared__ long long buf[kPlanThreads / 32];
   __shared__ SeqInfo info[kPlanThreads];
   __shared__ int ends[kPlanThreads];  // row tiles up to and with each sequence of the chunk
@@ -342,7 +347,7 @@ struct ExpandStage {
 // tile of one (sequence, kv head): the keys row by row, the values eight keys of eight dims at a time,
 // which leaves the transposed 16-byte chunks in registers.
 template <int DIM, bool PARTS>
-__global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs m) {
+__global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const ManyArgs<PARTS> m) {
   griddep_launch();
   if (blockIdx.x == 0) {
     make_plan<PARTS>(m, ManyCfg<DIM>::kPairRows);
@@ -362,20 +367,20 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
   int k0, keys, at = b;
   if (is_together<PARTS>(m.a)) {
     if (t >= s.kv / kBK) return;
-    const int shared = (m.a.shared_len[b] + kBK - 1) / kBK;
+    const int shared = (as_part(m.a).shared_len[b] + kBK - 1) / kBK;
     if (t < shared) {
-      k0 = t * kBK, keys = m.a.shared_len[b] - k0, at = kv.rows[b];
+      k0 = t * kBK, keys = as_part(m.a).shared_len[b] - k0, at = as_part(m.a).rows[b];
     } else {
-      int lo = m.a.seq_off[b], hi = m.a.seq_off[b + 1] - 1;  // the last sequence whose own tiles begin at or before it
-      const int x = t - shared + m.a.own_tile[lo];
+      int lo = as_part(m.a).seq_off[b], hi = as_part(m.a).seq_off[b + 1] - 1;  // the last sequence whose own tiles begin at or before it
+      const int x = t - shared + as_part(m.a).own_tile[lo];
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (m.a.own_tile[mid] <= x)
+        if (as_part(m.a).own_tile[mid] <= x)
           lo = mid;
         else
           hi = mid - 1;
       }
-      k0 = (x - m.a.own_tile[lo]) * kBK, keys = m.a.own_len[lo] - k0, k0 += m.a.skip[lo], at = lo;
+      k0 = (x - as_part(m.a).own_tile[lo]) * kBK, keys = as_part(m.a).own_len[lo] - k0, k0 += as_part(m.a).skip[lo], at = lo;
     }
   } else {
     const Range r = seq_range(m, s);
@@ -390,8 +395,12 @@ __global__ void __launch_bounds__(kPlanThreads) attention_expand_kernel(const Ma
       const int k = k0 + 16 * threadIdx.x;
       long long row = -1;
       if (16 * int(threadIdx.x) < keys && (k + 16 > lo || k < m.a.sinks)) {
-        row = is_together<PARTS>(m.a) ? kv_page_row(kv, at, k >> kv.page_bits, m.h0 + h)
-                                      : kv_page_row<PARTS>(kv, b, k >> kv.page_bits, m.h0 + h);
+        if (is_together<PARTS>(m.a)) {
+          row = kv_page_row(kv, at, k >> kv.page_bits, m.h0 + h);
+        } else {
+          const KvTable tb = kv_table<PARTS>(m.a, b);
+          row = kv_page_row_at(kv, tb.entry, tb.n, k >> kv.page_bits, m.h0 + h);
+        }
         missing = row < 0;
         if (row >= 0) row += k & ((1 << kv.page_bits) - 1);
       }
@@ -705,11 +714,11 @@ __device__ __forceinline__ int tiles_before(long long u, long long u0, int n) {
 // units more than key tiles; a part that holds none of the latter is skipped.
 template <bool PARTS>
 struct Cursor {
-  const ManyArgs& m;
+  const ManyArgs<PARTS>& m;
   long long u, end, units;
   int rt, head;
   const int pair = blockIdx.x >> 1, rank = blockIdx.x & 1;
-  __device__ Cursor(const ManyArgs& args) : m(args) {
+  __device__ Cursor(const ManyArgs<PARTS>& args) : m(args) {
     const PairRange r = m.range[pair];
     units = m.plan->units;
     u = r.begin;
@@ -752,7 +761,8 @@ struct Cursor {
 };
 
 // (apart from the descriptor: it takes loads that depend on one another, and is needed only at the segment's end)
-__device__ __forceinline__ PartInfo part_info(const ManyArgs& m, const Segment& s) {
+template <typename M>
+__device__ __forceinline__ PartInfo part_info(const M& m, const Segment& s) {
   const int pair = s.part >> 2;
   PartInfo p{0, pair, pair, 0};
   const long long end = s.u0 + kTileCost + s.n;
@@ -780,7 +790,7 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
 }
 
 template <int DIM, bool PARTS>
-__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs m) {
+__global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyArgs<PARTS> m) {
   using C = ManyCfg<DIM>;
   constexpr int QT = C::QT, UN = C::UN, kRing = C::kRing;
   constexpr bool kOwnP = C::kOwnP, kHalves = C::kHalves, kTurns = C::kTurns;
@@ -806,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
   PartInfo* infos = reinterpret_cast<PartInfo*>(gbase + C::kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
-  const AttnArgs& a = m.a;
+  const Attn<PARTS>& a = m.a;
   WsHeader* hdr = a.kv.hdr;
   const int warp = __shfl_sync(~0u, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // (known to be warp-uniform)
 
@@ -1067,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
       const int r0 = s.row0 + q * 128;
       int pos, minpos, maxpos, low = 0, sink = 0;  // (low, sink: kTogether's)
       if (is_together<PARTS>(a)) {
-        const RowView v = row_view(a, m.b0 + s.seq, s.first + m.token(min(r0 + row, s.last)));
+        const RowView v = row_view(as_part(a), m.b0 + s.seq, s.first + m.token(min(r0 + row, s.last)));
         pos = v.pos, low = v.lo, sink = v.sink;
         minpos = maxpos = 0;
       } else {
@@ -1229,10 +1239,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
         const long long prow = (long long)s.part * C::kRows + r;
         float with = 0.f;  // weight of the row's own part, if this is the shared one
         if (!part && valid && is_shared<PARTS>(a)) {
-          const Join j = join_of(lse, a.own_lse[at]);
+          const Join j = join_of(lse, as_part(a).own_lse[at]);
           inv *= j.shared, with = j.own, lse = j.lse;
         }
-        float* dst32 = part ? m.part_o + prow * DIM : a.own_o + at * DIM;
+        float* dst32 = PARTS && !part ? as_part(a).own_o + at * DIM : m.part_o + prow * DIM;
 #pragma unroll 1
         for (int cc = 0; cc < kOCols; cc += 32) {
           uint32_t o[32];
@@ -1250,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
             if (with != 0.f) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(a.own_o + at * DIM + d + e);
+                const float4 u = *reinterpret_cast<const float4*>(as_part(a).own_o + at * DIM + d + e);
                 const float x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[e + k] = __float_as_uint(__uint_as_float(o[e + k]) * inv + with * x[k]);
@@ -1275,7 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           if (part)
             m.part_lse[prow] = lse;
           else if (valid && own)
-            a.own_lse[at] = lse;
+            as_part(a).own_lse[at] = lse;
           else if (valid && a.lse)
             a.lse[at] = lse * 0.6931471805599453f;
         }
@@ -1321,10 +1331,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
           const bool own = to_own<PARTS>(a, m.b0 + s.seq);
           float my_shared = 1.f, my_own = 0.f, my_lse = tot != 0.f ? top + log2f(tot) : -INFINITY;
           if (has_row && is_shared<PARTS>(a)) {
-            const Join j = join_of(my_lse, a.own_lse[my_at]);
+            const Join j = join_of(my_lse, as_part(a).own_lse[my_at]);
             my_shared = j.shared, my_own = j.own, my_lse = j.lse;
           }
-          if (has_row && own) a.own_lse[my_at] = my_lse;
+          if (has_row && own) as_part(a).own_lse[my_at] = my_lse;
           if (has_row && !own && a.lse) a.lse[my_at] = my_lse * 0.6931471805599453f;
           for (int b0 = 0; warp + kSoftWarps * b0 < s.n_rows; b0 += kBatch) {
             float4 o[kBatch][kV];
@@ -1359,13 +1369,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
               if (!mine || !there) continue;
               if (own) {
 #pragma unroll
-                for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(a.own_o + at * DIM)[lane + 32 * k] = o[b][k];
+                for (int k = 0; k < kV; ++k) reinterpret_cast<float4*>(as_part(a).own_o + at * DIM)[lane + 32 * k] = o[b][k];
                 continue;
               }
               if (with != 0.f)
 #pragma unroll
                 for (int k = 0; k < kV; ++k) {
-                  const float4 u = reinterpret_cast<const float4*>(a.own_o + at * DIM)[lane + 32 * k];
+                  const float4 u = reinterpret_cast<const float4*>(as_part(a).own_o + at * DIM)[lane + 32 * k];
                   o[b][k].x += with * u.x, o[b][k].y += with * u.y, o[b][k].z += with * u.z, o[b][k].w += with * u.w;
                 }
 #pragma unroll
@@ -1395,7 +1405,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 // weights are made. Which parts there are is looked up before the parts are
 // awaited: the ranges are older than the kernel that writes these.
 template <int DIM, bool PARTS>
-__global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs m) {
+__global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyArgs<PARTS> m) {
   constexpr int kRows = ManyCfg<DIM>::kRows, kSplit = ManyCfg<DIM>::kCombineSplit, kBatch = 8;
   __shared__ long long begins[kMaxPairs + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1467,15 +1477,15 @@ __global__ void __launch_bounds__(256) attention_many_combine_kernel(const ManyA
   float lse = sum != 0.f ? top + log2f(sum) : -INFINITY;
   o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
   if (to_own<PARTS>(m.a, t.seq)) {
-    if (mine) *reinterpret_cast<float4*>(m.a.own_o + dst * DIM + d) = o;
-    if (d == 0) m.a.own_lse[dst] = lse;
+    if (mine) *reinterpret_cast<float4*>(as_part(m.a).own_o + dst * DIM + d) = o;
+    if (d == 0) as_part(m.a).own_lse[dst] = lse;
     return;
   }
   if (is_shared<PARTS>(m.a)) {
-    const Join j = join_of(lse, m.a.own_lse[dst]);
+    const Join j = join_of(lse, as_part(m.a).own_lse[dst]);
     lse = j.lse;
     if (mine) {
-      const float4 u = *reinterpret_cast<const float4*>(m.a.own_o + dst * DIM + d);
+      const float4 u = *reinterpret_cast<const float4*>(as_part(m.a).own_o + dst * DIM + d);
       o.x = j.shared * o.x + j.own * u.x, o.y = j.shared * o.y + j.own * u.y;
       o.z = j.shared * o.z + j.own * u.z, o.w = j.shared * o.w + j.own * u.w;
     }
@@ -1558,8 +1568,12 @@ cudaError_t launch_beside(const KvCall& c, const char* name, void (*kernel)(KArg
   return c.launched(name);
 }
 
+// Whether a call's first kernel is launched beside the one before.
+bool starts_beside(const AttnArgs&) { return false; }
+bool starts_beside(const PartArgs& a) { return a.part == PartArgs::kShared; }
+
 template <int DIM, bool PARTS>
-cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
+cudaError_t launch(ManyArgs<PARTS> m, const ManyPlan& p, const KvCall& c) {
   using C = ManyCfg<DIM>;
   if (!ensure_smem_limit(reinterpret_cast<const void*>(&attention_many_kernel<DIM, PARTS>), C::kSmem)) return cudaErrorInvalidValue;
   for (m.b0 = 0; m.b0 < m.a.kv.n_seqs; m.b0 += p.nb)
@@ -1569,7 +1583,7 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
       const long long grid = 1 + 2ll * m.nb * m.nh * p.tiles_max;
       if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
       // the shared part's first expansion runs beside the own part's last kernel; it touches nothing of that
-      if (PARTS && m.a.part == AttnArgs::kShared && m.b0 == 0 && m.h0 == 0) {
+      if (starts_beside(m.a) && m.b0 == 0 && m.h0 == 0) {
         if (cudaError_t e = launch_beside(c, "attention_expand", attention_expand_kernel<DIM, PARTS>, dim3(unsigned(grid)),
                                           kPlanThreads, 0, 1, m))
           return e;
@@ -1589,19 +1603,16 @@ cudaError_t launch(ManyArgs m, const ManyPlan& p, const KvCall& c) {
 }
 
 template <bool PARTS>
-cudaError_t launch_as(const ManyArgs& m, const ManyPlan& p, const KvCall& c) {
+cudaError_t launch_as(const ManyArgs<PARTS>& m, const ManyPlan& p, const KvCall& c) {
   const int dim = m.a.kv.dim;
   return dim == 64 ? launch<64, PARTS>(m, p, c) : dim == 128 ? launch<128, PARTS>(m, p, c) : launch<256, PARTS>(m, p, c);
 }
 
-}  // namespace
-
-size_t attention_many_workspace(const AttnArgs& a) { return a.kv.n_seqs > 0 ? plan(a).total : 0; }
-
-cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCall& c) {
+template <bool PARTS>
+cudaError_t start(const Attn<PARTS>& a, int max_few, void* ws, const KvCall& c) {
   const ManyPlan p = plan(a);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  ManyArgs m{};
+  ManyArgs<PARTS> m{};
   m.a = a;
   m.max_few = max_few;
   m.tiles_max = p.tiles_max;
@@ -1626,7 +1637,16 @@ cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCal
   m.part_o = reinterpret_cast<float*>(w + p.part_o);
   m.part_lse = reinterpret_cast<float*>(w + p.part_lse);
   m.inv_group = ((1ull << 32) + a.group - 1) / a.group;
-  return a.part == AttnArgs::kWhole ? launch_as<false>(m, p, c) : launch_as<true>(m, p, c);
+  return launch_as<PARTS>(m, p, c);
+}
+
+}  // namespace
+
+size_t attention_many_workspace(const AttnArgs& a) { return a.kv.n_seqs > 0 ? plan(a).total : 0; }
+
+cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCall& c) { return start<false>(a, max_few, ws, c); }
+cudaError_t attention_many_part(const PartArgs& a, int max_few, void* ws, const KvCall& c) {
+  return start<true>(a, max_few, ws, c);
 }
 
 }  // namespace moe

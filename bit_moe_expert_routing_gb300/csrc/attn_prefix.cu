@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
 long long together_rows(int dim) { return dim == 64 ? 192 : 64; }
 
 struct PrefixPlan {
-  AttnArgs own, shared, together;
+  PartArgs own, shared, together;
   int few_own, few_shared;
   bool is_together;
   size_t group_off, group_len, group_row, own_len, skip, shares, lse, o, attend_own, attend_shared, total;
@@ -239,13 +239,13 @@ bool shares(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x, 
 }
 
 PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
-  PrefixPlan p{a, a, a};
+  PrefixPlan p{PartArgs{a}, PartArgs{a}, PartArgs{a}};
   p.own.kv.max_kv = std::min(x.max_own, a.kv.max_kv);
-  p.own.part = AttnArgs::kOwn;
+  p.own.part = PartArgs::kOwn;
   p.shared.kv.n_seqs = x.n_groups;
   p.shared.kv.max_new = std::min(x.max_tokens, a.kv.n_tokens);
   p.shared.kv.max_kv = x.max_len;
-  p.shared.part = AttnArgs::kShared;
+  p.shared.part = PartArgs::kShared;
   p.few_own = few_rows(p.own, opt);
   p.few_shared = few_rows(p.shared, opt);
   size_t o = 0;
@@ -268,7 +268,7 @@ PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
   // The same for the whole of it in one go, if it has a place in that: what is there for the parts is not needed then.
   const long long tile = kKeyTile, rows = (long long)a.kv.n_tokens * a.group;
   const long long tiles = (x.max_len + tile - 1) / tile + a.kv.n_seqs * ((p.own.kv.max_kv + tile - 1) / tile);
-  p.together.part = AttnArgs::kTogether;
+  p.together.part = PartArgs::kTogether;
   p.together.kv.n_seqs = x.n_groups;
   p.together.kv.max_new = a.kv.n_tokens;
   p.together.kv.max_kv = int(std::min(tiles * tile, 1ll << 24));
@@ -290,6 +290,14 @@ PrefixPlan plan(const AttnArgs& a, const moe_kv_prefix& x, const Options& opt) {
 size_t bytes_for(const AttnArgs& a, const moe_attention& at, const moe_kv_prefix& x, const Options& opt) {
   const size_t whole = workspace_bytes_for(a, few_rows(a, opt));
   return at.window ? whole : std::max(whole, plan(a, x, opt).total);
+}
+
+// A part of the attention, as attend(); the shared part's first kernel is launched beside the own part's last.
+cudaError_t attend_part(const PartArgs& a, int few, void* workspace, const KvCall& c) {
+  const bool many = any_many(a, few);
+  if (many)
+    if (cudaError_t e = attention_many_part(a, few, static_cast<char*>(workspace) + few_bytes(a, few), c)) return e;
+  return any_few(a, few) ? attention_few_part(a, few, workspace, many || a.part == PartArgs::kShared, c) : cudaSuccess;
 }
 
 }  // namespace
@@ -351,10 +359,10 @@ moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_
       args);
   if (cudaError_t e = c.launched("attention_prefix_plan")) return status_of(e);
   if (p.is_together) {
-    AttnArgs& t = p.together;
+    PartArgs& t = p.together;
     t.kv.q_off = args.group_off;
     t.kv.kv_len = args.group_len;
-    t.kv.rows = args.group_row;
+    t.rows = args.group_row;
     t.shares = args.shares;
     t.seq_off = args.seqs;
     t.step_off = a.q_off;
@@ -362,20 +370,20 @@ moe_status moe_attention_prefix_forward(const moe_kv_cache* cache, const moe_kv_
     t.own_len = args.own_len;
     t.own_tile = args.own_tile;
     t.shared_len = args.shared_len;
-    return status_of(attention_many(t, 0, w + p.attend_together, c));
+    return status_of(attention_many_part(t, 0, w + p.attend_together, c));
   }
-  for (AttnArgs* part : {&p.own, &p.shared}) {
+  for (PartArgs* part : {&p.own, &p.shared}) {
     part->own_o = reinterpret_cast<float*>(w + p.o);
     part->own_lse = reinterpret_cast<float*>(w + p.lse);
     part->shares = args.shares;
   }
   p.own.kv.kv_len = args.own_len;
-  p.own.kv.skip = args.skip;
+  p.own.skip = args.skip;
   p.shared.kv.q_off = args.group_off;
   p.shared.kv.kv_len = args.group_len;
-  p.shared.kv.rows = args.group_row;
-  if (cudaError_t e = attend(p.own, p.few_own, w + p.attend_own, c)) return status_of(e);
-  return status_of(attend(p.shared, p.few_shared, w + p.attend_shared, c));
+  p.shared.rows = args.group_row;
+  if (cudaError_t e = attend_part(p.own, p.few_own, w + p.attend_own, c)) return status_of(e);
+  return status_of(attend_part(p.shared, p.few_shared, w + p.attend_shared, c));
 }
 
 }  // extern "C"

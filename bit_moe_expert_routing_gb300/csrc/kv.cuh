@@ -1,6 +1,8 @@
 // Shared by the kernels of the 4-bit key/value cache and its attention.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -20,38 +22,24 @@ struct KvArgs {
   int table_stride;
   int n_seqs, n_tokens, max_new, max_kv;
   int n_pages, page_bits, kv_heads, dim;
-  // A part of every sequence (set by the kernels' callers within the library):
-  const int32_t* rows;  // [n_seqs] its row of the table; NULL: its own number
-  const int32_t* skip;  // [n_seqs] positions before the part's first, whole pages; NULL: none
 };
-
-// A sequence's entries of the table, from its position 0 on.
-struct KvTable {
-  const int32_t* entry;
-  int n;
-};
-template <bool PARTS = false>
-__device__ __forceinline__ KvTable kv_table(const KvArgs& a, int seq) {
-  if (!PARTS) return KvTable{a.table + (long long)seq * a.table_stride, a.table_stride};
-  const int row = a.rows ? a.rows[seq] : seq, before = a.skip ? a.skip[seq] >> a.page_bits : 0;
-  return KvTable{a.table + (long long)row * a.table_stride + before, a.table_stride - before};
-}
 
 // Device-side checks recorded in the cache's status word (its detail).
 constexpr int kKvBadPage = 200, kKvBadNumber = 201, kKvBadBatch = 202;
 
-// First page row (row = one head of one slot) of a sequence's page `j`, or -1
-// (recorded) when the table has no valid entry for it.
-template <bool PARTS = false>
-__device__ __forceinline__ long long kv_page_row(const KvArgs& a, int seq, int j, int head) {
+// First page row (row = one head of one slot) of page `j` of a sequence whose
+// table entries are entry[0 .. n), or -1 (recorded) when there is no valid one.
+__device__ __forceinline__ long long kv_page_row_at(const KvArgs& a, const int32_t* entry, int n, int j, int head) {
   int p = -1;
-  const KvTable t = kv_table<PARTS>(a, seq);
-  if (j < t.n) p = t.entry[j];
+  if (j < n) p = entry[j];
   if (p < 0 || p >= a.n_pages) {
     report(a.hdr, MOE_ERR_DEVICE_CHECK, kKvBadPage);
     return -1;
   }
   return ((long long)p * a.kv_heads + head) << a.page_bits;
+}
+__device__ __forceinline__ long long kv_page_row(const KvArgs& a, int seq, int j, int head) {
+  return kv_page_row_at(a, a.table + (long long)seq * a.table_stride, a.table_stride, j, head);
 }
 
 // Sequence of step token `i` (0 <= i < n_tokens): the last one whose first
@@ -109,35 +97,50 @@ struct AttnArgs {
   int heads, group;  // query heads, query heads per kv head
   int window, sinks;
   float scale;
-  // Attention in two parts. kOwn: causal as ever, over the positions from
-  // kv.skip on; outputs of sequences that skip any go to own_o, own_lse (fp32,
-  // the lse in base 2). kShared, behind it: every row sees all positions, and
-  // the rows of tokens that `shares` marks are joined with what kOwn left and
-  // written; no others are.
-  //
-  // kTogether: groups as sequences in one go, over the positions of all of a
-  // group's sequences laid out one behind the other: the shared ones, then each
-  // sequence's own, every part beginning on a key tile of the many-row kernels
-  // (the only ones that take it). A row sees the first skip[its sequence], and
-  // its sequence's own up to itself.
-  enum Part { kWhole, kOwn, kShared, kTogether };
+};
+
+// A part of the attention of sequences that share their first positions.
+//
+// kOwn: causal as ever, over the positions from skip on; outputs of sequences
+// that skip any go to own_o, own_lse (fp32, the lse in base 2). kShared, behind
+// it: every row sees all positions, and the rows of tokens that `shares` marks
+// are joined with what kOwn left and written; no others are.
+//
+// kTogether: groups as sequences in one go, over the positions of all of a
+// group's sequences laid out one behind the other: the shared ones, then each
+// sequence's own, every part beginning on a key tile of the many-row kernels
+// (the only ones that take it). A row sees the first skip[its sequence], and
+// its sequence's own up to itself.
+struct PartArgs : AttnArgs {
+  enum Part { kOwn, kShared, kTogether };
   int part;
+  const int32_t* skip;    // [sequences] shared positions, whole pages; kShared: NULL
+  const int32_t* rows;    // [groups] their row of the table; kOwn: NULL
   float* own_o;           // [n_tokens, heads, dim]
   float* own_lse;         // [n_tokens, heads]
   const uint8_t* shares;  // [n_tokens]; kTogether: whether the token is to be written
-  // kTogether, besides kv.rows:
+  // kTogether:
   const int32_t* seq_off;     // [groups + 1] sequences of each group
   const int32_t* step_off;    // [sequences + 1] step tokens of each sequence
-  const int32_t* skip;        // [sequences] shared positions
-  const int32_t* own_len;     // [sequences] positions past them
+  const int32_t* own_len;     // [sequences] positions past the shared ones
   const int32_t* own_tile;    // [sequences + 1] key tiles of the own positions of the sequences before
   const int32_t* shared_len;  // [groups] shared positions
 };
 
-// (The kernels are compiled for whole calls and for PARTS apart: what the latter need cost the former registers.)
+// The kernels are compiled for whole calls and for PARTS apart: what the latter
+// need cost the former registers, and their longer arguments 0.1 to 0.5 us.
+template <bool PARTS>
+using Attn = std::conditional_t<PARTS, PartArgs, AttnArgs>;
+// (of the kernels compiled for PARTS)
+__device__ __forceinline__ const PartArgs& as_part(const AttnArgs& a) { return static_cast<const PartArgs&>(a); }
+
 template <bool PARTS>
 __device__ __forceinline__ bool is_shared(const AttnArgs& a) {
-  return PARTS && a.part == AttnArgs::kShared;
+  return PARTS && as_part(a).part == PartArgs::kShared;
+}
+template <bool PARTS>
+__device__ __forceinline__ bool is_together(const AttnArgs& a) {
+  return PARTS && as_part(a).part == PartArgs::kTogether;
 }
 // Position of a sequence's step token 0, and of its step token t.
 template <bool PARTS>
@@ -151,16 +154,26 @@ __device__ __forceinline__ int pos_of(const AttnArgs& a, int base, int t) {
 // Whether a sequence's outputs are to be joined with a shared part.
 template <bool PARTS>
 __device__ __forceinline__ bool to_own(const AttnArgs& a, int seq) {
-  return PARTS && a.part == AttnArgs::kOwn && a.kv.skip[seq] > 0;
+  return PARTS && as_part(a).part == PartArgs::kOwn && as_part(a).skip[seq] > 0;
 }
 // Whether a step token's rows are written.
 template <bool PARTS>
 __device__ __forceinline__ bool is_written(const AttnArgs& a, int token) {
-  return !PARTS || a.part < AttnArgs::kShared || a.shares[token];
+  return !PARTS || as_part(a).part < PartArgs::kShared || as_part(a).shares[token];
 }
+// A sequence's entries of the table, from its position 0 on (kOwn, kShared, and whole calls).
+struct KvTable {
+  const int32_t* entry;
+  int n;
+};
 template <bool PARTS>
-__device__ __forceinline__ bool is_together(const AttnArgs& a) {
-  return PARTS && a.part == AttnArgs::kTogether;
+__device__ __forceinline__ KvTable kv_table(const AttnArgs& a, int seq) {
+  int row = seq, before = 0;
+  if (PARTS) {
+    if (as_part(a).rows) row = as_part(a).rows[seq];
+    if (as_part(a).skip) before = as_part(a).skip[seq] >> a.kv.page_bits;
+  }
+  return KvTable{a.kv.table + (long long)row * a.kv.table_stride + before, a.kv.table_stride - before};
 }
 // Weights of a row's two parts, both normalised, in the whole, from their log-sum-exps (base 2; -inf: it saw nothing).
 struct Join {
@@ -185,5 +198,8 @@ cudaError_t attention_few(const AttnArgs& a, int max_rows, void* ws, bool beside
 // Sequences with more rows than that.
 size_t attention_many_workspace(const AttnArgs& a);
 cudaError_t attention_many(const AttnArgs& a, int max_few, void* ws, const KvCall& c);
+// The same for a part. (kShared's first kernel is launched beside kOwn's last.)
+cudaError_t attention_few_part(const PartArgs& a, int max_rows, void* ws, bool beside, const KvCall& c);
+cudaError_t attention_many_part(const PartArgs& a, int max_few, void* ws, const KvCall& c);
 
 }  // namespace moe

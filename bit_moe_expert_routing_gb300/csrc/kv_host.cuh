@@ -130,13 +130,12 @@ inline KvCall begin_call(void* stream, const Options& opt = options_snapshot()) 
   return c;
 }
 
-// The attention of a step: of its sequences of many rows, then of those of few. (A shared part is launched beside the own
-// part's last kernel.)
+// The attention of a step: of its sequences of many rows, then of those of few, beside the last of the former.
 inline cudaError_t attend(const AttnArgs& a, int few, void* workspace, const KvCall& c) {
   const bool many = any_many(a, few);
   if (many)
     if (cudaError_t e = attention_many(a, few, static_cast<char*>(workspace) + few_bytes(a, few), c)) return e;
-  return any_few(a, few) ? attention_few(a, few, workspace, many || a.part == AttnArgs::kShared, c) : cudaSuccess;
+  return any_few(a, few) ? attention_few(a, few, workspace, many, c) : cudaSuccess;
 }
 
 }  // namespace
