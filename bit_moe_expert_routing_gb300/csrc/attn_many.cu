@@ -1364,8 +1364,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_many_kernel(const ManyA
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
               const long long at = __shfl_sync(~0u, my_at, (b0 + b) & 31);
-              const float with = __shfl_sync(~0u, my_own, (b0 + b) & 31);
-              const bool there = __shfl_sync(~0u, int(has_row), (b0 + b) & 31);
+              const float with = PARTS ? __shfl_sync(~0u, my_own, (b0 + b) & 31) : 0.f;
+              const bool there = PARTS ? __shfl_sync(~0u, int(has_row), (b0 + b) & 31) : warp + kSoftWarps * (b0 + b) < s.n_rows;
               if (!mine || !there) continue;
               if (own) {
 #pragma unroll
