@@ -25,6 +25,13 @@
 // them, as it does with a window and sinks. A tile of rows then meets the own
 // positions of its few sequences besides the shared ones, and nothing has to be
 // joined.
+//
+// Measured, replayed: 64 sequences of one token behind 32768 shared positions, 16
+// heads over 2 of 256 dims, 63 us (201 without sharing, although the shared pages
+// stay in L2): the plan 3, the own part beside the expansion 23, products 28, join
+// 9. In one go: a dozen questions on 16001 positions, heads of 64, 194 us (278
+// without sharing, 214 in parts); 8 tails of 12000 and 20001 positions, heads of
+// 256, 217 to 223 us, tensor cores 81% (300, 254).
 #include "kv_host.cuh"
 
 namespace moe {

@@ -10,6 +10,13 @@
 // registers. A thread stays with one token and steps through its heads: the
 // angles are made once per token, by all of the CTA, and then kept in
 // registers, as is the token's place in the cache.
+//
+// Measured, replayed: 14593 tokens of 32 heads over 8 of 128 dims 67 us, 316 MB,
+// 4.7 TB/s (queries alone 47, 5.1 TB/s): 38 million warp instructions, half of
+// them the quantisation's, at half of the issue rate, since 124 registers leave
+// 15 warps to an SM and a thread's steps stand in line. 4096 tokens of 16 over 2
+// of 256 dims 16.7 us, 4.66 TB/s. 8 tokens 4.6 us: the launch and the chain token,
+// sequence, length, page, angles, head.
 #include "kv_host.cuh"
 #include "kv_quant.cuh"
 

@@ -75,7 +75,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // that starts early can rely on everything before its predecessor; but for
 // the down GEMM, whose dependent waits before it reads anything, and the
 // few-row attention kernel, which waits at its end and whose dependent relies
-// until its own wait on what was there before the call alone. Whoever is
+// until its own wait on what was there before the call alone; and of the
+// attention in two parts the own part's join and the shared part's expansion,
+// whose dependents rely until their waits on what the plan kernel left, which
+// the part's first kernel was launched behind in the ordinary way. Whoever is
 // launched this way waits before its last thread leaves, whether it reads
 // anything or not: what follows it on the stream is ordered behind it, and
 // only through that wait behind its predecessor.
