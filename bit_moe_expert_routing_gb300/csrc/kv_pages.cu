@@ -180,7 +180,8 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
     const bool ok = kv >= 0 && kv <= s.max_kv && n >= 0 && n <= s.max_new && need <= a.columns;
     if (!ok) report(a.hdr, MOE_ERR_DEVICE_CHECK, kPageBad);
     need_s[b] = ok ? need : -1;
-    first_s[b] = ok && n > 0 ? max(kv - n, 0) >> a.page_bits : a.columns;
+    // (of one that is not to be touched, too: what its tokens may be written to. Offsets out of order may lead anywhere)
+    first_s[b] = n == 0 || kv < 0 ? a.columns : n < 0 ? 0 : min((kv > n ? kv - n : 0) >> a.page_bits, a.columns);
     held_s[b] = held;
   }
   __syncthreads();
@@ -219,8 +220,15 @@ __device__ __forceinline__ void plan_step(const PagesArgs& a, const StepArgs& s)
   // what every sequence wants: pages that it shares and writes, and pages that it has not
   for (int b0 = mine; b0 < a.n_seqs; b0 += kPlanWarps * kAbreast)
     each(b0, [&](int i, int b, int need, int first, int held) {
-      const int32_t* row = a.table + (long long)b * a.columns;
+      int32_t* row = a.table + (long long)b * a.columns;
       int n = 0;
+      if (need < 0)  // what others hold, too, and it might be written leaves it
+        for (int j = first + lane; j < held; j += 32) {
+          const int p = row[j];
+          if (!is_page(a, p) || get(snap + p) <= 1) continue;
+          row[j] = -1;
+          atomicAdd(a.refs + p, -1);
+        }
       for (int j = first + lane; j < min(need, held); j += 32) {
         const int p = b0 == mine && j < first + 32 ? kept[i] : row[j];
         n += is_page(a, p) && get(snap + p) > 1;

@@ -116,6 +116,12 @@ class Model:
                 self.held[b] = min(self.held[b], -(-k // self.size))
         free = [p for p in range(len(self.refs)) if self.refs[p] == 0]
         shared = self.refs > 1
+        for b, (k, n) in enumerate(zip(kv, new)):
+            if not ok[b] and n and k >= 0:  # what it might write leaves it, if others hold it
+                for j in range(max(k - n, 0) // self.size if n > 0 else 0, self.held[b]):
+                    if self.table[b, j] >= 0 and shared[self.table[b, j]]:
+                        self.refs[self.table[b, j]] -= 1
+                        self.table[b, j] = -1
         old, words = self.table.copy(), self.words.copy()
         out = False
         for b, (k, n) in enumerate(zip(kv, new)):
@@ -317,6 +323,31 @@ def test_wishes_past_32_bits():
     pages.update(pages.batch(q_off, kv, 0, 0, 2 ** 24))
     pages.check()
     assert pages.table[:7, 0].tolist() == list(range(7)) and pages.table[-1, 0] == 7
+
+
+@pytest.mark.gpu
+def test_a_step_past_its_bounds_writes_into_no_other_sequence():
+    """Sequences that update() does not touch may still be appended to: what they share leaves them from there on."""
+    cs = caches(1, 40, 16, 1, 64)
+    pages, m = moe.KVPages(cs, 5, 8), Model(40, 16, 5, 8)
+    kv, new = [100, 0, 0, 0, 0], [100, 0, 0, 0, 0]
+    pages.update(step(pages, kv, new)), m.update(kv, new, 100, 128)
+    pages.fork(i32(0, 0, 0, 0), i32(1, 2, 3, 4)), m.fork([0] * 4, [1, 2, 3, 4])
+    check_same(pages, m)
+    # 1: more tokens than max_new; 2: past max_kv; 3: past the table; 4: as it should be
+    kv, new = [100, 103, 113, 130, 101], [0, 3, 20, 1, 1]
+    b = step(pages, kv, new, max_new=2, max_kv=110)
+    pages.update(b), m.update(kv, new, 2, 110)
+    assert m.bad and m.table[0].tolist() == list(range(7)) + [-1] and m.table[1, 5:].tolist() == [5, -1, -1]
+    assert m.table[2, 4:].tolist() == [4, -1, -1, -1] and m.table[3, 6] == 6 and m.table[4, 6] == 7
+    check_same(pages, m)
+    before = [t[:7].clone() for t in (cs[0].k_codes, cs[0].k_scales, cs[0].v_codes)]
+    x = torch.randn(b.n_tokens, 1, 64, device="cuda").bfloat16()
+    cs[0].append(x, x, b)
+    for t, was in zip((cs[0].k_codes, cs[0].k_scales, cs[0].v_codes), before):
+        assert torch.equal(t[:7].view(torch.int16), was.view(torch.int16))
+    with pytest.raises(moe.MoEError):
+        cs[0].check()
 
 
 @pytest.mark.gpu

@@ -199,6 +199,33 @@ def test_long_prefixes_and_many_rows():
 
 
 @pytest.mark.gpu
+def test_several_passes():
+    """More expanded keys than one pass has room for, group by group and head by head; against the same without sharing."""
+    dim, kvh, page, shared, seqs, new = 256, 8, 256, 131072, 8, 70
+    pages = 4 * shared // page
+    cache = moe.KVCache.empty(pages + 2 * seqs, page, kvh, dim)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for t in (cache.k_codes, cache.v_codes):
+        t.random_(generator=g)
+    for name, scale in (("k", 2.0 ** -6), ("v", 2.0 ** -3)):  # values of +-1: a score of a few units
+        getattr(cache, name + "_scales").fill_(scale)
+        getattr(cache, name + "_biases").fill_(-8 * scale)
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.cat([torch.arange(pages).view(4, -1).repeat_interleave(2, 0), pages + torch.arange(2 * seqs).view(seqs, 2)], 1)
+    batch = moe.KVBatch(i([new * b for b in range(seqs + 1)]), i([shared + new + 31 * b for b in range(seqs)]),
+                        table.int().cuda().contiguous(), seqs * new, new, shared + 512)
+    q = rows(seqs * new, 8, dim)
+    prefix = moe.KVPrefix(i([0, 2, 4, 6, 8]), i([shared] * 4), 2 * new, shared, 512)
+    ref, ref_lse = cache.attention(q, batch, lse=True)
+    out, lse = cache.attention(q, batch, lse=True, prefix=prefix)
+    cache.check()
+    # both are within 2^-8 (|o| + sum p |v|) of the value, |v| at most 1
+    assert ((out.double() - ref.double()).abs() <= 2.0 ** -7 * (ref.double().abs() + 1)).all()
+    torch.testing.assert_close(lse, ref_lse, atol=2.0 ** -15, rtol=2.0 ** -17)
+    assert ref.float().std() > 0.001
+
+
+@pytest.mark.gpu
 def test_a_window_reads_near_positions_only(each_path):
     batch = Shared([(300, [(2, 20), (1, 1)])], 16)
     cache = junk_cache(moe, batch.n_pages, 16, 2, 128)
