@@ -7,15 +7,15 @@
 // key's or value's read (2) and stored (0.5625). So a thread holds sixteen
 // elements of a head, the two chunks of eight whose elements are turned
 // together, and nothing but a norm's sum and a key's re-ordering leaves its
-// registers. A thread stays with one token and steps through its heads: the
-// angles are made once per token, by all of the CTA, and then kept in
-// registers, as is the token's place in the cache.
+// registers. A thread stays with one token and steps through its heads; what
+// the elements are multiplied with (weights times cosines and sines) is made
+// once per token, by all of the CTA, in shared memory.
 //
-// Measured, replayed: 14593 tokens of 32 heads over 8 of 128 dims 67 us, 316 MB,
-// 4.7 TB/s (queries alone 47, 5.1 TB/s): 38 million warp instructions, half of
-// them the quantisation's, at half of the issue rate, since 124 registers leave
-// 15 warps to an SM and a thread's steps stand in line. 4096 tokens of 16 over 2
-// of 256 dims 16.7 us, 4.66 TB/s. 8 tokens 4.6 us: the launch and the chain token,
+// Measured, replayed: 14593 tokens of 32 heads over 8 of 128 dims 61.5 us, 316 MB,
+// 5.1 TB/s: some 40 million warp instructions, half of them the quantisation's,
+// and a thread's steps stand in line; what helps is warps, 24 to an SM. (With
+// the factors in registers, 15 warps, 67 us.) 4096 tokens of 16 over 2 of 256 dims
+// 18 us, 4.3 TB/s, one wave. 8 tokens 4.2 us: the launch and the chain token,
 // sequence, length, page, angles, head.
 #include "kv_host.cuh"
 #include "kv_quant.cuh"
@@ -23,8 +23,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;  // (CTAs of 256 threads are 4% slower, of 64 the same)
-constexpr int kBatch = 4;  // query heads of a thread whose loads are in flight together
+constexpr int kThreads = 64;  // (CTAs of 128 threads are the same, of 256 2 to 9% slower)
+constexpr int kBatch = 2;     // query heads of a thread whose loads are in flight together (four, with ten CTAs to an SM: 66.8 us)
 
 struct RotaryArgs {
   KvArgs kv;
@@ -104,31 +104,19 @@ __device__ __forceinline__ float inverse_norm(const Wide& x, float eps, unsigned
 // (1 without a norm) times cosines and sines of its eight angles, where it has
 // any. For chunks p and q of elements that are turned together:
 //   p' = p pc - q qs,  q' = q qc + p ps
+// In shared memory, for each token and for queries and keys: float4 j of lane w
+// is (pc, qc) of its angles 2 j and 2 j + 1, float4 4 + j (ps, -qs). (In
+// registers they leave room for two thirds of the warps.)
+template <int W>
 struct Turn {
-  float2 pc[4], qc[4], ps[4], qs[4];
+  const float4* at;  // this lane's
+  bool on;           // it turns its elements; else ps and qs are not there
+  __device__ __forceinline__ float4 operator[](int j) const { return at[j * W]; }
 };
-template <bool INTERLEAVED>
-__device__ __forceinline__ Turn turn_of(const Wide& weight, const float2 (&cos)[4], const float2 (&sin)[4]) {
-  Turn t;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 p, q;
-    if (INTERLEAVED) {  // angles 2 j, 2 j + 1 turn the pairs of elements 4 j .. 4 j + 3
-      const float2 u = weight.v[j / 2][2 * (j % 2)], v = weight.v[j / 2][2 * (j % 2) + 1];
-      p = make_float2(u.x, v.x), q = make_float2(u.y, v.y);
-    } else {
-      p = weight.v[0][j], q = weight.v[1][j];
-    }
-    t.pc[j] = mul(p, cos[j]), t.ps[j] = mul(p, sin[j]);
-    t.qc[j] = mul(q, cos[j]), t.qs[j] = mul(q, make_float2(-sin[j].x, -sin[j].y));
-  }
-  return t;
-}
 
-// Norms (if asked) and turns a head's elements. `on`: this thread's are turned; else they meet their weights alone, in
-// t.pc and t.qc.
+// Norms (if asked) and turns a head's elements.
 template <int W, bool INTERLEAVED>
-__device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, float eps, bool on, const Turn& t, unsigned lanes) {
+__device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, float eps, const Turn<W>& t, unsigned lanes) {
   Wide y = widen(x);
   if (norm) {
     const float2 inv = both(inverse_norm<W>(y, eps, lanes));
@@ -141,11 +129,14 @@ __device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, float eps, 
   for (int j = 0; j < 4; ++j) {
     float2 &u = INTERLEAVED ? y.v[j / 2][2 * (j % 2)] : y.v[0][j], &v = INTERLEAVED ? y.v[j / 2][2 * (j % 2) + 1] : y.v[1][j];
     const float2 p = INTERLEAVED ? make_float2(u.x, v.x) : u, q = INTERLEAVED ? make_float2(u.y, v.y) : v;
+    const float4 c = t[j];
+    const float2 pc = make_float2(c.x, c.y), qc = make_float2(c.z, c.w);
     float2 a, b;
-    if (on) {
-      a = fma(p, t.pc[j], mul(q, t.qs[j])), b = fma(q, t.qc[j], mul(p, t.ps[j]));
+    if (t.on) {
+      const float4 s = t[4 + j];
+      a = fma(p, pc, mul(q, make_float2(s.z, s.w))), b = fma(q, qc, mul(p, make_float2(s.x, s.y)));
     } else {
-      a = mul(p, t.pc[j]), b = mul(q, t.qc[j]);
+      a = mul(p, pc), b = mul(q, qc);
     }
     u = INTERLEAVED ? make_float2(a.x, b.x) : a;
     v = INTERLEAVED ? make_float2(a.y, b.y) : b;
@@ -160,9 +151,9 @@ __device__ __forceinline__ Chunks turned(const Chunks& x, bool norm, float eps, 
 // CTA (tokens, part of their heads): W threads to a head, 2^lanes_log heads of
 // a token side by side.
 template <int DIM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const RotaryArgs r) {
+__global__ void __launch_bounds__(kThreads, 768 / kThreads) kv_append_rotary_kernel(const RotaryArgs r) {
   constexpr int W = DIM / 16, kRows = kThreads / W;
-  extern __shared__ float4 cs[];  // [token][4][pairs]: cosines and sines of a lane's angles 2 j, 2 j + 1
+  extern __shared__ float4 co[];  // [token][queries, keys][8][W]: see Turn
   __shared__ int pos_s[kRows], page_s[kRows];
   const KvArgs& a = r.kv;
   const int tokens = kRows >> r.lanes_log, side = 1 << r.lanes_log;
@@ -205,49 +196,47 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const Rot
     page_s[threadIdx.x] = pg;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < n * r.half; e += kThreads) {
-    const int tt = e / r.half, f = e - tt * r.half;
-    int p = pos_s[tt];
-    if (r.positions) {
-      const int ax = r.axis ? r.axis[f] : 0;
-      p = r.positions[(long long)(ax < r.axes ? ax : 0) * a.n_tokens + i0 + tt];
+  for (int e = threadIdx.x; e < n * 4 * W; e += kThreads) {
+    const int lw = e % W, j = e / W % 4, tt = e / (4 * W), f = 8 * lw + 2 * j;
+    float2 cs[2] = {make_float2(1.f, 0.f), make_float2(1.f, 0.f)};
+    if (lw < pairs)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int p = pos_s[tt];
+        if (r.positions) {
+          const int ax = r.axis ? r.axis[f + k] : 0;
+          p = r.positions[(long long)(ax < r.axes ? ax : 0) * a.n_tokens + i0 + tt];
+        }
+        cs[k] = turned_by(r.turns[f + k], p);
+      }
+    const float2 c = make_float2(cs[0].x, cs[1].x), sn = make_float2(cs[0].y, cs[1].y);
+    // the elements that these angles turn
+    const bool halves = !INTERLEAVED && lw < pairs;
+    const int p0 = INTERLEAVED ? 16 * lw + 4 * j : halves ? 8 * lw + 2 * j : 16 * lw + 2 * j;
+    const int p1 = INTERLEAVED ? p0 + 2 : p0 + 1, q0 = INTERLEAVED ? p0 + 1 : halves ? p0 + r.half : p0 + 8;
+    const int q1 = INTERLEAVED ? p0 + 3 : q0 + 1;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const float* wt = r.weight[kind];
+      const float2 wp = wt ? make_float2(wt[p0], wt[p1]) : both(1.f), wq = wt ? make_float2(wt[q0], wt[q1]) : both(1.f);
+      const float2 pc = mul(wp, c), qc = mul(wq, c), ps = mul(wp, sn), qs = mul(wq, make_float2(-sn.x, -sn.y));
+      float4* at = co + ((tt * 2 + kind) * 8 + j) * W + lw;
+      at[0] = make_float4(pc.x, pc.y, qc.x, qc.y);
+      at[4 * W] = make_float4(ps.x, ps.y, qs.x, qs.y);
     }
-    // lane f / 8's angle f % 8: its float4 (f % 8) / 2, so that neighbouring lanes read neighbouring words
-    const float2 v = turned_by(r.turns[f], p);
-    float* at = reinterpret_cast<float*>(cs + (tt * 4 + (f % 8) / 2) * pairs + f / 8) + (f & 1);
-    at[0] = v.x;
-    at[2] = v.y;
   }
   __syncthreads();
   if (t >= n) return;
-  float2 cos[4], sin[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    cos[j] = both(1.f), sin[j] = both(0.f);
-    if (on) {
-      const float4 v = cs[(t * 4 + j) * pairs + w];
-      cos[j] = make_float2(v.x, v.y);
-      sin[j] = make_float2(v.z, v.w);
-    }
-  }
-  auto weights = [&](const float* p) {
-    Wide y;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y.v[k][j] = p ? *reinterpret_cast<const float2*>(p + 8 * (k ? c1 : c0) + 2 * j) : both(1.f);
-    return y;
-  };
 
   {
-    const Turn turn = turn_of<INTERLEAVED>(weights(r.weight[0]), cos, sin);
+    const Turn<W> turn{co + t * 16 * W + w, on};
     uint16_t* dst = r.q_out + (long long)i * r.heads * DIM;
     for (int h = h0 + g; h < q_end; h += kBatch * side) {
       if (h != h0 + g) load(h);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (h + u * side >= q_end) break;
-        const Chunks y = turned<W, INTERLEAVED>(x[u], r.weight[0], r.eps, on, turn, lanes);
+        const Chunks y = turned<W, INTERLEAVED>(x[u], r.weight[0], r.eps, turn, lanes);
         uint16_t* p = dst + (h + u * side) * DIM;
         *reinterpret_cast<uint4*>(p + 8 * c0) = y.c[0];
         *reinterpret_cast<uint4*>(p + 8 * c1) = y.c[1];
@@ -258,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const Rot
   const int page = page_s[t], slot = pos_s[t] & ((1 << a.page_bits) - 1);
   if (page < 0) return;
   bool bad = false;
-  const Turn turn = turn_of<INTERLEAVED>(weights(r.weight[1]), cos, sin);
+  const Turn<W> turn{co + (t * 16 + 8) * W + w, on};
   for (int h = max(h0, r.heads) - r.heads + g; h < h1 - r.heads; h += side) {
     const uint16_t *k = r.src[1] + i * r.stride[1] + h * DIM, *v = r.src[2] + i * r.stride[2] + h * DIM;
     Chunks kx, vx;
@@ -266,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const Rot
     kx.c[1] = *reinterpret_cast<const uint4*>(k + 8 * c1);
     vx.c[0] = *reinterpret_cast<const uint4*>(v + 16 * w);
     vx.c[1] = *reinterpret_cast<const uint4*>(v + 16 * w + 8);
-    kx = turned<W, INTERLEAVED>(kx, r.weight[1], r.eps, on, turn, lanes);
+    kx = turned<W, INTERLEAVED>(kx, r.weight[1], r.eps, turn, lanes);
     if (!INTERLEAVED) {
       // the quantisation takes a head's elements in order: chunks 2 w and 2 w + 1, from where they are
       Chunks z;
@@ -300,11 +289,11 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_rotary_kernel(const Rot
 }
 
 // Heads side by side: what makes 512 bytes of a token, so that a thread makes
-// the most of its token's angles and loads stay long, or more where that leaves
-// SMs without CTAs; then the heads are divided, too. (Measured, us: 4096 tokens
-// of 16 heads over 2 of 256 dims, one side by side 16.9, two 18.1, four 22.0;
-// 14593 tokens of 32 over 8 of 128, one 79, two 67, four 68, eight 73; 3282
-// tokens of 8 over 4 of 64, two 7.7, four 5.8, eight 8.1.)
+// the most of its token's factors and loads stay long, or more where that leaves
+// SMs without CTAs; then the heads are divided, too. (Measured with four heads'
+// loads in flight, us: 4096 tokens of 16 heads over 2 of 256 dims, one side by side
+// 16.9, two 18.1, four 22.0; 14593 tokens of 32 over 8 of 128, one 79, two 67, four
+// 68, eight 73; 3282 tokens of 8 over 4 of 64, two 7.7, four 5.8, eight 8.1.)
 template <int DIM>
 cudaError_t launch(RotaryArgs r, const KvCall& c) {
   constexpr int kRows = kThreads / (DIM / 16);
@@ -317,7 +306,7 @@ cudaError_t launch(RotaryArgs r, const KvCall& c) {
   const int tokens = kRows >> r.lanes_log;
   const dim3 grid(ctas(), (heads + r.part - 1) / r.part);
   (r.interleaved ? kv_append_rotary_kernel<DIM, true> : kv_append_rotary_kernel<DIM, false>)<<<
-      grid, kThreads, tokens * r.half * sizeof(float2), c.stream>>>(r);
+      grid, kThreads, tokens * 16 * (DIM / 16) * sizeof(float4), c.stream>>>(r);
   return c.launched("kv_append_rotary");
 }
 
