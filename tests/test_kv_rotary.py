@@ -121,6 +121,11 @@ CASES = [
     (64, 32, 64, 1, [301], [400], 256, False, 1, False),
     (128, 112, 2, 2, [9, 8, 7], [9, 800, 70], 16, False, 3, True),
     (256, 192, 2, 2, [600], [600], 64, True, 1, True),
+    (128, 128, 32, 8, [2001, 0, 2999], [2001, 7, 3500], 16, False, 1, True),
+    (256, 256, 40, 8, [1, 2], [400, 2], 32, False, 1, True),
+    (64, 48, 40, 8, [1], [65], 16, True, 2, True),
+    (64, 64, 7, 7, [900], [1000], 64, False, 1, True),
+    (256, 16, 1, 1, [3] * 40, [3 + 5 * i for i in range(40)], 16, False, 1, False),
 ]
 
 
