@@ -56,7 +56,7 @@ struct PrefixArgs {
 };
 
 constexpr int kPlanThreads = 256;
-constexpr int kFew = 8;
+constexpr int kFew = 8, kNone = 0x7fffffff;
 constexpr int kBadGroups = 204;  // detail in the status word
 
 // Marks the tokens of the warp's sequences (one per lane: n tokens from q0 on): a few at once, more of them by the warp,
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
     p.group_off[g] = t0;
     if (g == p.n_groups - 1) p.group_off[g + 1] = t1;
     (TOGETHER ? p.shared_len : p.group_len)[g] = whole_pages(len);
-    p.group_row[g] = ok ? min(s0, a.n_seqs - 1) : 0;
+    p.group_row[g] = kNone;
     if (TOGETHER) {
       p.seqs[g] = s0;
       if (g == p.n_groups - 1) p.seqs[g + 1] = s1;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
       if (!TOGETHER) {
         p.group_len[g] = -1;  // the kernels leave it out
       } else {  // one group of all sequences, and empty ones (offsets out of order: nothing is done)
-        p.shared_len[g] = p.group_row[g] = 0;
+        p.shared_len[g] = 0;
         p.group_off[g + 1] = off ? 0 : a.n_tokens;
         p.seqs[g + 1] = a.n_seqs;
         if (g == 0) p.group_off[0] = p.seqs[0] = 0;
@@ -134,13 +134,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
   for (int c0 = 0; c0 < a.n_seqs; c0 += kPlanThreads) {
     const int b = c0 + b0;
     bool flag = false;
-    int n = 0, tiles = 0;
+    int n = 0, tiles = 0, group = 0;
     if (b < a.n_seqs) {
       if (c0 > 0) q0 = a.q_off[b], q1 = a.q_off[b + 1], kv = a.kv_len[b];
       n = q1 - q0;
       int skip = 0;
       if (!bad && kv <= a.max_kv) {
-        const int len = whole_pages(p.length[group_of(p, b)]);
+        group = group_of(p, b);
+        const int len = whole_pages(p.length[group]);
         if (kv - n >= len) skip = len;
       }
       int own = kv < 0 || kv > a.max_kv ? -1 : kv - skip;
@@ -156,6 +157,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
       }
       p.skip[b] = skip;
       p.own_len[b] = own;
+      // the shared positions are read through the first sequence that attends to them: others may have ended, their pages gone
+      if (in && skip > 0 && n > 0) atomicMin(p.group_row + group, b);
     }
     if (TOGETHER) {
       int s = tiles;
@@ -177,12 +180,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attention_prefix_plan_kernel(
     }
     if (TOGETHER ? !off : !bad) mark(p.shares, q0, n, flag);  // (else no token is looked at)
   }
-  if (TOGETHER) {
-    __syncthreads();
-    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+  __syncthreads();
+  for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+    const bool none = __ldcg(p.group_row + g) == kNone;  // nobody shares
+    if (none) p.group_row[g] = 0;
+    if (TOGETHER) {
+      if (none) p.shared_len[g] = 0;
       const int s0 = __ldcg(p.seqs + g), s1 = __ldcg(p.seqs + g + 1);
-      const int shared = (__ldcg(p.shared_len + g) + kKeyTile - 1) / kKeyTile;
+      const int shared = none ? 0 : (__ldcg(p.shared_len + g) + kKeyTile - 1) / kKeyTile;
       p.group_len[g] = off ? -1 : (shared + __ldcg(p.own_tile + s1) - __ldcg(p.own_tile + s0)) * kKeyTile;
+    } else if (none && !bad) {
+      p.group_len[g] = 0;
     }
   }
 }

@@ -550,7 +550,8 @@ moe_status moe_kv_copy_pages(const moe_kv_cache* const* caches, int n_caches, co
  *            .. seq_off[g + 1] - 1; ascending, from 0 to n_seqs
  *   length   device int32 [n_groups]: how many first positions the group shares;
  *            of these the whole pages count. They are read through the table
- *            of the group's first sequence.
+ *            row of its first sequence that has step tokens behind them, so
+ *            that others may have ended.
  *   max_tokens  upper bound of a group's step tokens
  *   max_len     upper bound of the lengths
  *   max_own     upper bound of kv_len less its group's shared positions in whole pages

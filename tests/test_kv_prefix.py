@@ -256,6 +256,33 @@ def test_sequences_that_begin_inside_the_shared_part_are_on_their_own(heads, new
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,new", [(8, [1, 3, 1]), (16, [70, 60, 90])])
+def test_sequences_that_ended_and_groups_of_which_nobody_shares(dim, heads, new, each_path):
+    """A group's first sequence has ended and its pages are gone, or is there without step tokens, or all begin inside."""
+    groups = [(160, [(0, 0), (new[0], new[0] + 8), (new[1], new[1])]), (96, [(0, 7), (0, 3), (new[2], 99)]),
+              (400, [(new[0], new[0]), (new[1], new[1])]), (64, [(0, 0), (0, 0)])]
+    batch = Shared(groups, 16)
+    batch.kv[6], batch.kv[7] = 70, 90  # inside the shared 400
+    cache = junk_cache(moe, batch.n_pages, 16, 2, dim)
+    held = share(cache, batch, fill(cache, batch))
+    table = batch.table.copy()
+    batch.kv[0] = batch.kv[3] = batch.kv[8] = batch.kv[9] = 0
+    table[[0, 3, 8, 9]] = -1
+    dev = batch.device(moe, max_kv=1000)
+    dev._t[2].copy_(torch.from_numpy(table))
+    for per_seq in held:
+        for b in (0, 3, 8, 9):
+            per_seq[b] = per_seq[b][:0]
+    q = rows(batch.n_tokens, heads, dim)
+    ref = attention_reference(q, batch, *held, float(np.float32(dim ** -0.5)))
+    for path in each_path():
+        out, lse = cache.attention(q, dev, lse=True, prefix=batch.prefix(max_own=600))
+        cache.check()
+        check_attention(out, lse, ref, path)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads,new", [(8, [1, 3, 1]), (16, [40, 30, 60])])
 def test_groups_out_of_order_or_past_their_bounds_share_nothing(heads, new, each_path):
     batch = Shared([(160, [(new[0], new[0] + 8), (new[1], new[1])]), (64, [(new[2], 99)])], 16)
