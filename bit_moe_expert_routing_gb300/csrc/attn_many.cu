@@ -9,7 +9,10 @@
 //            the workspace, laid out exactly as the MMA reads shared memory
 //            (128-byte-swizzled, keys K-major; values transposed, so K-major
 //            in the second product too), each tile as the halves that the two
-//            CTAs of a pair keep. It stays in L2.
+//            CTAs of a pair keep. It stays in L2. A tile's codes, scales and
+//            biases are taken into shared memory first, all at once: by rows of
+//            the cache they come in 16-byte pieces, and the transposed chunks of
+//            the values are then eight keys of one word each.
 //            One extra CTA cuts the work (below).
 //   many     S = Q K^T per 128-row tile and 128 keys into tensor memory, the
 //            softmax warps turn it into P (bf16, there too), O += P V with
@@ -58,6 +61,11 @@
 // ALU 30%, issue slots 36%, tensor cores 19%. A row tile of 512 rows meets six key tiles
 // and the sinks', and every S tile's chain of product, softmax and hand-over stands
 // in line, as do each segment's set-up and output; SMs are active in 79% of the time.
+//
+// Groups of sequences that share their first positions may be taken as one
+// sequence each (kTogether): the positions of all of them are key tiles one behind
+// the other, and a row's mask is that of a window with sinks, the window from its
+// sequence's own positions on.
 //
 // Probabilities meet the values as bf16: the products take both operands in one
 // type, and the values are bf16. Each is rounded by 2^-9 at most, after the sum

@@ -127,8 +127,8 @@ struct PartArgs : AttnArgs {
   const int32_t* shared_len;  // [groups] shared positions
 };
 
-// The kernels are compiled for whole calls and for PARTS apart: what the latter
-// need cost the former registers, and their longer arguments 0.1 to 0.5 us.
+// The kernels are compiled for whole calls and for PARTS apart, each with its own
+// arguments: what the latter need cost the former registers.
 template <bool PARTS>
 using Attn = std::conditional_t<PARTS, PartArgs, AttnArgs>;
 // (of the kernels compiled for PARTS)
